@@ -27,6 +27,9 @@ GD_OK, GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_EHIP, GD_ERANGE = 0, -1, -2, -3, -4, 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
+_I32 = ctypes.c_int32
+_SZ = ctypes.c_size_t
 
 
 class GemmDecodeError(RuntimeError):
@@ -45,6 +48,24 @@ class TernaryProblem(ctypes.Structure):
     """gd_ternary_problem: one problem of ternary_gemv_grouped."""
     _fields_ = [("w_pos", _P), ("w_neg", _P), ("x_planes", _P), ("y", _P),
                 ("dot_out", _P), ("w_scale", _F32), ("x_scale", _F32), ("x_scale_dev", _P)]
+
+
+class _KVQ8(ctypes.Structure):
+    """gd_kv_q8."""
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("n_pages", _I64),
+                ("page_size", _I64), ("n_kv_heads", _I64), ("head_dim", _I64)]
+
+
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_LLAMA3 = range(5)
+
+
+class RopeScaling(ctypes.Structure):
+    """gd_rope_scaling: how rope_table scales the rotary frequencies for long contexts."""
+    _fields_ = [("kind", _I32), ("reserved", _I32), ("factor", _F64), ("original_len", _F64), ("low", _F64),
+                ("high", _F64), ("attention", _F64)]
+
+    def __init__(self, kind, factor=1.0, original_len=0.0, low=0.0, high=0.0, attention=0.0):
+        super().__init__(kind, 0, factor, original_len, low, high, attention)
 
 
 def _declare():
@@ -75,6 +96,16 @@ def _declare():
         "attn_decode_splitk": [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _F32, _I64, _P, ctypes.c_size_t, _P],
         "attn_decode_splitk_noalloc": [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _F32, _I64, _P],
         "ternary_quantize_act": [_P, _I64, _I64, _P, _P, _P],
+        "rmsnorm_q8_0": [_P, _P, _P, _P, _P, _I64, _I64, _F32, _I32, _P],
+        "rmsnorm_ternary_act": [_P, _P, _P, _P, _P, _P, _I64, _I64, _F32, _I32, _P],
+        "q8_0_dequantize": [_P, _P, _I64, _I64, _I32, _P],
+        "ternary_dequantize_act": [_P, _P, _P, _I64, _I64, _I32, _P],
+        "rope_table": [_P, _I64, _I64, _F64, _P, _P],
+        "kv_q8_store": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I32, _P, _P, _I64, _I64, _I32, _P],
+        "kv_q8_load": [_P, _P, _P, _P, _I64, _I32, _P],
+        "attn_decode_q8": [_P, _P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _F32, _F32, _I32, _P, _SZ,
+                           _P],
+        "attn_decode_q8_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_SZ)],
         "gemm_decode_fill": [_P, ctypes.c_size_t, ctypes.c_uint32, _P],
         "gemm_decode_stream_read": [_P, ctypes.c_size_t, ctypes.c_int32, _P, _I64, _P],
     }
@@ -367,6 +398,240 @@ def attn_decode_splitk_noalloc(q, k_cache, v_cache, out, n_heads: int, n_kv_head
                                            _dev(out, torch.float32, n_heads * head_dim, "out"),
                                            n_heads, n_kv_heads, head_dim, kv_len, kv_stride, float(scale),
                                            num_splits, _stream()))
+
+
+# -------------------------------------------- norm with an 8-bit output
+
+_dtype_code = {}
+
+
+def _dtype(t, name):
+    """The GD_F32 / GD_F16 / GD_BF16 code of a tensor's type."""
+    if not _dtype_code:
+        import torch
+        _dtype_code.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    try:
+        return _dtype_code[t.dtype]
+    except (KeyError, AttributeError):
+        raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor") from None
+
+
+def _current():
+    """(index of the current device, torch's current stream on it)."""
+    import torch
+    i = torch.cuda.current_device()
+    return i, torch.cuda.current_stream(i).cuda_stream
+
+
+def _on(index, t, dtype, numel, name):
+    """data_ptr of a contiguous tensor of this type and size on device `index`, the one the call launches on."""
+    p = _dev(t, dtype, numel, name)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
+    return p
+
+
+def rmsnorm_q8_0(x, residual, weight, h_out, a_q8, n: int, K: int, eps: float):
+    """h = x + residual, and the RMS norm of h times `weight` as q8_0 blocks
+    (uint8 [n * K/32 * 34], what q1_q8_gemv reads). x, residual (or None) and
+    h_out (or None; may be x or residual) are [n, K] of one type (float32,
+    float16, bfloat16); weight float32 [K]."""
+    import torch
+    dt, (i, stream) = _dtype(x, "x"), _current()
+    _check(_lib.rmsnorm_q8_0(_on(i, x, x.dtype, n * K, "x"),
+                             None if residual is None else _on(i, residual, x.dtype, n * K, "residual"),
+                             _on(i, weight, torch.float32, K, "weight"),
+                             None if h_out is None else _on(i, h_out, x.dtype, n * K, "h_out"),
+                             _on(i, a_q8, torch.uint8, n * (K // 32) * 34 if K % 32 == 0 else None, "a_q8"),
+                             n, K, eps, dt, stream))
+
+
+def rmsnorm_ternary_act(x, residual, weight, h_out, planes, x_scale, n: int, K: int, eps: float):
+    """rmsnorm_q8_0 with one scale per row: int8 bit planes (int32
+    [n * 8 * K/32]) and scales (float32 [n]), what ternary_gemv reads."""
+    import torch
+    dt, (i, stream) = _dtype(x, "x"), _current()
+    _check(_lib.rmsnorm_ternary_act(_on(i, x, x.dtype, n * K, "x"),
+                                    None if residual is None else _on(i, residual, x.dtype, n * K, "residual"),
+                                    _on(i, weight, torch.float32, K, "weight"),
+                                    None if h_out is None else _on(i, h_out, x.dtype, n * K, "h_out"),
+                                    _on(i, planes, torch.int32, n * 8 * (K // 32) if K % 32 == 0 else None, "planes"),
+                                    _on(i, x_scale, torch.float32, n, "x_scale"), n, K, eps, dt, stream))
+
+
+def q8_0_dequantize(a_q8, y, n: int, K: int):
+    """The values of q8_0 blocks: y [n, K] (float32, float16 or bfloat16)."""
+    import torch
+    dt, (i, stream) = _dtype(y, "y"), _current()
+    _check(_lib.q8_0_dequantize(_on(i, a_q8, torch.uint8, n * (K // 32) * 34 if K % 32 == 0 else None, "a_q8"),
+                                _on(i, y, y.dtype, n * K, "y"), n, K, dt, stream))
+
+
+def ternary_dequantize_act(planes, x_scale, y, n: int, K: int):
+    """The values of int8 bit planes and scales: y [n, K]."""
+    import torch
+    dt, (i, stream) = _dtype(y, "y"), _current()
+    _check(_lib.ternary_dequantize_act(_on(i, planes, torch.int32, n * 8 * (K // 32) if K % 32 == 0 else None, "planes"),
+                                       _on(i, x_scale, torch.float32, n, "x_scale"), _on(i, y, y.dtype, n * K, "y"),
+                                       n, K, dt, stream))
+
+
+# ------------------------------------------------------------ 8-bit cache
+
+class KVCacheQ8:
+    """A pool of pages of 8-bit keys and values (gd_kv_q8): codes int8
+    [n_pages, n_kv_heads, page_size, head_dim] and scales float16
+    [n_pages, n_kv_heads, page_size, head_dim/32] for keys and for values. The
+    handle checks the four tensors once and keeps them alive."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        import torch
+        if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+            raise ValueError("k_codes must be [n_pages, n_kv_heads, page_size, head_dim]")
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_codes.shape
+        n = k_codes.numel()
+        codes = [_dev(t, torch.int8, n, name) for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes"))]
+        scales = [_dev(t, torch.float16, n // 32, name) for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales"))]
+        self.device = k_codes.device
+        if any(t.device != self.device for t in (k_scales, v_codes, v_scales)):
+            raise ValueError("the cache's planes must be on one device")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self._c = _KVQ8(codes[0], scales[0], codes[1], scales[1], self.n_pages, self.page_size, self.n_kv_heads,
+                        self.head_dim)
+        self._ref = ctypes.addressof(self._c)
+
+    def _on(self, index):
+        if self.device.index != index:
+            raise ValueError(f"the cache is on {self.device}, the current device is cuda:{index}")
+        return self._ref
+
+
+def kv_q8_alloc(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda") -> KVCacheQ8:
+    """Allocates a cache pool (contents undefined until stored)."""
+    import torch
+    shape = (n_pages, n_kv_heads, page_size)
+    codes = [torch.empty(shape + (head_dim,), dtype=torch.int8, device=device) for _ in range(2)]
+    scales = [torch.empty(shape + (head_dim // 32,), dtype=torch.float16, device=device) for _ in range(2)]
+    return KVCacheQ8(codes[0], scales[0], codes[1], scales[1])
+
+
+def rope_table(table, n_pos: int, rot_dim: int, base: float = 10000.0, scaling: RopeScaling = None):
+    """Fills table (float32 [n_pos, rot_dim/2, 2]) with the (cos, sin) of every
+    position's rotary angles, frequencies scaled by `scaling` if given."""
+    import torch
+    i, stream = _current()
+    if scaling is not None and not isinstance(scaling, RopeScaling):
+        raise TypeError("scaling must be a RopeScaling")
+    _check(_lib.rope_table(_on(i, table, torch.float32, n_pos * (rot_dim // 2) * 2, "table"), n_pos, rot_dim, base,
+                           None if scaling is None else ctypes.addressof(scaling), stream))
+
+
+def _token_rows(i, t, dtype, n_tok, width, name):
+    """(data_ptr, stride between tokens) of a tensor of n_tok rows of `width`
+    elements: [n_tok, width] or [n_tok, heads, head_dim], each row contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != i:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{i}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3:
+        rows, inner = shape[1] * shape[2], strides[2] == 1 and (strides[1] == shape[2] or shape[1] == 1)
+    elif len(shape) == 2:
+        rows, inner = shape[1], strides[1] == 1
+    else:
+        raise ValueError(f"{name} must be [n_tok, heads, head_dim] or [n_tok, heads * head_dim]")
+    if shape[0] != n_tok or rows != width:
+        raise ValueError(f"{name} must hold {n_tok} rows of {width} elements, got {tuple(shape)}")
+    if not inner:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), strides[0] if n_tok > 1 else width
+
+
+def kv_q8_store(cache: KVCacheQ8, k, v, slots, n_tok: int, q=None, q_out=None, n_heads: int = 0, rope=None,
+                positions=None, interleaved: bool = False):
+    """Rotates q and k (rope from rope_table, positions int32 [n_tok]; both or
+    neither), writes q_out, and stores k and v in the cache at `slots` (int64
+    [n_tok]; -1: not stored). q, k and v may be parts of one projection's rows
+    (token strides are free); q_out [n_tok, n_heads, head_dim] may be q."""
+    import torch
+    dt, (i, stream) = _dtype(k, "k"), _current()
+    ref, D = cache._on(i), cache.head_dim
+    kp, ks = _token_rows(i, k, k.dtype, n_tok, cache.n_kv_heads * D, "k")
+    vp, vs = _token_rows(i, v, k.dtype, n_tok, cache.n_kv_heads * D, "v")
+    qp = qo = None
+    qs = 0
+    if n_heads:
+        qp, qs = _token_rows(i, q, k.dtype, n_tok, n_heads * D, "q")
+        qo = _on(i, q_out, k.dtype, n_tok * n_heads * D, "q_out")
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out need n_heads")
+    rp = pp = None
+    n_pos = rot = 0
+    if rope is not None:
+        rp = _on(i, rope, torch.float32, None, "rope")
+        if rope.dim() != 3 or rope.shape[2] != 2:
+            raise ValueError("rope must be [n_pos, rot_dim/2, 2]")
+        n_pos, rot = rope.shape[0], 2 * rope.shape[1]
+    if positions is not None:
+        pp = _on(i, positions, torch.int32, n_tok, "positions")
+    _check(_lib.kv_q8_store(ref, qp, qs, kp, ks, vp, vs, qo, rp, n_pos, rot, bool(interleaved), pp,
+                            _on(i, slots, torch.int64, n_tok, "slots"), n_tok, n_heads, dt, stream))
+
+
+def kv_q8_load(cache: KVCacheQ8, slots, k_out, v_out, n_tok: int):
+    """The cached rows at `slots` (int64 [n_tok]; outside the pool: zeros) as
+    k_out and v_out [n_tok, n_kv_heads, head_dim]; either may be None."""
+    import torch
+    one = v_out if k_out is None else k_out
+    dt, (i, stream) = _dtype(one, "k_out" if k_out is not None else "v_out"), _current()
+    n = n_tok * cache.n_kv_heads * cache.head_dim
+    _check(_lib.kv_q8_load(cache._on(i), _on(i, slots, torch.int64, n_tok, "slots"),
+                           None if k_out is None else _on(i, k_out, one.dtype, n, "k_out"),
+                           None if v_out is None else _on(i, v_out, one.dtype, n, "v_out"), n_tok, dt, stream))
+
+
+def attn_decode_q8_workspace_bytes(n_seqs: int, n_q: int, n_heads: int, n_kv_heads: int, head_dim: int, max_q: int,
+                                   max_kv_len: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.attn_decode_q8_workspace_bytes(n_seqs, n_q, n_heads, n_kv_heads, head_dim, max_q, max_kv_len,
+                                               ctypes.byref(b)))
+    return b.value
+
+
+def attn_decode_q8(q, cache: KVCacheQ8, page_table, kv_lens, q_start, tree_mask, out, n_heads: int, max_q: int,
+                   max_kv_len: int, scale: float, softcap: float = 0.0, workspace=None):
+    """Attention of each sequence's last tokens over the 8-bit cache. q and out
+    are [n_q, n_heads, head_dim]; page_table int32 [n_seqs, max_pages] or None
+    (sequence b is page b); kv_lens int32 [n_seqs]; q_start int32 [n_seqs + 1]
+    or None (max_q rows per sequence); tree_mask int64 [n_q] (the bits of each
+    word: the drafted tokens of its sequence that the row sees) or None (a
+    chain). The workspace (uint8) is allocated here when not given."""
+    import torch
+    dt, (i, stream) = _dtype(q, "q"), _current()
+    ref, D = cache._on(i), cache.head_dim
+    lens = _on(i, kv_lens, torch.int32, None, "kv_lens")
+    n_seqs = kv_lens.numel()
+    n_q, rest = divmod(q.numel(), n_heads * D) if n_heads > 0 else (0, 1)
+    if rest or n_q == 0:
+        raise ValueError(f"q must be [n_q, {n_heads}, {D}], got {tuple(q.shape)}")
+    n = n_q * n_heads * D
+    table, max_pages = None, 1
+    if page_table is not None:
+        table = _on(i, page_table, torch.int32, None, "page_table")
+        if page_table.dim() != 2 or page_table.shape[0] != n_seqs:
+            raise ValueError(f"page_table must be [{n_seqs}, max_pages], got {tuple(page_table.shape)}")
+        max_pages = page_table.shape[1]
+    need = attn_decode_q8_workspace_bytes(n_seqs, n_q, n_heads, cache.n_kv_heads, D, max_q, max_kv_len)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(_lib.attn_decode_q8(ref, _on(i, q, q.dtype, n, "q"), _on(i, out, q.dtype, n, "out"), table, max_pages, lens,
+                               None if q_start is None else _on(i, q_start, torch.int32, n_seqs + 1, "q_start"),
+                               None if tree_mask is None else _on(i, tree_mask, torch.int64, n_q, "tree_mask"),
+                               n_seqs, n_q, n_heads, max_q, max_kv_len, scale, softcap, dt,
+                               _on(i, workspace, torch.uint8, None, "workspace"), workspace.numel(), stream))
 
 
 # ------------------------------------------------------------ measurement

@@ -33,6 +33,9 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t *out) {
     return true;
 }
 
+// The checks every entry point makes of an 8-bit cache's description.
+int check_kv_q8(const gd_kv_q8 *cache, const char *name);
+
 // Checks the launch that was just enqueued.
 int check_launch(const char *what);
 

@@ -1,0 +1,284 @@
+// norm_quant.hip -- root-mean-square norm with the residual's addition and an
+// 8-bit output: the step between the residual stream and a product, in the
+// activation formats of the products (q8_0 blocks for q1_q8_gemv, per-token
+// int8 bit planes for ternary_gemv), and the readers of those formats.
+//
+// With h = x + residual (rounded to the stream's type), p = h * w and
+// rstd = 1 / sqrt(mean h^2 + eps), the norm is y = rstd * p. The quantization
+// rule rounds y times 127 over max|y|: rstd divides out, so the codes depend on p
+// alone and only the scale, max|p| * rstd / 127, needs the row's sum. p is a
+// product of two f32 values, exact in f64, and the sum of squares is taken in
+// f64, so codes and scales do not depend on the order of the sum (up to f64's
+// own rounding, 2^-29 of an f32 step).
+#include "gd_internal.h"
+#include "gd_quant.h"
+#include "gd_types.h"
+
+namespace {
+
+using namespace gd;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int64_t kMaxThreads = (INT64_C(1) << 32) - 1;   // of one launch
+
+// h = x + residual of four elements, as stored; both terms are read before h
+// is written, so h may overwrite either.
+template <typename T>
+__device__ __forceinline__ f32x4 load_h(const T *x, const T *res, int64_t e4) {
+    f32x4 v = load4(x + 4 * e4);
+    if (res) v = round_to<T>(v + load4(res + 4 * e4));
+    return v;
+}
+
+__device__ __forceinline__ double square4(f32x4 h) {
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) s = __builtin_fma(static_cast<double>(h[j]), static_cast<double>(h[j]), s);
+    return s;
+}
+
+struct Products {
+    double p[4];
+    __device__ __forceinline__ Products(f32x4 h, f32x4 w) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) p[j] = static_cast<double>(h[j]) * static_cast<double>(w[j]);
+    }
+    __device__ __forceinline__ double absmax() const {
+        return fmax(fmax(fabs(p[0]), fabs(p[1])), fmax(fabs(p[2]), fabs(p[3])));
+    }
+    // Byte j: the code of element j under the rule, inv = factor_of(absmax).
+    __device__ __forceinline__ uint32_t codes(double inv) const {
+        uint32_t packed = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++) packed |= (static_cast<uint32_t>(round_code(p[j] * inv)) & 0xffu) << (8 * j);
+        return packed;
+    }
+};
+
+__device__ __forceinline__ double shfl_xor_f64(double v, int o) { return __shfl_xor(v, o); }
+
+__device__ __forceinline__ double max8d(double v) {   // max over the eight lanes of a block
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) v = fmax(v, shfl_xor_f64(v, o));
+    return v;
+}
+
+// Sum and max over the workgroup (every thread gets both).
+__device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*red)[2]) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        sum += shfl_xor_f64(sum, o);
+        mx = fmax(mx, shfl_xor_f64(mx, o));
+    }
+    if (threadIdx.x % 64 == 0) {
+        red[threadIdx.x / 64][0] = sum;
+        red[threadIdx.x / 64][1] = mx;
+    }
+    __syncthreads();
+    sum = (red[0][0] + red[1][0]) + (red[2][0] + red[3][0]);
+    mx = fmax(fmax(red[0][1], red[1][1]), fmax(red[2][1], red[3][1]));
+}
+
+// One workgroup per row; thread t holds float4s t, t + 256, ... of it, the
+// first R of them in registers (rows of up to 1024 R elements are read once);
+// what is past them is read again in the second pass, from h_out if that is
+// written (it may overwrite an input), each thread reading back its own.
+template <typename T, int R, bool kTernary>
+__global__ __launch_bounds__(kThreads) void rmsnorm_quant_kernel(const T *x, const T *res, const float *__restrict__ weight,
+                                                                 T *h_out, void *__restrict__ out,
+                                                                 float *__restrict__ x_scale, int64_t K, float eps) {
+    __shared__ double red[kWaves][2];
+    const int64_t row = blockIdx.x;
+    const int64_t nq = K / 4;
+    x += row * K;
+    if (res) res += row * K;
+    if (h_out) h_out += row * K;
+    f32x4 h[R];
+    double ss = 0.0, amax = 0.0;
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+        const int64_t e4 = i * kThreads + static_cast<int64_t>(threadIdx.x);
+        h[i] = load_h(x, res, e4 < nq ? e4 : nq - 1);   // clamped: issued, not used
+    }
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+        const int64_t e4 = i * kThreads + static_cast<int64_t>(threadIdx.x);
+        if (e4 < nq) {
+            if (h_out) store4(h_out + 4 * e4, h[i]);
+            ss += square4(h[i]);
+            if (kTernary) amax = fmax(amax, Products(h[i], load4(weight + 4 * e4)).absmax());
+        }
+    }
+    for (int64_t e4 = R * kThreads + static_cast<int64_t>(threadIdx.x); e4 < nq; e4 += kThreads) {
+        const f32x4 v = load_h(x, res, e4);
+        if (h_out) store4(h_out + 4 * e4, v);
+        ss += square4(v);
+        if (kTernary) amax = fmax(amax, Products(v, load4(weight + 4 * e4)).absmax());
+    }
+    group_sum_max(ss, amax, red);
+    const double rstd = 1.0 / sqrt(ss / static_cast<double>(K) + static_cast<double>(eps));
+    const double row_inv = factor_of(amax);
+    if (kTernary && threadIdx.x == 0) x_scale[row] = static_cast<float>(amax * rstd / 127.0);
+    const int lane = threadIdx.x % 64, k8 = lane % 8;
+    const NibbleTranspose tr(k8);
+    const int64_t W = K / 32;
+    const auto finish = [&](f32x4 v, int64_t e4) {   // whole groups of eight lanes come here together
+        const Products pr(v, load4(weight + 4 * e4));
+        if constexpr (kTernary) {
+            const uint32_t w = tr(bits_to_nibbles(pr.codes(row_inv)));
+            static_cast<uint32_t *>(out)[(row * 8 + k8) * W + e4 / 8] = w;
+        } else {
+            const double a = max8d(pr.absmax());
+            const uint32_t packed = pr.codes(factor_of(a));
+            uint16_t *o = static_cast<uint16_t *>(out) + (row * W + e4 / 8) * 17;   // 34 bytes = 17 halves
+            o[1 + 2 * k8] = static_cast<uint16_t>(packed & 0xffffu);
+            o[2 + 2 * k8] = static_cast<uint16_t>(packed >> 16);
+            if (k8 == 0) {
+                const _Float16 d = static_cast<_Float16>(static_cast<float>(a * rstd / 127.0));
+                o[0] = __builtin_bit_cast(uint16_t, d);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+        const int64_t e4 = i * kThreads + static_cast<int64_t>(threadIdx.x);
+        if (e4 < nq) finish(h[i], e4);
+    }
+    for (int64_t e4 = R * kThreads + static_cast<int64_t>(threadIdx.x); e4 < nq; e4 += kThreads)
+        finish(h_out ? load4(h_out + 4 * e4) : load_h(x, res, e4), e4);
+}
+
+// ------------------------------------------------------------- readers
+// Four elements per thread: code * scale, one f32 product, rounded to T.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void q8_0_dequantize_kernel(const uint16_t *__restrict__ a, T *__restrict__ y,
+                                                                   int64_t quads) {
+    const int64_t gid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (gid >= quads) return;
+    const uint16_t *b = a + (gid / 8) * 17;
+    const int k8 = static_cast<int>(gid % 8);
+    const float d = static_cast<float>(__builtin_bit_cast(_Float16, b[0]));
+    const uint32_t lo = b[1 + 2 * k8], hi = b[2 + 2 * k8];
+    const f32x4 c = {static_cast<float>(static_cast<int8_t>(lo)), static_cast<float>(static_cast<int8_t>(lo >> 8)),
+                     static_cast<float>(static_cast<int8_t>(hi)), static_cast<float>(static_cast<int8_t>(hi >> 8))};
+    store4(y + 4 * gid, c * d);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void ternary_dequantize_kernel(const uint32_t *__restrict__ planes,
+                                                                      const float *__restrict__ x_scale,
+                                                                      T *__restrict__ y, int64_t K, int64_t quads) {
+    const int64_t gid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (gid >= quads) return;
+    const int64_t row = gid / (K / 4), e4 = gid % (K / 4), W = K / 32;
+    const uint32_t *p = planes + row * 8 * W + e4 / 8;
+    const int sh = static_cast<int>(e4 % 8) * 4;
+    int32_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int b = 0; b < 8; b++) {
+        const uint32_t n = p[b * W] >> sh;
+#pragma unroll
+        for (int j = 0; j < 4; j++) c[j] |= static_cast<int32_t>((n >> j) & 1u) << b;
+    }
+    const float s = x_scale[row];
+    f32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = static_cast<float>(static_cast<int8_t>(c[j])) * s;
+    store4(y + 4 * gid, v);
+}
+
+int check_norm(const char *name, const void *x, const void *residual, const float *weight, const void *h_out, int64_t n,
+               int64_t K, float eps, int32_t dtype) {
+    GD_REQUIRE(x && weight, GD_EINVAL, "%s: null pointer", name);
+    GD_REQUIRE(n >= 1 && K >= 1, GD_EINVAL, "%s: n (%lld) and K (%lld) must be >= 1", name, (long long)n, (long long)K);
+    GD_REQUIRE(dtype_ok(dtype), GD_EINVAL, "%s: unknown dtype %d", name, dtype);
+    GD_REQUIRE(eps >= 0.0f && eps <= 3.40282347e38f, GD_EINVAL, "%s: eps must be finite and >= 0", name);
+    GD_REQUIRE(K % 32 == 0, GD_ESHAPE, "%s: K (%lld) must be a multiple of 32", name, (long long)K);
+    GD_REQUIRE(n <= kMaxThreads / kThreads && K <= (INT64_C(1) << 30), GD_ERANGE, "%s: n or K too large", name);
+    GD_REQUIRE(aligned(x, 16) && aligned(residual, 16) && aligned(weight, 16) && aligned(h_out, 16), GD_EALIGN,
+               "%s: x, residual, weight and h_out must be 16-byte aligned", name);
+    return GD_OK;
+}
+
+template <bool kTernary>
+void launch_norm(const void *x, const void *residual, const float *weight, void *h_out, void *out, float *x_scale,
+                 int64_t n, int64_t K, float eps, int32_t dtype, hipStream_t hs) {
+    const dim3 grid(static_cast<uint32_t>(n)), block(kThreads);
+    dispatch_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        const T *xt = static_cast<const T *>(x), *rt = static_cast<const T *>(residual);
+        T *ht = static_cast<T *>(h_out);
+        if (K <= 1024 * 4)
+            hipLaunchKernelGGL((rmsnorm_quant_kernel<T, 4, kTernary>), grid, block, 0, hs, xt, rt, weight, ht, out,
+                               x_scale, K, eps);
+        else
+            hipLaunchKernelGGL((rmsnorm_quant_kernel<T, 8, kTernary>), grid, block, 0, hs, xt, rt, weight, ht, out,
+                               x_scale, K, eps);
+    });
+}
+
+int check_reader(const char *name, const void *in, const void *y, int64_t n, int64_t K, int32_t dtype, int64_t *quads) {
+    GD_REQUIRE(in && y, GD_EINVAL, "%s: null pointer", name);
+    GD_REQUIRE(n >= 1 && K >= 1, GD_EINVAL, "%s: n (%lld) and K (%lld) must be >= 1", name, (long long)n, (long long)K);
+    GD_REQUIRE(dtype_ok(dtype), GD_EINVAL, "%s: unknown dtype %d", name, dtype);
+    GD_REQUIRE(K % 32 == 0, GD_ESHAPE, "%s: K (%lld) must be a multiple of 32", name, (long long)K);
+    GD_REQUIRE(mul_ok(n, K / 4, quads) && *quads <= kMaxThreads - kThreads, GD_ERANGE, "%s: n * K too large", name);
+    GD_REQUIRE(aligned(y, 16), GD_EALIGN, "%s: y must be 16-byte aligned", name);
+    return GD_OK;
+}
+
+}  // namespace
+
+extern "C" int rmsnorm_q8_0(const void *x, const void *residual, const float *weight, void *h_out, void *a_q8, int64_t n,
+                            int64_t K, float eps, int32_t dtype, void *stream) {
+    int st = check_norm("rmsnorm_q8_0", x, residual, weight, h_out, n, K, eps, dtype);
+    if (st) return st;
+    GD_REQUIRE(a_q8, GD_EINVAL, "rmsnorm_q8_0: null pointer");
+    GD_REQUIRE(aligned(a_q8, 2), GD_EALIGN, "rmsnorm_q8_0: a_q8 must be 2-byte aligned");
+    launch_norm<false>(x, residual, weight, h_out, a_q8, nullptr, n, K, eps, dtype, as_stream(stream));
+    return check_launch("rmsnorm_q8_0");
+}
+
+extern "C" int rmsnorm_ternary_act(const void *x, const void *residual, const float *weight, void *h_out,
+                                   uint32_t *planes, float *x_scale, int64_t n, int64_t K, float eps, int32_t dtype,
+                                   void *stream) {
+    int st = check_norm("rmsnorm_ternary_act", x, residual, weight, h_out, n, K, eps, dtype);
+    if (st) return st;
+    GD_REQUIRE(planes && x_scale, GD_EINVAL, "rmsnorm_ternary_act: null pointer");
+    GD_REQUIRE(aligned(planes, 4) && aligned(x_scale, 4), GD_EALIGN,
+               "rmsnorm_ternary_act: planes and x_scale must be 4-byte aligned");
+    launch_norm<true>(x, residual, weight, h_out, planes, x_scale, n, K, eps, dtype, as_stream(stream));
+    return check_launch("rmsnorm_ternary_act");
+}
+
+extern "C" int q8_0_dequantize(const void *a_q8, void *y, int64_t n, int64_t K, int32_t dtype, void *stream) {
+    int64_t quads;
+    int st = check_reader("q8_0_dequantize", a_q8, y, n, K, dtype, &quads);
+    if (st) return st;
+    GD_REQUIRE(aligned(a_q8, 2), GD_EALIGN, "q8_0_dequantize: a_q8 must be 2-byte aligned");
+    const dim3 grid(static_cast<uint32_t>((quads + kThreads - 1) / kThreads));
+    dispatch_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        hipLaunchKernelGGL((q8_0_dequantize_kernel<T>), grid, dim3(kThreads), 0, as_stream(stream),
+                           static_cast<const uint16_t *>(a_q8), static_cast<T *>(y), quads);
+    });
+    return check_launch("q8_0_dequantize");
+}
+
+extern "C" int ternary_dequantize_act(const uint32_t *planes, const float *x_scale, void *y, int64_t n, int64_t K,
+                                      int32_t dtype, void *stream) {
+    int64_t quads;
+    int st = check_reader("ternary_dequantize_act", planes, y, n, K, dtype, &quads);
+    if (st) return st;
+    GD_REQUIRE(x_scale, GD_EINVAL, "ternary_dequantize_act: null pointer");
+    GD_REQUIRE(aligned(planes, 4) && aligned(x_scale, 4), GD_EALIGN,
+               "ternary_dequantize_act: planes and x_scale must be 4-byte aligned");
+    const dim3 grid(static_cast<uint32_t>((quads + kThreads - 1) / kThreads));
+    dispatch_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        hipLaunchKernelGGL((ternary_dequantize_kernel<T>), grid, dim3(kThreads), 0, as_stream(stream), planes, x_scale,
+                           static_cast<T *>(y), K, quads);
+    });
+    return check_launch("ternary_dequantize_act");
+}

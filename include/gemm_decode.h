@@ -419,6 +419,193 @@ int attn_decode_splitk_noalloc(const float *q, const float *k_cache, const float
                                int64_t kv_stride, float scale, int64_t num_splits, void *stream);
 
 /* ====================================================================
+ * Norm with an 8-bit output, and readers of the activation formats
+ * ====================================================================
+ * The step between the residual stream and a product. With
+ *   h = x + residual                (rounded to the stream's type)
+ *   p = h * weight,  rstd = 1 / sqrt(mean over the row of h^2 + eps)
+ * the norm is y = rstd * p, quantized by the rule above. rstd divides out of
+ * y * (127 / max|y|), so the codes are Math.round(p * (127 * (1 / max|p|)))
+ * (each step rounded in f64, where p is exact) and the scale is max|p| * rstd
+ * / 127, evaluated in f64 from left to right and rounded to f32. A group whose
+ * products are all 0 gets scale 0 and zero codes. Sums are f64; inputs must be
+ * finite.
+ *
+ * Element types of the entry points from here on that take a `dtype`: */
+#define GD_F32  0
+#define GD_F16  1
+#define GD_BF16 2
+
+/* h = x + residual, and the norm of h as q8_0 blocks (what q1_q8_gemv reads;
+ * one scale per 32 elements, the f32 scale rounded to f16).
+ *   x         device dtype [n][K].
+ *   residual  device dtype [n][K] or NULL (h = x).
+ *   weight    device f32 [K].
+ *   h_out     device dtype [n][K], the sum h, or NULL. May be x or residual
+ *             itself (the stream updated in place); must not overlap them
+ *             otherwise.
+ *   a_q8      device, n * (K/32) * 34 bytes, 2-byte aligned; written whole.
+ * x, residual, weight and h_out 16-byte aligned. Requires K % 32 == 0,
+ * K <= 2^30, 1 <= n < 2^24, finite eps >= 0. Errors: GD_EINVAL, GD_ESHAPE,
+ * GD_EALIGN, GD_ERANGE, GD_EHIP. */
+int rmsnorm_q8_0(const void *x, const void *residual, const float *weight, void *h_out,
+                 void *a_q8, int64_t n, int64_t K, float eps, int32_t dtype, void *stream);
+
+/* The same with one scale per row, as the bit planes and scale that
+ * ternary_gemv reads (the outputs of ternary_quantize_act).
+ *   planes   device u32 [n][8][K/32], 4-byte aligned (ternary_gemv itself
+ *            needs 16).
+ *   x_scale  device f32 [n].
+ * Limits and errors as rmsnorm_q8_0. */
+int rmsnorm_ternary_act(const void *x, const void *residual, const float *weight, void *h_out,
+                        uint32_t *planes, float *x_scale, int64_t n, int64_t K, float eps,
+                        int32_t dtype, void *stream);
+
+/* The values that activations stand for: f32(code) * scale in f32, rounded
+ * to dtype. y device dtype [n][K], 16-byte aligned. Requires K % 32 == 0 and
+ * n * K < 2^34 - 1024. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE,
+ * GD_EHIP. */
+int q8_0_dequantize(const void *a_q8, void *y, int64_t n, int64_t K, int32_t dtype, void *stream);
+int ternary_dequantize_act(const uint32_t *planes, const float *x_scale, void *y, int64_t n, int64_t K,
+                           int32_t dtype, void *stream);
+
+/* ====================================================================
+ * 8-bit cache of keys and values
+ * ====================================================================
+ * A pool of pages, each of page_size positions of every KV head. A row (one
+ * position of one head) is head_dim int8 codes with an f16 scale per 32 dims,
+ * quantized as q8_0_quantize does but for the factor, 127 * (1 / absmax) (a
+ * code can differ only where it falls on an exact half); it stands for code *
+ * scale. Position p of
+ * page g of head h is row (g * n_kv_heads + h) * page_size + p of each plane;
+ * slot s names position s % page_size of page s / page_size. A cache without
+ * paging is a pool whose page b holds all of sequence b.
+ * The struct is read on the host during the call; the planes are device
+ * memory, 16-byte aligned. head_dim is 64, 128 or 256, page_size a multiple
+ * of 16, n_kv_heads <= 4096. Row contents that were never stored are never
+ * used (any bytes may be there). */
+typedef struct gd_kv_q8 {
+    int8_t *k_codes;      /* [n_pages][n_kv_heads][page_size][head_dim]          */
+    uint16_t *k_scales;   /* f16 bits, [n_pages][n_kv_heads][page_size][head_dim/32] */
+    int8_t *v_codes;
+    uint16_t *v_scales;
+    int64_t n_pages, page_size, n_kv_heads, head_dim;
+} gd_kv_q8;
+
+/* Rotary frequencies f_i = base^(-2i/rot_dim), i < rot_dim/2, for contexts
+ * past the trained length (`factor` >= 1 in all kinds but NONE). */
+#define GD_ROPE_NONE   0
+#define GD_ROPE_LINEAR 1 /* f_i / factor                                       */
+#define GD_ROPE_NTK    2 /* base * factor^(rot_dim / (rot_dim - 2)) as base     */
+#define GD_ROPE_YARN   3 /* f_i for pairs that turn more than `high` times over
+                            original_len, f_i / factor below `low` times, a
+                            linear ramp over the pair index between; cos and
+                            sin times `attention` (0: 0.1 ln(factor) + 1)      */
+#define GD_ROPE_LLAMA3 4 /* as YARN with the ramp linear in the number of turns
+                            and no attention factor                            */
+typedef struct gd_rope_scaling {
+    int32_t kind;
+    int32_t reserved;     /* 0 */
+    double factor;
+    double original_len;  /* YARN, LLAMA3: the trained length                  */
+    double low, high;     /* YARN, LLAMA3: turns, 0 < low < high (1 and 32, 1 and 4) */
+    double attention;     /* YARN */
+} gd_rope_scaling;
+
+/* The table kv_q8_store reads: table[p][i] = (cos, sin) of p * f_i, angles in
+ * f64, rounded once to f32. Written once per model.
+ *   table    device f32 [n_pos][rot_dim/2][2], 16-byte aligned.
+ *   scaling  host struct or NULL (GD_ROPE_NONE).
+ * Requires rot_dim % 8 == 0, rot_dim <= 256, base > 1, n_pos * rot_dim/2 <
+ * 2^32 - 256. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE, GD_EHIP. */
+int rope_table(float *table, int64_t n_pos, int64_t rot_dim, double base,
+               const gd_rope_scaling *scaling, void *stream);
+
+/* Rotates q and k by their tokens' positions and writes k and v to the cache.
+ * Pair (x1, x2) becomes (x1 cos - x2 sin, x2 cos + x1 sin); the pairs are
+ * dims (i, i + rot_dim/2), or (2i, 2i+1) if `interleaved`; dims from rot_dim
+ * on stay. The sum of the two products is taken in f64 (they are exact there)
+ * and rounded to f32; q_out rounds that to dtype, the cache quantizes it.
+ *   q, k, v    device dtype, token t's heads at q + t * q_stride (n_heads head
+ *              rows of head_dim), k + t * k_stride, v + t * v_stride
+ *              (n_kv_heads): parts of one projection's row, for instance.
+ *              Strides in elements, multiples of 16 bytes. All values finite,
+ *              below 65504 * 127 in k and v (the scales are f16).
+ *   q_out      device dtype [n_tok][n_heads][head_dim]; may be q itself if
+ *              q_stride is n_heads * head_dim. n_heads may be 0, with q and
+ *              q_out NULL (only the cache is written).
+ *   rope       device f32 [n_pos][rot_dim/2][2] from rope_table, with
+ *   positions  device int32 [n_tok]; both NULL: nothing is rotated (n_pos and
+ *              rot_dim are then ignored). A token whose position is outside
+ *              [0, n_pos) is left out: its q_out row and its slot stay as
+ *              they were.
+ *   slots      device int64 [n_tok], the slot each token is stored at. A token
+ *              whose slot is outside the pool (-1: padding) is not stored;
+ *              its q is still rotated. Slots of one call must differ: of two
+ *              tokens with one slot, the row is left as a mixture.
+ * rot_dim a multiple of 8, at most head_dim; n_heads <= 65536; n_tok *
+ * (n_heads + 2 n_kv_heads) * head_dim / 4 < 2^32 - 256. q, k, v, q_out and
+ * rope 16-byte aligned. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE,
+ * GD_EHIP. */
+int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                const void *v, int64_t v_stride, void *q_out, const float *rope, int64_t n_pos,
+                int64_t rot_dim, int32_t interleaved, const int32_t *positions, const int64_t *slots,
+                int64_t n_tok, int64_t n_heads, int32_t dtype, void *stream);
+
+/* Reads rows back: token t of k_out and v_out is the row that slots[t] names,
+ * f32(code) * f32(scale) rounded to dtype; a slot outside the pool reads as
+ * zeros.
+ *   slots         device int64 [n_tok] (any order, repeats allowed).
+ *   k_out, v_out  device dtype [n_tok][n_kv_heads][head_dim], 16-byte aligned;
+ *                 one of them may be NULL.
+ * n_tok * n_kv_heads * head_dim / 2 < 2^32 - 256. Errors as kv_q8_store. */
+int kv_q8_load(const gd_kv_q8 *cache, const int64_t *slots, void *k_out, void *v_out, int64_t n_tok,
+               int32_t dtype, void *stream);
+
+/* Attention of the last tokens of each of n_seqs sequences over the cache: one
+ * decode token, a chain, or a tree of drafted tokens (at most 64, stored in
+ * the cache beforehand). Sequence b has kv_lens[b] keys, its T_b query tokens
+ * the last of them. Query token t sees every key before the drafted ones, and
+ * drafted key i if bit i of its mask word is set (a tree's token: itself and
+ * its ancestors) or, without masks, if i <= t.
+ *   s_j = scale * q . k_j, then softcap * tanh(s_j / softcap) if softcap > 0;
+ *   out = sum over seen j of exp(s_j - max s) v_j / sum of exp(s_j - max s);
+ * a row that sees no key gets zeros.
+ *   q, out      device dtype [n_q][n_heads][head_dim], finite; head h reads KV
+ *               head h / (n_heads / n_kv_heads). 16-byte aligned; out must not
+ *               overlap q.
+ *   page_table  device int32 [n_seqs][max_pages]: page_table[b][i] holds the
+ *               positions i * page_size .. of sequence b. Keys on a page
+ *               outside the pool are not seen. NULL: sequence b is page b
+ *               (needs n_pages >= n_seqs; max_pages is ignored).
+ *   kv_lens     device int32 [n_seqs], taken as at most max_kv_len (0: the
+ *               sequence's rows get zeros).
+ *   q_start     device int32 [n_seqs + 1], increasing: the query rows of
+ *               sequence b are q_start[b] .. q_start[b + 1] - 1, at most max_q
+ *               (rows past that, and rows of no sequence, stay as they were).
+ *               NULL: max_q rows each (needs n_q = n_seqs * max_q).
+ *   tree_mask   device u64 [n_q], one word per query row, or NULL.
+ *   max_kv_len  the longest kv_lens: sets the split of the keys, at most
+ *               max_pages * page_size.
+ *   workspace   device, attn_decode_q8_workspace_bytes(...) bytes, 16-byte
+ *               aligned; calls that share it must be ordered.
+ * f32 inputs: within 1e-5 of the largest |v| seen (plus 2^-22 max|s|, as
+ * attn_decode_splitk). f16 and bf16: the products run on operands rounded to
+ * f16 (weights of the softmax included), sums in f32.
+ * Requires n_heads % n_kv_heads == 0, max_q <= 64, n_q <= n_seqs * max_q,
+ * n_heads <= 4096, n_seqs <= 65535, max_kv_len < 2^31, finite scale, finite
+ * softcap >= 0. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE, GD_EHIP. */
+int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, const int32_t *page_table,
+                   int64_t max_pages, const int32_t *kv_lens, const int32_t *q_start,
+                   const uint64_t *tree_mask, int64_t n_seqs, int64_t n_q, int64_t n_heads,
+                   int64_t max_q, int64_t max_kv_len, float scale, float softcap, int32_t dtype,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of such a call. Host only. Errors as its size checks. */
+int attn_decode_q8_workspace_bytes(int64_t n_seqs, int64_t n_q, int64_t n_heads, int64_t n_kv_heads,
+                                   int64_t head_dim, int64_t max_q, int64_t max_kv_len, size_t *bytes);
+
+/* ====================================================================
  * Measurement kernels  ("roofline.html": the FILL kernel writes a non-zero,
  * incompressible pattern so reads reach real DRAM; the read kernel streams
  * 16-byte words through an XOR into a sink)

@@ -1,0 +1,348 @@
+"""GPU parity of attention over the 8-bit cache, against the f64 definition.
+
+Bars. A score is computed to 4 * 2^-22 of S = scale * sum |q k| (22 bits of q,
+f32 sums), which softmax turns into the same relative error of a weight, twice
+over (numerator and denominator). f32: a weight keeps 21 bits and the sums over
+the at most 5000 keys here round each partial result at most 160 times: 1e-5 of
+the largest |v| covers both. f16 and bf16: a weight is rounded to f16, half a
+step being 2^-11 of it (2^-12 of the largest in its binade), q may lose what is
+below 2^-25 of its row's largest value, and the result is rounded once, half a
+step of its type: eps / 2 of it."""
+import numpy as np
+import pytest
+
+from oracle import layer
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def gd():
+    if not torch.cuda.is_available():
+        pytest.fail("a GPU test ran without a visible HIP device")
+    import gemm_decode_amd
+    return gemm_decode_amd
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda")
+
+
+def chain(t):
+    return (1 << (t + 1)) - 1
+
+
+class Case:
+    """Sequences over a shared pool: codes and scales random, everything that no sequence holds filled with noise (NaN
+    and infinite scales among it)."""
+
+    def __init__(self, gd, lens, qs, H, Hkv, D, page=16, T=F32, seed=0, paged=True, words=None, qscale=1.0, max_len=None,
+                 spare=2):
+        rng = np.random.default_rng(seed)
+        self.gd, self.lens, self.qs, self.H, self.Hkv, self.D, self.T = gd, lens, qs, H, Hkv, D, T
+        B, self.page = len(lens), page
+        self.max_len = max(max(lens), 1) if max_len is None else max_len
+        self.max_q = max(max(qs), 1)
+        per = -(-self.max_len // page)
+        pages = (B * per if paged else B) + spare
+        if not paged:
+            self.page = page = per * page
+            per = 1
+        self.k, self.v = [], []
+        codes = rng.integers(-127, 128, (2, pages, Hkv, page, D)).astype(np.int8)
+        scales = rng.integers(0, 65536, (2, pages, Hkv, page, D // 32)).astype(np.uint16).view(np.float16)
+        table = rng.permutation(pages)[:B * per].reshape(B, per) if paged else np.arange(B)[:, None]
+        for b, n in enumerate(lens):
+            x = np.zeros((2, Hkv, max(n, 1), D))
+            for j in range(n):
+                g, p = table[b, j // page], j % page
+                scales[:, g, :, p] = (rng.uniform(0.3, 1.0, (2, Hkv, D // 32)) / 60).astype(np.float16)
+                x[:, :, j] = codes[:, g, :, p] * np.repeat(scales[:, g, :, p].astype(np.float64), 32, -1)
+            self.k.append(x[0][:, :n])
+            self.v.append(x[1][:, :n])
+        self.codes, self.scales, self.table = codes, scales, table
+        self.cache = gd.KVCacheQ8(dev(codes[0]), dev(scales[0]), dev(codes[1]), dev(scales[1]))
+        self.page_table = dev(table.astype(np.int32)) if paged else None
+        self.kv_lens = dev(np.array(lens, np.int32))
+        self.start = np.concatenate([[0], np.cumsum(qs)]).astype(np.int32)
+        n_q = int(self.start[-1])
+        self.q = torch.from_numpy((rng.standard_normal((n_q, H, D)) * qscale).astype(np.float32)).to(T)
+        self.words = words
+        self.tree = None if words is None else dev(np.array(words, np.uint64).view(np.int64))
+
+    def run(self, scale=None, cap=0.0, out=None, q_start=True, **kw):
+        scale = self.D ** -0.5 if scale is None else scale
+        out = torch.full(self.q.shape, float("nan"), dtype=self.T, device="cuda") if out is None else out
+        self.gd.attn_decode_q8(self.q.cuda(), self.cache, self.page_table, self.kv_lens,
+                               dev(self.start) if q_start else None, self.tree, out, self.H, self.max_q, self.max_len,
+                               scale, softcap=cap, **kw)
+        return out
+
+    def want(self, scale=None, cap=0.0, gone=None):
+        """(f64 rows, bar per row); gone[b]: positions of sequence b that nobody sees."""
+        scale = self.D ** -0.5 if scale is None else scale
+        outs, bars = [], []
+        for b, (n, t) in enumerate(zip(self.lens, self.qs)):
+            ctx = max(n - t, 0)
+            sees = np.zeros((t, n), bool)
+            sees[:, :ctx] = True
+            for i in range(t):
+                w = chain(i) if self.words is None else self.words[self.start[b] + i]
+                for j in range(ctx, n):
+                    sees[i, j] = w >> (j - ctx) & 1
+            if gone is not None:
+                sees[:, gone[b]] = False
+            q = self.q[self.start[b]:self.start[b + 1]].double().numpy()
+            o, vmax, smax = layer.attention_rows(q, self.k[b], self.v[b], sees, scale, cap)
+            outs.append(o)
+            bar = 1e-5 * vmax + 2.0 ** -19 * smax * vmax
+            if self.T != F32:
+                bar += 2.0 ** -11 * vmax
+            bars.append(np.full(o.shape, bar) + (torch.finfo(self.T).eps / 2 * np.abs(o) if self.T != F32 else 0))
+        return np.concatenate(outs), np.concatenate(bars)
+
+    def check(self, got, want=None, **kw):
+        want, bar = self.want(**kw) if want is None else want
+        err = np.abs(got.double().cpu().numpy() - want)
+        assert np.all(np.isfinite(got.float().cpu().numpy()))
+        worst = float(np.max(err - bar))
+        assert worst <= 0, f"off by {err.max():.3e}, {worst:.3e} over the bar"
+
+
+SHAPES = [  # lens, rows, H, Hkv, D, page
+    ([1], [1], 4, 1, 128, 16), ([1], [1], 1, 1, 64, 16), ([15, 16, 17], [1, 1, 1], 8, 2, 64, 16),
+    ([31, 32, 33], [1, 1, 1], 8, 8, 128, 16), ([127, 128, 129, 130], [1] * 4, 3, 1, 128, 48),
+    ([700], [1], 32, 8, 128, 64), ([4097], [1], 16, 2, 64, 64), ([2500, 3, 900], [1, 1, 1], 10, 5, 128, 32),
+    ([257], [1], 4, 2, 256, 16), ([40, 300], [3, 7], 8, 2, 128, 16), ([65, 64, 64], [64, 64, 5], 2, 1, 64, 16),
+    ([600, 70], [33, 1], 6, 2, 256, 32), ([500], [17], 40, 5, 128, 16), ([1200, 5, 64], [2, 5, 16], 64, 4, 128, 16)]
+
+
+@pytest.mark.parametrize("T", [F32, F16, BF16])
+@pytest.mark.parametrize("lens,qs,H,Hkv,D,page", SHAPES)
+def test_parity(gd, T, lens, qs, H, Hkv, D, page):
+    c = Case(gd, lens, qs, H, Hkv, D, page, T, seed=sum(lens) + H)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+@pytest.mark.parametrize("H,Hkv,D", [(8, 2, 128), (5, 5, 64), (6, 1, 256)])
+def test_trees(gd, T, H, Hkv, D):
+    """Random trees, a row that sees nothing drafted, a word with bits past the drafted tokens and bits of later
+    ones, and the last of 64."""
+    rng = np.random.default_rng(D)
+    qs, lens, words = [64, 9, 1], [200, 9, 33], []
+    for t in qs:
+        seen = []
+        for i in range(t):
+            seen.append((seen[rng.integers(0, i)] if i else 0) | 1 << i)
+        words += seen
+    words[3] = 0
+    words[5] = (1 << 64) - 1
+    words[64] = 0                       # the 9-token sequence has no context: this row sees no key at all
+    words[66] = 0b101000110 | 1 << 40
+    c = Case(gd, lens, qs, H, Hkv, D, 16, T, seed=5, words=words)
+    got = c.run()
+    c.check(got)
+    assert not got[64].any()
+    c.check(c.run(cap=2.0), cap=2.0)
+
+
+@pytest.mark.parametrize("T", [F32, F16])
+def test_softcap(gd, T):
+    c = Case(gd, [300, 77], [2, 3], 8, 2, 128, 16, T, seed=3, qscale=8.0)
+    for cap in (0.5, 30.0, 1e4):
+        c.check(c.run(cap=cap), cap=cap)
+
+
+def test_unpaged(gd):
+    c = Case(gd, [130, 1, 95], [1, 1, 1], 8, 2, 128, 16, paged=False)
+    c.check(c.run())
+    c.check(c.run(q_start=False))
+    assert torch.equal(c.run(), c.run(q_start=False))
+
+
+def test_uniform_rows_without_starts(gd):
+    c = Case(gd, [130, 61], [4, 4], 8, 2, 64, 16)
+    assert torch.equal(c.run(), c.run(q_start=False))
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+def test_empty_sequences_and_rows_of_none(gd, T):
+    """Lengths of zero, sequences without rows, a length shorter than its rows; rows behind the last stay as they were."""
+    c = Case(gd, [0, 50, 3, 20], [2, 0, 5, 1], 8, 2, 64, 16, T, seed=2)
+    n_q = int(c.start[-1])
+    extra = torch.randn(6, 8, 64).to(T)
+    q = torch.cat([c.q, extra])
+    out = torch.full(q.shape, 5.0, dtype=T, device="cuda")
+    gd.attn_decode_q8(q.cuda(), c.cache, c.page_table, c.kv_lens, dev(c.start), None, out, 8, 5, c.max_len, 0.125)
+    assert not out[:2].any() and bool((out[n_q:] == 5).all())
+    c.check(out[:n_q], scale=0.125)
+
+
+def test_lengths_and_starts_out_of_range_are_clamped(gd):
+    """Device values that the host cannot check never reach past the buffers: lengths above max_kv_len or below zero, starts
+    above n_q, below zero and falling."""
+    c = Case(gd, [40, 40, 40], [1, 1, 1], 4, 2, 64, 16)
+    ref = c.run()
+    out = torch.full_like(ref, 5.0)
+    call = lambda lens, start, out: gd.attn_decode_q8(c.q.cuda(), c.cache, c.page_table, dev(np.array(lens, np.int32)),
+                                                      dev(np.array(start, np.int32)), None, out, 4, 1, 40, 0.125)
+    call([1 << 30, -5, 40], [0, 1, 2, 3], out)
+    assert torch.equal(out[0], ref[0]) and not out[1].any() and torch.equal(out[2], ref[2])
+    out.fill_(5.0)
+    call([40, 40, 40], [0, 1, 1 << 30, 3], out)
+    assert torch.equal(out[0], ref[0]) and bool((out[2] == 5).all())
+    out.fill_(5.0)
+    call([40, 40, 40], [-7, 1, 0, 0], out)
+    assert torch.equal(out[0], ref[0]) and bool((out[1:] == 5).all())
+
+
+def test_pages_outside_the_pool_are_not_seen(gd):
+    c = Case(gd, [100, 64], [1, 1], 8, 2, 64, 16)
+    t = c.table.astype(np.int32).copy()
+    t[0, 2], t[0, 6] = -1, 1 << 30      # positions 32..47 and the last, 96..99
+    t[1, :] = -9                        # everything: the row is empty
+    c.page_table = dev(t)
+    gone = [np.r_[32:48, 96:100], np.arange(64)]
+    got = c.run()
+    c.check(got, gone=gone)
+    assert not got[1].any()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
+def test_scales(gd, scale):
+    """Means, negative scales, and scores in the hundreds."""
+    c = Case(gd, [333], [2], 8, 2, 128, 16, seed=9, qscale=4.0)
+    c.check(c.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("T,top", [(F32, 1e30), (F32, 1e-30), (BF16, 1e30), (F16, 6e4), (F16, 6e-8)])
+def test_query_range(gd, T, top):
+    """Rows of any finite size: the scale brings the scores back to ordinary ones."""
+    c = Case(gd, [200], [1], 4, 2, 64, 16, T, seed=4)
+    q = c.q.double()
+    c.q = (q / q.abs().max() * top).to(T)
+    c.check(c.run(scale=0.5 / top), scale=0.5 / top)
+
+
+def test_value_scales_of_any_size(gd):
+    """Value scales from f16's smallest to its largest, side by side: the bar follows the largest value seen."""
+    c = Case(gd, [160], [1], 4, 2, 64, 16, seed=6)
+    rng = np.random.default_rng(1)
+    for lo, hi in ((2.0 ** -24, 2.0 ** -20), (6e4, 65504.0), (2.0 ** -24, 65504.0)):
+        s = np.exp(rng.uniform(np.log(lo), np.log(hi), c.scales[1].shape)).astype(np.float16)
+        c.cache.v_scales.copy_(dev(s))
+        for j in range(160):
+            g, p = c.table[0, j // 16], j % 16
+            c.v[0][:, j] = c.codes[1, g, :, p] * np.repeat(s[g, :, p].astype(np.float64), 32, -1)
+        c.check(c.run())
+
+
+def test_zero_values_and_queries(gd):
+    c = Case(gd, [80], [1], 4, 2, 64, 16)
+    ref = c.run()
+    c.cache.v_scales.copy_(torch.where(c.cache.v_scales.isfinite(), 0.0, c.cache.v_scales))
+    out = c.run()
+    assert not out.any() and ref.any()
+    c = Case(gd, [80], [1], 4, 2, 64, 16)
+    c.q = torch.zeros_like(c.q)
+    c.check(c.run())
+
+
+def test_one_key_returns_its_value(gd):
+    c = Case(gd, [1], [1], 4, 2, 128, 16)
+    got = c.run().cpu().numpy().reshape(2, 2, 128)
+    assert np.abs(got - c.v[0][:, None, 0]).max() <= 2.0 ** -20 * np.abs(c.v[0]).max()
+
+
+def test_long_sequence_and_splits(gd):
+    """Thousands of keys with a single row: many splits; and the same sequence beside 40 short ones."""
+    c = Case(gd, [5000], [1], 8, 1, 128, 64, seed=8)
+    c.check(c.run())
+    c = Case(gd, [3000] + [5] * 40, [1] * 41, 4, 1, 64, 16, seed=8)
+    c.check(c.run())
+
+
+def test_workspace_contents_do_not_matter(gd):
+    c = Case(gd, [900, 20], [2, 1], 8, 2, 128, 16)
+    ref = c.run()
+    need = gd.attn_decode_q8_workspace_bytes(2, 3, 8, 2, 128, 2, c.max_len)
+    for fill in (0xFF, 0x00, 0x7F):
+        ws = torch.full((need + 64,), fill, dtype=torch.uint8, device="cuda")
+        assert torch.equal(c.run(workspace=ws[:need]), ref)
+        assert bool((ws[need:] == fill).all())
+    with pytest.raises(gd.GemmDecodeError, match="GD_ERANGE"):
+        c.run(workspace=ws[:need - 1])
+
+
+def test_graph_replays_and_two_graphs_on_one_workspace(gd):
+    """Captured calls of two shapes that share a workspace, replayed in turn with changed inputs."""
+    a = Case(gd, [700, 300], [1, 1], 8, 2, 128, 16, seed=1)
+    b = Case(gd, [900], [5], 8, 2, 128, 16, BF16, seed=2)
+    need = max(gd.attn_decode_q8_workspace_bytes(2, 2, 8, 2, 128, 1, 700),
+               gd.attn_decode_q8_workspace_bytes(1, 5, 8, 2, 128, 5, 900))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c in (a, b):
+        q, start, out = c.q.cuda(), dev(c.start), torch.empty(c.q.shape, dtype=c.T, device="cuda")
+        call = lambda out, c=c, q=q, start=start: gd.attn_decode_q8(
+            q, c.cache, c.page_table, c.kv_lens, start, None, out, 8, c.max_q, c.max_len, 0.1, workspace=ws)
+        call(out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(out)
+        graphs.append((g, q, out, call, c))
+    for i in range(4):
+        for g, q, out, call, c in graphs:
+            q.normal_()
+            c.kv_lens.sub_(7)
+            g.replay()
+        torch.cuda.synchronize()
+        for g, q, out, call, c in graphs:
+            want = torch.empty_like(out)
+            call(want)
+            assert torch.equal(want, out), i
+
+
+def test_side_stream(gd):
+    c = Case(gd, [800], [2], 8, 2, 128, 16)
+    ref = c.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        outs = [c.run() for _ in range(3)]
+    side.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+
+
+def test_repeats_are_equal(gd):
+    c = Case(gd, [1500, 800, 9], [4, 2, 9], 16, 2, 128, 16, BF16)
+    ref = c.run()
+    for _ in range(5):
+        assert torch.equal(c.run(), ref)
+
+
+def test_refusals(gd):
+    c = Case(gd, [40, 40], [1, 1], 4, 2, 64, 16)
+    with pytest.raises(gd.GemmDecodeError, match="GD_EINVAL"):
+        c.run(cap=-1.0)
+    with pytest.raises(ValueError):
+        c.run(out=torch.empty(3, 4, 64, device="cuda"))
+    with pytest.raises(TypeError):
+        c.run(out=torch.empty(2, 4, 64, dtype=F16, device="cuda"))
+    c.max_len = 49
+    with pytest.raises(gd.GemmDecodeError, match="GD_EINVAL"):
+        c.run()
+    c.max_len, c.max_q = 40, 65
+    with pytest.raises(gd.GemmDecodeError, match="GD_ERANGE"):
+        c.run()
+    c.max_q = 1
+    c.page_table = c.page_table[:, :2]
+    with pytest.raises(ValueError):
+        c.run()
+    c.page_table = c.page_table.contiguous()
+    with pytest.raises(gd.GemmDecodeError, match="GD_EINVAL"):
+        c.run()
