@@ -1,11 +1,57 @@
 // attention_q8.hip -- attention of the last tokens of several sequences (one
 // decode token, a chain or a tree of drafted ones) over the 8-bit cache.
+//
+// Mathematics. One pass over the keys with a running maximum m, sum l and
+// weighted sum o per query row, both rescaled when m grows; several passes
+// over parts of the keys are joined by bringing them to the largest m.
+//
+// Shape of the work. The rows that read one KV head (its n_heads / n_kv_heads
+// query heads of every query token) are taken together, 16 to a matrix-core
+// tile, so that each key and value is read once for all of them. A workgroup
+// of four waves serves one KV head, one part of the keys of one sequence and
+// RT tiles of rows; its waves take 32 keys each in turn and never wait for one
+// another until the end, where they are joined through LDS. A second launch
+// joins the parts of a sequence, if it has more than one.
+//
+// No operand passes through LDS. Scores are taken transposed, S^T = K Q^T:
+// lane (n, g) = (lane % 16, lane / 16) loads 8 dims of key n per 32-dim group,
+// one matrix instruction contracts exactly one group, and its result, multiplied
+// by the group's scale, is added up in f32. The result has lane (n, g) hold keys
+// 4g .. 4g+3 of query row n, which is how the second product, O^T = V^T P^T,
+// takes its weights: they never leave their lane. For V^T the lane (n, g) loads
+// D/16 dims (from n D/16 on) of the same keys; these dims lie in one scale
+// group, so a value is its code times one scale per key.
+//
+// Precision. Codes are whole numbers below 2^8, exact in f16. f32 inputs: q (as
+// a power of two times its row) and the weights are split into two f16 parts, 22
+// bits; code * scale has at most 19 bits and is split exactly; the product of the
+// two low parts, below 2^-22 of the result, is dropped. f16 and bf16 inputs: q is
+// exact in f16 at its row's power of two, a weight and code * scale are rounded to
+// f16, half a step being 2^-12 to 2^-11 of them, which is below a bf16 result's
+// rounding and near a f16 result's. Sums, maxima and the softmax are f32. The
+// scales of the values are brought near f16's upper end by a power of two per
+// wave, which follows the largest scale seen.
+#include <type_traits>
+
 #include "gd_internal.h"
 #include "gd_types.h"
 
 namespace {
 
 using namespace gd;
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kStep = 32;                  // keys per wave and step
+constexpr int kGroupKeys = kStep * kWaves; // keys per workgroup and step
+constexpr float kNone = -3.0e38f;          // the maximum of no scores: below any, and finite
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kWeightBits = 14.0f;       // weights are held times 2^14, so that small ones keep their f16 bits
 
 struct AttnArgs {
     gd_kv_q8 c;
@@ -14,7 +60,13 @@ struct AttnArgs {
     const int32_t *page_table, *kv_lens, *q_start;
     const uint64_t *tree;
     int64_t max_pages, n_seqs, n_q, n_heads, max_q, max_kv_len;
+    int64_t chunk;         // keys per part, a multiple of kGroupKeys
+    int32_t splits;        // parts of the longest sequence
+    int32_t row_blocks;    // workgroups that share the rows of a KV head
+    uint32_t page_magic;   // tile / (page_size / 16) = tile * page_magic >> page_shift
+    int32_t page_shift;
     float scale, softcap;
+    float *part_o, *part_ml;
 };
 
 // What the kernels read of one sequence, clamped to what the host checked.
@@ -39,56 +91,484 @@ struct Seq {
     }
 };
 
-// The page that holds position j of sequence b, or -1 if its entry is none.
-__device__ __forceinline__ int64_t page_of(const AttnArgs &a, int64_t b, int64_t j) {
-    const int64_t i = j / a.c.page_size;
-    const int64_t p = a.page_table ? a.page_table[b * a.max_pages + i] : b;
-    return p >= 0 && p < a.c.n_pages ? p : -1;
+// The parts that a sequence of `len` keys has (at least one, which also serves
+// the rows of an empty sequence).
+__device__ __forceinline__ int parts_of(const AttnArgs &a, int64_t len) {
+    const int n = static_cast<int>((len + a.chunk - 1) / a.chunk);
+    return n < 1 ? 1 : n;
 }
 
-__device__ __forceinline__ float capped(float s, float cap) { return cap > 0.0f ? cap * tanhf(s / cap) : s; }
+// 16 positions of one KV head: the cache row of the first, and whether they are
+// there (a page outside the pool is read as page 0 and masked).
+struct Tile {
+    int64_t row;
+    bool ok;
+};
 
-// One wave per query row and head, one key at a time.
-template <typename T>
-__global__ __launch_bounds__(64) void attn_q8_kernel(AttnArgs a) {
-    const int64_t b = blockIdx.z;
-    const int t = blockIdx.y;
-    const int h = blockIdx.x, lane = threadIdx.x;
-    const Seq sq(a, b);
-    if (t >= sq.rows) return;
-    const int D = static_cast<int>(a.c.head_dim), Hkv = static_cast<int>(a.c.n_kv_heads);
-    const int kvh = h / static_cast<int>(a.n_heads / Hkv), n = D / 64;
-    const int64_t row = sq.row0 + t;
-    const T *q = static_cast<const T *>(a.q) + (row * a.n_heads + h) * D;
-    const uint64_t word = a.tree ? a.tree[row] : (t >= 63 ? ~0ull : (1ull << (t + 1)) - 1);
-    float qv[4], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = 0; i < n; i++) qv[i] = static_cast<float>(q[lane + 64 * i]);
-    float m = -__builtin_inff(), l = 0.0f;
-    for (int64_t j = 0; j < sq.len; j++) {
-        if (j >= sq.ctx && !((word >> (j - sq.ctx)) & 1)) continue;
-        const int64_t page = page_of(a, b, j);
-        if (page < 0) continue;
-        const int64_t r = (page * Hkv + kvh) * a.c.page_size + j % a.c.page_size;
-        float s = 0.0f;
-        for (int i = 0; i < n; i++) {
-            const int d = lane + 64 * i;
-            s += qv[i] * static_cast<float>(a.c.k_codes[r * D + d]) *
-                 static_cast<float>(__builtin_bit_cast(_Float16, a.c.k_scales[r * (D / 32) + d / 32]));
-        }
-        for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
-        s = capped(s * a.scale, a.softcap);
-        const float mn = fmaxf(m, s), corr = m == -__builtin_inff() ? 0.0f : expf(m - mn), p = expf(s - mn);
-        l = l * corr + p;
-        for (int i = 0; i < n; i++) {
-            const int d = lane + 64 * i;
-            const float v = static_cast<float>(a.c.v_codes[r * D + d]) *
-                            static_cast<float>(__builtin_bit_cast(_Float16, a.c.v_scales[r * (D / 32) + d / 32]));
-            acc[i] = acc[i] * corr + p * v;
-        }
-        m = mn;
+__device__ __forceinline__ Tile tile_at(const AttnArgs &a, int64_t b, int kvh, int tile) {
+    const int i = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(tile)) * a.page_magic) >> a.page_shift);
+    const int per = static_cast<int>(a.c.page_size / 16);
+    int64_t page = a.page_table ? a.page_table[b * a.max_pages + i] : b;
+    const bool ok = page >= 0 && page < a.c.n_pages;
+    page = ok ? page : 0;
+    return {(page * a.c.n_kv_heads + kvh) * a.c.page_size + static_cast<int64_t>(tile - i * per) * 16, ok};
+}
+
+// v of this lane and of the lane 16 (32) further round, in some order.
+template <int kLanes>
+__device__ __forceinline__ f32x2 with_other(float v) {
+    const uint32_t x = __builtin_bit_cast(uint32_t, v);
+    u32x2 r;
+    if constexpr (kLanes == 16)
+        r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    else
+        r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return __builtin_bit_cast(f32x2, r);   // whole: a bit cast of r[1] alone is compiled as one of r[0]
+}
+
+__device__ __forceinline__ float max_across(float v) {   // over the four lanes that share lane % 16
+    f32x2 r = with_other<16>(v);
+    r = with_other<32>(fmaxf(r[0], r[1]));
+    return fmaxf(r[0], r[1]);
+}
+
+__device__ __forceinline__ float sum_across(float v) {
+    f32x2 r = with_other<16>(v);
+    r = with_other<32>(r[0] + r[1]);
+    return r[0] + r[1];
+}
+
+__device__ __forceinline__ f16x2 as_h2(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
+
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+union Frag {   // one matrix operand of a lane: eight f16 along the contraction
+    f16x8 v;
+    f16x2 h[4];
+};
+
+// Eight codes (bytes of w) as f16: 0x6400 | (code + 128) is 1024 + 128 + code.
+__device__ __forceinline__ f16x8 codes_f16(u32x2 w) {
+    Frag f;
+    const f16x2 bias = {static_cast<_Float16>(-1152.0f), static_cast<_Float16>(-1152.0f)};
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t u = w[i] ^ 0x80808080u;
+        f.h[2 * i] = as_h2(__builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) + bias;
+        f.h[2 * i + 1] = as_h2(__builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) + bias;
     }
-    T *o = static_cast<T *>(a.out) + (row * a.n_heads + h) * D;
-    for (int i = 0; i < n; i++) o[lane + 64 * i] = static_cast<T>(l > 0.0f ? acc[i] / l : 0.0f);
+    return f.v;
+}
+
+// 2^k as f16 and f32, for powers in the range of either.
+__device__ __forceinline__ _Float16 pow2_f16(int k) { return __builtin_bit_cast(_Float16, static_cast<uint16_t>((k + 15) << 10)); }
+
+// The keys and values of one step of a wave, as loaded: for each of its two
+// tiles of 16 keys the lane's K codes (8 dims of key n per group), its V codes
+// (D/16 dims of keys 4g .. 4g+3) and the scales of keys 4g .. 4g+3, K and V.
+template <int D>
+struct Step {
+    static constexpr int C = D / 32, VB = D / 16;   // scale groups; V bytes per key and lane
+    u32x2 k[2][C];
+    uint32_t v[2][4][VB / 4];
+    u32x2 ks[2][C], vs[2][C];   // 4 keys x C f16, key-major
+};
+
+template <int D>
+__device__ __forceinline__ void load_keys(const AttnArgs &a, const Tile (&t)[2], int lane, Step<D> &s) {
+    const int n = lane % 16, g = lane / 16;
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+        const int8_t *p = a.c.k_codes + t[u].row * D;
+        const uint16_t *d = a.c.k_scales + t[u].row * (D / 32);
+#pragma unroll
+        for (int c = 0; c < D / 32; c++)
+            s.k[u][c] = *reinterpret_cast<const u32x2 *>(p + (n * D + 8 * g + 32 * c));
+#pragma unroll
+        for (int c = 0; c < D / 32; c++) s.ks[u][c] = reinterpret_cast<const u32x2 *>(d + 4 * g * (D / 32))[c];
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(const AttnArgs &a, const Tile (&t)[2], int lane, Step<D> &s) {
+    constexpr int VB = D / 16;
+    const int n = lane % 16, g = lane / 16;
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+        const int8_t *p = a.c.v_codes + t[u].row * D;
+        const uint16_t *d = a.c.v_scales + t[u].row * (D / 32);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int w = 0; w < VB / 4; w++)
+                s.v[u][i][w] = reinterpret_cast<const uint32_t *>(p + ((4 * g + i) * D + n * VB))[w];
+#pragma unroll
+        for (int c = 0; c < D / 32; c++) s.vs[u][c] = reinterpret_cast<const u32x2 *>(d + 4 * g * (D / 32))[c];
+    }
+}
+
+// f16 number `i` of the lane's 4 x C scales.
+template <int C>
+__device__ __forceinline__ uint32_t scale_word(const u32x2 (&s)[C], int i) {   // the pair 2i, 2i + 1
+    return s[i / 2][i % 2];
+}
+
+// NS = 2: operands in two f16 parts (f32 inputs), NS = 1: in one. A workgroup
+// serves RT tiles of 16 query rows.
+template <typename T, int D, int NS, int RT>
+__global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
+    constexpr int C = D / 32, VB = D / 16, R = 16 * RT;
+    __shared__ f32x4 lds_o[kWaves][R][D / 4 + 1];   // padded: 16 lanes write one column of it
+    __shared__ float lds_m[kWaves][R], lds_l[kWaves][R];
+    const int Hkv = static_cast<int>(a.c.n_kv_heads);
+    const int kvh = blockIdx.x % Hkv, r0 = (blockIdx.x / Hkv) * R;
+    const int split = blockIdx.y;
+    const int64_t b = blockIdx.z;
+    const Seq sq(a, b);
+    const int G = static_cast<int>(a.n_heads) / Hkv;
+    const int rows = sq.rows * G;   // of this KV head
+    const int parts = parts_of(a, sq.len);
+    if (r0 >= rows || split >= parts) return;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / 64);
+    const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
+    const int len = static_cast<int>(sq.len), ctx = static_cast<int>(sq.ctx);
+    const int j0 = static_cast<int>(split * a.chunk);
+    const int j1 = j0 + static_cast<int>(a.chunk) < len ? j0 + static_cast<int>(a.chunk) : len;
+
+    // The query rows: row r0 + 16 rt + n of this lane, times a power of two that
+    // brings its largest value into [2^13, 2^14).
+    Frag q[RT][C][NS];
+    float scale2[RT];       // from a contraction to a score (times log2 e without a cap)
+    uint64_t word[RT];      // the drafted keys that the row sees
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int r = r0 + 16 * rt + n;
+        const bool live = r < rows;
+        const int t = live ? r / G : 0, h = kvh * G + (live ? r - t * G : 0);
+        const T *p = static_cast<const T *>(a.q) + ((sq.row0 + t) * a.n_heads + h) * D;
+        word[rt] = a.tree ? a.tree[sq.row0 + t] : (t >= 63 ? ~0ull : (1ull << (t + 1)) - 1);
+        f32x4 x[C][2];
+        float mx = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                x[c][i] = live ? load4(p + 32 * c + 8 * g + 4 * i) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < 4; j++) mx = fmaxf(mx, fabsf(x[c][i][j]));
+            }
+        mx = max_across(mx);
+        const int e = mx > 0.0f && mx <= 3.40282347e38f ? 14 - __builtin_amdgcn_frexp_expf(mx) : 0;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float v0 = ldexpf(x[c][i / 4][i % 4], e), v1 = ldexpf(x[c][i / 4][i % 4 + 1], e);
+                const f16x2 hi = {static_cast<_Float16>(v0), static_cast<_Float16>(v1)};
+                q[rt][c][0].h[i / 2] = hi;
+                if constexpr (NS == 2)
+                    q[rt][c][NS - 1].h[i / 2] = f16x2{static_cast<_Float16>(v0 - static_cast<float>(hi[0])),
+                                                      static_cast<_Float16>(v1 - static_cast<float>(hi[1]))};
+            }
+        scale2[rt] = ldexpf(a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e, -e);
+    }
+
+    f32x4 o[RT][VB];   // dims (4g + i) VB + t of row n
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        m[rt] = kNone;
+        l[rt] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < VB; t++) o[rt][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // Powers of two on the V scales: 2^vk in all, so that the largest seen lies
+    // below 2^15 (below 2^15 without a change: vlim of the raw scale).
+    int vk = 15;
+    _Float16 vmul = pow2_f16(15);
+    _Float16 vlim = static_cast<_Float16>(0.0f);   // the largest scale that vk was made for
+
+    Step<D> st;
+    int j = j0 + kStep * wave;
+    const auto tiles = [&](int at, Tile (&t)[2]) {
+        const int last = (j1 - 1) / 16;   // a tile past the end is the last one again, masked by its positions
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const int i = at / 16 + u;
+            t[u] = tile_at(a, b, kvh, __builtin_amdgcn_readfirstlane(i < last ? i : last));
+        }
+    };
+    Tile tl[2];
+    if (j < j1) {
+        tiles(j, tl);
+        load_keys<D>(a, tl, lane, st);
+        load_values<D>(a, tl, lane, st);
+    }
+    for (; j < j1; j += kGroupKeys) {
+        const bool more = j + kGroupKeys < j1;
+        const bool plain = j + kStep <= (ctx < j1 ? ctx : j1) && tl[0].ok && tl[1].ok;   // every row sees every key
+        float s[RT][2][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) s[rt][u][i] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                const f16x8 kf = codes_f16(st.k[u][c]);
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++) {
+                    f32x4 d = mfma(kf, q[rt][c][0].v, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                    if constexpr (NS == 2) d = mfma(kf, q[rt][c][NS - 1].v, d);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const f16x2 w = as_h2(scale_word<C>(st.ks[u], (i * C + c) / 2));
+                        s[rt][u][i] = __builtin_fmaf(d[i], static_cast<float>(w[c % 2]), s[rt][u][i]);
+                    }
+                }
+            }
+        const Tile here[2] = {tl[0], tl[1]};
+        if (more) {
+            tiles(j + kGroupKeys, tl);
+            load_keys<D>(a, tl, lane, st);
+        }
+        // Weights, each lane its 8 keys of row n.
+        Frag p[RT][NS];
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            float mx = kNone;
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    float x = s[rt][u][i] * scale2[rt];
+                    if (a.softcap > 0.0f) x = tanhf(x) * (a.softcap * kLog2e);
+                    if (!plain) {
+                        const int jj = j + 16 * u + 4 * g + i;
+                        const bool sees = here[u].ok && jj < j1 && (jj < ctx || ((word[rt] >> ((jj - ctx) & 63)) & 1));
+                        x = sees ? x : -__builtin_inff();
+                    }
+                    s[rt][u][i] = x;
+                    mx = fmaxf(mx, x);
+                }
+            const float mn = fmaxf(m[rt], max_across(mx));
+            const float corr = __builtin_amdgcn_exp2f(m[rt] - mn);
+            m[rt] = mn;
+            l[rt] *= corr;
+#pragma unroll
+            for (int t = 0; t < VB; t++) o[rt][t] *= corr;
+            const float off = mn - kWeightBits;
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const float p0 = __builtin_amdgcn_exp2f(s[rt][u][i] - off), p1 = __builtin_amdgcn_exp2f(s[rt][u][i + 1] - off);
+                    l[rt] += p0 + p1;
+                    const f16x2 hi = {static_cast<_Float16>(p0), static_cast<_Float16>(p1)};
+                    p[rt][0].h[2 * u + i / 2] = hi;
+                    if constexpr (NS == 2)
+                        p[rt][NS - 1].h[2 * u + i / 2] = f16x2{static_cast<_Float16>(p0 - static_cast<float>(hi[0])),
+                                                               static_cast<_Float16>(p1 - static_cast<float>(hi[1]))};
+                }
+        }
+        // The V scales of the lane's 8 keys at its dims' group, in pairs.
+        f16x2 vs[2][2];
+        {
+            const int cl = n * VB / 32;
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    w[i] = scale_word<C>(st.vs[u], i * C / 2);
+#pragma unroll
+                    for (int k = 1; k < C / 2; k++) w[i] = cl / 2 == k ? scale_word<C>(st.vs[u], i * C / 2 + k) : w[i];
+                }
+                const uint32_t sel = cl % 2 ? 0x07060302u : 0x05040100u;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    uint32_t pr = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], sel);
+                    if (!plain) {   // scales that no one stored may be anything, and weights of 0 do not hide it
+                        const int jj = j + 16 * u + 4 * g + 2 * i;
+                        if (!here[u].ok || jj >= j1 || (pr & 0x7c00u) == 0x7c00u) pr &= 0xffff0000u;
+                        if (!here[u].ok || jj + 1 >= j1 || (pr & 0x7c000000u) == 0x7c000000u) pr &= 0x0000ffffu;
+                    }
+                    vs[u][i] = as_h2(pr);
+                }
+            }
+        }
+        f16x2 top = __builtin_elementwise_max(__builtin_elementwise_max(vs[0][0], vs[0][1]),
+                                              __builtin_elementwise_max(vs[1][0], vs[1][1]));
+        _Float16 lane_top = top[0] > top[1] ? top[0] : top[1];
+        if (__any(lane_top > vlim)) {   // a scale above those that vk was made for (rare after the first steps)
+            float w = static_cast<float>(lane_top);
+#pragma unroll
+            for (int x = 32; x >= 1; x >>= 1) w = fmaxf(w, __shfl_xor(w, x));
+            int k = 15 - __builtin_amdgcn_frexp_expf(w);   // w 2^k in [2^14, 2^15)
+            k = k < vk ? k : vk;
+            vlim = static_cast<_Float16>(k < 15 ? ldexpf(1.0f, 15 - k) : 1.0f);   // exact, at most 2^16 (infinity)
+            if (k != vk) {
+                const float f = ldexpf(1.0f, k - vk);
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                    for (int t = 0; t < VB; t++) o[rt][t] *= f;
+                vk = k;
+                vmul = pow2_f16(k);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) vs[u][i] *= f16x2{vmul, vmul};
+        uint32_t vx[2][4][VB / 4];
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int w = 0; w < VB / 4; w++) vx[u][i][w] = st.v[u][i][w] ^ 0x80808080u;
+#pragma unroll
+        for (int t = 0; t < VB; t++) {
+            // byte t of two keys as (code + 128) 2^-24 (f16's smallest steps), times 2^14, less 2^-3: code 2^-10
+            const uint32_t sel = 0x0c000c00u | static_cast<uint32_t>((4 + t % 4) << 16) | static_cast<uint32_t>(t % 4);
+            const f16x2 up = {pow2_f16(14), pow2_f16(14)}, off = {static_cast<_Float16>(-0.125f), static_cast<_Float16>(-0.125f)};
+            Frag vh, vl;
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const f16x2 x = as_h2(__builtin_amdgcn_perm(vx[u][2 * i + 1][t / 4], vx[u][2 * i][t / 4], sel));
+                    const f16x2 c = __builtin_elementwise_fma(x, up, off);
+                    vh.h[2 * u + i] = c * vs[u][i];
+                    if constexpr (NS == 2) vl.h[2 * u + i] = __builtin_elementwise_fma(c, vs[u][i], -vh.h[2 * u + i]);
+                }
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++) {
+                o[rt][t] = mfma(vh.v, p[rt][0].v, o[rt][t]);
+                if constexpr (NS == 2) {
+                    o[rt][t] = mfma(vl.v, p[rt][0].v, o[rt][t]);
+                    o[rt][t] = mfma(vh.v, p[rt][NS - 1].v, o[rt][t]);
+                }
+            }
+        }
+        if (more) load_values<D>(a, tl, lane, st);
+    }
+
+    // Join the four waves.
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int r = 16 * rt + n;
+        const float sum = sum_across(l[rt]);
+        if (g == 0) {
+            lds_m[wave][r] = m[rt];
+            lds_l[wave][r] = sum;
+        }
+        const float f = ldexpf(1.0f, 10 - vk);   // codes were held times 2^-10
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int t = 0; t < VB; t += 4)
+                lds_o[wave][r][((4 * g + i) * VB + t) / 4] =
+                    f32x4{o[rt][t][i], o[rt][t + 1][i], o[rt][t + 2][i], o[rt][t + 3][i]} * f;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < R * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), d4 = e % (D / 4);
+        if (r0 + r >= rows) break;
+        float mx = lds_m[0][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; w++) mx = fmaxf(mx, lds_m[w][r]);
+        float sum = 0.0f;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) {
+            const float f = __builtin_amdgcn_exp2f(lds_m[w][r] - mx);
+            sum += lds_l[w][r] * f;
+            x += lds_o[w][r][d4] * f;
+        }
+        const int t = (r0 + r) / G, h = kvh * G + (r0 + r) - t * G;
+        const int64_t at = (sq.row0 + t) * a.n_heads + h;
+        if (parts == 1) {
+            store4(static_cast<T *>(a.out) + at * D + 4 * d4, sum > 0.0f ? x * (1.0f / sum) : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        } else {
+            *reinterpret_cast<f32x4 *>(a.part_o + (at * a.splits + split) * D + 4 * d4) = x;
+            if (d4 == 0) *reinterpret_cast<f32x2 *>(a.part_ml + (at * a.splits + split) * 2) = f32x2{mx, sum};
+        }
+    }
+}
+
+// Joins the parts of one query row and head: four waves, each every fourth part,
+// D / 64 dims to a lane.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
+    constexpr int E = D / 64;
+    __shared__ float lds_o[kWaves][D], lds_m[kWaves], lds_l[kWaves];
+    const Seq sq(a, blockIdx.z);
+    const int parts = parts_of(a, sq.len);
+    if (static_cast<int>(blockIdx.y) >= sq.rows || parts == 1) return;
+    const int64_t at = (sq.row0 + blockIdx.y) * a.n_heads + blockIdx.x;
+    const float *po = a.part_o + at * a.splits * D, *pml = a.part_ml + at * a.splits * 2;
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    float m = kNone, l = 0.0f, o[E];
+#pragma unroll
+    for (int i = 0; i < E; i++) o[i] = 0.0f;
+    for (int s = wave; s < parts; s += kWaves) {
+        const float pm = pml[2 * s], pl = pml[2 * s + 1];
+        const float mn = fmaxf(m, pm), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(pm - mn);
+        m = mn;
+        l = l * f0 + pl * f1;
+#pragma unroll
+        for (int i = 0; i < E; i++) o[i] = o[i] * f0 + po[s * D + lane * E + i] * f1;
+    }
+#pragma unroll
+    for (int i = 0; i < E; i++) lds_o[wave][lane * E + i] = o[i];
+    if (lane == 0) {
+        lds_m[wave] = m;
+        lds_l[wave] = l;
+    }
+    __syncthreads();
+    float mx = kNone, f[kWaves], sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) mx = fmaxf(mx, lds_m[w]);
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) {
+        f[w] = __builtin_amdgcn_exp2f(lds_m[w] - mx);
+        sum += lds_l[w] * f[w];
+    }
+    for (int d = threadIdx.x; d < D; d += kThreads) {
+        float x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) x += lds_o[w][d] * f[w];
+        static_cast<T *>(a.out)[at * D + d] = static_cast<T>(sum > 0.0f ? x / sum : 0.0f);
+    }
+}
+
+constexpr int kTargetGroups = 1024;   // workgroups that keep the card's 256 CUs busy to the end
+
+// How the work is cut: rows per workgroup, and keys per part.
+struct Plan {
+    int row_tiles;       // RT
+    int64_t row_blocks, chunk, splits;
+};
+
+Plan plan_of(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim, int64_t max_q, int64_t max_kv_len) {
+    Plan p;
+    const int64_t rows = max_q * (n_heads / n_kv_heads);
+    p.row_tiles = rows > 16 && head_dim <= 128 ? 2 : 1;
+    p.row_blocks = (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
+    const int64_t groups = n_seqs * n_kv_heads * p.row_blocks;   // at one part each
+    int64_t parts = (kTargetGroups + groups - 1) / groups;
+    const int64_t steps = (max_kv_len + kGroupKeys - 1) / kGroupKeys;
+    parts = parts < steps ? parts : steps;
+    p.chunk = (steps + parts - 1) / parts * kGroupKeys;
+    p.splits = (max_kv_len + p.chunk - 1) / p.chunk;
+    return p;
 }
 
 int check_sizes(const char *name, int64_t n_seqs, int64_t n_q, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim,
@@ -102,7 +582,7 @@ int check_sizes(const char *name, int64_t n_seqs, int64_t n_q, int64_t n_heads, 
     GD_REQUIRE(n_heads % n_kv_heads == 0, GD_ESHAPE, "%s: n_heads (%lld) not a multiple of n_kv_heads (%lld)", name,
                (long long)n_heads, (long long)n_kv_heads);
     GD_REQUIRE(max_q <= 64 && n_heads <= 4096 && n_seqs <= 65535 && n_q <= n_seqs * max_q &&
-                   max_kv_len <= INT64_C(2147483647),
+                   max_kv_len <= (INT64_C(1) << 30),
                GD_ERANGE, "%s: max_q (%lld) above 64, n_q (%lld) above n_seqs * max_q, or a size too large", name,
                (long long)max_q, (long long)n_q);
     return GD_OK;
@@ -115,7 +595,9 @@ extern "C" int attn_decode_q8_workspace_bytes(int64_t n_seqs, int64_t n_q, int64
     GD_REQUIRE(bytes, GD_EINVAL, "attn_decode_q8_workspace_bytes: null output pointer");
     int st = check_sizes("attn_decode_q8_workspace_bytes", n_seqs, n_q, n_heads, n_kv_heads, head_dim, max_q, max_kv_len);
     if (st) return st;
-    *bytes = 16;
+    const Plan p = plan_of(n_seqs, n_heads, n_kv_heads, head_dim, max_q, max_kv_len);
+    // a sum of head_dim values, a maximum and a denominator per row, head and part
+    *bytes = p.splits > 1 ? static_cast<size_t>(n_q * n_heads * p.splits * (head_dim + 2) * 4) : 16;
     clear_error();
     return GD_OK;
 }
@@ -135,8 +617,8 @@ extern "C" int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, c
                "attn_decode_q8: without q_start every sequence has max_q (%lld) rows: n_q (%lld) must be n_seqs * max_q",
                (long long)max_q, (long long)n_q);
     GD_REQUIRE(scale - scale == 0.0f, GD_EINVAL, "attn_decode_q8: scale must be finite");
-    GD_REQUIRE(softcap >= 0.0f && softcap <= 3.40282347e38f, GD_EINVAL,
-               "attn_decode_q8: softcap must be finite and >= 0 (0: none)");
+    GD_REQUIRE(softcap >= 0.0f && softcap <= 1e30f, GD_EINVAL,
+               "attn_decode_q8: softcap must be in [0, 1e30] (0: none)");
     GD_REQUIRE(page_table ? max_pages >= 1 : cache->n_pages >= n_seqs, GD_EINVAL,
                "attn_decode_q8: max_pages must be >= 1 with a page table, the cache must have a page per sequence without");
     int64_t cap;
@@ -154,14 +636,46 @@ extern "C" int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, c
     GD_REQUIRE(aligned(workspace, 16), GD_EALIGN, "attn_decode_q8: workspace must be 16-byte aligned");
     GD_REQUIRE(workspace_bytes >= need, GD_ERANGE, "attn_decode_q8: workspace of %zu bytes, %zu needed",
                workspace_bytes, need);
+    const Plan p = plan_of(n_seqs, n_heads, cache->n_kv_heads, cache->head_dim, max_q, max_kv_len);
     AttnArgs a;
     a.c = *cache;
     a.q = q, a.out = out, a.page_table = page_table, a.kv_lens = kv_lens, a.q_start = q_start, a.tree = tree_mask;
     a.max_pages = max_pages, a.n_seqs = n_seqs, a.n_q = n_q, a.n_heads = n_heads, a.max_q = max_q;
     a.max_kv_len = max_kv_len, a.scale = scale, a.softcap = softcap;
-    const dim3 grid(static_cast<uint32_t>(n_heads), static_cast<uint32_t>(max_q), static_cast<uint32_t>(n_seqs));
+    a.chunk = p.chunk, a.splits = static_cast<int32_t>(p.splits), a.row_blocks = static_cast<int32_t>(p.row_blocks);
+    // 16-key tiles (fewer than 2^27) to pages by a multiplication: with 2^(L-1) < per <= 2^L and
+    // magic = ceil(2^(31+L) / per), tile * (magic * per - 2^(31+L)) < 2^(27+L), so the quotient is exact.
+    const uint64_t per = static_cast<uint64_t>(cache->page_size / 16);
+    int shift = 31;
+    while ((UINT64_C(1) << (shift - 31)) < per) shift++;
+    a.page_magic = static_cast<uint32_t>(((UINT64_C(1) << shift) + per - 1) / per);
+    a.page_shift = shift;
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = a.part_o + n_q * n_heads * p.splits * cache->head_dim;
+    const dim3 grid(static_cast<uint32_t>(cache->n_kv_heads * p.row_blocks), static_cast<uint32_t>(p.splits),
+                    static_cast<uint32_t>(n_seqs));
+    const dim3 merge_grid(static_cast<uint32_t>(n_heads), static_cast<uint32_t>(max_q), static_cast<uint32_t>(n_seqs));
+    hipStream_t hs = as_stream(stream);
     dispatch_dtype(dtype, [&](auto t) {
-        hipLaunchKernelGGL((attn_q8_kernel<decltype(t)>), grid, dim3(64), 0, as_stream(stream), a);
+        using T = decltype(t);
+        constexpr int NS = sizeof(T) == 4 ? 2 : 1;
+        const auto launch = [&](auto dim) {
+            constexpr int D = decltype(dim)::value;
+            if (p.row_tiles == 2) {
+                if constexpr (D <= 128)
+                    hipLaunchKernelGGL((attn_q8_kernel<T, D, NS, 2>), grid, dim3(kThreads), 0, hs, a);
+            } else {
+                hipLaunchKernelGGL((attn_q8_kernel<T, D, NS, 1>), grid, dim3(kThreads), 0, hs, a);
+            }
+            if (p.splits > 1)
+                hipLaunchKernelGGL((attn_q8_merge_kernel<T, D>), merge_grid, dim3(kThreads), 0, hs, a);
+        };
+        if (cache->head_dim == 64)
+            launch(std::integral_constant<int, 64>{});
+        else if (cache->head_dim == 128)
+            launch(std::integral_constant<int, 128>{});
+        else
+            launch(std::integral_constant<int, 256>{});
     });
     return check_launch("attn_decode_q8");
 }

@@ -593,8 +593,8 @@ int kv_q8_load(const gd_kv_q8 *cache, const int64_t *slots, void *k_out, void *v
  * attn_decode_splitk). f16 and bf16: the products run on operands rounded to
  * f16 (weights of the softmax included), sums in f32.
  * Requires n_heads % n_kv_heads == 0, max_q <= 64, n_q <= n_seqs * max_q,
- * n_heads <= 4096, n_seqs <= 65535, max_kv_len < 2^31, finite scale, finite
- * softcap >= 0. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE, GD_EHIP. */
+ * n_heads <= 4096, n_seqs <= 65535, max_kv_len <= 2^30, finite scale,
+ * 0 <= softcap <= 1e30. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE, GD_EHIP. */
 int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, const int32_t *page_table,
                    int64_t max_pages, const int32_t *kv_lens, const int32_t *q_start,
                    const uint64_t *tree_mask, int64_t n_seqs, int64_t n_q, int64_t n_heads,

@@ -133,14 +133,14 @@ def test_attention_refusals(gd):
     nan, inf = float("nan"), float("inf")
     for bad in (dict(q=None), dict(out=None), dict(lens=None), dict(n_seqs=0), dict(n_q=0), dict(heads=0),
                 dict(max_q=0), dict(max_len=0), dict(dt=3), dict(scale=nan), dict(scale=inf), dict(cap=-1.0),
-                dict(cap=nan), dict(cap=inf), dict(ws=None), dict(max_pages=0), dict(max_len=257),
+                dict(cap=nan), dict(cap=inf), dict(cap=2e30), dict(ws=None), dict(max_pages=0), dict(max_len=257),
                 dict(start=None), dict(table=None, max_len=33), dict(table=None, n_seqs=5, n_q=5, max_len=20)):
         assert attn(gd, ref, **bad) == INVAL, bad
     assert attn(gd, ref, heads=3) == SHAPE
     for bad in (dict(q=FAKE + 8), dict(out=FAKE + 4), dict(table=FAKE + 2), dict(lens=FAKE + 1), dict(start=FAKE + 2),
                 dict(tree=FAKE + 4), dict(ws=FAKE + 8)):
         assert attn(gd, ref, **bad) == ALIGN, bad
-    for bad in (dict(max_q=65), dict(n_q=5), dict(heads=8192), dict(n_seqs=65536, n_q=3), dict(max_len=1 << 31),
+    for bad in (dict(max_q=65), dict(n_q=5), dict(heads=8192), dict(n_seqs=65536, n_q=3), dict(max_len=(1 << 30) + 1),
                 dict(ws_bytes=8)):
         assert attn(gd, ref, **bad) == RANGE, bad
 

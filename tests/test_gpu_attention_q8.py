@@ -211,6 +211,18 @@ def test_pages_outside_the_pool_are_not_seen(gd):
     assert not got[1].any()
 
 
+@pytest.mark.parametrize("T", [F32, BF16])
+def test_drafted_keys_that_nobody_sees_may_be_unstored(gd, T):
+    """Rows of a tree call whose words leave out a drafted key, whose row holds NaN scales and any codes."""
+    words = [1 << 0, 1 << 0, 0b1001]
+    c = Case(gd, [40], [3], 4, 2, 64, 16, T, words=words)
+    for at in (38, 39):
+        g, p = c.table[0, at // 16], at % 16
+        for t in (c.cache.k_scales, c.cache.v_scales):
+            t[g, :, p] = float("nan") if at == 38 else float("inf")
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_scales(gd, scale):
     """Means, negative scales, and scores in the hundreds."""
