@@ -403,6 +403,7 @@ def attn_decode_splitk_noalloc(q, k_cache, v_cache, out, n_heads: int, n_kv_head
 # -------------------------------------------- norm with an 8-bit output
 
 _dtype_code = {}
+_attn_bytes = {}   # workspace bytes by sizes: a pure function of them, called for each launch
 
 
 def _dtype(t, name):
@@ -420,12 +421,17 @@ def _current():
     """(index of the current device, torch's current stream on it)."""
     import torch
     i = torch.cuda.current_device()
-    return i, torch.cuda.current_stream(i).cuda_stream
+    return i, torch._C._cuda_getCurrentRawStream(i)   # 0.1 us; a torch.cuda.Stream object takes 1.1
 
 
 def _on(index, t, dtype, numel, name):
     """data_ptr of a contiguous tensor of this type and size on device `index`, the one the call launches on."""
-    p = _dev(t, dtype, numel, name)
+    try:
+        if t.dtype == dtype and t.get_device() == index and t.is_contiguous() and (numel is None or t.numel() == numel):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _dev(t, dtype, numel, name)   # says what is wrong
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
     return p
@@ -529,12 +535,13 @@ def rope_table(table, n_pos: int, rot_dim: int, base: float = 10000.0, scaling: 
 def _token_rows(i, t, dtype, n_tok, width, name):
     """(data_ptr, stride between tokens) of a tensor of n_tok rows of `width`
     elements: [n_tok, width] or [n_tok, heads, head_dim], each row contiguous."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != i:
+    try:
+        good = t.dtype == dtype and t.get_device() == i
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if not good:
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{i}")
     shape, strides = t.shape, t.stride()
     if len(shape) == 3:
@@ -624,8 +631,14 @@ def attn_decode_q8(q, cache: KVCacheQ8, page_table, kv_lens, q_start, tree_mask,
         if page_table.dim() != 2 or page_table.shape[0] != n_seqs:
             raise ValueError(f"page_table must be [{n_seqs}, max_pages], got {tuple(page_table.shape)}")
         max_pages = page_table.shape[1]
-    need = attn_decode_q8_workspace_bytes(n_seqs, n_q, n_heads, cache.n_kv_heads, D, max_q, max_kv_len)
     if workspace is None:
+        sizes = (n_seqs, n_q, n_heads, cache.n_kv_heads, D, max_q, max_kv_len)
+        need = _attn_bytes.get(sizes)
+        if need is None:
+            need = attn_decode_q8_workspace_bytes(*sizes)
+            if len(_attn_bytes) >= 4096:
+                _attn_bytes.clear()
+            _attn_bytes[sizes] = need
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check(_lib.attn_decode_q8(ref, _on(i, q, q.dtype, n, "q"), _on(i, out, q.dtype, n, "out"), table, max_pages, lens,
                                None if q_start is None else _on(i, q_start, torch.int32, n_seqs + 1, "q_start"),
