@@ -64,7 +64,7 @@ struct AttnArgs {
     int32_t splits;        // parts of the longest sequence
     int32_t row_blocks;    // workgroups that share the rows of a KV head
     uint32_t page_magic;   // tile / (page_size / 16) = tile * page_magic >> page_shift
-    int32_t page_shift;
+    int32_t page_shift, page_tiles;   // page_size / 16
     float scale, softcap;
     float *part_o, *part_ml;
 };
@@ -98,20 +98,37 @@ __device__ __forceinline__ int parts_of(const AttnArgs &a, int64_t len) {
     return n < 1 ? 1 : n;
 }
 
-// 16 positions of one KV head: the cache row of the first, and whether they are
-// there (a page outside the pool is read as page 0 and masked).
-struct Tile {
-    int64_t row;
-    bool ok;
+// 32 positions of one KV head, as two tiles of 16: where their codes begin (the
+// scales at a sixteenth of that), and whether they are there (a page outside the
+// pool is read as page 0 and masked; a tile past the end is the last one again,
+// masked by its positions).
+struct Place {
+    int64_t at[2];
+    bool ok[2];
 };
 
-__device__ __forceinline__ Tile tile_at(const AttnArgs &a, int64_t b, int kvh, int tile) {
-    const int i = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(tile)) * a.page_magic) >> a.page_shift);
-    const int per = static_cast<int>(a.c.page_size / 16);
-    int64_t page = a.page_table ? a.page_table[b * a.max_pages + i] : b;
-    const bool ok = page >= 0 && page < a.c.n_pages;
-    page = ok ? page : 0;
-    return {(page * a.c.n_kv_heads + kvh) * a.c.page_size + static_cast<int64_t>(tile - i * per) * 16, ok};
+// Page `i` of sequence b, 0 and false if there is none.
+__device__ __forceinline__ int32_t page_of(const AttnArgs &a, int64_t b, int i, bool &ok) {
+    const int32_t page = a.page_table ? a.page_table[b * a.max_pages + i] : static_cast<int32_t>(b);
+    ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.n_pages);
+    return ok ? page : 0;
+}
+
+template <int D>
+__device__ __forceinline__ Place place_of(const AttnArgs &a, int64_t b, int kvh, int tile, int last) {
+    const int per = a.page_tiles, Hkv = static_cast<int>(a.c.n_kv_heads);
+    Place p;
+    int i = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(tile)) * a.page_magic) >> a.page_shift);
+    int in = tile - i * per;
+    p.at[0] = ((static_cast<int64_t>(page_of(a, b, i, p.ok[0])) * Hkv + kvh) * per + in) * (16 * D);
+    if (tile == last) {
+        p.at[1] = p.at[0], p.ok[1] = p.ok[0];
+    } else if (in + 1 < per) {
+        p.at[1] = p.at[0] + 16 * D, p.ok[1] = p.ok[0];
+    } else {
+        p.at[1] = (static_cast<int64_t>(page_of(a, b, i + 1, p.ok[1])) * Hkv + kvh) * per * (16 * D);
+    }
+    return p;
 }
 
 // v of this lane and of the lane 16 (32) further round, in some order.
@@ -162,7 +179,21 @@ __device__ __forceinline__ f16x8 codes_f16(u32x2 w) {
     return f.v;
 }
 
-// 2^k as f16 and f32, for powers in the range of either.
+// tanh to about 2^-21 of itself: its series below 0.35 (the first term left out,
+// x^12 / 277, is 2^-26 there), 1 - 2 / (e^2|x| + 1) above.
+__device__ __forceinline__ float tanh_f32(float x) {
+    const float y = x * x;
+    float r = __builtin_fmaf(y, -1382.0f / 155925.0f, 62.0f / 2835.0f);
+    r = __builtin_fmaf(y, r, -17.0f / 315.0f);
+    r = __builtin_fmaf(y, r, 2.0f / 15.0f);
+    r = __builtin_fmaf(y, r, -1.0f / 3.0f);
+    r = __builtin_fmaf(x * y, r, x);
+    const float e = __builtin_amdgcn_exp2f(fabsf(x) * (2.0f * kLog2e));
+    const float t = __builtin_copysignf(1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f), x);
+    return fabsf(x) < 0.35f ? r : t;
+}
+
+// 2^k as f16, -14 <= k <= 15.
 __device__ __forceinline__ _Float16 pow2_f16(int k) { return __builtin_bit_cast(_Float16, static_cast<uint16_t>((k + 15) << 10)); }
 
 // The keys and values of one step of a wave, as loaded: for each of its two
@@ -177,35 +208,35 @@ struct Step {
 };
 
 template <int D>
-__device__ __forceinline__ void load_keys(const AttnArgs &a, const Tile (&t)[2], int lane, Step<D> &s) {
+__device__ __forceinline__ void load_keys(const AttnArgs &a, const Place &t, int lane, Step<D> &s) {
     const int n = lane % 16, g = lane / 16;
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-        const int8_t *p = a.c.k_codes + t[u].row * D;
-        const uint16_t *d = a.c.k_scales + t[u].row * (D / 32);
+        const int8_t *p = a.c.k_codes + t.at[u];
+        const char *d = reinterpret_cast<const char *>(a.c.k_scales) + t.at[u] / 16;
 #pragma unroll
         for (int c = 0; c < D / 32; c++)
             s.k[u][c] = *reinterpret_cast<const u32x2 *>(p + (n * D + 8 * g + 32 * c));
 #pragma unroll
-        for (int c = 0; c < D / 32; c++) s.ks[u][c] = reinterpret_cast<const u32x2 *>(d + 4 * g * (D / 32))[c];
+        for (int c = 0; c < D / 32; c++) s.ks[u][c] = reinterpret_cast<const u32x2 *>(d + g * (D / 4))[c];
     }
 }
 
 template <int D>
-__device__ __forceinline__ void load_values(const AttnArgs &a, const Tile (&t)[2], int lane, Step<D> &s) {
+__device__ __forceinline__ void load_values(const AttnArgs &a, const Place &t, int lane, Step<D> &s) {
     constexpr int VB = D / 16;
     const int n = lane % 16, g = lane / 16;
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-        const int8_t *p = a.c.v_codes + t[u].row * D;
-        const uint16_t *d = a.c.v_scales + t[u].row * (D / 32);
+        const int8_t *p = a.c.v_codes + t.at[u];
+        const char *d = reinterpret_cast<const char *>(a.c.v_scales) + t.at[u] / 16;
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int w = 0; w < VB / 4; w++)
                 s.v[u][i][w] = reinterpret_cast<const uint32_t *>(p + ((4 * g + i) * D + n * VB))[w];
 #pragma unroll
-        for (int c = 0; c < D / 32; c++) s.vs[u][c] = reinterpret_cast<const u32x2 *>(d + 4 * g * (D / 32))[c];
+        for (int c = 0; c < D / 32; c++) s.vs[u][c] = reinterpret_cast<const u32x2 *>(d + g * (D / 4))[c];
     }
 }
 
@@ -292,30 +323,19 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
 
     Step<D> st;
     int j = j0 + kStep * wave;
-    const auto tiles = [&](int at, Tile (&t)[2]) {
-        const int last = (j1 - 1) / 16;   // a tile past the end is the last one again, masked by its positions
-#pragma unroll
-        for (int u = 0; u < 2; u++) {
-            const int i = at / 16 + u;
-            t[u] = tile_at(a, b, kvh, __builtin_amdgcn_readfirstlane(i < last ? i : last));
-        }
-    };
-    Tile tl[2];
+    const int last = (j1 - 1) / 16;
+    Place next = {};
     if (j < j1) {
-        tiles(j, tl);
-        load_keys<D>(a, tl, lane, st);
-        load_values<D>(a, tl, lane, st);
+        next = place_of<D>(a, b, kvh, j / 16, last);
+        load_keys<D>(a, next, lane, st);
+        load_values<D>(a, next, lane, st);
     }
     for (; j < j1; j += kGroupKeys) {
         const bool more = j + kGroupKeys < j1;
-        const bool plain = j + kStep <= (ctx < j1 ? ctx : j1) && tl[0].ok && tl[1].ok;   // every row sees every key
+        const bool ok[2] = {next.ok[0], next.ok[1]};
+        const bool plain = j + kStep <= (ctx < j1 ? ctx : j1) && ok[0] && ok[1];   // every row sees every key
+        if (more) next = place_of<D>(a, b, kvh, (j + kGroupKeys) / 16, last);
         float s[RT][2][4];
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-            for (int u = 0; u < 2; u++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) s[rt][u][i] = 0.0f;
 #pragma unroll
         for (int u = 0; u < 2; u++)
 #pragma unroll
@@ -328,41 +348,43 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         const f16x2 w = as_h2(scale_word<C>(st.ks[u], (i * C + c) / 2));
-                        s[rt][u][i] = __builtin_fmaf(d[i], static_cast<float>(w[c % 2]), s[rt][u][i]);
+                        const float before = c == 0 ? 0.0f : s[rt][u][i];
+                        s[rt][u][i] = __builtin_fmaf(d[i], static_cast<float>(w[c % 2]), before);
                     }
                 }
             }
-        const Tile here[2] = {tl[0], tl[1]};
-        if (more) {
-            tiles(j + kGroupKeys, tl);
-            load_keys<D>(a, tl, lane, st);
-        }
+        if (more) load_keys<D>(a, next, lane, st);
         // Weights, each lane its 8 keys of row n.
         Frag p[RT][NS];
 #pragma unroll
         for (int rt = 0; rt < RT; rt++) {
-            float mx = kNone;
 #pragma unroll
-            for (int u = 0; u < 2; u++)
+            for (int x = 0; x < 8; x++) s[rt][x / 4][x % 4] *= scale2[rt];
+            if (a.softcap > 0.0f) {
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    float x = s[rt][u][i] * scale2[rt];
-                    if (a.softcap > 0.0f) x = tanhf(x) * (a.softcap * kLog2e);
-                    if (!plain) {
-                        const int jj = j + 16 * u + 4 * g + i;
-                        const bool sees = here[u].ok && jj < j1 && (jj < ctx || ((word[rt] >> ((jj - ctx) & 63)) & 1));
-                        x = sees ? x : -__builtin_inff();
-                    }
-                    s[rt][u][i] = x;
-                    mx = fmaxf(mx, x);
+                for (int x = 0; x < 8; x++)
+                    s[rt][x / 4][x % 4] = tanh_f32(s[rt][x / 4][x % 4]) * (a.softcap * kLog2e);
+            }
+            if (!plain) {
+#pragma unroll
+                for (int x = 0; x < 8; x++) {
+                    const int jj = j + 16 * (x / 4) + 4 * g + x % 4;
+                    const bool sees = ok[x / 4] && jj < j1 && (jj < ctx || ((word[rt] >> ((jj - ctx) & 63)) & 1));
+                    s[rt][x / 4][x % 4] = sees ? s[rt][x / 4][x % 4] : -__builtin_inff();
                 }
-            const float mn = fmaxf(m[rt], max_across(mx));
-            const float corr = __builtin_amdgcn_exp2f(m[rt] - mn);
-            m[rt] = mn;
-            l[rt] *= corr;
+            }
+            float mx = m[rt];
 #pragma unroll
-            for (int t = 0; t < VB; t++) o[rt][t] *= corr;
-            const float off = mn - kWeightBits;
+            for (int x = 0; x < 8; x++) mx = fmaxf(mx, s[rt][x / 4][x % 4]);
+            if (__any(mx > m[rt])) {   // no row's maximum grows in most steps of a long sequence
+                const float mn = max_across(mx);
+                const float corr = __builtin_amdgcn_exp2f(m[rt] - mn);
+                m[rt] = mn;
+                l[rt] *= corr;
+#pragma unroll
+                for (int t = 0; t < VB; t++) o[rt][t] *= corr;
+            }
+            const float off = m[rt] - kWeightBits;
 #pragma unroll
             for (int u = 0; u < 2; u++)
 #pragma unroll
@@ -377,9 +399,10 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
                 }
         }
         // The V scales of the lane's 8 keys at its dims' group, in pairs.
-        f16x2 vs[2][2];
+        uint32_t pr[2][2];
         {
             const int cl = n * VB / 32;
+            const uint32_t sel = cl % 2 ? 0x07060302u : 0x05040100u;
 #pragma unroll
             for (int u = 0; u < 2; u++) {
                 uint32_t w[4];
@@ -389,19 +412,21 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
 #pragma unroll
                     for (int k = 1; k < C / 2; k++) w[i] = cl / 2 == k ? scale_word<C>(st.vs[u], i * C / 2 + k) : w[i];
                 }
-                const uint32_t sel = cl % 2 ? 0x07060302u : 0x05040100u;
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    uint32_t pr = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], sel);
-                    if (!plain) {   // scales that no one stored may be anything, and weights of 0 do not hide it
-                        const int jj = j + 16 * u + 4 * g + 2 * i;
-                        if (!here[u].ok || jj >= j1 || (pr & 0x7c00u) == 0x7c00u) pr &= 0xffff0000u;
-                        if (!here[u].ok || jj + 1 >= j1 || (pr & 0x7c000000u) == 0x7c000000u) pr &= 0x0000ffffu;
-                    }
-                    vs[u][i] = as_h2(pr);
-                }
+                for (int i = 0; i < 2; i++) pr[u][i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], sel);
             }
         }
+        if (!plain) {   // scales that no one stored may be anything, and weights of 0 do not hide it
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                const int u = x / 2, i = x % 2, jj = j + 16 * u + 4 * g + 2 * i;
+                if (!ok[u] || jj >= j1 || (pr[u][i] & 0x7c00u) == 0x7c00u) pr[u][i] &= 0xffff0000u;
+                if (!ok[u] || jj + 1 >= j1 || (pr[u][i] & 0x7c000000u) == 0x7c000000u) pr[u][i] &= 0x0000ffffu;
+            }
+        }
+        f16x2 vs[2][2];
+#pragma unroll
+        for (int x = 0; x < 4; x++) vs[x / 2][x % 2] = as_h2(pr[x / 2][x % 2]);
         f16x2 top = __builtin_elementwise_max(__builtin_elementwise_max(vs[0][0], vs[0][1]),
                                               __builtin_elementwise_max(vs[1][0], vs[1][1]));
         _Float16 lane_top = top[0] > top[1] ? top[0] : top[1];
@@ -457,7 +482,7 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
                 }
             }
         }
-        if (more) load_values<D>(a, tl, lane, st);
+        if (more) load_values<D>(a, next, lane, st);
     }
 
     // Join the four waves.
@@ -650,6 +675,7 @@ extern "C" int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, c
     while ((UINT64_C(1) << (shift - 31)) < per) shift++;
     a.page_magic = static_cast<uint32_t>(((UINT64_C(1) << shift) + per - 1) / per);
     a.page_shift = shift;
+    a.page_tiles = static_cast<int32_t>(per);
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = a.part_o + n_q * n_heads * p.splits * cache->head_dim;
     const dim3 grid(static_cast<uint32_t>(cache->n_kv_heads * p.row_blocks), static_cast<uint32_t>(p.splits),
