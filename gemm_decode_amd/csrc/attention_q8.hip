@@ -13,14 +13,19 @@
 // another until the end, where they are joined through LDS. A second launch
 // joins the parts of a sequence, if it has more than one.
 //
-// No operand passes through LDS. Scores are taken transposed, S^T = K Q^T:
-// lane (n, g) = (lane % 16, lane / 16) loads 8 dims of key n per 32-dim group,
-// one matrix instruction contracts exactly one group, and its result, multiplied
-// by the group's scale, is added up in f32. The result has lane (n, g) hold keys
-// 4g .. 4g+3 of query row n, which is how the second product, O^T = V^T P^T,
-// takes its weights: they never leave their lane. For V^T the lane (n, g) loads
-// D/16 dims (from n D/16 on) of the same keys; these dims lie in one scale
-// group, so a value is its code times one scale per key.
+// No operand passes through LDS, and every load of codes is 16 bytes a lane, past
+// the caches (loads of 8 bytes a lane, four to a line, ran at 4.2 TB/s, the same
+// bytes as these at 6.3). Scores are taken transposed, S^T = K Q^T: lane (n, g) =
+// (lane % 16, lane / 16) loads 16 dims of key n, half of them is swapped with lane
+// (n, g ^ 2), and then one matrix instruction contracts exactly one 32-dim group;
+// its result, multiplied by the group's scale, is added up in f32. The result has
+// lane (n, g) hold keys 4g .. 4g+3 of query row n, which is how the second product,
+// O^T = V^T P^T, takes its weights: they never leave their lane. For V^T the lane
+// has to hold D/16 dims of the same four keys; a row of D bytes is D/16 lanes' loads,
+// so up to four lanes load one key each and exchange parts. The dims of a lane lie in
+// one scale group, so a value is its code times one scale per key. The scales come
+// as one number a lane and tile, and are handed round as the operand of the
+// instruction that uses them (DPP).
 //
 // Precision. Codes are whole numbers below 2^8, exact in f16. f32 inputs: q (as
 // a power of two times its row) and the weights are split into two f16 parts, 22
@@ -196,16 +201,24 @@ __device__ __forceinline__ float tanh_f32(float x) {
 // 2^k as f16, -14 <= k <= 15.
 __device__ __forceinline__ _Float16 pow2_f16(int k) { return __builtin_bit_cast(_Float16, static_cast<uint16_t>((k + 15) << 10)); }
 
-// The keys and values of one step of a wave, as loaded: for each of its two
-// tiles of 16 keys the lane's K codes (8 dims of key n per group), its V codes
-// (D/16 dims of keys 4g .. 4g+3) and the scales of keys 4g .. 4g+3, K and V.
+// Dims of the lane's V operand: VB of them from v_dim on, for operand row m.
+template <int D>
+__device__ __forceinline__ int v_dim(int m) {
+    return D == 64 ? 16 * (m % 4) + 4 * (m / 4) : D == 128 ? 16 * (m % 8) + 8 * (m / 8) : 16 * m;
+}
+
+// The keys and values of one step of a wave, as loaded, for each of its two tiles
+// of 16 keys: 16 dims of key n from 64 i + 16 g on; 16 dims of one of the keys
+// 4g .. 4g+3, of which several lanes with one g load all; and scales.
 template <int D>
 struct Step {
-    static constexpr int C = D / 32, VB = D / 16;   // scale groups; V bytes per key and lane
-    u32x2 k[2][C];
-    uint32_t v[2][4][VB / 4];
-    u32x2 ks[2][C], vs[2][C];   // 4 keys x C f16, key-major
+    u32x4 k[2][D / 64], v[2][D / 64];
+    uint32_t ks[2], vs[2];
 };
+
+__device__ __forceinline__ u32x4 load16(const int8_t *p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+}
 
 template <int D>
 __device__ __forceinline__ void load_keys(const AttnArgs &a, const Place &t, int lane, Step<D> &s) {
@@ -213,37 +226,122 @@ __device__ __forceinline__ void load_keys(const AttnArgs &a, const Place &t, int
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         const int8_t *p = a.c.k_codes + t.at[u];
-        const char *d = reinterpret_cast<const char *>(a.c.k_scales) + t.at[u] / 16;
+        const uint16_t *d = a.c.k_scales + t.at[u] / 32;
 #pragma unroll
-        for (int c = 0; c < D / 32; c++)
-            s.k[u][c] = *reinterpret_cast<const u32x2 *>(p + (n * D + 8 * g + 32 * c));
-#pragma unroll
-        for (int c = 0; c < D / 32; c++) s.ks[u][c] = reinterpret_cast<const u32x2 *>(d + g * (D / 4))[c];
+        for (int i = 0; i < D / 64; i++) s.k[u][i] = load16(p + (n * D + 64 * i + 16 * g));
+        // scale number n (two of them for D = 256) of the D/8 of keys 4g .. 4g+3, key-major
+        if constexpr (D == 256)
+            s.ks[u] = reinterpret_cast<const uint32_t *>(d)[lane];
+        else
+            s.ks[u] = d[D == 128 ? lane : 8 * g + n % 8];
     }
 }
 
 template <int D>
 __device__ __forceinline__ void load_values(const AttnArgs &a, const Place &t, int lane, Step<D> &s) {
-    constexpr int VB = D / 16;
     const int n = lane % 16, g = lane / 16;
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         const int8_t *p = a.c.v_codes + t.at[u];
-        const char *d = reinterpret_cast<const char *>(a.c.v_scales) + t.at[u] / 16;
+        const uint32_t *d = reinterpret_cast<const uint32_t *>(a.c.v_scales + t.at[u] / 32);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int w = 0; w < VB / 4; w++)
-                s.v[u][i][w] = reinterpret_cast<const uint32_t *>(p + ((4 * g + i) * D + n * VB))[w];
-#pragma unroll
-        for (int c = 0; c < D / 32; c++) s.vs[u][c] = reinterpret_cast<const u32x2 *>(d + g * (D / 4))[c];
+        for (int i = 0; i < D / 64; i++) {
+            const int key = D == 64 ? n / 4 : D == 128 ? 2 * (n / 8) + i : i;
+            const int piece = D == 64 ? n % 4 : D == 128 ? n % 8 : n;
+            s.v[u][i] = load16(p + ((4 * g + key) * D + 16 * piece));
+        }
+        // the pair of scales with the lane's group in it, of key 4g + n % 4 (a quad of lanes has all four)
+        s.vs[u] = d[(4 * g + n % 4) * (D / 64) + v_dim<D>(n) / 64];
     }
 }
 
-// f16 number `i` of the lane's 4 x C scales.
-template <int C>
-__device__ __forceinline__ uint32_t scale_word(const u32x2 (&s)[C], int i) {   // the pair 2i, 2i + 1
-    return s[i / 2][i % 2];
+// The lane's K operand of every group, from what load_keys loaded: the groups
+// 2i and 2i + 1 lie in lanes g < 2 and g >= 2; the upper lanes' first halves
+// change places with the lower lanes' second halves.
+template <int D>
+__device__ __forceinline__ void spread_keys(const u32x4 (&k)[D / 64], u32x2 (&out)[D / 32]) {
+#pragma unroll
+    for (int i = 0; i < D / 64; i++)
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            const u32x2 r = __builtin_amdgcn_permlane32_swap(k[i][w], k[i][w + 2], false, false);
+            out[2 * i][w] = r[0];
+            out[2 * i + 1][w] = r[1];
+        }
+}
+
+// lo and hi of the lanes change places between lane n and the lane kBy further
+// in its row of 16: the lanes of the banks kLow keep lo and take the other's lo
+// as hi, the others keep hi and take the other's hi as lo.
+template <int kBy, int kLow>
+__device__ __forceinline__ void exchange(uint32_t &lo, uint32_t &hi) {
+    const int l = static_cast<int>(lo), h = static_cast<int>(hi);
+    lo = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(l, h, 0x120 + kBy, 0xF, 0xF & ~kLow, false));
+    hi = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(h, l, 0x120 + 16 - kBy, 0xF, kLow, false));
+}
+
+// out[i][w]: dims v_dim + 4w .. of key 4g + i.
+template <int D>
+__device__ __forceinline__ void spread_values(const u32x4 (&v)[D / 64], uint32_t (&out)[4][D / 64]) {
+    if constexpr (D == 64) {   // lane n: key n / 4, to be dims 4 (n / 4) .. of every key
+        uint32_t x[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
+        exchange<8, 0x3>(x[0], x[2]);
+        exchange<8, 0x3>(x[1], x[3]);
+        exchange<4, 0x5>(x[0], x[1]);
+        exchange<4, 0x5>(x[2], x[3]);
+#pragma unroll
+        for (int i = 0; i < 4; i++) out[i][0] = x[i];
+    } else if constexpr (D == 128) {   // lanes n < 8: keys 0 and 1, n >= 8: 2 and 3; to be dims 8 (n / 8) .. of every key
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int w = 0; w < 2; w++) {
+                uint32_t lo = v[i][w], hi = v[i][w + 2];
+                exchange<8, 0x3>(lo, hi);
+                out[i][w] = lo;
+                out[2 + i][w] = hi;
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int w = 0; w < 4; w++) out[i][w] = v[i][w];
+    }
+}
+
+// x of lane kLane of each row of 16 lanes.
+template <int kLane>
+__device__ __forceinline__ float row_lane(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x150 + kLane, 0xF, 0xF, true));
+}
+
+template <int kLane>
+__device__ __forceinline__ uint32_t quad_lane(uint32_t x) {   // of each quad
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), kLane * 0x55, 0xF, 0xF, true));
+}
+
+// The scale of key 4g + kKey and group kC from a lane's share of them (f32; the
+// second word holds the odd ones for D = 256).
+template <int D, int kKey, int kC>
+__device__ __forceinline__ float key_scale(const float (&x)[2]) {
+    constexpr int at = kKey * (D / 32) + kC;
+    return D == 256 ? row_lane<(at / 2) % 16>(x[at % 2]) : row_lane<at % 16>(x[0]);
+}
+
+// s[i] += d[i] * the scale of key 4g + i and group kC.
+template <int D, int kC>
+__device__ __forceinline__ void add_scaled(float (&s)[4], f32x4 d, const float (&x)[2]) {
+    if constexpr (kC == 0) {
+        s[0] = d[0] * key_scale<D, 0, 0>(x);
+        s[1] = d[1] * key_scale<D, 1, 0>(x);
+        s[2] = d[2] * key_scale<D, 2, 0>(x);
+        s[3] = d[3] * key_scale<D, 3, 0>(x);
+    } else {
+        s[0] = __builtin_fmaf(key_scale<D, 0, kC>(x), d[0], s[0]);
+        s[1] = __builtin_fmaf(key_scale<D, 1, kC>(x), d[1], s[1]);
+        s[2] = __builtin_fmaf(key_scale<D, 2, kC>(x), d[2], s[2]);
+        s[3] = __builtin_fmaf(key_scale<D, 3, kC>(x), d[3], s[3]);
+    }
 }
 
 // NS = 2: operands in two f16 parts (f32 inputs), NS = 1: in one. A workgroup
@@ -286,7 +384,7 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
         for (int c = 0; c < C; c++)
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                x[c][i] = live ? load4(p + 32 * c + 8 * g + 4 * i) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                x[c][i] = live ? load4(p + 32 * c + 16 * (g % 2) + 8 * (g / 2) + 4 * i) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int j = 0; j < 4; j++) mx = fmaxf(mx, fabsf(x[c][i][j]));
             }
@@ -306,7 +404,7 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
         scale2[rt] = ldexpf(a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e, -e);
     }
 
-    f32x4 o[RT][VB];   // dims (4g + i) VB + t of row n
+    f32x4 o[RT][VB];   // o[rt][t][i]: dim v_dim(4g + i) + t of row n
     float m[RT], l[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
@@ -337,22 +435,34 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
         if (more) next = place_of<D>(a, b, kvh, (j + kGroupKeys) / 16, last);
         float s[RT][2][4];
 #pragma unroll
-        for (int u = 0; u < 2; u++)
-#pragma unroll
-            for (int c = 0; c < C; c++) {
-                const f16x8 kf = codes_f16(st.k[u][c]);
+        for (int u = 0; u < 2; u++) {
+            u32x2 kw[C];
+            spread_keys<D>(st.k[u], kw);
+            const f16x2 ks = as_h2(st.ks[u]);
+            const float x[2] = {static_cast<float>(ks[0]), static_cast<float>(ks[1])};
+            const auto group = [&](auto cc) {
+                constexpr int c = decltype(cc)::value;
+                const f16x8 kf = codes_f16(kw[c]);
 #pragma unroll
                 for (int rt = 0; rt < RT; rt++) {
                     f32x4 d = mfma(kf, q[rt][c][0].v, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
                     if constexpr (NS == 2) d = mfma(kf, q[rt][c][NS - 1].v, d);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const f16x2 w = as_h2(scale_word<C>(st.ks[u], (i * C + c) / 2));
-                        const float before = c == 0 ? 0.0f : s[rt][u][i];
-                        s[rt][u][i] = __builtin_fmaf(d[i], static_cast<float>(w[c % 2]), before);
-                    }
+                    add_scaled<D, c>(s[rt][u], d, x);
                 }
+            };
+            group(std::integral_constant<int, 0>{});
+            group(std::integral_constant<int, 1>{});
+            if constexpr (C > 2) {
+                group(std::integral_constant<int, 2>{});
+                group(std::integral_constant<int, 3>{});
             }
+            if constexpr (C > 4) {
+                group(std::integral_constant<int, 4>{});
+                group(std::integral_constant<int, 5>{});
+                group(std::integral_constant<int, 6>{});
+                group(std::integral_constant<int, 7>{});
+            }
+        }
         if (more) load_keys<D>(a, next, lane, st);
         // Weights, each lane its 8 keys of row n.
         Frag p[RT][NS];
@@ -401,19 +511,11 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
         // The V scales of the lane's 8 keys at its dims' group, in pairs.
         uint32_t pr[2][2];
         {
-            const int cl = n * VB / 32;
-            const uint32_t sel = cl % 2 ? 0x07060302u : 0x05040100u;
+            const uint32_t sel = (v_dim<D>(n) / 32) % 2 ? 0x07060302u : 0x05040100u;
 #pragma unroll
             for (int u = 0; u < 2; u++) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    w[i] = scale_word<C>(st.vs[u], i * C / 2);
-#pragma unroll
-                    for (int k = 1; k < C / 2; k++) w[i] = cl / 2 == k ? scale_word<C>(st.vs[u], i * C / 2 + k) : w[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 2; i++) pr[u][i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], sel);
+                pr[u][0] = __builtin_amdgcn_perm(quad_lane<1>(st.vs[u]), quad_lane<0>(st.vs[u]), sel);
+                pr[u][1] = __builtin_amdgcn_perm(quad_lane<3>(st.vs[u]), quad_lane<2>(st.vs[u]), sel);
             }
         }
         if (!plain) {   // scales that no one stored may be anything, and weights of 0 do not hide it
@@ -453,11 +555,12 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
             for (int i = 0; i < 2; i++) vs[u][i] *= f16x2{vmul, vmul};
         uint32_t vx[2][4][VB / 4];
 #pragma unroll
-        for (int u = 0; u < 2; u++)
+        for (int u = 0; u < 2; u++) {
+            u32x4 biased[D / 64];
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int w = 0; w < VB / 4; w++) vx[u][i][w] = st.v[u][i][w] ^ 0x80808080u;
+            for (int i = 0; i < D / 64; i++) biased[i] = st.v[u][i] ^ 0x80808080u;
+            spread_values<D>(biased, vx[u]);
+        }
 #pragma unroll
         for (int t = 0; t < VB; t++) {
             // byte t of two keys as (code + 128) 2^-24 (f16's smallest steps), times 2^14, less 2^-3: code 2^-10
@@ -499,7 +602,7 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
         for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int t = 0; t < VB; t += 4)
-                lds_o[wave][r][((4 * g + i) * VB + t) / 4] =
+                lds_o[wave][r][(v_dim<D>(4 * g + i) + t) / 4] =
                     f32x4{o[rt][t][i], o[rt][t + 1][i], o[rt][t + 2][i], o[rt][t + 3][i]} * f;
     }
     __syncthreads();
