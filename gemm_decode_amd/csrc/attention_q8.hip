@@ -119,19 +119,21 @@ __device__ __forceinline__ int32_t page_of(const AttnArgs &a, int64_t b, int i, 
     return ok ? page : 0;
 }
 
+// Tile `tile` (16 positions) of sequence b and the one behind it. `of_page`:
+// bytes of codes between pages; `of_head`: where the KV head's lie in a page.
 template <int D>
-__device__ __forceinline__ Place place_of(const AttnArgs &a, int64_t b, int kvh, int tile, int last) {
-    const int per = a.page_tiles, Hkv = static_cast<int>(a.c.n_kv_heads);
+__device__ __forceinline__ Place place_of(const AttnArgs &a, int64_t b, int64_t of_page, int64_t of_head, int tile, int last) {
+    const int per = a.page_tiles;
     Place p;
-    int i = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(tile)) * a.page_magic) >> a.page_shift);
-    int in = tile - i * per;
-    p.at[0] = ((static_cast<int64_t>(page_of(a, b, i, p.ok[0])) * Hkv + kvh) * per + in) * (16 * D);
+    const int i = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(tile)) * a.page_magic) >> a.page_shift);
+    const int in = tile - i * per;
+    p.at[0] = page_of(a, b, i, p.ok[0]) * of_page + of_head + static_cast<int64_t>(in) * (16 * D);
     if (tile == last) {
         p.at[1] = p.at[0], p.ok[1] = p.ok[0];
     } else if (in + 1 < per) {
         p.at[1] = p.at[0] + 16 * D, p.ok[1] = p.ok[0];
     } else {
-        p.at[1] = (static_cast<int64_t>(page_of(a, b, i + 1, p.ok[1])) * Hkv + kvh) * per * (16 * D);
+        p.at[1] = page_of(a, b, i + 1, p.ok[1]) * of_page + of_head;
     }
     return p;
 }
@@ -171,31 +173,36 @@ union Frag {   // one matrix operand of a lane: eight f16 along the contraction
     f16x2 h[4];
 };
 
-// Eight codes (bytes of w) as f16: 0x6400 | (code + 128) is 1024 + 128 + code.
-__device__ __forceinline__ f16x8 codes_f16(u32x2 w) {
+// Eight codes (bytes, code + 128) as f16: 0x6400 | (code + 128) is 1024 + 128 + code.
+__device__ __forceinline__ f16x8 codes_f16(u32x2 biased) {
     Frag f;
     const f16x2 bias = {static_cast<_Float16>(-1152.0f), static_cast<_Float16>(-1152.0f)};
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const uint32_t u = w[i] ^ 0x80808080u;
+        const uint32_t u = biased[i];
         f.h[2 * i] = as_h2(__builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) + bias;
         f.h[2 * i + 1] = as_h2(__builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) + bias;
     }
     return f.v;
 }
 
-// tanh to about 2^-21 of itself: its series below 0.35 (the first term left out,
+// tanh to about 2^-21 of itself: its series below kSeries (the first term left out,
 // x^12 / 277, is 2^-26 there), 1 - 2 / (e^2|x| + 1) above.
-__device__ __forceinline__ float tanh_f32(float x) {
+constexpr float kSeries = 0.35f;
+
+__device__ __forceinline__ float tanh_series(float x) {
     const float y = x * x;
     float r = __builtin_fmaf(y, -1382.0f / 155925.0f, 62.0f / 2835.0f);
     r = __builtin_fmaf(y, r, -17.0f / 315.0f);
     r = __builtin_fmaf(y, r, 2.0f / 15.0f);
     r = __builtin_fmaf(y, r, -1.0f / 3.0f);
-    r = __builtin_fmaf(x * y, r, x);
+    return __builtin_fmaf(x * y, r, x);
+}
+
+__device__ __forceinline__ float tanh_any(float x) {
     const float e = __builtin_amdgcn_exp2f(fabsf(x) * (2.0f * kLog2e));
     const float t = __builtin_copysignf(1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f), x);
-    return fabsf(x) < 0.35f ? r : t;
+    return fabsf(x) < kSeries ? tanh_series(x) : t;
 }
 
 // 2^k as f16, -14 <= k <= 15.
@@ -208,8 +215,8 @@ __device__ __forceinline__ int v_dim(int m) {
 }
 
 // The keys and values of one step of a wave, as loaded, for each of its two tiles
-// of 16 keys: 16 dims of key n from 64 i + 16 g on; 16 dims of one of the keys
-// 4g .. 4g+3, of which several lanes with one g load all; and scales.
+// of 16 keys: the K codes as they lie in memory, 16 bytes a lane; 16 dims of one of
+// the keys 4g .. 4g+3, of which several lanes with one g load all; and scales.
 template <int D>
 struct Step {
     u32x4 k[2][D / 64], v[2][D / 64];
@@ -228,7 +235,7 @@ __device__ __forceinline__ void load_keys(const AttnArgs &a, const Place &t, int
         const int8_t *p = a.c.k_codes + t.at[u];
         const uint16_t *d = a.c.k_scales + t.at[u] / 32;
 #pragma unroll
-        for (int i = 0; i < D / 64; i++) s.k[u][i] = load16(p + (n * D + 64 * i + 16 * g));
+        for (int i = 0; i < D / 64; i++) s.k[u][i] = load16(p + (1024 * i + 16 * lane));
         // scale number n (two of them for D = 256) of the D/8 of keys 4g .. 4g+3, key-major
         if constexpr (D == 256)
             s.ks[u] = reinterpret_cast<const uint32_t *>(d)[lane];
@@ -255,16 +262,34 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, const Place &t, i
     }
 }
 
-// The lane's K operand of every group, from what load_keys loaded: the groups
-// 2i and 2i + 1 lie in lanes g < 2 and g >= 2; the upper lanes' first halves
-// change places with the lower lanes' second halves.
+// A tile's K codes turned through the wave's own part of LDS from the order of
+// memory (lane after lane, D/16 lanes to a key) to 16 dims of key n per lane, from
+// 64 i + 16 g on. The 16-byte pieces of a key are stored in an order that differs
+// between the eight keys that one cycle reads, so that they lie in distinct banks.
+template <int D>
+__device__ __forceinline__ int piece_at(int key, int piece) {
+    return key * (D / 16) + (piece ^ (D == 64 ? key / 2 % 4 : key % 8));
+}
+
+template <int D>
+__device__ __forceinline__ void turn_keys(u32x4 (&k)[D / 64], u32x4 *lds, int lane) {
+    constexpr int P = D / 16;   // pieces of a key
+#pragma unroll
+    for (int i = 0; i < D / 64; i++) lds[piece_at<D>(64 / P * i + lane / P, lane % P)] = k[i];
+#pragma unroll
+    for (int i = 0; i < D / 64; i++) k[i] = lds[piece_at<D>(lane % 16, 4 * i + lane / 16)];
+}
+
+// The lane's K operand of every group: the groups 2i and 2i + 1 lie in lanes g < 2
+// and g >= 2; the upper lanes' first halves change places with the lower lanes'
+// second halves. Codes come out as code + 128.
 template <int D>
 __device__ __forceinline__ void spread_keys(const u32x4 (&k)[D / 64], u32x2 (&out)[D / 32]) {
 #pragma unroll
     for (int i = 0; i < D / 64; i++)
 #pragma unroll
         for (int w = 0; w < 2; w++) {
-            const u32x2 r = __builtin_amdgcn_permlane32_swap(k[i][w], k[i][w + 2], false, false);
+            const u32x2 r = __builtin_amdgcn_permlane32_swap(k[i][w] ^ 0x80808080u, k[i][w + 2] ^ 0x80808080u, false, false);
             out[2 * i][w] = r[0];
             out[2 * i + 1][w] = r[1];
         }
@@ -349,7 +374,11 @@ __device__ __forceinline__ void add_scaled(float (&s)[4], f32x4 d, const float (
 template <typename T, int D, int NS, int RT>
 __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
     constexpr int C = D / 32, VB = D / 16, R = 16 * RT;
-    __shared__ f32x4 lds_o[kWaves][R][D / 4 + 1];   // padded: 16 lanes write one column of it
+    typedef f32x4 Joined[R][D / 4 + 1];   // a wave's sums, padded: 16 lanes write one column
+    __shared__ union {
+        Joined o[kWaves];
+        u32x4 k[kWaves][2][D];   // the K codes of a wave's two tiles
+    } lds;
     __shared__ float lds_m[kWaves][R], lds_l[kWaves][R];
     const int Hkv = static_cast<int>(a.c.n_kv_heads);
     const int kvh = blockIdx.x % Hkv, r0 = (blockIdx.x / Hkv) * R;
@@ -365,6 +394,22 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
     const int len = static_cast<int>(sq.len), ctx = static_cast<int>(sq.ctx);
     const int j0 = static_cast<int>(split * a.chunk);
     const int j1 = j0 + static_cast<int>(a.chunk) < len ? j0 + static_cast<int>(a.chunk) : len;
+
+    Step<D> st;
+    int j = j0 + kStep * wave;
+    const int last = (j1 - 1) / 16;
+    const int64_t of_page = a.c.page_size * Hkv * D, of_head = a.c.page_size * kvh * D;
+    Place next = {};
+    // Keys are loaded before values everywhere, and the scheduler is kept from mixing
+    // the two: loads complete in order, and a wait for the keys must not include the
+    // values behind them.
+    if (j < j1) {
+        next = place_of<D>(a, b, of_page, of_head, j / 16, last);
+        load_keys<D>(a, next, lane, st);
+        __builtin_amdgcn_sched_barrier(0);
+        load_values<D>(a, next, lane, st);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 
     // The query rows: row r0 + 16 rt + n of this lane, times a power of two that
     // brings its largest value into [2^13, 2^14).
@@ -419,24 +464,16 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
     _Float16 vmul = pow2_f16(15);
     _Float16 vlim = static_cast<_Float16>(0.0f);   // the largest scale that vk was made for
 
-    Step<D> st;
-    int j = j0 + kStep * wave;
-    const int last = (j1 - 1) / 16;
-    Place next = {};
-    if (j < j1) {
-        next = place_of<D>(a, b, kvh, j / 16, last);
-        load_keys<D>(a, next, lane, st);
-        load_values<D>(a, next, lane, st);
-    }
     for (; j < j1; j += kGroupKeys) {
         const bool more = j + kGroupKeys < j1;
         const bool ok[2] = {next.ok[0], next.ok[1]};
         const bool plain = j + kStep <= (ctx < j1 ? ctx : j1) && ok[0] && ok[1];   // every row sees every key
-        if (more) next = place_of<D>(a, b, kvh, (j + kGroupKeys) / 16, last);
+        if (more) next = place_of<D>(a, b, of_page, of_head, (j + kGroupKeys) / 16, last);
         float s[RT][2][4];
 #pragma unroll
         for (int u = 0; u < 2; u++) {
             u32x2 kw[C];
+            turn_keys<D>(st.k[u], lds.k[wave][u], lane);
             spread_keys<D>(st.k[u], kw);
             const f16x2 ks = as_h2(st.ks[u]);
             const float x[2] = {static_cast<float>(ks[0]), static_cast<float>(ks[1])};
@@ -462,8 +499,15 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
                 group(std::integral_constant<int, 6>{});
                 group(std::integral_constant<int, 7>{});
             }
+            // One tile's operands at a time in registers: its scores are made here, not
+            // where they are used next.
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+                asm volatile("" : "+v"(s[rt][u][0]), "+v"(s[rt][u][1]), "+v"(s[rt][u][2]), "+v"(s[rt][u][3]));
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (more) load_keys<D>(a, next, lane, st);
+        __builtin_amdgcn_sched_barrier(0);
         // Weights, each lane its 8 keys of row n.
         Frag p[RT][NS];
 #pragma unroll
@@ -471,9 +515,16 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
 #pragma unroll
             for (int x = 0; x < 8; x++) s[rt][x / 4][x % 4] *= scale2[rt];
             if (a.softcap > 0.0f) {
+                float far = 0.0f;
 #pragma unroll
-                for (int x = 0; x < 8; x++)
-                    s[rt][x / 4][x % 4] = tanh_f32(s[rt][x / 4][x % 4]) * (a.softcap * kLog2e);
+                for (int x = 0; x < 8; x++) far = fmaxf(far, fabsf(s[rt][x / 4][x % 4]));
+                if (__any(far >= kSeries)) {
+#pragma unroll
+                    for (int x = 0; x < 8; x++) s[rt][x / 4][x % 4] = tanh_any(s[rt][x / 4][x % 4]) * (a.softcap * kLog2e);
+                } else {   // scores well below the cap, the usual ones: no exponential for them
+#pragma unroll
+                    for (int x = 0; x < 8; x++) s[rt][x / 4][x % 4] = tanh_series(s[rt][x / 4][x % 4]) * (a.softcap * kLog2e);
+                }
             }
             if (!plain) {
 #pragma unroll
@@ -585,10 +636,13 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         if (more) load_values<D>(a, next, lane, st);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     // Join the four waves.
+    __syncthreads();   // the K codes are no longer needed by any
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
         const int r = 16 * rt + n;
@@ -602,7 +656,7 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
         for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int t = 0; t < VB; t += 4)
-                lds_o[wave][r][(v_dim<D>(4 * g + i) + t) / 4] =
+                lds.o[wave][r][(v_dim<D>(4 * g + i) + t) / 4] =
                     f32x4{o[rt][t][i], o[rt][t + 1][i], o[rt][t + 2][i], o[rt][t + 3][i]} * f;
     }
     __syncthreads();
@@ -618,7 +672,7 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
         for (int w = 0; w < kWaves; w++) {
             const float f = __builtin_amdgcn_exp2f(lds_m[w][r] - mx);
             sum += lds_l[w][r] * f;
-            x += lds_o[w][r][d4] * f;
+            x += lds.o[w][r][d4] * f;
         }
         const int t = (r0 + r) / G, h = kvh * G + (r0 + r) - t * G;
         const int64_t at = (sq.row0 + t) * a.n_heads + h;
@@ -631,53 +685,68 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
     }
 }
 
-// Joins the parts of one query row and head: four waves, each every fourth part,
-// D / 64 dims to a lane.
+// Joins the parts of one query row and head. A step takes 64 parts: lane i of every
+// wave holds part i's maximum and sum, wave w adds up the parts 16 w .. 16 w + 15, D/64
+// dims to a lane, all of them loaded before any is used.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
-    constexpr int E = D / 64;
-    __shared__ float lds_o[kWaves][D], lds_m[kWaves], lds_l[kWaves];
+    constexpr int E = D / 64, kPer = 64 / kWaves;
+    __shared__ float lds_o[kWaves][D];
     const Seq sq(a, blockIdx.z);
     const int parts = parts_of(a, sq.len);
     if (static_cast<int>(blockIdx.y) >= sq.rows || parts == 1) return;
     const int64_t at = (sq.row0 + blockIdx.y) * a.n_heads + blockIdx.x;
     const float *po = a.part_o + at * a.splits * D, *pml = a.part_ml + at * a.splits * 2;
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / 64), lane = threadIdx.x % 64;
     float m = kNone, l = 0.0f, o[E];
 #pragma unroll
     for (int i = 0; i < E; i++) o[i] = 0.0f;
-    for (int s = wave; s < parts; s += kWaves) {
-        const float pm = pml[2 * s], pl = pml[2 * s + 1];
-        const float mn = fmaxf(m, pm), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(pm - mn);
-        m = mn;
-        l = l * f0 + pl * f1;
+    for (int p0 = 0; p0 < parts; p0 += 64) {
+        const int mine = p0 + lane < parts ? p0 + lane : parts - 1;   // clamped: weighed 0 below
+        const f32x2 ml = *reinterpret_cast<const f32x2 *>(pml + 2 * mine);
+        float x[kPer][E];
 #pragma unroll
-        for (int i = 0; i < E; i++) o[i] = o[i] * f0 + po[s * D + lane * E + i] * f1;
+        for (int k = 0; k < kPer; k++) {
+            const int part = p0 + kPer * wave + k < parts ? p0 + kPer * wave + k : parts - 1;
+#pragma unroll
+            for (int i = 0; i < E; i++) x[k][i] = po[static_cast<int64_t>(part) * D + lane * E + i];
+        }
+        const float pm = p0 + lane < parts ? ml[0] : kNone;
+        float mn = fmaxf(m, pm);
+#pragma unroll
+        for (int s = 32; s >= 1; s >>= 1) mn = fmaxf(mn, __shfl_xor(mn, s));
+        const float before = __builtin_amdgcn_exp2f(m - mn);
+        const float w = p0 + lane < parts ? __builtin_amdgcn_exp2f(pm - mn) : 0.0f;
+        l = l * before + w * ml[1];   // per lane
+        m = mn;
+#pragma unroll
+        for (int i = 0; i < E; i++) o[i] *= before;
+#pragma unroll
+        for (int k = 0; k < kPer; k++) {
+            const float f = __builtin_bit_cast(
+                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), kPer * wave + k));
+#pragma unroll
+            for (int i = 0; i < E; i++) o[i] = __builtin_fmaf(x[k][i], f, o[i]);
+        }
     }
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) l += __shfl_xor(l, s);   // every wave has all parts' sums
 #pragma unroll
     for (int i = 0; i < E; i++) lds_o[wave][lane * E + i] = o[i];
-    if (lane == 0) {
-        lds_m[wave] = m;
-        lds_l[wave] = l;
-    }
     __syncthreads();
-    float mx = kNone, f[kWaves], sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; w++) mx = fmaxf(mx, lds_m[w]);
-#pragma unroll
-    for (int w = 0; w < kWaves; w++) {
-        f[w] = __builtin_amdgcn_exp2f(lds_m[w] - mx);
-        sum += lds_l[w] * f[w];
-    }
     for (int d = threadIdx.x; d < D; d += kThreads) {
-        float x = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; w++) x += lds_o[w][d] * f[w];
-        static_cast<T *>(a.out)[at * D + d] = static_cast<T>(sum > 0.0f ? x / sum : 0.0f);
+        const float x = (lds_o[0][d] + lds_o[1][d]) + (lds_o[2][d] + lds_o[3][d]);
+        static_cast<T *>(a.out)[at * D + d] = static_cast<T>(l > 0.0f ? x / l : 0.0f);
     }
 }
 
-constexpr int kTargetGroups = 1024;   // workgroups that keep the card's 256 CUs busy to the end
+// Parts per sequence. At least enough workgroups for every CU to have its two or
+// three (kFill), however short the parts; beyond that, parts of no fewer than
+// kMinSteps steps a wave, up to kFine workgroups in all: many short ones even out the
+// end of the launch and sequences of different lengths (32 of 16k to 32k keys: 389 us
+// with 1024 workgroups, 319 with 2048, 303 with 4096, 324 with 8192), but each reads
+// its queries and joins its waves anew.
+constexpr int kFill = 768, kFine = 4096, kMinSteps = 4;
 
 // How the work is cut: rows per workgroup, and keys per part.
 struct Plan {
@@ -691,8 +760,10 @@ Plan plan_of(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_d
     p.row_tiles = rows > 16 && head_dim <= 128 ? 2 : 1;
     p.row_blocks = (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
     const int64_t groups = n_seqs * n_kv_heads * p.row_blocks;   // at one part each
-    int64_t parts = (kTargetGroups + groups - 1) / groups;
     const int64_t steps = (max_kv_len + kGroupKeys - 1) / kGroupKeys;
+    const int64_t fill = (kFill + groups - 1) / groups, fine = (kFine + groups - 1) / groups;
+    int64_t parts = fine < steps / kMinSteps ? fine : steps / kMinSteps;
+    parts = parts > fill ? parts : fill;
     parts = parts < steps ? parts : steps;
     p.chunk = (steps + parts - 1) / parts * kGroupKeys;
     p.splits = (max_kv_len + p.chunk - 1) / p.chunk;
