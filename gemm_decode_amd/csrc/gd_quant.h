@@ -79,6 +79,12 @@ __device__ __forceinline__ float max8(float v) {   // max over the 8 lanes of a 
     return v;
 }
 
+// The same over four lanes.
+__device__ __forceinline__ float max4(float v) {
+    v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, false)));
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, false)));
+}
+
 // ------------------------------------------------------ bit planes
 __device__ __forceinline__ uint32_t bits_to_nibbles(uint32_t x) {   // bit 8j + b -> bit 4b + j
     uint32_t t;

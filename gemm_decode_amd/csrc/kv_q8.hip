@@ -8,6 +8,7 @@
 // in the order of the dims: a token's write and a position's read are runs of
 // head_dim bytes, and a tile of 16 positions of one head is contiguous.
 #include <cmath>
+#include <type_traits>
 
 #include "gd_internal.h"
 #include "gd_quant.h"
@@ -20,6 +21,7 @@ using namespace gd;
 constexpr int kThreads = 256;
 constexpr int64_t kMaxThreads = (INT64_C(1) << 32) - 1;   // of one launch
 constexpr int kMaxRot = 256;
+constexpr int64_t kManyTokens = 1024;   // from here on a workgroup per token (or four) fills the card
 
 // ------------------------------------------------------- rotary table
 struct RopeFreqs {
@@ -46,120 +48,225 @@ struct StoreArgs {
     const int32_t *positions;
     const int64_t *slots;
     int64_t q_stride, k_stride, v_stride, n_pos, n_tok;
-    int32_t n_heads, rot, interleaved;
+    int32_t n_heads, rot, interleaved, page_shift;
     gd_kv_q8 c;
 };
 
-// Four dims d0 .. d0 + 3 of a head row, turned by the row's angles: the f64
-// sum of products that are exact in f64, rounded to f32.
-template <typename T>
-__device__ __forceinline__ f32x4 rotated(const T *row, int d0, const f32x2 *cs, int rot, bool interleaved) {
-    const f32x4 x = load4(row + d0);
-    if (d0 >= rot) return x;
-    f32x4 y;
-    if (interleaved) {   // pairs (2i, 2i + 1), both here
-        const f32x4 t = *reinterpret_cast<const f32x4 *>(cs + d0 / 2);
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const double a = x[2 * i], b = x[2 * i + 1], c = t[2 * i], s = t[2 * i + 1];
-            y[2 * i] = static_cast<float>(a * c - b * s);
-            y[2 * i + 1] = static_cast<float>(b * c + a * s);
-        }
-    } else {   // pairs (i, i + rot / 2): the partners are another lane's
-        const int half = rot / 2;
-        const bool first = d0 < half;
-        const int i0 = first ? d0 : d0 - half;
-        const f32x4 o = load4(row + (first ? d0 + half : d0 - half));
-        const f32x4 t0 = *reinterpret_cast<const f32x4 *>(cs + i0);
-        const f32x4 t1 = *reinterpret_cast<const f32x4 *>(cs + i0 + 2);
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const double a = x[j], b = o[j];
-            const double c = j < 2 ? t0[2 * j] : t1[2 * j - 4], s = j < 2 ? t0[2 * j + 1] : t1[2 * j - 3];
-            y[j] = static_cast<float>(a * c + (first ? -(b * s) : b * s));
-        }
+// Where a slot lies. A division of 64-bit numbers is some hundred scalar
+// instructions, as many as the rest of a workgroup's start: pages of a power of two
+// (shift >= 0), the usual ones, do without.
+struct Slot {
+    int64_t page, off;
+    __device__ __forceinline__ Slot(int64_t slot, int64_t page_size, int shift) {
+        page = shift >= 0 ? slot >> shift : slot / page_size;
+        off = slot - page * page_size;
     }
-    return y;
+};
+
+int page_shift_of(int64_t page_size) {
+    return (page_size & (page_size - 1)) == 0 ? __builtin_ctzll(static_cast<uint64_t>(page_size)) : -1;
 }
 
-// Four dims per thread, head_dim / 4 threads per head row (a row never leaves
-// its wave, so q_out may be q itself: a wave reads its rows before it writes
-// them). Rows of a token in the order q heads, k heads, v heads.
-template <typename T>
+// E consecutive elements as f32, in one load of 4 E or 2 E bytes.
+template <int E, typename T>
+__device__ __forceinline__ void load_n(const T *p, f32x4 (&x)[E / 4]) {
+    typedef T Vec __attribute__((ext_vector_type(E)));
+    const Vec v = *reinterpret_cast<const Vec *>(p);
+#pragma unroll
+    for (int i = 0; i < E; i++) x[i / 4][i % 4] = static_cast<float>(v[i]);
+}
+
+// Written past the caches: what is written here is read by a later launch (a long
+// read back 145 -> 138 us).
+template <int E, typename T>
+__device__ __forceinline__ void store_n(T *p, const f32x4 (&x)[E / 4]) {
+    typedef T Vec __attribute__((ext_vector_type(E)));
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < E; i++) v[i] = static_cast<T>(x[i / 4][i % 4]);
+    __builtin_nontemporal_store(v, reinterpret_cast<Vec *>(p));
+}
+
+// a c - b s. Queries: the second product rounded, the first one fused with the sum.
+// Keys (kExact): rounded to f32 from about twice its bits, since a code next to a half
+// must not change sides: the two products' errors (exact, by fma) and their sum's
+// (exact, by the usual six operations) are added up before the last rounding. In f64,
+// where both products are exact, the same took a third of a long store's time.
+template <bool kExact>
+__device__ __forceinline__ float turn1(float a, float b, float c, float s) {
+    const float q = b * s;
+    if constexpr (!kExact) return __builtin_fmaf(a, c, -q);
+    const float p = a * c;
+    const float low = __builtin_fmaf(a, c, -p) - __builtin_fmaf(b, s, -q);
+    const float h = p - q, t = h - p;
+    const float err = (p - (h - t)) - (q + t);
+    return h + (err + low);
+}
+
+// E dims of a head row turned by the token's angles: x are these dims, o their
+// partners (half layout), c and s the angles of x's pairs (E of them, or E/2).
+template <bool kExact, int E>
+__device__ __forceinline__ void turn(f32x4 (&x)[E / 4], const f32x4 (&o)[E / 4], const float (&c)[E], const float (&s)[E],
+                                     bool first, bool interleaved) {
+    if (interleaved) {   // pairs (2i, 2i + 1), both in x
+#pragma unroll
+        for (int i = 0; i < E / 2; i++) {
+            const float a = x[i / 2][2 * (i % 2)], b = x[i / 2][2 * (i % 2) + 1];
+            x[i / 2][2 * (i % 2)] = turn1<kExact>(a, b, c[i], s[i]);
+            x[i / 2][2 * (i % 2) + 1] = turn1<kExact>(b, a, c[i], -s[i]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; j++)
+            x[j / 4][j % 4] = turn1<kExact>(x[j / 4][j % 4], o[j / 4][j % 4], c[j], first ? s[j] : -s[j]);
+    }
+}
+
+// A workgroup serves one token (or its rows blockIdx.y, blockIdx.y + gridDim.y, ...
+// of kRows at a time): D/E threads per head row, E dims each, so that a thread has the
+// same dims in every row it takes and its angles are loaded once. Rows in the order q
+// heads, k heads, v heads, kBatch of them loaded before any is used. A row never
+// leaves its wave, so q_out may be q itself: a wave reads a row before it writes it.
+template <typename T, int D, int E>
 __global__ __launch_bounds__(kThreads) void kv_q8_store_kernel(StoreArgs a) {
-    const int64_t gid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int D = static_cast<int>(a.c.head_dim), lanes = D / 4;
-    const int Hkv = static_cast<int>(a.c.n_kv_heads);
-    const int rows = a.n_heads + 2 * Hkv;
-    const int64_t r = gid / lanes;
-    const int64_t tok = r / rows;
-    if (tok >= a.n_tok) return;
-    int h = static_cast<int>(r % rows);
-    const int d0 = static_cast<int>(gid % lanes) * 4;
+    constexpr int kLanes = D / E, kRows = kThreads / kLanes, kBatch = 2;
+    const int64_t tok = blockIdx.x;
+    const int Hkv = static_cast<int>(a.c.n_kv_heads), Hq = a.n_heads;
+    const int d0 = static_cast<int>(threadIdx.x % kLanes) * E;
     const int64_t slot = a.slots[tok];
     const bool live = slot >= 0 && slot < a.c.n_pages * a.c.page_size;
-    const f32x2 *cs = nullptr;
+    const bool turned = a.rope && d0 < a.rot;
+    const int half = a.rot / 2;
+    const bool first = d0 < half;
+    float c[E] = {}, s[E] = {};
     if (a.rope) {
         const int64_t pos = a.positions[tok];
         if (pos < 0 || pos >= a.n_pos) return;   // no angles for it: the token is left out
-        cs = a.rope + pos * (a.rot / 2);
+        if (turned) {
+            const f32x4 *t = reinterpret_cast<const f32x4 *>(
+                a.rope + pos * half + (a.interleaved ? d0 / 2 : first ? d0 : d0 - half));
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                if (i >= E / 2 && a.interleaved) break;
+                const f32x4 v = t[i / 2];
+                c[i] = v[0], s[i] = v[1], c[i + 1] = v[2], s[i + 1] = v[3];
+            }
+        }
     }
-    const int rot = a.rope ? a.rot : 0;
-    if (h < a.n_heads) {
-        const f32x4 y = rotated(static_cast<const T *>(a.q) + tok * a.q_stride + h * D, d0, cs, rot, a.interleaved);
-        store4(static_cast<T *>(a.q_out) + (tok * a.n_heads + h) * D + d0, y);
-        return;
+    const int partner = turned && !a.interleaved ? (first ? half : -half) : 0;   // where a dim's partner lies
+    const T *q = static_cast<const T *>(a.q) + tok * a.q_stride + d0;
+    const T *k = static_cast<const T *>(a.k) + tok * a.k_stride + d0;
+    const T *v = static_cast<const T *>(a.v) + tok * a.v_stride + d0;
+    T *qo = static_cast<T *>(a.q_out) + tok * Hq * D + d0;
+    const Slot at(live ? slot : 0, a.c.page_size, a.page_shift);
+    const int rows = Hq + (live ? 2 * Hkv : 0);
+    const int step = kRows * static_cast<int>(gridDim.y);
+    for (int r0 = kRows * static_cast<int>(blockIdx.y) + static_cast<int>(threadIdx.x) / kLanes; r0 < rows;
+         r0 += kBatch * step) {
+        f32x4 x[kBatch][E / 4], o[kBatch][E / 4];
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+            const int r = r0 + i * step;
+            if (r >= rows) break;
+            const T *p = r < Hq ? q + r * D : r < Hq + Hkv ? k + (r - Hq) * D : v + (r - Hq - Hkv) * D;
+            load_n<E>(p, x[i]);
+            if (partner != 0 && r < Hq + Hkv) load_n<E>(p + partner, o[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+            const int r = r0 + i * step;
+            if (r >= rows) break;
+            if (r < Hq) {
+                if (turned) turn<false, E>(x[i], o[i], c, s, first, a.interleaved);
+                store_n<E>(qo + r * D, x[i]);
+                continue;
+            }
+            const bool is_v = r >= Hq + Hkv;
+            const int h = is_v ? r - Hq - Hkv : r - Hq;
+            if (turned && !is_v) turn<true, E>(x[i], o[i], c, s, first, a.interleaved);
+            float m = 0.0f;   // the largest of the 32 dims that the lane's are among: 32 / E lanes
+#pragma unroll
+            for (int w = 0; w < E / 4; w++) m = fmaxf(m, absmax4(float4{x[i][w][0], x[i][w][1], x[i][w][2], x[i][w][3]}));
+            m = E == 4 ? max8(m) : max4(m);
+            uint32_t packed[E / 4] = {};
+            _Float16 d = 0;
+            if (m > 0.0f) {
+                const float inv32 = recip127(m);
+                const bool f64_only = !(inv32 <= 3.40282347e38f);   // the reciprocal overflowed
+#pragma unroll
+                for (int w = 0; w < E / 4; w++)
+                    packed[w] = codes4(float4{x[i][w][0], x[i][w][1], x[i][w][2], x[i][w][3]}, inv32, m, f64_only);
+                d = static_cast<_Float16>(scale_of(m));
+            }
+            const int64_t row = (at.page * Hkv + h) * a.c.page_size + at.off;
+            uint32_t *codes = reinterpret_cast<uint32_t *>((is_v ? a.c.v_codes : a.c.k_codes) + row * D + d0);
+            if constexpr (E == 4)
+                codes[0] = packed[0];
+            else
+                *reinterpret_cast<uint2 *>(codes) = uint2{packed[0], packed[E / 4 - 1]};
+            if (d0 % 32 == 0)
+                (is_v ? a.c.v_scales : a.c.k_scales)[row * (D / 32) + d0 / 32] = __builtin_bit_cast(uint16_t, d);
+        }
     }
-    if (!live) return;
-    h -= a.n_heads;
-    const bool is_v = h >= Hkv;
-    if (is_v) h -= Hkv;
-    const f32x4 y = is_v ? load4(static_cast<const T *>(a.v) + tok * a.v_stride + h * D + d0)
-                         : rotated(static_cast<const T *>(a.k) + tok * a.k_stride + h * D, d0, cs, rot, a.interleaved);
-    const float4 y4 = {y[0], y[1], y[2], y[3]};
-    const float m = max8(absmax4(y4));
-    uint32_t packed = 0;
-    _Float16 d = 0;
-    if (m > 0.0f) {
-        const float inv32 = recip127(m);
-        packed = codes4(y4, inv32, m, !(inv32 <= 3.40282347e38f));   // f64 only if the reciprocal overflowed
-        d = static_cast<_Float16>(scale_of(m));
-    }
-    const int64_t page = slot / a.c.page_size, off = slot % a.c.page_size;
-    const int64_t row = (page * Hkv + h) * a.c.page_size + off;
-    *reinterpret_cast<uint32_t *>((is_v ? a.c.v_codes : a.c.k_codes) + row * D + d0) = packed;
-    if (d0 % 32 == 0)
-        (is_v ? a.c.v_scales : a.c.k_scales)[row * (D / 32) + d0 / 32] = __builtin_bit_cast(uint16_t, d);
 }
 
 // ---------------------------------------------------------------- load
-template <typename T>
+// A workgroup serves kTok tokens, D/E threads per head row, E = 16 / sizeof(T) dims
+// each (16-byte stores, and the outputs are most of the traffic): the keys' rows
+// first, then the values'; the loads of its tokens are all issued before any is used.
+template <typename T, int D, int kTok>
 __global__ __launch_bounds__(kThreads) void kv_q8_load_kernel(gd_kv_q8 c, const int64_t *__restrict__ slots,
                                                               T *__restrict__ k_out, T *__restrict__ v_out,
-                                                              int64_t n_tok) {
-    const int64_t gid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int D = static_cast<int>(c.head_dim), lanes = D / 4;
+                                                              int64_t n_tok, int page_shift) {
+    constexpr int E = 16 / sizeof(T), kLanes = D / E, kRows = kThreads / kLanes;
+    typedef int8_t Codes __attribute__((ext_vector_type(E)));
+    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * kTok;
     const int Hkv = static_cast<int>(c.n_kv_heads);
-    const int64_t r = gid / lanes;
-    const int64_t tok = r / (2 * Hkv);
-    if (tok >= n_tok) return;
-    int h = static_cast<int>(r % (2 * Hkv));
-    const bool is_v = h >= Hkv;
-    if (is_v) h -= Hkv;
-    const int d0 = static_cast<int>(gid % lanes) * 4;
-    T *out = is_v ? v_out : k_out;
-    if (!out) return;
-    const int64_t slot = slots[tok];
-    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (slot >= 0 && slot < c.n_pages * c.page_size) {
-        const int64_t row = ((slot / c.page_size) * Hkv + h) * c.page_size + slot % c.page_size;
-        const uint32_t w = *reinterpret_cast<const uint32_t *>((is_v ? c.v_codes : c.k_codes) + row * D + d0);
-        const float d = static_cast<float>(
-            __builtin_bit_cast(_Float16, (is_v ? c.v_scales : c.k_scales)[row * (D / 32) + d0 / 32]));
+    const int d0 = static_cast<int>(threadIdx.x % kLanes) * E;
+    int64_t at[kTok];   // row of KV head 0; -1: none
 #pragma unroll
-        for (int j = 0; j < 4; j++) y[j] = static_cast<float>(static_cast<int8_t>(w >> (8 * j))) * d;
+    for (int i = 0; i < kTok; i++) {
+        const int64_t slot = tok0 + i < n_tok ? slots[tok0 + i] : -1;
+        const bool live = slot >= 0 && slot < c.n_pages * c.page_size;
+        const Slot s(live ? slot : 0, c.page_size, page_shift);
+        at[i] = live ? s.page * Hkv * c.page_size + s.off : -1;
     }
-    store4(out + (tok * Hkv + h) * D + d0, y);
+    for (int r = threadIdx.x / kLanes; r < 2 * Hkv; r += kRows) {
+        const bool is_v = r >= Hkv;
+        const int h = is_v ? r - Hkv : r;
+        T *out = is_v ? v_out : k_out;
+        if (!out) continue;
+        const int8_t *codes = is_v ? c.v_codes : c.k_codes;
+        const uint16_t *scales = is_v ? c.v_scales : c.k_scales;
+        Codes w[kTok];
+        uint16_t d[kTok];
+#pragma unroll
+        for (int i = 0; i < kTok; i++) {
+            const int64_t row = (at[i] < 0 ? 0 : at[i]) + h * c.page_size;   // row 0 of none: loaded, not used
+            w[i] = *reinterpret_cast<const Codes *>(codes + row * D + d0);
+            d[i] = scales[row * (D / 32) + d0 / 32];
+        }
+#pragma unroll
+        for (int i = 0; i < kTok; i++) {
+            if (tok0 + i >= n_tok) break;
+            const float f = static_cast<float>(__builtin_bit_cast(_Float16, d[i]));
+            f32x4 y[E / 4];
+#pragma unroll
+            for (int j = 0; j < E; j++) y[j / 4][j % 4] = at[i] < 0 ? 0.0f : static_cast<float>(w[i][j]) * f;
+            store_n<E>(out + ((tok0 + i) * Hkv + h) * D + d0, y);
+        }
+    }
+}
+
+// Calls fn with the head dim as a constant.
+template <typename F>
+void dispatch_dim(int64_t head_dim, F fn) {
+    if (head_dim == 64)
+        fn(std::integral_constant<int, 64>{});
+    else if (head_dim == 128)
+        fn(std::integral_constant<int, 128>{});
+    else
+        fn(std::integral_constant<int, 256>{});
 }
 
 // The row stride of an input of `heads` head rows per token.
@@ -283,10 +390,8 @@ extern "C" int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_strid
     GD_REQUIRE((n_heads == 0 || stride_ok(q_stride, n_heads, D, dtype)) && stride_ok(k_stride, Hkv, D, dtype) &&
                    stride_ok(v_stride, Hkv, D, dtype),
                GD_ESHAPE, "kv_q8_store: a row stride must cover the token's heads and be a multiple of 16 bytes");
-    int64_t threads;
-    GD_REQUIRE(n_heads <= 65536 && mul_ok(n_tok, (n_heads + 2 * Hkv) * (D / 4), &threads) &&
-                   threads <= kMaxThreads - kThreads,
-               GD_ERANGE, "kv_q8_store: n_tok * heads too large");
+    GD_REQUIRE(n_heads <= 65536 && n_tok <= kMaxThreads / kThreads, GD_ERANGE,
+               "kv_q8_store: n_tok (%lld) or n_heads (%lld) too large", (long long)n_tok, (long long)n_heads);
     GD_REQUIRE(aligned(k, 16) && aligned(v, 16) && (n_heads == 0 || (aligned(q, 16) && aligned(q_out, 16))) &&
                    aligned(slots, 8),
                GD_EALIGN, "kv_q8_store: q, k, v and q_out must be 16-byte aligned, slots 8-byte");
@@ -296,10 +401,26 @@ extern "C" int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_strid
     a.positions = positions, a.slots = slots;
     a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.n_pos = n_pos, a.n_tok = n_tok;
     a.n_heads = static_cast<int32_t>(n_heads), a.rot = static_cast<int32_t>(rot_dim), a.interleaved = interleaved != 0;
+    a.page_shift = page_shift_of(cache->page_size);
     a.c = *cache;
-    const dim3 grid(static_cast<uint32_t>((threads + kThreads - 1) / kThreads));
+    // 16-byte loads, unless a pair's halves would not start on one (16-bit types, rot_dim not a multiple of 16).
+    const bool wide = dtype != GD_F32 && (!rope || rot_dim % 16 == 0);
+    const int64_t at_once = kThreads / (D / (wide ? 8 : 4));
+    // few tokens: their rows over as many workgroups as they fill
+    const int64_t chunks = n_tok >= kManyTokens ? 1 : (n_heads + 2 * Hkv + at_once - 1) / at_once;
+    const dim3 grid(static_cast<uint32_t>(n_tok), static_cast<uint32_t>(chunks));
     dispatch_dtype(dtype, [&](auto t) {
-        hipLaunchKernelGGL((kv_q8_store_kernel<decltype(t)>), grid, dim3(kThreads), 0, as_stream(stream), a);
+        using T = decltype(t);
+        dispatch_dim(D, [&](auto dim) {
+            constexpr int kD = decltype(dim)::value;
+            if constexpr (sizeof(T) == 2) {
+                if (wide) {
+                    hipLaunchKernelGGL((kv_q8_store_kernel<T, kD, 8>), grid, dim3(kThreads), 0, as_stream(stream), a);
+                    return;
+                }
+            }
+            hipLaunchKernelGGL((kv_q8_store_kernel<T, kD, 4>), grid, dim3(kThreads), 0, as_stream(stream), a);
+        });
     });
     return check_launch("kv_q8_store");
 }
@@ -311,17 +432,24 @@ extern "C" int kv_q8_load(const gd_kv_q8 *cache, const int64_t *slots, void *k_o
     GD_REQUIRE(slots && (k_out || v_out), GD_EINVAL, "kv_q8_load: null pointer");
     GD_REQUIRE(n_tok >= 1, GD_EINVAL, "kv_q8_load: n_tok (%lld) must be >= 1", (long long)n_tok);
     GD_REQUIRE(dtype_ok(dtype), GD_EINVAL, "kv_q8_load: unknown dtype %d", dtype);
-    int64_t threads;
-    GD_REQUIRE(mul_ok(n_tok, 2 * cache->n_kv_heads * (cache->head_dim / 4), &threads) &&
-                   threads <= kMaxThreads - kThreads,
-               GD_ERANGE, "kv_q8_load: n_tok (%lld) too large", (long long)n_tok);
+    GD_REQUIRE(n_tok <= kMaxThreads / kThreads, GD_ERANGE, "kv_q8_load: n_tok (%lld) too large", (long long)n_tok);
     GD_REQUIRE(aligned(slots, 8) && aligned(k_out, 16) && aligned(v_out, 16), GD_EALIGN,
                "kv_q8_load: outputs must be 16-byte aligned, slots 8-byte");
-    const dim3 grid(static_cast<uint32_t>((threads + kThreads - 1) / kThreads));
+    const bool many = n_tok >= kManyTokens;
+    const int shift = page_shift_of(cache->page_size);
+    const dim3 grid(static_cast<uint32_t>(many ? (n_tok + 3) / 4 : n_tok));
     dispatch_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        hipLaunchKernelGGL((kv_q8_load_kernel<T>), grid, dim3(kThreads), 0, as_stream(stream), *cache, slots,
-                           static_cast<T *>(k_out), static_cast<T *>(v_out), n_tok);
+        T *ko = static_cast<T *>(k_out), *vo = static_cast<T *>(v_out);
+        dispatch_dim(cache->head_dim, [&](auto dim) {
+            constexpr int kD = decltype(dim)::value;
+            if (many)
+                hipLaunchKernelGGL((kv_q8_load_kernel<T, kD, 4>), grid, dim3(kThreads), 0, as_stream(stream), *cache,
+                                   slots, ko, vo, n_tok, shift);
+            else
+                hipLaunchKernelGGL((kv_q8_load_kernel<T, kD, 1>), grid, dim3(kThreads), 0, as_stream(stream), *cache,
+                                   slots, ko, vo, n_tok, shift);
+        });
     });
     return check_launch("kv_q8_load");
 }

@@ -524,8 +524,10 @@ int rope_table(float *table, int64_t n_pos, int64_t rot_dim, double base,
 /* Rotates q and k by their tokens' positions and writes k and v to the cache.
  * Pair (x1, x2) becomes (x1 cos - x2 sin, x2 cos + x1 sin); the pairs are
  * dims (i, i + rot_dim/2), or (2i, 2i+1) if `interleaved`; dims from rot_dim
- * on stay. The sum of the two products is taken in f64 (they are exact there)
- * and rounded to f32; q_out rounds that to dtype, the cache quantizes it.
+ * on stay. For k the sum of the two products is taken to 2^-46 of the larger
+ * one and rounded to f32, which the cache quantizes; for q the second product
+ * is rounded to f32 and the first fused with the sum, and q_out rounds that to
+ * dtype.
  *   q, k, v    device dtype, token t's heads at q + t * q_stride (n_heads head
  *              rows of head_dim), k + t * k_stride, v + t * v_stride
  *              (n_kv_heads): parts of one projection's row, for instance.
@@ -543,9 +545,8 @@ int rope_table(float *table, int64_t n_pos, int64_t rot_dim, double base,
  *              whose slot is outside the pool (-1: padding) is not stored;
  *              its q is still rotated. Slots of one call must differ: of two
  *              tokens with one slot, the row is left as a mixture.
- * rot_dim a multiple of 8, at most head_dim; n_heads <= 65536; n_tok *
- * (n_heads + 2 n_kv_heads) * head_dim / 4 < 2^32 - 256. q, k, v, q_out and
- * rope 16-byte aligned. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE,
+ * rot_dim a multiple of 8, at most head_dim; n_heads <= 65536; n_tok < 2^24.
+ * q, k, v, q_out and rope 16-byte aligned. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE,
  * GD_EHIP. */
 int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                 const void *v, int64_t v_stride, void *q_out, const float *rope, int64_t n_pos,
@@ -558,7 +559,7 @@ int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_stride, const vo
  *   slots         device int64 [n_tok] (any order, repeats allowed).
  *   k_out, v_out  device dtype [n_tok][n_kv_heads][head_dim], 16-byte aligned;
  *                 one of them may be NULL.
- * n_tok * n_kv_heads * head_dim / 2 < 2^32 - 256. Errors as kv_q8_store. */
+ * n_tok < 2^24. Errors as kv_q8_store. */
 int kv_q8_load(const gd_kv_q8 *cache, const int64_t *slots, void *k_out, void *v_out, int64_t n_tok,
                int32_t dtype, void *stream);
 

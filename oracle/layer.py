@@ -72,8 +72,10 @@ def rope_table(n_pos: int, rot: int, base: float, scaling=None):
     return np.stack([np.cos(a) * factor, np.sin(a) * factor], -1)
 
 
-def rotate(x, table, positions, interleaved: bool):
-    """f32 [n, heads, D] turned by the f32 table's angles: f64 sums rounded to f32."""
+def rotate(x, table, positions, interleaved: bool, fused: bool = False):
+    """f32 [n, heads, D] turned by the f32 table's angles: f64 sums rounded to f32;
+    with `fused`, the second product is rounded to f32 before the sum."""
+    second = (lambda v: v.astype(np.float32).astype(np.float64)) if fused else (lambda v: v)
     y = np.asarray(x, np.float32).astype(np.float64)
     cs = np.asarray(table, np.float32).astype(np.float64)[np.asarray(positions)]
     half = cs.shape[1]
@@ -82,8 +84,8 @@ def rotate(x, table, positions, interleaved: bool):
     c, s = cs[:, None, :, 0], cs[:, None, :, 1]
     x1, x2 = y[..., a], y[..., b]
     out = y.copy()
-    out[..., a] = x1 * c - x2 * s
-    out[..., b] = x2 * c + x1 * s
+    out[..., a] = x1 * c - second(x2 * s)
+    out[..., b] = x2 * c + second(x1 * s)
     return out.astype(np.float32)
 
 
