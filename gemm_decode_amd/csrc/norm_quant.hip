@@ -4,12 +4,14 @@
 // int8 bit planes for ternary_gemv), and the readers of those formats.
 //
 // With h = x + residual (rounded to the stream's type), p = h * w and
-// rstd = 1 / sqrt(mean h^2 + eps), the norm is y = rstd * p. The quantization
-// rule rounds y times 127 over max|y|: rstd divides out, so the codes depend on p
-// alone and only the scale, max|p| * rstd / 127, needs the row's sum. p is a
-// product of two f32 values, exact in f64, and the sum of squares is taken in
-// f64, so codes and scales do not depend on the order of the sum (up to f64's
-// own rounding, 2^-29 of an f32 step).
+// rstd = 1 / sqrt(mean h^2 + eps), the norm is y = rstd * p. The quantization rule
+// rounds y times 127 over max|y|: rstd divides out, so the codes depend on p alone
+// and only the scale, max|p| * rstd / 127, needs the row's sum. p is a product of two
+// f32 values, exact in f64, and the sum of squares is taken in f64, so codes and
+// scales do not depend on the order of the sum (up to f64's own rounding, 2^-29 of an
+// f32 step).
+#include <type_traits>
+
 #include "gd_internal.h"
 #include "gd_quant.h"
 #include "gd_types.h"
@@ -19,7 +21,6 @@ namespace {
 using namespace gd;
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int64_t kMaxThreads = (INT64_C(1) << 32) - 1;   // of one launch
 
 // h = x + residual of four elements, as stored; both terms are read before h
@@ -38,115 +39,177 @@ __device__ __forceinline__ double square4(f32x4 h) {
     return s;
 }
 
+// Codes and scales are decided in f32 where that gives what the f64 rule gives, and
+// as the rule is written in the rest. With P = f32(h w), A = max|P| (which is
+// f32(max|h w|)) and I = f32(127 / A), the value t = P I is off the rule's by four
+// roundings, 127 * 4 * 2^-24 = 3.1e-5 at most, so that the code is the rule's unless t
+// lies within kTieGuard = 6.4e-5 of a half; the f32 scale A r is off by three, so that
+// its f16 rounding is the rule's unless its 13 dropped bits lie within 4 steps of a
+// half. Where any lane of a wave is in doubt (in about one wave of thirty, of f32
+// values) the wave decides again in f64.
 struct Products {
-    double p[4];
-    __device__ __forceinline__ Products(f32x4 h, f32x4 w) {
+    f32x4 h, w;
+    float p[4];
+    __device__ __forceinline__ Products(f32x4 h_, f32x4 w_) : h(h_), w(w_) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) p[j] = static_cast<double>(h[j]) * static_cast<double>(w[j]);
+        for (int j = 0; j < 4; j++) p[j] = h[j] * w[j];
     }
-    __device__ __forceinline__ double absmax() const {
-        return fmax(fmax(fabs(p[0]), fabs(p[1])), fmax(fabs(p[2]), fabs(p[3])));
+    __device__ __forceinline__ float absmax() const { return absmax4(float4{p[0], p[1], p[2], p[3]}); }
+    __device__ __forceinline__ double exact(int j) const { return static_cast<double>(h[j]) * static_cast<double>(w[j]); }
+    __device__ __forceinline__ double exact_absmax() const {
+        return fmax(fmax(fabs(exact(0)), fabs(exact(1))), fmax(fabs(exact(2)), fabs(exact(3))));
     }
-    // Byte j: the code of element j under the rule, inv = factor_of(absmax).
-    __device__ __forceinline__ uint32_t codes(double inv) const {
+    // Byte j: the code of element j, inv = 127 / absmax; doubt: whether one is.
+    __device__ __forceinline__ uint32_t codes(float inv, bool &doubt) const {
         uint32_t packed = 0;
 #pragma unroll
-        for (int j = 0; j < 4; j++) packed |= (static_cast<uint32_t>(round_code(p[j] * inv)) & 0xffu) << (8 * j);
+        for (int j = 0; j < 4; j++) {
+            const float t = p[j] * inv;
+            packed |= (static_cast<uint32_t>(static_cast<int32_t>(floorf(t + 0.5f))) & 0xffu) << (8 * j);
+            doubt |= !(fabsf(__builtin_amdgcn_fractf(t) - 0.5f) >= kTieGuard);
+        }
+        return packed;
+    }
+    __device__ __forceinline__ uint32_t exact_codes(double inv) const {
+        uint32_t packed = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++) packed |= (static_cast<uint32_t>(round_code(exact(j) * inv)) & 0xffu) << (8 * j);
         return packed;
     }
 };
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int o) { return __shfl_xor(v, o); }
+// An f32 A whose reciprocal and products stay in f32's normal range: others are
+// decided in f64.
+__device__ __forceinline__ bool in_range(float a) { return a >= 1e-30f && a <= 1e30f; }
+
+// f16 rounding of t, an f32 value up to 4 f32 steps off: whether it is in doubt.
+__device__ __forceinline__ bool f16_doubt(float t) {
+    const uint32_t dropped = __builtin_bit_cast(uint32_t, t) & 0x1fffu;
+    return !(t >= 6.2e-5f && t <= 65000.0f) || (dropped >= 0x1000u - 4 && dropped <= 0x1000u + 4);   // normal in f16
+}
 
 __device__ __forceinline__ double max8d(double v) {   // max over the eight lanes of a block
 #pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) v = fmax(v, shfl_xor_f64(v, o));
+    for (int o = 4; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o));
     return v;
 }
 
-// Sum and max over the workgroup (every thread gets both).
+// 1 / sqrt(x), x > 0 finite, to f64's last bits: the hardware's estimate (some 24
+// bits) and two Newton steps.
+__device__ __forceinline__ double rsqrt_f64(double x) {
+    double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+    for (int i = 0; i < 2; i++) y = y * __builtin_fma(-0.5 * x * y, y, 1.5);
+    return y;
+}
+
+// Sum (and max) over the workgroup; every thread gets them.
+template <int kWaves, bool kMax>
 __device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*red)[2]) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
-        sum += shfl_xor_f64(sum, o);
-        mx = fmax(mx, shfl_xor_f64(mx, o));
+        sum += __shfl_xor(sum, o);
+        if (kMax) mx = fmax(mx, __shfl_xor(mx, o));
     }
     if (threadIdx.x % 64 == 0) {
         red[threadIdx.x / 64][0] = sum;
-        red[threadIdx.x / 64][1] = mx;
+        if (kMax) red[threadIdx.x / 64][1] = mx;
     }
     __syncthreads();
-    sum = (red[0][0] + red[1][0]) + (red[2][0] + red[3][0]);
-    mx = fmax(fmax(red[0][1], red[1][1]), fmax(red[2][1], red[3][1]));
+    sum = red[0][0];
+    if (kMax) mx = red[0][1];
+#pragma unroll
+    for (int w = 1; w < kWaves; w++) {
+        sum += red[w][0];
+        if (kMax) mx = fmax(mx, red[w][1]);
+    }
 }
 
-// One workgroup per row; thread t holds float4s t, t + 256, ... of it, the
-// first R of them in registers (rows of up to 1024 R elements are read once);
-// what is past them is read again in the second pass, from h_out if that is
-// written (it may overwrite an input), each thread reading back its own.
-template <typename T, int R, bool kTernary>
-__global__ __launch_bounds__(kThreads) void rmsnorm_quant_kernel(const T *x, const T *res, const float *__restrict__ weight,
-                                                                 T *h_out, void *__restrict__ out,
-                                                                 float *__restrict__ x_scale, int64_t K, float eps) {
-    __shared__ double red[kWaves][2];
+// One workgroup of 64 W threads per row; thread t holds float4s t, t + 64 W, ... of
+// it, the first R of them in registers (rows of up to 256 W R elements are read once);
+// what is past them is read again in the second pass, from h_out if that is written
+// (it may overwrite an input), each thread reading back its own.
+template <typename T, int R, int W, bool kTernary>
+__global__ __launch_bounds__(64 * W) void rmsnorm_quant_kernel(const T *x, const T *res, const float *__restrict__ weight,
+                                                               T *h_out, void *__restrict__ out,
+                                                               float *__restrict__ x_scale, int64_t K, float eps) {
+    constexpr int kT = 64 * W;
+    __shared__ double red[W][2];
     const int64_t row = blockIdx.x;
-    const int64_t nq = K / 4;
+    const int nq = static_cast<int>(K / 4);
     x += row * K;
     if (res) res += row * K;
     if (h_out) h_out += row * K;
-    f32x4 h[R];
+    f32x4 h[R], w[R];
     double ss = 0.0, amax = 0.0;
 #pragma unroll
     for (int i = 0; i < R; i++) {
-        const int64_t e4 = i * kThreads + static_cast<int64_t>(threadIdx.x);
-        h[i] = load_h(x, res, e4 < nq ? e4 : nq - 1);   // clamped: issued, not used
+        const int e4 = i * kT + static_cast<int>(threadIdx.x);
+        const int at = e4 < nq ? e4 : nq - 1;   // clamped: issued, not used
+        h[i] = load_h(x, res, at);
+        w[i] = load4(weight + 4 * at);
     }
+    float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; i++) {
-        const int64_t e4 = i * kThreads + static_cast<int64_t>(threadIdx.x);
+        const int e4 = i * kT + static_cast<int>(threadIdx.x);
         if (e4 < nq) {
-            if (h_out) store4(h_out + 4 * e4, h[i]);
+            if (h_out) store4(h_out + 4 * static_cast<int64_t>(e4), h[i]);
             ss += square4(h[i]);
-            if (kTernary) amax = fmax(amax, Products(h[i], load4(weight + 4 * e4)).absmax());
+            if (kTernary) top = fmaxf(top, Products(h[i], w[i]).absmax());
         }
     }
-    for (int64_t e4 = R * kThreads + static_cast<int64_t>(threadIdx.x); e4 < nq; e4 += kThreads) {
-        const f32x4 v = load_h(x, res, e4);
-        if (h_out) store4(h_out + 4 * e4, v);
-        ss += square4(v);
-        if (kTernary) amax = fmax(amax, Products(v, load4(weight + 4 * e4)).absmax());
+    if constexpr (kTernary) {   // the largest product in f64: among those whose f32 rounding is the largest
+#pragma unroll
+        for (int i = 0; i < R; i++) {
+            const int e4 = i * kT + static_cast<int>(threadIdx.x);
+            const Products pr(h[i], w[i]);
+            if (e4 < nq && (pr.absmax() == top || !in_range(top))) amax = fmax(amax, pr.exact_absmax());
+        }
     }
-    group_sum_max(ss, amax, red);
-    const double rstd = 1.0 / sqrt(ss / static_cast<double>(K) + static_cast<double>(eps));
-    const double row_inv = factor_of(amax);
-    if (kTernary && threadIdx.x == 0) x_scale[row] = static_cast<float>(amax * rstd / 127.0);
+    for (int e4 = R * kT + static_cast<int>(threadIdx.x); e4 < nq; e4 += kT) {
+        const f32x4 v = load_h(x, res, e4);
+        if (h_out) store4(h_out + 4 * static_cast<int64_t>(e4), v);
+        ss += square4(v);
+        if (kTernary) amax = fmax(amax, Products(v, load4(weight + 4 * e4)).exact_absmax());
+    }
+    group_sum_max<W, kTernary>(ss, amax, red);
+    const double rstd127 = rsqrt_f64(ss / static_cast<double>(K) + static_cast<double>(eps)) * (1.0 / 127.0);
+    const float r32 = static_cast<float>(rstd127);
+    const float row_top = static_cast<float>(amax), row_inv = row_top > 0.0f ? recip127(row_top) : 0.0f;
+    if (kTernary && threadIdx.x == 0) x_scale[row] = amax > 0.0 ? static_cast<float>(amax * rstd127) : 0.0f;
     const int lane = threadIdx.x % 64, k8 = lane % 8;
     const NibbleTranspose tr(k8);
-    const int64_t W = K / 32;
-    const auto finish = [&](f32x4 v, int64_t e4) {   // whole groups of eight lanes come here together
-        const Products pr(v, load4(weight + 4 * e4));
+    const int64_t groups = K / 32;
+    const auto finish = [&](const Products &pr, int e4) {   // whole groups of eight lanes come here together
         if constexpr (kTernary) {
-            const uint32_t w = tr(bits_to_nibbles(pr.codes(row_inv)));
-            static_cast<uint32_t *>(out)[(row * 8 + k8) * W + e4 / 8] = w;
+            bool doubt = !in_range(row_top);
+            uint32_t packed = pr.codes(row_inv, doubt);
+            if (__any(doubt)) packed = pr.exact_codes(factor_of(amax));
+            static_cast<uint32_t *>(out)[(row * 8 + k8) * groups + e4 / 8] = tr(bits_to_nibbles(packed));
         } else {
-            const double a = max8d(pr.absmax());
-            const uint32_t packed = pr.codes(factor_of(a));
-            uint16_t *o = static_cast<uint16_t *>(out) + (row * W + e4 / 8) * 17;   // 34 bytes = 17 halves
+            const float a = max8(pr.absmax());
+            float d32 = a * r32;
+            bool doubt = !in_range(a) || f16_doubt(d32);
+            uint32_t packed = pr.codes(a > 0.0f ? recip127(a) : 0.0f, doubt);
+            if (__any(doubt)) {
+                const double exact = max8d(pr.exact_absmax());
+                packed = pr.exact_codes(factor_of(exact));
+                d32 = exact > 0.0 ? static_cast<float>(exact * rstd127) : 0.0f;
+            }
+            uint16_t *o = static_cast<uint16_t *>(out) + (row * groups + e4 / 8) * 17;   // 34 bytes = 17 halves
             o[1 + 2 * k8] = static_cast<uint16_t>(packed & 0xffffu);
             o[2 + 2 * k8] = static_cast<uint16_t>(packed >> 16);
-            if (k8 == 0) {
-                const _Float16 d = static_cast<_Float16>(static_cast<float>(a * rstd / 127.0));
-                o[0] = __builtin_bit_cast(uint16_t, d);
-            }
+            if (k8 == 0) o[0] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(d32));
         }
     };
 #pragma unroll
     for (int i = 0; i < R; i++) {
-        const int64_t e4 = i * kThreads + static_cast<int64_t>(threadIdx.x);
-        if (e4 < nq) finish(h[i], e4);
+        const int e4 = i * kT + static_cast<int>(threadIdx.x);
+        if (e4 < nq) finish(Products(h[i], w[i]), e4);
     }
-    for (int64_t e4 = R * kThreads + static_cast<int64_t>(threadIdx.x); e4 < nq; e4 += kThreads)
-        finish(h_out ? load4(h_out + 4 * e4) : load_h(x, res, e4), e4);
+    for (int e4 = R * kT + static_cast<int>(threadIdx.x); e4 < nq; e4 += kT)
+        finish(Products(h_out ? load4(h_out + 4 * static_cast<int64_t>(e4)) : load_h(x, res, e4), load4(weight + 4 * e4)), e4);
 }
 
 // ------------------------------------------------------------- readers
@@ -204,17 +267,19 @@ int check_norm(const char *name, const void *x, const void *residual, const floa
 template <bool kTernary>
 void launch_norm(const void *x, const void *residual, const float *weight, void *h_out, void *out, float *x_scale,
                  int64_t n, int64_t K, float eps, int32_t dtype, hipStream_t hs) {
-    const dim3 grid(static_cast<uint32_t>(n)), block(kThreads);
+    const dim3 grid(static_cast<uint32_t>(n));
     dispatch_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const T *xt = static_cast<const T *>(x), *rt = static_cast<const T *>(residual);
         T *ht = static_cast<T *>(h_out);
+        const auto launch = [&](auto r, auto w) {
+            hipLaunchKernelGGL((rmsnorm_quant_kernel<T, decltype(r)::value, decltype(w)::value, kTernary>), grid,
+                               dim3(64 * decltype(w)::value), 0, hs, xt, rt, weight, ht, out, x_scale, K, eps);
+        };
         if (K <= 1024 * 4)
-            hipLaunchKernelGGL((rmsnorm_quant_kernel<T, 4, kTernary>), grid, block, 0, hs, xt, rt, weight, ht, out,
-                               x_scale, K, eps);
+            launch(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
         else
-            hipLaunchKernelGGL((rmsnorm_quant_kernel<T, 8, kTernary>), grid, block, 0, hs, xt, rt, weight, ht, out,
-                               x_scale, K, eps);
+            launch(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
     });
 }
 
