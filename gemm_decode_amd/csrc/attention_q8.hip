@@ -96,11 +96,10 @@ struct Seq {
     }
 };
 
-// The parts that a sequence of `len` keys has (at least one, which also serves
-// the rows of an empty sequence).
-__device__ __forceinline__ int parts_of(const AttnArgs &a, int64_t len) {
-    const int n = static_cast<int>((len + a.chunk - 1) / a.chunk);
-    return n < 1 ? 1 : n;
+// r / G for r < 64 G: the f32 quotient is off by less than 2^-16, half a step of it
+// is 2^-13 or more.
+__device__ __forceinline__ int over_group(int r, int G) {
+    return static_cast<int>((static_cast<float>(r) + 0.5f) * __builtin_amdgcn_rcpf(static_cast<float>(G)));
 }
 
 // 32 positions of one KV head, as two tiles of 16: where their codes begin (the
@@ -262,7 +261,7 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, const Place &t, i
     }
 }
 
-// A tile's K codes turned through the wave's own part of LDS from the order of
+// The two tiles' K codes turned through the wave's own part of LDS from the order of
 // memory (lane after lane, D/16 lanes to a key) to 16 dims of key n per lane, from
 // 64 i + 16 g on. The 16-byte pieces of a key are stored in an order that differs
 // between the eight keys that one cycle reads, so that they lie in distinct banks.
@@ -272,12 +271,16 @@ __device__ __forceinline__ int piece_at(int key, int piece) {
 }
 
 template <int D>
-__device__ __forceinline__ void turn_keys(u32x4 (&k)[D / 64], u32x4 *lds, int lane) {
+__device__ __forceinline__ void turn_keys(u32x4 (&k)[2][D / 64], u32x4 (*lds)[D], int lane) {
     constexpr int P = D / 16;   // pieces of a key
 #pragma unroll
-    for (int i = 0; i < D / 64; i++) lds[piece_at<D>(64 / P * i + lane / P, lane % P)] = k[i];
+    for (int u = 0; u < 2; u++)
 #pragma unroll
-    for (int i = 0; i < D / 64; i++) k[i] = lds[piece_at<D>(lane % 16, 4 * i + lane / 16)];
+        for (int i = 0; i < D / 64; i++) lds[u][piece_at<D>(64 / P * i + lane / P, lane % P)] = k[u][i];
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < D / 64; i++) k[u][i] = lds[u][piece_at<D>(lane % 16, 4 * i + lane / 16)];
 }
 
 // The lane's K operand of every group: the groups 2i and 2i + 1 lie in lanes g < 2
@@ -372,7 +375,7 @@ __device__ __forceinline__ void add_scaled(float (&s)[4], f32x4 d, const float (
 // NS = 2: operands in two f16 parts (f32 inputs), NS = 1: in one. A workgroup
 // serves RT tiles of 16 query rows.
 template <typename T, int D, int NS, int RT>
-__global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(AttnArgs a) {
     constexpr int C = D / 32, VB = D / 16, R = 16 * RT;
     typedef f32x4 Joined[R][D / 4 + 1];   // a wave's sums, padded: 16 lanes write one column
     __shared__ union {
@@ -391,8 +394,10 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
     const Seq sq(a, b);
     const int G = static_cast<int>(a.n_heads) / Hkv;
     const int rows = sq.rows * G;   // of this KV head
-    const int parts = parts_of(a, sq.len);
-    if (r0 >= rows || split >= parts) return;
+    // A sequence has ceil(len / chunk) parts, and at least one, which also serves the
+    // rows of an empty sequence.
+    if (r0 >= rows || (split > 0 && split * a.chunk >= sq.len)) return;
+    const bool only = sq.len <= a.chunk;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / 64);
     const int lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
     const int len = static_cast<int>(sq.len), ctx = static_cast<int>(sq.ctx);
@@ -420,30 +425,38 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
     Frag q[RT][C][NS];
     float scale2[RT];       // from a contraction to a score (times log2 e without a cap)
     uint64_t word[RT];      // the drafted keys that the row sees
+    f32x4 qx[RT][C][2];
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
         const int r = r0 + 16 * rt + n;
         const bool live = r < rows;
-        const int t = live ? r / G : 0, h = kvh * G + (live ? r - t * G : 0);
+        const int t = live ? over_group(r, G) : 0, h = kvh * G + (live ? r - t * G : 0);
         const T *p = static_cast<const T *>(a.q) + ((sq.row0 + t) * a.n_heads + h) * D;
         word[rt] = a.tree ? a.tree[sq.row0 + t] : (t >= 63 ? ~0ull : (1ull << (t + 1)) - 1);
-        f32x4 x[C][2];
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) {   // a row past the last repeats the first and counts as zeros
+                const f32x4 x = load4(p + 32 * c + 16 * (g % 2) + 8 * (g / 2) + 4 * i);
+                qx[rt][c][i] = live ? x : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
         float mx = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                x[c][i] = live ? load4(p + 32 * c + 16 * (g % 2) + 8 * (g / 2) + 4 * i) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < 2; i++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) mx = fmaxf(mx, fabsf(x[c][i][j]));
-            }
+                for (int j = 0; j < 4; j++) mx = fmaxf(mx, fabsf(qx[rt][c][i][j]));
         mx = max_across(mx);
         const int e = mx > 0.0f && mx <= 3.40282347e38f ? 14 - __builtin_amdgcn_frexp_expf(mx) : 0;
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                const float v0 = ldexpf(x[c][i / 4][i % 4], e), v1 = ldexpf(x[c][i / 4][i % 4 + 1], e);
+                const float v0 = ldexpf(qx[rt][c][i / 4][i % 4], e), v1 = ldexpf(qx[rt][c][i / 4][i % 4 + 1], e);
                 const f16x2 hi = {static_cast<_Float16>(v0), static_cast<_Float16>(v1)};
                 q[rt][c][0].h[i / 2] = hi;
                 if constexpr (NS == 2)
@@ -474,10 +487,10 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
         const bool plain = j + kStep <= (ctx < j1 ? ctx : j1) && ok[0] && ok[1];   // every row sees every key
         if (more) next = place_of<D>(a, b, of_page, of_head, (j + kGroupKeys) / 16, last);
         float s[RT][2][4];
+        turn_keys<D>(st.k, lds.k[wave], lane);
 #pragma unroll
         for (int u = 0; u < 2; u++) {
             u32x2 kw[C];
-            turn_keys<D>(st.k[u], lds.k[wave][u], lane);
             spread_keys<D>(st.k[u], kw);
             const f16x2 ks = as_h2(st.ks[u]);
             const float x[2] = {static_cast<float>(ks[0]), static_cast<float>(ks[1])};
@@ -664,29 +677,33 @@ __global__ __launch_bounds__(kThreads) void attn_q8_kernel(AttnArgs a) {
                     f32x4{o[rt][t][i], o[rt][t + 1][i], o[rt][t + 2][i], o[rt][t + 3][i]} * f;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < R * (D / 4); e += kThreads) {
-        const int r = e / (D / 4), d4 = e % (D / 4);
-        if (r0 + r >= rows) break;
-        float mx = lds_m[0][r];
+    constexpr int kPerRow = kThreads / R;   // threads of a row
+    const int r = threadIdx.x / kPerRow;
+    if (r0 + r >= rows) return;
+    float mx = lds_m[0][r];
 #pragma unroll
-        for (int w = 1; w < kWaves; w++) mx = fmaxf(mx, lds_m[w][r]);
-        float sum = 0.0f;
-        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int w = 1; w < kWaves; w++) mx = fmaxf(mx, lds_m[w][r]);
+    float sum = 0.0f, f[kWaves];
 #pragma unroll
-        for (int w = 0; w < kWaves; w++) {
-            const float f = __builtin_amdgcn_exp2f(lds_m[w][r] - mx);
-            sum += lds_l[w][r] * f;
-            x += lds.o[w][r][d4] * f;
-        }
-        const int t = (r0 + r) / G, h = kvh * G + (r0 + r) - t * G;
-        const int64_t at = (sq.row0 + t) * a.n_heads + h;
-        if (parts == 1) {
-            store4(static_cast<T *>(a.out) + at * D + 4 * d4, sum > 0.0f ? x * (1.0f / sum) : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-        } else {
-            *reinterpret_cast<f32x4 *>(a.part_o + (at * a.splits + split) * D + 4 * d4) = x;
-            if (d4 == 0) *reinterpret_cast<f32x2 *>(a.part_ml + (at * a.splits + split) * 2) = f32x2{mx, sum};
-        }
+    for (int w = 0; w < kWaves; w++) {
+        f[w] = __builtin_amdgcn_exp2f(lds_m[w][r] - mx);
+        sum += lds_l[w][r] * f[w];
     }
+    const int t = over_group(r0 + r, G), h = kvh * G + (r0 + r) - t * G;
+    const int64_t at = (sq.row0 + t) * a.n_heads + h;
+    const float inv = only ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
+    float *part = a.part_o + (at * a.splits + split) * D;
+    for (int d4 = threadIdx.x % kPerRow; d4 < D / 4; d4 += kPerRow) {
+        f32x4 x = lds.o[0][r][d4] * f[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; w++) x += lds.o[w][r][d4] * f[w];
+        if (only)
+            store4(static_cast<T *>(a.out) + at * D + 4 * d4, x * inv);
+        else
+            *reinterpret_cast<f32x4 *>(part + 4 * d4) = x;
+    }
+    if (!only && threadIdx.x % kPerRow == 0)
+        *reinterpret_cast<f32x2 *>(a.part_ml + (at * a.splits + split) * 2) = f32x2{mx, sum};
 }
 
 // Joins the parts of one query row and head. A step takes 64 parts: lane i of every
@@ -697,8 +714,8 @@ __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
     constexpr int E = D / 64, kPer = 64 / kWaves;
     __shared__ float lds_o[kWaves][D];
     const Seq sq(a, blockIdx.z);
-    const int parts = parts_of(a, sq.len);
-    if (static_cast<int>(blockIdx.y) >= sq.rows || parts == 1) return;
+    if (static_cast<int>(blockIdx.y) >= sq.rows || sq.len <= a.chunk) return;   // a single part is written by itself
+    const int parts = static_cast<int>(static_cast<uint32_t>(sq.len - 1) / static_cast<uint32_t>(a.chunk)) + 1;
     const int64_t at = (sq.row0 + blockIdx.y) * a.n_heads + blockIdx.x;
     const float *po = a.part_o + at * a.splits * D, *pml = a.part_ml + at * a.splits * 2;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / 64), lane = threadIdx.x % 64;
