@@ -420,7 +420,9 @@ def _dtype(t, name):
 def _current():
     """(index of the current device, torch's current stream on it)."""
     import torch
-    i = torch.cuda.current_device()
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    i = torch._C._cuda_getDevice()
     return i, torch._C._cuda_getCurrentRawStream(i)   # 0.1 us; a torch.cuda.Stream object takes 1.1
 
 
