@@ -761,13 +761,16 @@ __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
     }
 }
 
-// Parts per sequence. At least enough workgroups for every CU to have its two or
-// three (kFill), however short the parts; beyond that, parts of no fewer than
-// kMinSteps steps a wave, up to kFine workgroups in all: many short ones even out the
-// end of the launch and sequences of different lengths (32 of 16k to 32k keys: 389 us
-// with 1024 workgroups, 319 with 2048, 303 with 4096, 324 with 8192), but each reads
-// its queries and joins its waves anew.
-constexpr int kFill = 768, kFine = 4096, kMinSteps = 4;
+// Parts per sequence. While there is not a workgroup for every CU at one part each
+// (kCus), as many as give each two or three (kFill), however short they get. Beyond
+// that, parts of no fewer than kMinSteps steps a wave, up to kFine workgroups in all:
+// many of them even out the end of the launch and sequences of different lengths, but
+// each prepares its queries and joins its waves anew. Measured (head dim 128, 32 / 8
+// heads): 32 sequences of 16k to 32k keys 304 us with 2048 workgroups, 287 with 4096,
+// 293 with 6144; 128 sequences of 1k keys 68 us with parts of 2 steps, 61 with 4, 48
+// with 8; 16 of 2k keys (a workgroup for half the CUs) 26 us at 256 workgroups, 21 at
+// 768; 48 of 512 keys (one and a half for each CU) 17 us whole, 20 in two parts.
+constexpr int kCus = 256, kFill = 768, kFine = 4096, kMinSteps = 8;
 
 // How the work is cut: rows per workgroup, and keys per part.
 struct Plan {
@@ -782,7 +785,7 @@ Plan plan_of(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_d
     p.row_blocks = (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
     const int64_t groups = n_seqs * n_kv_heads * p.row_blocks;   // at one part each
     const int64_t steps = (max_kv_len + kGroupKeys - 1) / kGroupKeys;
-    const int64_t fill = (kFill + groups - 1) / groups, fine = (kFine + groups - 1) / groups;
+    const int64_t fill = groups < kCus ? (kFill + groups - 1) / groups : 1, fine = (kFine + groups - 1) / groups;
     int64_t parts = fine < steps / kMinSteps ? fine : steps / kMinSteps;
     parts = parts > fill ? parts : fill;
     parts = parts < steps ? parts : steps;

@@ -103,7 +103,7 @@ __device__ __forceinline__ double rsqrt_f64(double x) {
     return y;
 }
 
-// Sum (and max) over the workgroup; every thread gets them.
+// Sum (and max) over a row's waves; every thread gets them.
 template <int kWaves, bool kMax>
 __device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*red)[2]) {
 #pragma unroll
@@ -111,6 +111,7 @@ __device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*
         sum += __shfl_xor(sum, o);
         if (kMax) mx = fmax(mx, __shfl_xor(mx, o));
     }
+    if (kWaves == 1) return;
     if (threadIdx.x % 64 == 0) {
         red[threadIdx.x / 64][0] = sum;
         if (kMax) red[threadIdx.x / 64][1] = mx;
@@ -125,17 +126,21 @@ __device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*
     }
 }
 
-// One workgroup of 64 W threads per row; thread t holds float4s t, t + 64 W, ... of
-// it, the first R of them in registers (rows of up to 256 W R elements are read once);
+// W waves per row, and a workgroup per row (W = 1: four rows). Thread t of a row holds
+// float4s t, t + 64 W, ... of it, the first R of them in registers (rows of up to 256 W R
+// elements are read once);
 // what is past them is read again in the second pass, from h_out if that is written
 // (it may overwrite an input), each thread reading back its own.
 template <typename T, int R, int W, bool kTernary>
-__global__ __launch_bounds__(64 * W) void rmsnorm_quant_kernel(const T *x, const T *res, const float *__restrict__ weight,
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_quant_kernel(const T *x, const T *res, const float *__restrict__ weight,
                                                                T *h_out, void *__restrict__ out,
-                                                               float *__restrict__ x_scale, int64_t K, float eps) {
+                                                               float *__restrict__ x_scale, int64_t n, int64_t K,
+                                                               float eps) {
     constexpr int kT = 64 * W;
     __shared__ double red[W][2];
-    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x % kT;
+    const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64 : blockIdx.x;
+    if (row >= n) return;   // W = 1: a whole wave, and no barriers
     const int nq = static_cast<int>(K / 4);
     x += row * K;
     if (res) res += row * K;
@@ -144,7 +149,7 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_quant_kernel(const T *x, const
     double ss = 0.0, amax = 0.0;
 #pragma unroll
     for (int i = 0; i < R; i++) {
-        const int e4 = i * kT + static_cast<int>(threadIdx.x);
+        const int e4 = i * kT + tid;
         const int at = e4 < nq ? e4 : nq - 1;   // clamped: issued, not used
         h[i] = load_h(x, res, at);
         w[i] = load4(weight + 4 * at);
@@ -152,7 +157,7 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_quant_kernel(const T *x, const
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; i++) {
-        const int e4 = i * kT + static_cast<int>(threadIdx.x);
+        const int e4 = i * kT + tid;
         if (e4 < nq) {
             if (h_out) store4(h_out + 4 * static_cast<int64_t>(e4), h[i]);
             ss += square4(h[i]);
@@ -162,12 +167,12 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_quant_kernel(const T *x, const
     if constexpr (kTernary) {   // the largest product in f64: among those whose f32 rounding is the largest
 #pragma unroll
         for (int i = 0; i < R; i++) {
-            const int e4 = i * kT + static_cast<int>(threadIdx.x);
+            const int e4 = i * kT + tid;
             const Products pr(h[i], w[i]);
             if (e4 < nq && (pr.absmax() == top || !in_range(top))) amax = fmax(amax, pr.exact_absmax());
         }
     }
-    for (int e4 = R * kT + static_cast<int>(threadIdx.x); e4 < nq; e4 += kT) {
+    for (int e4 = R * kT + tid; e4 < nq; e4 += kT) {
         const f32x4 v = load_h(x, res, e4);
         if (h_out) store4(h_out + 4 * static_cast<int64_t>(e4), v);
         ss += square4(v);
@@ -177,7 +182,7 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_quant_kernel(const T *x, const
     const double rstd127 = rsqrt_f64(ss / static_cast<double>(K) + static_cast<double>(eps)) * (1.0 / 127.0);
     const float r32 = static_cast<float>(rstd127);
     const float row_top = static_cast<float>(amax), row_inv = row_top > 0.0f ? recip127(row_top) : 0.0f;
-    if (kTernary && threadIdx.x == 0) x_scale[row] = amax > 0.0 ? static_cast<float>(amax * rstd127) : 0.0f;
+    if (kTernary && tid == 0) x_scale[row] = amax > 0.0 ? static_cast<float>(amax * rstd127) : 0.0f;
     const int lane = threadIdx.x % 64, k8 = lane % 8;
     const NibbleTranspose tr(k8);
     const int64_t groups = K / 32;
@@ -205,10 +210,10 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_quant_kernel(const T *x, const
     };
 #pragma unroll
     for (int i = 0; i < R; i++) {
-        const int e4 = i * kT + static_cast<int>(threadIdx.x);
+        const int e4 = i * kT + tid;
         if (e4 < nq) finish(Products(h[i], w[i]), e4);
     }
-    for (int e4 = R * kT + static_cast<int>(threadIdx.x); e4 < nq; e4 += kT)
+    for (int e4 = R * kT + tid; e4 < nq; e4 += kT)
         finish(Products(h_out ? load4(h_out + 4 * static_cast<int64_t>(e4)) : load_h(x, res, e4), load4(weight + 4 * e4)), e4);
 }
 
@@ -267,18 +272,26 @@ int check_norm(const char *name, const void *x, const void *residual, const floa
 template <bool kTernary>
 void launch_norm(const void *x, const void *residual, const float *weight, void *h_out, void *out, float *x_scale,
                  int64_t n, int64_t K, float eps, int32_t dtype, hipStream_t hs) {
-    const dim3 grid(static_cast<uint32_t>(n));
     dispatch_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const T *xt = static_cast<const T *>(x), *rt = static_cast<const T *>(residual);
         T *ht = static_cast<T *>(h_out);
         const auto launch = [&](auto r, auto w) {
-            hipLaunchKernelGGL((rmsnorm_quant_kernel<T, decltype(r)::value, decltype(w)::value, kTernary>), grid,
-                               dim3(64 * decltype(w)::value), 0, hs, xt, rt, weight, ht, out, x_scale, K, eps);
+            constexpr int W = decltype(w)::value;
+            const dim3 grid(static_cast<uint32_t>(W == 1 ? (n + 3) / 4 : n));
+            hipLaunchKernelGGL((rmsnorm_quant_kernel<T, decltype(r)::value, W, kTernary>), grid,
+                               dim3(W == 1 ? 256 : 64 * W), 0, hs, xt, rt, weight, ht, out, x_scale, n, K, eps);
         };
-        // Eight waves: 5.5 us for a row of 4096 and its reader, 6.3 with four, 5.4 with sixteen, which take
-        // 50 us for 4099 rows where these take 47.
-        if (K <= 4096)
+        // Many short rows: a wave each (16384 rows of 512 in bf16: 29 us a pass with its reader, 74 with eight
+        // waves a row, most of them idle; a single row of 1024: 6.0 us, 5.2 with eight). Else eight waves a
+        // row (a row of 4096: 5.5 us with its reader, 6.3 with four waves, 5.4 with sixteen, which take 50 us
+        // for 4099 rows where eight take 47).
+        const bool many = n >= 1024;
+        if (K <= 512 && many)
+            launch(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
+        else if (K <= 1024 && many)
+            launch(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+        else if (K <= 4096)
             launch(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
         else
             launch(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});

@@ -74,7 +74,8 @@ def check(form, got, h, w, n, K):
 
 
 SHAPES = [(1, 32), (1, 64), (3, 96), (5, 1056), (2, 2560), (2, 4096), (7, 4128), (1, 6912), (3, 8192), (2, 8224),
-          (1, 16416), (2, 20000), (300, 160)]
+          (1, 16416), (2, 20000), (300, 160), (5, 512), (4, 1024),
+          (1030, 512), (1026, 544), (1025, 1024), (2050, 32)]   # the last four: a wave per row
 
 
 @pytest.mark.parametrize("form", ["q8_0", "ternary"])
