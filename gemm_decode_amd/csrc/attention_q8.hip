@@ -716,7 +716,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
 }
 
 // Joins the parts of one query row and head. A step takes 64 parts: lane i of every
-// wave holds part i's maximum and sum, wave w adds up the parts 16 w .. 16 w + 15, D/64
+// wave holds part i's maximum and sum, wave w adds up the parts w, w + 4, ..., D/64
 // dims to a lane, all of them loaded before any is used.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
@@ -737,7 +737,8 @@ __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
         float x[kPer][E];
 #pragma unroll
         for (int k = 0; k < kPer; k++) {
-            const int part = p0 + kPer * wave + k < parts ? p0 + kPer * wave + k : parts - 1;
+            if (p0 + kWaves * k >= parts) break;
+            const int part = p0 + kWaves * k + wave < parts ? p0 + kWaves * k + wave : parts - 1;
 #pragma unroll
             for (int i = 0; i < E; i++) x[k][i] = po[static_cast<int64_t>(part) * D + lane * E + i];
         }
@@ -753,8 +754,9 @@ __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
         for (int i = 0; i < E; i++) o[i] *= before;
 #pragma unroll
         for (int k = 0; k < kPer; k++) {
+            if (p0 + kWaves * k >= parts) break;
             const float f = __builtin_bit_cast(
-                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), kPer * wave + k));
+                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), kWaves * k + wave));
 #pragma unroll
             for (int i = 0; i < E; i++) o[i] = __builtin_fmaf(x[k][i], f, o[i]);
         }
