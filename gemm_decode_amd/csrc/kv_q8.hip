@@ -21,6 +21,7 @@ using namespace gd;
 constexpr int kThreads = 256;
 constexpr int64_t kMaxThreads = (INT64_C(1) << 32) - 1;   // of one launch
 constexpr int kMaxRot = 256;
+constexpr int64_t kMaxStride = INT64_C(1) << 36;   // elements between tokens
 constexpr int64_t kManyTokens = 1024;   // from here on a workgroup per token (or four) fills the card
 
 // ------------------------------------------------------- rotary table
@@ -271,7 +272,7 @@ void dispatch_dim(int64_t head_dim, F fn) {
 
 // The row stride of an input of `heads` head rows per token.
 bool stride_ok(int64_t stride, int64_t heads, int64_t D, int32_t dtype) {
-    return stride >= heads * D && (stride * dtype_size(dtype)) % 16 == 0 && stride <= (INT64_C(1) << 40);
+    return stride >= heads * D && stride % (16 / dtype_size(dtype)) == 0;
 }
 
 }  // namespace
@@ -387,11 +388,13 @@ extern "C" int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_strid
         GD_REQUIRE(aligned(rope, 16) && aligned(positions, 4), GD_EALIGN,
                    "kv_q8_store: rope must be 16-byte aligned, positions 4-byte");
     }
+    GD_REQUIRE(n_heads <= 65536 && n_tok <= kMaxThreads / kThreads, GD_ERANGE,
+               "kv_q8_store: n_tok (%lld) or n_heads (%lld) too large", (long long)n_tok, (long long)n_heads);
+    GD_REQUIRE(q_stride <= kMaxStride && k_stride <= kMaxStride && v_stride <= kMaxStride, GD_ERANGE,
+               "kv_q8_store: a row stride is too large");
     GD_REQUIRE((n_heads == 0 || stride_ok(q_stride, n_heads, D, dtype)) && stride_ok(k_stride, Hkv, D, dtype) &&
                    stride_ok(v_stride, Hkv, D, dtype),
                GD_ESHAPE, "kv_q8_store: a row stride must cover the token's heads and be a multiple of 16 bytes");
-    GD_REQUIRE(n_heads <= 65536 && n_tok <= kMaxThreads / kThreads, GD_ERANGE,
-               "kv_q8_store: n_tok (%lld) or n_heads (%lld) too large", (long long)n_tok, (long long)n_heads);
     GD_REQUIRE(aligned(k, 16) && aligned(v, 16) && (n_heads == 0 || (aligned(q, 16) && aligned(q_out, 16))) &&
                    aligned(slots, 8),
                GD_EALIGN, "kv_q8_store: q, k, v and q_out must be 16-byte aligned, slots 8-byte");

@@ -263,7 +263,7 @@ int check_norm(const char *name, const void *x, const void *residual, const floa
     GD_REQUIRE(dtype_ok(dtype), GD_EINVAL, "%s: unknown dtype %d", name, dtype);
     GD_REQUIRE(eps >= 0.0f && eps <= 3.40282347e38f, GD_EINVAL, "%s: eps must be finite and >= 0", name);
     GD_REQUIRE(K % 32 == 0, GD_ESHAPE, "%s: K (%lld) must be a multiple of 32", name, (long long)K);
-    GD_REQUIRE(n <= kMaxThreads / kThreads && K <= (INT64_C(1) << 30), GD_ERANGE, "%s: n or K too large", name);
+    GD_REQUIRE(n <= kMaxThreads / 512 && K <= (INT64_C(1) << 30), GD_ERANGE, "%s: n or K too large", name);
     GD_REQUIRE(aligned(x, 16) && aligned(residual, 16) && aligned(weight, 16) && aligned(h_out, 16), GD_EALIGN,
                "%s: x, residual, weight and h_out must be 16-byte aligned", name);
     return GD_OK;

@@ -428,8 +428,8 @@ int attn_decode_splitk_noalloc(const float *q, const float *k_cache, const float
  * y * (127 / max|y|), so the codes are Math.round(p * (127 * (1 / max|p|)))
  * (each step rounded in f64, where p is exact) and the scale is max|p| * rstd
  * / 127, evaluated in f64 from left to right and rounded to f32. A group whose
- * products are all 0 gets scale 0 and zero codes. Sums are f64; inputs must be
- * finite.
+ * products are all 0 gets scale 0 and zero codes. Sums are f64; inputs and h
+ * must be finite.
  *
  * Element types of the entry points from here on that take a `dtype`: */
 #define GD_F32  0
@@ -446,7 +446,7 @@ int attn_decode_splitk_noalloc(const float *q, const float *k_cache, const float
  *             otherwise.
  *   a_q8      device, n * (K/32) * 34 bytes, 2-byte aligned; written whole.
  * x, residual, weight and h_out 16-byte aligned. Requires K % 32 == 0,
- * K <= 2^30, 1 <= n < 2^24, finite eps >= 0. Errors: GD_EINVAL, GD_ESHAPE,
+ * K <= 2^30, 1 <= n < 2^23, finite eps >= 0. Errors: GD_EINVAL, GD_ESHAPE,
  * GD_EALIGN, GD_ERANGE, GD_EHIP. */
 int rmsnorm_q8_0(const void *x, const void *residual, const float *weight, void *h_out,
                  void *a_q8, int64_t n, int64_t K, float eps, int32_t dtype, void *stream);
@@ -482,8 +482,8 @@ int ternary_dequantize_act(const uint32_t *planes, const float *x_scale, void *y
  * paging is a pool whose page b holds all of sequence b.
  * The struct is read on the host during the call; the planes are device
  * memory, 16-byte aligned. head_dim is 64, 128 or 256, page_size a multiple
- * of 16, n_kv_heads <= 4096. Row contents that were never stored are never
- * used (any bytes may be there). */
+ * of 16, n_kv_heads <= 4096. Scales are finite and not negative in rows that
+ * are used; rows that were never stored are not used (any bytes may be there). */
 typedef struct gd_kv_q8 {
     int8_t *k_codes;      /* [n_pages][n_kv_heads][page_size][head_dim]          */
     uint16_t *k_scales;   /* f16 bits, [n_pages][n_kv_heads][page_size][head_dim/32] */

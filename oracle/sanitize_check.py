@@ -67,7 +67,7 @@ def main() -> int:
             return 2
         env = dict(base, LD_PRELOAD=clang_rt[-1])
         rc = _run([sys.executable, "-m", "pytest", "-q", "-m", "not gpu", "-p", "no:cacheprovider",
-                   os.path.join(tmp, "tests", "test_abi.py")], env, tmp)
+                   os.path.join(tmp, "tests", "test_abi.py"), os.path.join(tmp, "tests", "test_abi_layer.py")], env, tmp)
     return rc
 
 

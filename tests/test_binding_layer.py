@@ -1,0 +1,47 @@
+"""The binding's own refusals for the norm, rotary, 8-bit cache and attention
+calls, and the strides it takes (CPU tensors; no compute is launched here)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def gd():
+    import gemm_decode_amd
+    return gemm_decode_amd
+
+
+def test_binding_refuses_what_is_not_on_a_device(gd, monkeypatch):
+    """CPU tensors, other types, other sizes and other devices are refused before the library is called."""
+    t = torch.zeros(2, 64)
+    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+        gd.rmsnorm_q8_0(t, None, torch.ones(64), None, torch.zeros(136, dtype=torch.uint8), 2, 64, 1e-5)
+    with pytest.raises(TypeError):
+        gd.rmsnorm_q8_0(t.double(), None, torch.ones(64), None, torch.zeros(136, dtype=torch.uint8), 2, 64, 1e-5)
+    with pytest.raises(ValueError):
+        gd.kv_q8_alloc(2, 16, 1, 64, device="cpu")
+    with pytest.raises(ValueError):
+        gd.KVCacheQ8(torch.zeros(4), None, None, None)
+    with pytest.raises(TypeError):
+        monkeypatch.setattr(gd, "_current", lambda: (0, 0))
+        gd.rope_table(torch.zeros(4, 4, 2), 4, 8, scaling={"kind": 1})
+
+
+def test_binding_token_rows(gd):
+    """The strides that a token-strided input may have (checked on the CPU: the device index of a CPU tensor is -1)."""
+    rows = torch.zeros(5, 6, 64)
+    q, k, v = rows.split([4, 1, 1], dim=1)
+    assert gd._token_rows(-1, q, torch.float32, 5, 256, "q") == (rows.data_ptr(), 384)
+    assert gd._token_rows(-1, k, torch.float32, 5, 64, "k") == (rows.data_ptr() + 4 * 256, 384)
+    assert gd._token_rows(-1, rows.view(5, 384)[:, 64:192], torch.float32, 5, 128, "x")[1] == 384
+    assert gd._token_rows(-1, rows[:1, :4], torch.float32, 1, 256, "q")[1] == 256
+    with pytest.raises(ValueError):
+        gd._token_rows(-1, rows.transpose(0, 1), torch.float32, 6, 320, "x")
+    with pytest.raises(ValueError):
+        gd._token_rows(-1, rows[:, :, ::2], torch.float32, 5, 192, "x")
+    with pytest.raises(ValueError):
+        gd._token_rows(-1, rows, torch.float32, 4, 384, "x")
+    with pytest.raises(ValueError):
+        gd._token_rows(0, rows, torch.float32, 5, 384, "x")
+    with pytest.raises(TypeError):
+        gd._token_rows(-1, rows, torch.bfloat16, 5, 384, "x")

@@ -277,6 +277,34 @@ def test_long_sequence_and_splits(gd):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("T", [F32, BF16])
+def test_pool_past_32_bit_offsets(gd, T):
+    """A pool whose planes pass 4 GiB: a sequence on its first and last pages gives what the same rows give in a small pool."""
+    heads, D, page = 8, 128, 64
+    pages = (5 << 30) // (heads * D * page)
+    big = gd.kv_q8_alloc(pages, page, heads, D)
+    c = Case(gd, [150], [1], 16, heads, D, page, T, seed=12)
+    where = [pages - 1, 0, pages - 2]
+    for plane in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        for i, w in enumerate(where):
+            getattr(big, plane)[w] = getattr(c.cache, plane)[c.table[0, i]]
+    ref = c.run()
+    c.cache, c.page_table = big, dev(np.array([where], np.int32))
+    assert torch.equal(c.run(), ref)
+    c.check(ref)
+
+
+def test_many_sequences_and_rows(gd):
+    """More blocks of rows than one grid holds beside its sequences (80 x 1024 > 65535), most of them empty."""
+    B = 1024
+    qs = [0] * B
+    qs[3], qs[1000] = 64, 2
+    lens = [0] * B
+    lens[3], lens[1000] = 64, 9
+    c = Case(gd, lens, qs, 40, 1, 64, 16, BF16, seed=13, max_len=64)
+    c.check(c.run())
+
+
 def test_workspace_contents_do_not_matter(gd):
     c = Case(gd, [900, 20], [2, 1], 8, 2, 128, 16)
     ref = c.run()

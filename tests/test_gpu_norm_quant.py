@@ -140,6 +140,32 @@ def test_extreme_rows(gd, form):
         assert np.array_equal(got[1].cpu().numpy()[keep], scale[:, 0])
 
 
+@pytest.mark.parametrize("form", ["q8_0", "ternary"])
+def test_zero_rows_without_eps_and_zero_weights(gd, form):
+    """A zero row with eps 0 (its root mean square is 0), a zero block and zero weights: zero codes and scales, no NaN."""
+    K = 96
+    h = np.zeros((3, K), np.float32)
+    h[1] = np.arange(K) - 40
+    h[2, 32:64] = 1e-30
+    w = np.ones(K, np.float32)
+    w[:32] = 0
+    x, wd = torch.from_numpy(h).cuda(), torch.from_numpy(w).cuda()
+    if form == "q8_0":
+        a = torch.full((3 * 3 * 34,), 0xA5, dtype=torch.uint8, device="cuda")
+        gd.rmsnorm_q8_0(x, None, wd, None, a, 3, K, 0.0)
+        a = a.cpu().numpy().reshape(3, 3, 34)
+        assert not a[0].any() and not a[1, 0].any() and not a[2, [0, 2]].any()
+        codes, scale = layer.rmsnorm_codes(h[1:], w, 0.0, 32)
+        assert np.array_equal(a[1:].reshape(-1), blocks(codes, scale))
+    else:
+        p, s = torch.full((3 * 8 * 3,), -1, dtype=torch.int32, device="cuda"), torch.full((3,), -1.0, device="cuda")
+        gd.rmsnorm_ternary_act(x, None, wd, None, p, s, 3, K, 0.0)
+        codes, scale = layer.rmsnorm_codes(h[1:], w, 0.0, K)
+        assert s[0] == 0 and not p[:24].any()
+        assert np.array_equal(s[1:].cpu().numpy(), scale[:, 0])
+        assert np.array_equal(p[24:].cpu().numpy().view(np.uint32), planes_of(codes))
+
+
 def test_ties_go_up(gd):
     """Products at exact halves of a code step in every group: 127 in the group makes the step 1."""
     rng = np.random.default_rng(8)
