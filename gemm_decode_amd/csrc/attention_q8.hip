@@ -13,19 +13,27 @@
 // another until the end, where they are joined through LDS. A second launch
 // joins the parts of a sequence, if it has more than one.
 //
-// No operand passes through LDS, and every load of codes is 16 bytes a lane, past
-// the caches (loads of 8 bytes a lane, four to a line, ran at 4.2 TB/s, the same
-// bytes as these at 6.3). Scores are taken transposed, S^T = K Q^T: lane (n, g) =
-// (lane % 16, lane / 16) loads 16 dims of key n, half of them is swapped with lane
-// (n, g ^ 2), and then one matrix instruction contracts exactly one 32-dim group;
-// its result, multiplied by the group's scale, is added up in f32. The result has
-// lane (n, g) hold keys 4g .. 4g+3 of query row n, which is how the second product,
-// O^T = V^T P^T, takes its weights: they never leave their lane. For V^T the lane
-// has to hold D/16 dims of the same four keys; a row of D bytes is D/16 lanes' loads,
-// so up to four lanes load one key each and exchange parts. The dims of a lane lie in
-// one scale group, so a value is its code times one scale per key. The scales come
-// as one number a lane and tile, and are handed round as the operand of the
-// instruction that uses them (DPP).
+// Loads. Every load of codes is 16 bytes a lane, past the caches, and a wave's load is
+// 1 KB of consecutive memory (K) or whole rows (V): reading alone, loads of 8 bytes a
+// lane, four to a line, ran at 4.2 TB/s, these at 6.3. The K codes are turned into
+// operand order through the wave's own part of LDS; V is exchanged between lanes.
+//
+// Products. Scores are taken transposed, S^T = K Q^T: lane (n, g) = (lane % 16,
+// lane / 16) holds 16 dims of key n, half of them is swapped with lane (n, g ^ 2), and
+// then one matrix instruction contracts exactly one 32-dim group; its result,
+// multiplied by the group's scale, is added up in f32. The result has lane (n, g) hold
+// keys 4g .. 4g+3 of query row n, which is how the second product, O^T = V^T P^T, takes
+// its weights: they never leave their lane. For V^T the lane has to hold D/16 dims of
+// the same four keys; a row of D bytes is D/16 lanes' loads, so up to four lanes load
+// one key each and exchange parts. The dims of a lane lie in one scale group, so a value
+// is its code times one scale per key. The scales come as one number a lane and tile,
+// and are handed round by DPP.
+//
+// What bounds it. 32 sequences of 16k to 32k keys (32 / 8 heads, head dim 128, bf16,
+// 1.75 GB of cache): 281 us, 6.2 TB/s, 90 % of what a streaming read reaches; bound by
+// memory. Few keys (4096 of one sequence, f32: 7.9 us) are bound by the chain of
+// dependent loads before the first product, many rows (64 tokens of four sequences, 172
+// TFLOP/s) by vector instructions, some 590 for 32 keys and 32 rows.
 //
 // Precision. Codes are whole numbers below 2^8, exact in f16. f32 inputs: q (as
 // a power of two times its row) and the weights are split into two f16 parts, 22
@@ -717,7 +725,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
 
 // Joins the parts of one query row and head. A step takes 64 parts: lane i of every
 // wave holds part i's maximum and sum, wave w adds up the parts w, w + 4, ..., D/64
-// dims to a lane, all of them loaded before any is used.
+// dims to a lane, all of them loaded before any is used. 4.7 us for 1024 rows of 16
+// parts (8.5 MB), of which a launch is about 2: bound by its two loads in a chain.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
     constexpr int E = D / 64, kPer = 64 / kWaves;
