@@ -23,7 +23,7 @@ constexpr int64_t kMaxThreads = (INT64_C(1) << 32) - 1;   // of one launch
 constexpr int kMaxRot = 256;
 constexpr int64_t kMaxStride = INT64_C(1) << 36;   // elements between tokens
 // From here on a workgroup per token (store) or four tokens (load) fills the card: 8191
-// tokens stored and read back in 60 us, 86 with a workgroup per token's eight rows, and
+// tokens stored and read back in 60 us, 86 with a workgroup per 16 rows of a token, and
 // 65521 read in 138 us, 160 one by one; fewer tokens are spread as far as they go (one
 // token stored and read back in 5.6 us, 6.5 by one workgroup).
 constexpr int64_t kManyTokens = 1024;
@@ -133,7 +133,7 @@ __device__ __forceinline__ void turn(f32x4 (&x)[E / 4], const f32x4 (&o)[E / 4],
 // heads, k heads, v heads, kBatch of them loaded before any is used. A row never
 // leaves its wave, so q_out may be q itself: a wave reads a row before it writes it.
 // 8191 tokens of 32 / 8 heads of 128 in bf16: 44 us, 4.3 TB/s, near memory's rate with
-// the quantizer's arithmetic beside it (48 us with 1 or 3 rows loaded ahead, 52 with
+// the quantizer's arithmetic beside it (51 us with 1 or 3 rows loaded ahead, 55 with
 // four elements a thread); one token: 3.8 us, bound by its chain of loads.
 template <typename T, int D, int E>
 __global__ __launch_bounds__(kThreads) void kv_q8_store_kernel(StoreArgs a) {
