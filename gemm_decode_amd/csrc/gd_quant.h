@@ -99,6 +99,18 @@ __device__ __forceinline__ uint32_t bits_to_nibbles(uint32_t x) {   // bit 8j + 
     return x;
 }
 
+__device__ __forceinline__ uint32_t nibbles_to_bits(uint32_t x) {   // bit 4b + j -> bit 8j + b: the steps back
+    uint32_t t;
+    t = (x ^ (x >> 1)) & 0x22222222u;
+    x ^= t ^ (t << 1);
+    t = (x ^ (x >> 3)) & 0x0A0A0A0Au;
+    x ^= t ^ (t << 3);
+    t = (x ^ (x >> 6)) & 0x00CC00CCu;
+    x ^= t ^ (t << 6);
+    t = (x ^ (x >> 12)) & 0x0000F0F0u;
+    return x ^ t ^ (t << 12);
+}
+
 // One exchange step of the 8 x 8 nibble transpose: keep the nibbles whose
 // slot bit t equals this lane's bit t, take the partner's others, moved by
 // 2^t slots (a rotate by sh bits, sh per lane).
