@@ -356,6 +356,14 @@ __device__ __forceinline__ uint32_t quad_lane(uint32_t x) {   // of each quad
     return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), kLane * 0x55, 0xF, 0xF, true));
 }
 
+// The bits of all lanes of a row of 16.
+__device__ __forceinline__ uint32_t or_in_row(uint32_t x) {
+    x |= static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x121, 0xF, 0xF, true));
+    x |= static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x122, 0xF, 0xF, true));
+    x |= static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x124, 0xF, 0xF, true));
+    return x | static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x128, 0xF, 0xF, true));
+}
+
 // The scale of key 4g + kKey and group kC from a lane's share of them (f32; the
 // second word holds the odd ones for D = 256).
 template <int D, int kKey, int kC>
@@ -535,6 +543,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
         __builtin_amdgcn_sched_barrier(0);
         // Weights, each lane its 8 keys of row n.
         Frag p[RT][NS];
+        uint32_t seen = 0;   // bit x: a row of this lane sees key x of its eight (set where not all do)
 #pragma unroll
         for (int rt = 0; rt < RT; rt++) {
 #pragma unroll
@@ -557,6 +566,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
                     const int jj = j + 16 * (x / 4) + 4 * g + x % 4;
                     const bool sees = ok[x / 4] && jj < j1 && (jj < ctx || ((word[rt] >> ((jj - ctx) & 63)) & 1));
                     s[rt][x / 4][x % 4] = sees ? s[rt][x / 4][x % 4] : -__builtin_inff();
+                    seen |= sees ? 1u << x : 0u;
                 }
             }
             float mx = m[rt];
@@ -594,13 +604,14 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
                 pr[u][1] = __builtin_amdgcn_perm(quad_lane<3>(st.vs[u]), quad_lane<2>(st.vs[u]), sel);
             }
         }
-        if (!plain) {   // scales that no one stored may be anything, and weights of 0 do not hide it
+        // The row of a key that none of the 16 RT rows sees need not have been stored: its
+        // scales may be anything, and weights of 0 would hide neither an infinity nor, since
+        // the largest scale sets the others' power of two, a scale far above the others.
+        if (!plain) {
+            seen = or_in_row(seen);
 #pragma unroll
-            for (int x = 0; x < 4; x++) {
-                const int u = x / 2, i = x % 2, jj = j + 16 * u + 4 * g + 2 * i;
-                if (!ok[u] || jj >= j1 || (pr[u][i] & 0x7c00u) == 0x7c00u) pr[u][i] &= 0xffff0000u;
-                if (!ok[u] || jj + 1 >= j1 || (pr[u][i] & 0x7c000000u) == 0x7c000000u) pr[u][i] &= 0x0000ffffu;
-            }
+            for (int x = 0; x < 8; x += 2)
+                pr[x / 4][x / 2 % 2] &= ((seen >> x & 1) ? 0x0000ffffu : 0u) | ((seen >> (x + 1) & 1) ? 0xffff0000u : 0u);
         }
         f16x2 vs[2][2];
 #pragma unroll

@@ -223,6 +223,22 @@ def test_drafted_keys_that_nobody_sees_may_be_unstored(gd, T):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("T", [F32, F16, BF16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bad", [65504.0, -65504.0, -3.0, float("-inf"), float("nan")])
+def test_unstored_drafted_keys_leave_the_others_alone(gd, T, D, bad):
+    """A padded tree: drafted keys 1, 2 and 5 are seen by no row, and their rows hold scales far above the others',
+    negative or infinite ones. The bar follows the values that are seen."""
+    words = [1, 0, 0, 0b1001, 0b11001, 0, 0b1000001]
+    c = Case(gd, [150, 30], [7, 1], 12, 2, D, 16, T, seed=11, words=words + [1])
+    for i in (1, 2, 5):
+        g, p = c.table[0, (143 + i) // 16], (143 + i) % 16
+        for t in (c.cache.k_scales, c.cache.v_scales):
+            t[g, :, p] = bad
+        c.k[0][:, 143 + i] = c.v[0][:, 143 + i] = 0.0   # no row's bar takes it in
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_scales(gd, scale):
     """Means, negative scales, and scores in the hundreds."""
