@@ -583,6 +583,8 @@ def kv_q8_store(cache: KVCacheQ8, k, v, slots, n_tok: int, q=None, q_out=None, n
         rp = _on(i, rope, torch.float32, None, "rope")
         if rope.dim() != 3 or rope.shape[2] != 2:
             raise ValueError("rope must be [n_pos, rot_dim/2, 2]")
+        if rope.numel() == 0:   # its address would be NULL, which asks for no rotation
+            raise ValueError("rope is empty")
         n_pos, rot = rope.shape[0], 2 * rope.shape[1]
     if positions is not None:
         pp = _on(i, positions, torch.int32, n_tok, "positions")
@@ -632,6 +634,8 @@ def attn_decode_q8(q, cache: KVCacheQ8, page_table, kv_lens, q_start, tree_mask,
         table = _on(i, page_table, torch.int32, None, "page_table")
         if page_table.dim() != 2 or page_table.shape[0] != n_seqs:
             raise ValueError(f"page_table must be [{n_seqs}, max_pages], got {tuple(page_table.shape)}")
+        if page_table.numel() == 0:   # its address would be NULL, which stands for no table
+            raise ValueError("page_table is empty")
         max_pages = page_table.shape[1]
     if workspace is None:
         sizes = (n_seqs, n_q, n_heads, cache.n_kv_heads, D, max_q, max_kv_len)

@@ -403,6 +403,8 @@ extern "C" int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_strid
     GD_REQUIRE((n_heads == 0 || stride_ok(q_stride, n_heads, D, dtype)) && stride_ok(k_stride, Hkv, D, dtype) &&
                    stride_ok(v_stride, Hkv, D, dtype),
                GD_ESHAPE, "kv_q8_store: a row stride must cover the token's heads and be a multiple of 16 bytes");
+    GD_REQUIRE(n_heads == 0 || q_out != q || n_tok == 1 || q_stride == n_heads * D, GD_EINVAL,
+               "kv_q8_store: q_out may be q only if q_stride is n_heads * head_dim");
     GD_REQUIRE(aligned(k, 16) && aligned(v, 16) && (n_heads == 0 || (aligned(q, 16) && aligned(q_out, 16))) &&
                    aligned(slots, 8),
                GD_EALIGN, "kv_q8_store: q, k, v and q_out must be 16-byte aligned, slots 8-byte");

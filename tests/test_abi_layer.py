@@ -113,6 +113,13 @@ def test_store_refusals(gd):
     assert store(gd, ref, ks=-128) == SHAPE and store(gd, ref, n=-3) == INVAL
 
 
+def test_store_refuses_rotation_in_place_of_strided_queries(gd):
+    """q_out is contiguous: with q_out at q, the rows of a wider q would be overwritten before they are read."""
+    keep, ref = cache(gd)
+    assert store(gd, ref, q=FAKE, qo=FAKE, n=2, heads=2, qs=2 * 64 + 32) == INVAL
+    assert "q_stride" in gd.lib().gemm_decode_last_error().decode()
+
+
 def test_load_refusals(gd):
     keep, ref = cache(gd)
     L = gd.lib()

@@ -399,6 +399,9 @@ def test_refusals(gd):
     c.page_table = c.page_table[:, :2]
     with pytest.raises(ValueError):
         c.run()
-    c.page_table = c.page_table.contiguous()
+    c.page_table = c.page_table[:, :0].contiguous()
+    with pytest.raises(ValueError, match="empty"):
+        c.run()
+    c.page_table = dev(c.table.astype(np.int32))[:, :2].contiguous()
     with pytest.raises(gd.GemmDecodeError, match="GD_EINVAL"):
         c.run()

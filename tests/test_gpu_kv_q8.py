@@ -266,6 +266,8 @@ def test_refusals(gd):
     with pytest.raises(gd.GemmDecodeError, match="GD_ESHAPE"):
         gd.kv_q8_store(c, k, k, slots, 2, rope=torch.zeros(4, 36, 2, device="cuda"),
                        positions=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="empty"):
+        gd.kv_q8_store(c, k, k, slots, 2, rope=torch.zeros(0, 32, 2, device="cuda"))
     with pytest.raises(TypeError):
         gd.kv_q8_load(c, slots, None, None, 2)
     with pytest.raises(gd.GemmDecodeError, match="GD_ESHAPE"):
