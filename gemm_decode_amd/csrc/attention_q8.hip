@@ -47,6 +47,7 @@
 #include <type_traits>
 
 #include "gd_internal.h"
+#include "gd_quant.h"
 #include "gd_types.h"
 
 namespace {
@@ -364,6 +365,15 @@ __device__ __forceinline__ uint32_t or_in_row(uint32_t x) {
     return x | static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x128, 0xF, 0xF, true));
 }
 
+// The largest v of kPer lanes, 8 or 16, side by side in a row of 16.
+template <int kPer>
+__device__ __forceinline__ float max_of_row(float v) {
+    v = max8(v);
+    if constexpr (kPer == 16)
+        v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, true)));
+    return v;
+}
+
 // The scale of key 4g + kKey and group kC from a lane's share of them (f32; the
 // second word holds the odd ones for D = 256).
 template <int D, int kKey, int kC>
@@ -396,8 +406,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
     typedef f32x4 Joined[R][D / 4 + 1];   // a wave's sums, padded: 16 lanes write one column
     __shared__ union {
         Joined o[kWaves];
-        u32x4 k[kWaves][2][D];   // the K codes of a wave's two tiles
+        struct {
+            u32x4 k[kWaves][2][D];       // the K codes of a wave's two tiles
+            u32x4 q[NS][R][D / 8 + 1];   // query rows as f16, padded: 16 lanes read one column
+        } in;
     } lds;
+    __shared__ float lds_scale[R];
     __shared__ float lds_m[kWaves][R], lds_l[kWaves][R];
     const int Hkv = static_cast<int>(a.c.n_kv_heads);
     // Blocks of rows run slowest: in a ragged batch most of the later ones are empty,
@@ -420,66 +434,85 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
     const int j0 = static_cast<int>(split * a.chunk);
     const int j1 = j0 + static_cast<int>(a.chunk) < len ? j0 + static_cast<int>(a.chunk) : len;
 
+    // The query rows, prepared by all waves together: kPerRow threads to a row, E dims
+    // each. A row past the last repeats the first; what comes of it is not written.
+    constexpr int kPerRow = kThreads / R, E = D / kPerRow;
+    const int row = static_cast<int>(threadIdx.x) / kPerRow, d0 = static_cast<int>(threadIdx.x) % kPerRow * E;
+    typename Vec4<T>::type raw[E / 4];   // as loaded: a conversion here would wait for them
+    {
+        const int r = r0 + row < rows ? r0 + row : r0;
+        const int t = over_group(r, G), h = kvh * G + r - t * G;
+        const T *p = static_cast<const T *>(a.q) + ((sq.row0 + t) * a.n_heads + h) * D + d0;
+#pragma unroll
+        for (int i = 0; i < E / 4; i++) raw[i] = *reinterpret_cast<const typename Vec4<T>::type *>(p + 4 * i);
+    }
+    uint64_t word[RT];      // the drafted keys that the lane's rows see
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int r = r0 + 16 * rt + n < rows ? r0 + 16 * rt + n : r0;
+        const int t = over_group(r, G);
+        word[rt] = a.tree ? a.tree[sq.row0 + t] : (t >= 63 ? ~0ull : (1ull << (t + 1)) - 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
     Step<D> st;
     int j = j0 + kStep * wave;
-    const int last = (j1 - 1) / 16;
+    const int last = (j1 > 0 ? j1 - 1 : 0) / 16;
     const int64_t of_page = a.c.page_size * Hkv * D, of_head = a.c.page_size * kvh * D;
     Place next = {};
     // Keys are loaded before values everywhere, and the scheduler is kept from mixing
     // the two: loads complete in order, and a wait for the keys must not include the
     // values behind them.
-    if (j < j1) {
-        next = place_of<D>(a, b, of_page, of_head, j / 16, last);
-        load_keys<D>(a, next, lane, st);
-        __builtin_amdgcn_sched_barrier(0);
-        load_values<D>(a, next, lane, st);
-        __builtin_amdgcn_sched_barrier(0);
-    }
+    // A wave without keys loads the last tile and does not use it: with as many loads on
+    // every path, the wait for the queries is for them alone.
+    next = place_of<D>(a, b, of_page, of_head, j / 16 < last ? j / 16 : last, last);
+    load_keys<D>(a, next, lane, st);
+    __builtin_amdgcn_sched_barrier(0);
+    load_values<D>(a, next, lane, st);
+    __builtin_amdgcn_sched_barrier(0);
 
-    // The query rows: row r0 + 16 rt + n of this lane, times a power of two that
-    // brings its largest value into [2^13, 2^14).
-    Frag q[RT][C][NS];
-    float scale2[RT];       // from a contraction to a score (times log2 e without a cap)
-    uint64_t word[RT];      // the drafted keys that the row sees
-    f32x4 qx[RT][C][2];
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        const int r = r0 + 16 * rt + n;
-        const bool live = r < rows;
-        const int t = live ? over_group(r, G) : 0, h = kvh * G + (live ? r - t * G : 0);
-        const T *p = static_cast<const T *>(a.q) + ((sq.row0 + t) * a.n_heads + h) * D;
-        word[rt] = a.tree ? a.tree[sq.row0 + t] : (t >= 63 ? ~0ull : (1ull << (t + 1)) - 1);
-#pragma unroll
-        for (int c = 0; c < C; c++)
-#pragma unroll
-            for (int i = 0; i < 2; i++) {   // a row past the last repeats the first and counts as zeros
-                const f32x4 x = load4(p + 32 * c + 16 * (g % 2) + 8 * (g / 2) + 4 * i);
-                qx[rt][c][i] = live ? x : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            }
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
+    // A query row times a power of two that brings its largest value into [2^13, 2^14).
+    {
+        f32x4 qx[E / 4];
         float mx = 0.0f;
 #pragma unroll
-        for (int c = 0; c < C; c++)
+        for (int i = 0; i < E / 4; i++) {
+            qx[i] = __builtin_convertvector(raw[i], f32x4);
 #pragma unroll
-            for (int i = 0; i < 2; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) mx = fmaxf(mx, fabsf(qx[rt][c][i][j]));
-        mx = max_across(mx);
+            for (int x = 0; x < 4; x++) mx = fmaxf(mx, fabsf(qx[i][x]));
+        }
+        mx = max_of_row<kPerRow>(mx);
         const int e = mx > 0.0f && mx <= 3.40282347e38f ? 14 - __builtin_amdgcn_frexp_expf(mx) : 0;
+        if (d0 == 0) lds_scale[row] = ldexpf(a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e, -e);
+        f16x2 hi[E / 2], lo[E / 2];
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float v0 = ldexpf(qx[i / 4][i % 4], e), v1 = ldexpf(qx[i / 4][i % 4 + 1], e);
+            hi[i / 2] = f16x2{static_cast<_Float16>(v0), static_cast<_Float16>(v1)};
+            if constexpr (NS == 2)
+                lo[i / 2] = f16x2{static_cast<_Float16>(v0 - static_cast<float>(hi[i / 2][0])),
+                                  static_cast<_Float16>(v1 - static_cast<float>(hi[i / 2][1]))};
+        }
+        f16x2 *to = reinterpret_cast<f16x2 *>(lds.in.q[0][row]) + d0 / 2;
+#pragma unroll
+        for (int i = 0; i < E / 2; i++) to[i] = hi[i];
+        if constexpr (NS == 2) {
+            to = reinterpret_cast<f16x2 *>(lds.in.q[NS - 1][row]) + d0 / 2;
+#pragma unroll
+            for (int i = 0; i < E / 2; i++) to[i] = lo[i];
+        }
+    }
+    __syncthreads();
+    Frag q[RT][C][NS];
+    float scale2[RT];       // from a contraction to a score (times log2 e without a cap)
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        scale2[rt] = lds_scale[16 * rt + n];
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float v0 = ldexpf(qx[rt][c][i / 4][i % 4], e), v1 = ldexpf(qx[rt][c][i / 4][i % 4 + 1], e);
-                const f16x2 hi = {static_cast<_Float16>(v0), static_cast<_Float16>(v1)};
-                q[rt][c][0].h[i / 2] = hi;
-                if constexpr (NS == 2)
-                    q[rt][c][NS - 1].h[i / 2] = f16x2{static_cast<_Float16>(v0 - static_cast<float>(hi[0])),
-                                                      static_cast<_Float16>(v1 - static_cast<float>(hi[1]))};
-            }
-        scale2[rt] = ldexpf(a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e, -e);
+            for (int i = 0; i < NS; i++)
+                q[rt][c][i].v = __builtin_bit_cast(f16x8, lds.in.q[i][16 * rt + n][4 * c + 2 * (g % 2) + g / 2]);
     }
 
     f32x4 o[RT][VB];   // o[rt][t][i]: dim v_dim(4g + i) + t of row n
@@ -503,7 +536,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
         const bool plain = j + kStep <= (ctx < j1 ? ctx : j1) && ok[0] && ok[1];   // every row sees every key
         if (more) next = place_of<D>(a, b, of_page, of_head, (j + kGroupKeys) / 16, last);
         float s[RT][2][4];
-        turn_keys<D>(st.k, lds.k[wave], lane);
+        turn_keys<D>(st.k, lds.in.k[wave], lane);
 #pragma unroll
         for (int u = 0; u < 2; u++) {
             u32x2 kw[C];
@@ -705,8 +738,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
                     f32x4{o[rt][t][i], o[rt][t + 1][i], o[rt][t + 2][i], o[rt][t + 3][i]} * f;
     }
     __syncthreads();
-    constexpr int kPerRow = kThreads / R;   // threads of a row
-    const int r = threadIdx.x / kPerRow;
+    const int r = row;
     if (r0 + r >= rows) return;
     float mx = lds_m[0][r];
 #pragma unroll
