@@ -120,9 +120,15 @@ struct Place {
     bool ok[2];
 };
 
+// *p, the same for the whole wave and not written by the launch, as a scalar load: a
+// vector load would be waited for with every load before it.
+__device__ __forceinline__ int32_t uniform(const int32_t *p) {
+    return *(const __attribute__((address_space(4))) int32_t *)reinterpret_cast<uintptr_t>(p);
+}
+
 // Page `i` of sequence b, 0 and false if there is none.
 __device__ __forceinline__ int32_t page_of(const AttnArgs &a, int64_t b, int i, bool &ok) {
-    const int32_t page = a.page_table ? a.page_table[b * a.max_pages + i] : static_cast<int32_t>(b);
+    const int32_t page = a.page_table ? uniform(a.page_table + (b * a.max_pages + i)) : static_cast<int32_t>(b);
     ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.n_pages);
     return ok ? page : 0;
 }
@@ -401,7 +407,7 @@ __device__ __forceinline__ void add_scaled(float (&s)[4], f32x4 d, const float (
 // NS = 2: operands in two f16 parts (f32 inputs), NS = 1: in one. A workgroup
 // serves RT tiles of 16 query rows.
 template <typename T, int D, int NS, int RT>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D <= 128 || NS == 1 ? 2 : 1) void attn_q8_kernel(AttnArgs a) {
     constexpr int C = D / 32, VB = D / 16, R = 16 * RT;
     typedef f32x4 Joined[R][D / 4 + 1];   // a wave's sums, padded: 16 lanes write one column
     __shared__ union {
@@ -530,11 +536,14 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
     _Float16 vmul = pow2_f16(15);
     _Float16 vlim = static_cast<_Float16>(0.0f);   // the largest scale that vk was made for
 
-    for (; j < j1; j += kGroupKeys) {
-        const bool more = j + kGroupKeys < j1;
+    // One step; kMore: there is another, whose loads it issues. The last one is a copy of
+    // its own, since a wait for loads counts those behind them, which have to be there on
+    // every path.
+    const auto step = [&](auto more) {
+        constexpr bool kMore = decltype(more)::value;
         const bool ok[2] = {next.ok[0], next.ok[1]};
         const bool plain = j + kStep <= (ctx < j1 ? ctx : j1) && ok[0] && ok[1];   // every row sees every key
-        if (more) next = place_of<D>(a, b, of_page, of_head, (j + kGroupKeys) / 16, last);
+        if constexpr (kMore) next = place_of<D>(a, b, of_page, of_head, (j + kGroupKeys) / 16, last);
         float s[RT][2][4];
         turn_keys<D>(st.k, lds.in.k[wave], lane);
 #pragma unroll
@@ -572,7 +581,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
                 asm volatile("" : "+v"(s[rt][u][0]), "+v"(s[rt][u][1]), "+v"(s[rt][u][2]), "+v"(s[rt][u][3]));
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (more) load_keys<D>(a, next, lane, st);
+        if constexpr (kMore) load_keys<D>(a, next, lane, st);
         __builtin_amdgcn_sched_barrier(0);
         // Weights, each lane its 8 keys of row n.
         Frag p[RT][NS];
@@ -691,7 +700,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
 #pragma unroll
                 for (int w = 0; w < VB / 4; w++) asm volatile("" : "+v"(vx[u][i][w]));
         __builtin_amdgcn_sched_barrier(0);
-        if (more) load_values<D>(a, next, lane, st);
+        if constexpr (kMore) load_values<D>(a, next, lane, st);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < VB; t++) {
@@ -717,7 +726,9 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_q8_kernel(Att
                 }
             }
         }
-    }
+    };
+    for (; j + kGroupKeys < j1; j += kGroupKeys) step(std::true_type{});
+    if (j < j1) step(std::false_type{});
 
     // Join the four waves.
     __syncthreads();   // the K codes are no longer needed by any
