@@ -836,15 +836,19 @@ __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
 }
 
 // Parts per sequence. While there is not a workgroup for every CU at one part each
-// (kCus), as many as give each two or three (kFill), however short they get. Beyond
-// that, parts of no fewer than kMinSteps steps a wave, up to kFine workgroups in all:
-// many of them even out the end of the launch and sequences of different lengths, but
-// each prepares its queries and joins its waves anew. Measured (head dim 128, 32 / 8
-// heads): 32 sequences of 16k to 32k keys 304 us with 2048 workgroups, 287 with 4096,
-// 293 with 6144; 128 sequences of 1k keys 68 us with parts of 2 steps, 61 with 4, 48
-// with 8; 16 of 2k keys (a workgroup for half the CUs) 26 us at 256 workgroups, 21 at
-// 768; 48 of 512 keys (one and a half for each CU) 17 us whole, 20 in two parts.
-constexpr int kCus = 256, kFill = 768, kFine = 4096, kMinSteps = 8;
+// (kCus), as many as give each CU the two that it holds (kFill), however short they get:
+// one that starts when another has ended costs a whole round more. A call with more rows
+// than a block is planned for half as many again (kFillBlocks), since the later blocks
+// are empty in sequences of fewer rows. Beyond that, parts of no fewer than kMinSteps
+// steps a wave, up to kFine workgroups in all: many of them even out the end of the
+// launch and sequences of different lengths, but each prepares its queries and joins its
+// waves anew. Measured (bf16, head dim 128, 32 / 8 heads), planned for 384, 512 and 768:
+// 8 sequences of 2k to 4k keys 20.4, 16.6 and 17.9 us, one of 32k 21.0, 18.0 and 20.9,
+// trees of up to 13 over 2.5k to 5k keys (two blocks) 26.9, 29.6 and 24.6. 128 sequences of
+// 1k keys 50 us with parts of 4 steps, 41 with 8; 48 of 512 keys (one and a half for each
+// CU) 17 us whole, 20 in two parts; 32 sequences of 16k to 32k keys 281 with 4096
+// workgroups or 6144, and 6 % more with 2048.
+constexpr int kCus = 256, kFill = 512, kFillBlocks = 768, kFine = 4096, kMinSteps = 8;
 
 // How the work is cut: rows per workgroup, and keys per part.
 struct Plan {
@@ -861,7 +865,8 @@ Plan plan_of(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_d
     p.row_blocks = (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
     const int64_t groups = n_seqs * n_kv_heads * p.row_blocks;   // at one part each
     const int64_t steps = (max_kv_len + kGroupKeys - 1) / kGroupKeys;
-    const int64_t fill = groups < kCus ? (kFill + groups - 1) / groups : 1, fine = (kFine + groups - 1) / groups;
+    const int64_t most = p.row_blocks > 1 ? kFillBlocks : kFill;
+    const int64_t fill = groups < kCus ? (most + groups - 1) / groups : 1, fine = (kFine + groups - 1) / groups;
     int64_t parts = fine < steps / kMinSteps ? fine : steps / kMinSteps;
     parts = parts > fill ? parts : fill;
     parts = parts < steps ? parts : steps;
