@@ -72,11 +72,14 @@ int page_shift_of(int64_t page_size) {
     return (page_size & (page_size - 1)) == 0 ? __builtin_ctzll(static_cast<uint64_t>(page_size)) : -1;
 }
 
-// E consecutive elements as f32, in one load of 4 E or 2 E bytes.
+// E consecutive elements, in one load of 4 E or 2 E bytes; and as f32.
+template <typename T, int E>
+struct Elements {
+    typedef T type __attribute__((ext_vector_type(E)));
+};
+
 template <int E, typename T>
-__device__ __forceinline__ void load_n(const T *p, f32x4 (&x)[E / 4]) {
-    typedef T Vec __attribute__((ext_vector_type(E)));
-    const Vec v = *reinterpret_cast<const Vec *>(p);
+__device__ __forceinline__ void widen(typename Elements<T, E>::type v, f32x4 (&x)[E / 4]) {
 #pragma unroll
     for (int i = 0; i < E; i++) x[i / 4][i % 4] = static_cast<float>(v[i]);
 }
@@ -130,22 +133,45 @@ __device__ __forceinline__ void turn(f32x4 (&x)[E / 4], const f32x4 (&o)[E / 4],
 // A workgroup serves one token (or its rows blockIdx.y, blockIdx.y + gridDim.y, ...
 // of kRows at a time): D/E threads per head row, E dims each, so that a thread has the
 // same dims in every row it takes and its angles are loaded once. Rows in the order q
-// heads, k heads, v heads, kBatch of them loaded before any is used. A row never
-// leaves its wave, so q_out may be q itself: a wave reads a row before it writes it.
-// 8191 tokens of 32 / 8 heads of 128 in bf16: 44 us, 4.3 TB/s, near memory's rate with
-// the quantizer's arithmetic beside it (51 us with 1 or 3 rows loaded ahead, 55 with
-// four elements a thread); one token: 3.8 us, bound by its chain of loads.
+// heads, k heads, v heads; a batch of them is loaded while the one before it is turned and
+// quantized, the first while the token's slot, position and angles are looked up. A row
+// never leaves its wave and the batches differ in their rows, so q_out may be q itself.
+// 8191 tokens of 32 / 8 heads of 128 in bf16: 44 us, 4.3 TB/s (35 with the inputs still in
+// the last cache), near memory's rate with the quantizer's arithmetic beside it (36 with
+// loads behind the look-up and between the batches, 37 with batches of two rows, 53 at 80
+// registers; of f32, four elements a thread, 2000 tokens 17.4 us with one row, 16.7 with
+// two); one token: 2.9 us, bound by its chain of loads.
 template <typename T, int D, int E>
 __global__ __launch_bounds__(kThreads) void kv_q8_store_kernel(StoreArgs a) {
-    constexpr int kLanes = D / E, kRows = kThreads / kLanes, kBatch = 2;
+    constexpr int kLanes = D / E, kRows = kThreads / kLanes, kBatch = E == 4 ? 2 : 1;
     const int64_t tok = blockIdx.x;
     const int Hkv = static_cast<int>(a.c.n_kv_heads), Hq = a.n_heads;
     const int d0 = static_cast<int>(threadIdx.x % kLanes) * E;
-    const int64_t slot = a.slots[tok];
-    const bool live = slot >= 0 && slot < a.c.n_pages * a.c.page_size;
     const bool turned = a.rope && d0 < a.rot;
     const int half = a.rot / 2;
     const bool first = d0 < half;
+    const int partner = turned && !a.interleaved ? (first ? half : -half) : 0;   // where a dim's partner lies
+    const T *q = static_cast<const T *>(a.q) + tok * a.q_stride + d0;
+    const T *k = static_cast<const T *>(a.k) + tok * a.k_stride + d0;
+    const T *v = static_cast<const T *>(a.v) + tok * a.v_stride + d0;
+    typedef typename Elements<T, E>::type Vec;
+    Vec x_in[kBatch] = {}, o_in[kBatch] = {};
+    const int step = kRows * static_cast<int>(gridDim.y);
+    const auto load = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+            const int r = r0 + i * step;
+            if (r >= Hq + 2 * Hkv) break;
+            const T *p = r < Hq ? q + r * D : r < Hq + Hkv ? k + (r - Hq) * D : v + (r - Hq - Hkv) * D;
+            x_in[i] = *reinterpret_cast<const Vec *>(p);
+            if (partner != 0 && r < Hq + Hkv) o_in[i] = *reinterpret_cast<const Vec *>(p + partner);
+        }
+    };
+    int r0 = kRows * static_cast<int>(blockIdx.y) + static_cast<int>(threadIdx.x) / kLanes;
+    load(r0);   // on its way while the slot, the position and its angles are looked up
+    __builtin_amdgcn_sched_barrier(0);
+    const int64_t slot = a.slots[tok];
+    const bool live = slot >= 0 && slot < a.c.n_pages * a.c.page_size;
     float c[E] = {}, s[E] = {};
     if (a.rope) {
         const int64_t pos = a.positions[tok];
@@ -161,25 +187,15 @@ __global__ __launch_bounds__(kThreads) void kv_q8_store_kernel(StoreArgs a) {
             }
         }
     }
-    const int partner = turned && !a.interleaved ? (first ? half : -half) : 0;   // where a dim's partner lies
-    const T *q = static_cast<const T *>(a.q) + tok * a.q_stride + d0;
-    const T *k = static_cast<const T *>(a.k) + tok * a.k_stride + d0;
-    const T *v = static_cast<const T *>(a.v) + tok * a.v_stride + d0;
     T *qo = static_cast<T *>(a.q_out) + tok * Hq * D + d0;
     const Slot at(live ? slot : 0, a.c.page_size, a.page_shift);
     const int rows = Hq + (live ? 2 * Hkv : 0);
-    const int step = kRows * static_cast<int>(gridDim.y);
-    for (int r0 = kRows * static_cast<int>(blockIdx.y) + static_cast<int>(threadIdx.x) / kLanes; r0 < rows;
-         r0 += kBatch * step) {
+    for (int next; r0 < rows; r0 = next) {
         f32x4 x[kBatch][E / 4], o[kBatch][E / 4];
 #pragma unroll
-        for (int i = 0; i < kBatch; i++) {
-            const int r = r0 + i * step;
-            if (r >= rows) break;
-            const T *p = r < Hq ? q + r * D : r < Hq + Hkv ? k + (r - Hq) * D : v + (r - Hq - Hkv) * D;
-            load_n<E>(p, x[i]);
-            if (partner != 0 && r < Hq + Hkv) load_n<E>(p + partner, o[i]);
-        }
+        for (int i = 0; i < kBatch; i++) widen<E, T>(x_in[i], x[i]), widen<E, T>(o_in[i], o[i]);
+        next = r0 + kBatch * step;
+        load(next);
 #pragma unroll
         for (int i = 0; i < kBatch; i++) {
             const int r = r0 + i * step;

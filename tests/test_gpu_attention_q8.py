@@ -255,9 +255,10 @@ def test_query_range(gd, T, top):
     c.check(c.run(scale=0.5 / top), scale=0.5 / top)
 
 
-def test_value_scales_of_any_size(gd):
+@pytest.mark.parametrize("T,D", [(F32, 64), (BF16, 64), (BF16, 128), (F32, 256)])
+def test_value_scales_of_any_size(gd, T, D):
     """Value scales from f16's smallest to its largest, side by side: the bar follows the largest value seen."""
-    c = Case(gd, [160], [1], 4, 2, 64, 16, seed=6)
+    c = Case(gd, [160], [1], 4, 2, D, 16, T, seed=6)
     rng = np.random.default_rng(1)
     for lo, hi in ((2.0 ** -24, 2.0 ** -20), (6e4, 65504.0), (2.0 ** -24, 65504.0)):
         s = np.exp(rng.uniform(np.log(lo), np.log(hi), c.scales[1].shape)).astype(np.float16)
