@@ -23,13 +23,28 @@ using namespace gd;
 constexpr int kThreads = 256;
 constexpr int64_t kMaxThreads = (INT64_C(1) << 32) - 1;   // of one launch
 
-// h = x + residual of four elements, as stored; both terms are read before h
-// is written, so h may overwrite either.
-template <typename T>
-__device__ __forceinline__ f32x4 load_h(const T *x, const T *res, int64_t e4) {
-    f32x4 v = load4(x + 4 * e4);
-    if (res) v = round_to<T>(v + load4(res + 4 * e4));
-    return v;
+// h = x + residual of P groups of four elements side by side, as stored; both terms are
+// read before h is written, so h may overwrite either.
+template <int P, typename T>
+__device__ __forceinline__ void load_groups(const T *x, const T *res, int64_t e4, f32x4 *h) {
+    typedef T Vec __attribute__((ext_vector_type(4 * P)));
+    typedef float Wide __attribute__((ext_vector_type(4 * P)));
+    Wide v = __builtin_convertvector(*reinterpret_cast<const Vec *>(x + 4 * e4), Wide);
+    if (res) {
+        v += __builtin_convertvector(*reinterpret_cast<const Vec *>(res + 4 * e4), Wide);
+        v = __builtin_convertvector(__builtin_convertvector(v, Vec), Wide);
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * P; i++) h[i / 4][i % 4] = v[i];
+}
+
+template <int P, typename T>
+__device__ __forceinline__ void store_groups(T *x, int64_t e4, const f32x4 *h) {
+    typedef T Vec __attribute__((ext_vector_type(4 * P)));
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < 4 * P; i++) v[i] = static_cast<T>(h[i / 4][i % 4]);
+    *reinterpret_cast<Vec *>(x + 4 * e4) = v;
 }
 
 __device__ __forceinline__ double square4(f32x4 h) {
@@ -88,9 +103,9 @@ __device__ __forceinline__ bool f16_doubt(float t) {
     return !(t >= 6.2e-5f && t <= 65000.0f) || (dropped >= 0x1000u - 4 && dropped <= 0x1000u + 4);   // normal in f16
 }
 
-__device__ __forceinline__ double max8d(double v) {   // max over the eight lanes of a block
+__device__ __forceinline__ double max4d(double v) {   // max over the four lanes of a block
 #pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o));
+    for (int o = 2; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o));
     return v;
 }
 
@@ -102,6 +117,19 @@ __device__ __forceinline__ double rsqrt_f64(double x) {
     for (int i = 0; i < 2; i++) y = y * __builtin_fma(-0.5 * x * y, y, 1.5);
     return y;
 }
+
+// The 4 x 4 byte transpose among four lanes: lane k holds byte k of every lane.
+struct ByteTranspose {
+    uint32_t one, two;   // what the exchanges with the lanes k ^ 1 and k ^ 2 keep
+    __device__ __forceinline__ explicit ByteTranspose(int k)
+        : one(k % 2 ? 0x03070105u : 0x06020400u), two(k / 2 ? 0x03020706u : 0x05040100u) {}
+    __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+        uint32_t p = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0xB1, 0xF, 0xF, false));
+        x = __builtin_amdgcn_perm(p, x, one);
+        p = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x4E, 0xF, 0xF, false));
+        return __builtin_amdgcn_perm(p, x, two);
+    }
+};
 
 // Sum (and max) over a row's waves; every thread gets them.
 template <int kWaves, bool kMax>
@@ -127,12 +155,14 @@ __device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*
 }
 
 // W waves per row, and a workgroup per row (W = 1: four rows). Thread t of a row holds
-// float4s t, t + 64 W, ... of it, the first R of them in registers (rows of up to 256 W R
-// elements are read once);
-// what is past them is read again in the second pass, from h_out if that is written
-// (it may overwrite an input), each thread reading back its own. 4099 rows of 4096 in
-// bf16: 33 us, 3.6 TB/s, bound by memory with the row's sum between its reads and its
-// writes; one row: 3.6 us, bound by the chain load, sum, barrier, codes, store.
+// pairs of float4s t, t + 64 W, ... of it, R float4s of them in registers (rows of up to
+// 256 W R elements are read once); what is past them is read again in the second pass,
+// from h_out if that is written (it may overwrite an input), each thread reading back its
+// own. A pair is one load of a 16-bit type, and four lanes make a block of 32 (one float4
+// a thread and eight lanes: 4099 rows of 4096 in bf16 30.5 us to q8_0 and 33.8 to planes,
+// where this takes 26.6 and 30.8). That is 4.5 TB/s, bound by memory with the row's sum
+// between its reads and its writes; one row: 3.3 us, bound by the chain load, sum,
+// barrier, codes, store.
 template <typename T, int R, int W, bool kTernary>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_quant_kernel(const T *x, const T *res, const float *__restrict__ weight,
                                                                T *h_out, void *__restrict__ out,
@@ -147,76 +177,107 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_quant_kernel(co
     x += row * K;
     if (res) res += row * K;
     if (h_out) h_out += row * K;
+    // Groups of four elements, in pairs of neighbours: pair i / 2 of the thread, i even.
+    const auto group_of = [&](int i) { return i * kT + 2 * tid; };
     f32x4 h[R], w[R];
     double ss = 0.0, amax = 0.0;
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-        const int e4 = i * kT + tid;
-        const int at = e4 < nq ? e4 : nq - 1;   // clamped: issued, not used
-        h[i] = load_h(x, res, at);
-        w[i] = load4(weight + 4 * at);
+    for (int i = 0; i < R; i += 2) {
+        const int e4 = group_of(i);
+        const int at = e4 < nq ? e4 : nq - 2;   // clamped: issued, not used
+        load_groups<2>(x, res, at, h + i);
+        load_groups<2, float>(weight, nullptr, at, w + i);
     }
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-        const int e4 = i * kT + tid;
+    for (int i = 0; i < R; i += 2) {
+        const int e4 = group_of(i);
         if (e4 < nq) {
-            if (h_out) store4(h_out + 4 * static_cast<int64_t>(e4), h[i]);
-            ss += square4(h[i]);
-            if (kTernary) top = fmaxf(top, Products(h[i], w[i]).absmax());
+            if (h_out) store_groups<2>(h_out, e4, h + i);
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                ss += square4(h[i + j]);
+                if (kTernary) top = fmaxf(top, Products(h[i + j], w[i + j]).absmax());
+            }
         }
     }
     if constexpr (kTernary) {   // the largest product in f64: among those whose f32 rounding is the largest
 #pragma unroll
         for (int i = 0; i < R; i++) {
-            const int e4 = i * kT + tid;
             const Products pr(h[i], w[i]);
-            if (e4 < nq && (pr.absmax() == top || !in_range(top))) amax = fmax(amax, pr.exact_absmax());
+            if (group_of(i - i % 2) < nq && (pr.absmax() == top || !in_range(top))) amax = fmax(amax, pr.exact_absmax());
         }
     }
-    for (int e4 = R * kT + tid; e4 < nq; e4 += kT) {
-        const f32x4 v = load_h(x, res, e4);
-        if (h_out) store4(h_out + 4 * static_cast<int64_t>(e4), v);
-        ss += square4(v);
-        if (kTernary) amax = fmax(amax, Products(v, load4(weight + 4 * e4)).exact_absmax());
+    for (int e4 = R * kT + 2 * tid; e4 < nq; e4 += 2 * kT) {
+        f32x4 v[2];
+        load_groups<2>(x, res, e4, v);
+        if (h_out) store_groups<2>(h_out, e4, v);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            ss += square4(v[j]);
+            if (kTernary) amax = fmax(amax, Products(v[j], load4(weight + 4 * (e4 + j))).exact_absmax());
+        }
     }
     group_sum_max<W, kTernary>(ss, amax, red);
     const double rstd127 = rsqrt_f64(ss / static_cast<double>(K) + static_cast<double>(eps)) * (1.0 / 127.0);
     const float r32 = static_cast<float>(rstd127);
     const float row_top = static_cast<float>(amax), row_inv = row_top > 0.0f ? recip127(row_top) : 0.0f;
     if (kTernary && tid == 0) x_scale[row] = amax > 0.0 ? static_cast<float>(amax * rstd127) : 0.0f;
-    const int lane = threadIdx.x % 64, k8 = lane % 8;
-    const NibbleTranspose tr(k8);
+    const int k4 = threadIdx.x % 4;
+    const ByteTranspose tr(k4);
     const int64_t groups = K / 32;
-    const auto finish = [&](const Products &pr, int e4) {   // whole groups of eight lanes come here together
-        if constexpr (kTernary) {
-            bool doubt = !in_range(row_top);
-            uint32_t packed = pr.codes(row_inv, doubt);
-            if (__any(doubt)) packed = pr.exact_codes(factor_of(amax));
-            static_cast<uint32_t *>(out)[(row * 8 + k8) * groups + e4 / 8] = tr(bits_to_nibbles(packed));
-        } else {
-            const float a = max8(pr.absmax());
-            float d32 = a * r32;
-            bool doubt = !in_range(a) || f16_doubt(d32);
-            uint32_t packed = pr.codes(a > 0.0f ? recip127(a) : 0.0f, doubt);
-            if (__any(doubt)) {
-                const double exact = max8d(pr.exact_absmax());
-                packed = pr.exact_codes(factor_of(exact));
-                d32 = exact > 0.0 ? static_cast<float>(exact * rstd127) : 0.0f;
-            }
-            uint16_t *o = static_cast<uint16_t *>(out) + (row * groups + e4 / 8) * 17;   // 34 bytes = 17 halves
-            o[1 + 2 * k8] = static_cast<uint16_t>(packed & 0xffffu);
-            o[2 + 2 * k8] = static_cast<uint16_t>(packed >> 16);
-            if (k8 == 0) o[0] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(d32));
+    const auto planes = [&](const Products &p0, const Products &p1, int e4) {   // four lanes to 32 elements
+        bool doubt = !in_range(row_top);
+        uint32_t lo = p0.codes(row_inv, doubt), hi = p1.codes(row_inv, doubt);
+        if (__any(doubt)) {
+            const double factor = factor_of(amax);
+            lo = p0.exact_codes(factor);
+            hi = p1.exact_codes(factor);
         }
+        lo = bits_to_nibbles(lo);
+        hi = bits_to_nibbles(hi);
+        // A byte of each plane: the even planes', the odd planes'.
+        uint32_t *o = static_cast<uint32_t *>(out) + (row * 8 + 2 * k4) * groups + e4 / 8;
+        o[0] = tr((lo & 0x0F0F0F0Fu) | ((hi & 0x0F0F0F0Fu) << 4));
+        o[groups] = tr(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u));
+    };
+    const auto block = [&](const Products &p0, const Products &p1, int e4) {   // likewise
+        const float a = max4(fmaxf(p0.absmax(), p1.absmax()));
+        float d32 = a * r32;
+        bool doubt = !in_range(a) || f16_doubt(d32);
+        const float inv = a > 0.0f ? recip127(a) : 0.0f;
+        uint32_t lo = p0.codes(inv, doubt), hi = p1.codes(inv, doubt);
+        if (__any(doubt)) {
+            const double exact = max4d(fmax(p0.exact_absmax(), p1.exact_absmax())), factor = factor_of(exact);
+            lo = p0.exact_codes(factor);
+            hi = p1.exact_codes(factor);
+            d32 = exact > 0.0 ? static_cast<float>(exact * rstd127) : 0.0f;
+        }
+        uint16_t *o = static_cast<uint16_t *>(out) + (row * groups + e4 / 8) * 17;   // 34 bytes = 17 halves
+        typedef uint32_t Words __attribute__((ext_vector_type(2), aligned(2)));
+        *reinterpret_cast<Words *>(o + 1 + 4 * k4) = Words{lo, hi};
+        if (k4 == 0) o[0] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(d32));
     };
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-        const int e4 = i * kT + tid;
-        if (e4 < nq) finish(Products(h[i], w[i]), e4);
+    for (int i = 0; i < R; i += 2) {
+        const int e4 = group_of(i);
+        if (e4 >= nq) continue;
+        if constexpr (kTernary)
+            planes(Products(h[i], w[i]), Products(h[i + 1], w[i + 1]), e4);
+        else
+            block(Products(h[i], w[i]), Products(h[i + 1], w[i + 1]), e4);
     }
-    for (int e4 = R * kT + tid; e4 < nq; e4 += kT)
-        finish(Products(h_out ? load4(h_out + 4 * static_cast<int64_t>(e4)) : load_h(x, res, e4), load4(weight + 4 * e4)), e4);
+    for (int e4 = R * kT + 2 * tid; e4 < nq; e4 += 2 * kT) {   // past the registers, read once more
+        if (h_out)
+            load_groups<2, T>(h_out, nullptr, e4, h);
+        else
+            load_groups<2>(x, res, e4, h);
+        load_groups<2, float>(weight, nullptr, e4, w);
+        if constexpr (kTernary)
+            planes(Products(h[0], w[0]), Products(h[1], w[1]), e4);
+        else
+            block(Products(h[0], w[0]), Products(h[1], w[1]), e4);
+    }
 }
 
 // ------------------------------------------------------------- readers
