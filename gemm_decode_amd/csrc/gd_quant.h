@@ -143,4 +143,19 @@ struct NibbleTranspose {
     }
 };
 
+// The 4 x 4 byte transpose among four lanes, its own inverse: lane k holds byte k of
+// every lane. With a byte of each even plane in one word and of each odd one in another,
+// lane k comes to hold the words of the planes 2 k and 2 k + 1.
+struct ByteTranspose {
+    uint32_t one, two;   // what the exchanges with the lanes k ^ 1 and k ^ 2 keep
+    __device__ __forceinline__ explicit ByteTranspose(int k)
+        : one(k % 2 ? 0x03070105u : 0x06020400u), two(k / 2 ? 0x03020706u : 0x05040100u) {}
+    __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+        uint32_t p = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0xB1, 0xF, 0xF, false));
+        x = __builtin_amdgcn_perm(p, x, one);
+        p = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x4E, 0xF, 0xF, false));
+        return __builtin_amdgcn_perm(p, x, two);
+    }
+};
+
 }  // namespace gd

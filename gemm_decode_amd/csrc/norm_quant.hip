@@ -118,19 +118,6 @@ __device__ __forceinline__ double rsqrt_f64(double x) {
     return y;
 }
 
-// The 4 x 4 byte transpose among four lanes: lane k holds byte k of every lane.
-struct ByteTranspose {
-    uint32_t one, two;   // what the exchanges with the lanes k ^ 1 and k ^ 2 keep
-    __device__ __forceinline__ explicit ByteTranspose(int k)
-        : one(k % 2 ? 0x03070105u : 0x06020400u), two(k / 2 ? 0x03020706u : 0x05040100u) {}
-    __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
-        uint32_t p = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0xB1, 0xF, 0xF, false));
-        x = __builtin_amdgcn_perm(p, x, one);
-        p = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x4E, 0xF, 0xF, false));
-        return __builtin_amdgcn_perm(p, x, two);
-    }
-};
-
 // Sum (and max) over a row's waves; every thread gets them.
 template <int kWaves, bool kMax>
 __device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*red)[2]) {
@@ -281,41 +268,62 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_quant_kernel(co
 }
 
 // ------------------------------------------------------------- readers
-// Four elements per thread: code * scale, one f32 product, rounded to T. Bound by
-// memory: 16.8 M values from q8_0 blocks to f32 in 13.6 us, 6.2 TB/s.
+// code * scale, one f32 product, rounded to T: of the four codes in a word, or eight in
+// two. A thread has 16 bytes to write: eight elements of a 16-bit type (four: 4096 rows of
+// 4096 in bf16 10.3 us from q8_0 and 12.5 from planes, where these take 8.5 and 10.0),
+// four of f32 (eight, as two stores: 2048 rows of 6912 13.5 and 14.9, where these take
+// 11.8 and 13.5). Bound by memory: 16.8 M values from q8_0 to f32 in 13.6 us, 6.2 TB/s.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void q8_0_dequantize_kernel(const uint16_t *__restrict__ a, T *__restrict__ y,
-                                                                   int64_t quads) {
-    const int64_t gid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (gid >= quads) return;
-    const uint16_t *b = a + (gid / 8) * 17;
-    const int k8 = static_cast<int>(gid % 8);
-    const float d = static_cast<float>(__builtin_bit_cast(_Float16, b[0]));
-    const uint32_t lo = b[1 + 2 * k8], hi = b[2 + 2 * k8];
-    const f32x4 c = {static_cast<float>(static_cast<int8_t>(lo)), static_cast<float>(static_cast<int8_t>(lo >> 8)),
-                     static_cast<float>(static_cast<int8_t>(hi)), static_cast<float>(static_cast<int8_t>(hi >> 8))};
-    store4(y + 4 * gid, c * d);
+constexpr int kWords = 4 / sizeof(T);   // of codes, a thread
+template <typename T>
+__device__ __forceinline__ void store_codes(T *y, int64_t unit, const uint32_t *codes, float d) {
+    f32x4 v[kWords<T>];
+#pragma unroll
+    for (int j = 0; j < 4 * kWords<T>; j++)
+        v[j / 4][j % 4] = static_cast<float>(static_cast<int8_t>(codes[j / 4] >> (8 * (j % 4)))) * d;
+    store_groups<kWords<T>>(y, kWords<T> * unit, v);
 }
 
-// The same from bit planes: lane k8 of a block's eight loads plane k8's word, and the
-// norm's transpose, taken back, gives it its four codes (4096 rows of 4096 to bf16: 12.8 us,
-// 3.9 TB/s; with eight loads a lane, each word by all eight, 17.6).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void q8_0_dequantize_kernel(const uint16_t *__restrict__ a, T *__restrict__ y,
+                                                                   int64_t units) {
+    constexpr int kPer = 8 / kWords<T>;   // threads of a block
+    const int64_t gid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (gid >= units) return;
+    const uint16_t *b = a + (gid / kPer) * 17;
+    typedef uint32_t Word __attribute__((aligned(2)));
+    uint32_t codes[kWords<T>];
+#pragma unroll
+    for (int i = 0; i < kWords<T>; i++)
+        codes[i] = reinterpret_cast<const Word *>(b + 1)[kWords<T> * (gid % kPer) + i];
+    store_codes(y, gid, codes, static_cast<float>(__builtin_bit_cast(_Float16, b[0])));
+}
+
+// Eight elements: lane k of a block's four loads the words of the planes 2 k and 2 k + 1,
+// and the norm's transpose, taken back, gives it its codes. Four: lane k of eight loads
+// plane k's word, and nibbles are transposed.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ternary_dequantize_kernel(const uint32_t *__restrict__ planes,
                                                                       const float *__restrict__ x_scale,
-                                                                      T *__restrict__ y, int64_t K, int64_t quads) {
+                                                                      T *__restrict__ y, int64_t K, int64_t units) {
+    constexpr int kPer = 8 / kWords<T>;
     const int64_t gid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (gid >= quads) return;   // whole groups of eight lanes
-    const uint32_t q = static_cast<uint32_t>(K / 4), row = static_cast<uint32_t>(gid) / q, e4 = static_cast<uint32_t>(gid) % q;
+    if (gid >= units) return;   // whole blocks
+    const uint32_t q = static_cast<uint32_t>(K / (4 * kWords<T>));
+    const uint32_t row = static_cast<uint32_t>(gid) / q, at = static_cast<uint32_t>(gid) % q;
     const int64_t W = K / 32;
-    const int k8 = static_cast<int>(e4 % 8);
-    const uint32_t n = planes[(static_cast<int64_t>(row) * 8 + k8) * W + e4 / 8];
-    const uint32_t c = nibbles_to_bits(NibbleTranspose(k8)(n));   // byte j: element j's code
-    const float s = x_scale[row];
-    f32x4 v;
-#pragma unroll
-    for (int j = 0; j < 4; j++) v[j] = static_cast<float>(static_cast<int8_t>(c >> (8 * j))) * s;
-    store4(y + 4 * gid, v);
+    const int k = static_cast<int>(at % kPer);
+    const uint32_t *p = planes + (static_cast<int64_t>(row) * 8 + kWords<T> * k) * W + at / kPer;
+    uint32_t codes[kWords<T>];
+    if constexpr (kWords<T> == 1) {
+        codes[0] = nibbles_to_bits(NibbleTranspose(k)(p[0]));
+    } else {
+        const ByteTranspose tr(k);
+        const uint32_t even = tr(p[0]), odd = tr(p[W]);   // a byte of each even plane, of each odd one
+        codes[0] = nibbles_to_bits((even & 0x0F0F0F0Fu) | ((odd & 0x0F0F0F0Fu) << 4));
+        codes[1] = nibbles_to_bits(((even >> 4) & 0x0F0F0F0Fu) | (odd & 0xF0F0F0F0u));
+    }
+    store_codes(y, gid, codes, x_scale[row]);
 }
 
 int check_norm(const char *name, const void *x, const void *residual, const float *weight, const void *h_out, int64_t n,
@@ -399,11 +407,12 @@ extern "C" int q8_0_dequantize(const void *a_q8, void *y, int64_t n, int64_t K, 
     int st = check_reader("q8_0_dequantize", a_q8, y, n, K, dtype, &quads);
     if (st) return st;
     GD_REQUIRE(aligned(a_q8, 2), GD_EALIGN, "q8_0_dequantize: a_q8 must be 2-byte aligned");
-    const dim3 grid(static_cast<uint32_t>((quads + kThreads - 1) / kThreads));
     dispatch_dtype(dtype, [&](auto t) {
         using T = decltype(t);
+        const int64_t units = quads / kWords<T>;
+        const dim3 grid(static_cast<uint32_t>((units + kThreads - 1) / kThreads));
         hipLaunchKernelGGL((q8_0_dequantize_kernel<T>), grid, dim3(kThreads), 0, as_stream(stream),
-                           static_cast<const uint16_t *>(a_q8), static_cast<T *>(y), quads);
+                           static_cast<const uint16_t *>(a_q8), static_cast<T *>(y), units);
     });
     return check_launch("q8_0_dequantize");
 }
@@ -416,11 +425,12 @@ extern "C" int ternary_dequantize_act(const uint32_t *planes, const float *x_sca
     GD_REQUIRE(x_scale, GD_EINVAL, "ternary_dequantize_act: null pointer");
     GD_REQUIRE(aligned(planes, 4) && aligned(x_scale, 4), GD_EALIGN,
                "ternary_dequantize_act: planes and x_scale must be 4-byte aligned");
-    const dim3 grid(static_cast<uint32_t>((quads + kThreads - 1) / kThreads));
     dispatch_dtype(dtype, [&](auto t) {
         using T = decltype(t);
+        const int64_t units = quads / kWords<T>;
+        const dim3 grid(static_cast<uint32_t>((units + kThreads - 1) / kThreads));
         hipLaunchKernelGGL((ternary_dequantize_kernel<T>), grid, dim3(kThreads), 0, as_stream(stream), planes, x_scale,
-                           static_cast<T *>(y), K, quads);
+                           static_cast<T *>(y), K, units);
     });
     return check_launch("ternary_dequantize_act");
 }
