@@ -30,10 +30,17 @@
 // and are handed round by DPP.
 //
 // What bounds it. 32 sequences of 16k to 32k keys (32 / 8 heads, head dim 128, bf16,
-// 1.75 GB of cache): 281 us, 6.2 TB/s, 90 % of what a streaming read reaches; bound by
-// memory. Few keys (4096 of one sequence, f32: 7.9 us) are bound by the chain of
-// dependent loads before the first product, many rows (64 tokens of four sequences, 172
+// 1.75 GB of cache): 280 us, 6.2 TB/s, 91 % of what a streaming read reaches; bound by
+// memory. Few keys (4096 of one sequence, f32: 6.6 us) are bound by the chain of
+// dependent loads before the first product, many rows (64 tokens of four sequences, 200
 // TFLOP/s) by vector instructions, some 590 for 32 keys and 32 rows.
+//
+// Waits. Loads complete in order and a wait counts those behind the one it is for, so a
+// wait is only as exact as that count is the same on every path: loads stand outside
+// conditions, the last step is compiled apart, queries go out before keys, keys before
+// values, and page numbers come by scalar loads. Without that each step waited for all
+// of the next one's keys (32 sequences 286 us, f32 of 8k to 16k keys 205 where it is
+// 172, 64 tokens of four 94).
 //
 // Precision. Codes are whole numbers below 2^8, exact in f16. f32 inputs: q (as
 // a power of two times its row) and the weights are split into two f16 parts, 22
@@ -76,7 +83,7 @@ struct AttnArgs {
     int64_t max_pages, n_seqs, n_q, n_heads, max_q, max_kv_len;
     int64_t chunk;         // keys per part, a multiple of kGroupKeys
     int32_t splits;        // parts of the longest sequence
-    int32_t row_block0;    // the launch's first block of 16 RT rows
+    int32_t row_block0, row_blocks;   // the launch's first block of 16 RT rows, and how many
     uint32_t page_magic;   // tile / (page_size / 16) = tile * page_magic >> page_shift
     int32_t page_shift, page_tiles;   // page_size / 16
     float scale, softcap;
@@ -420,13 +427,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 || NS == 1 ? 2 : 1) void attn_q8
     __shared__ float lds_scale[R];
     __shared__ float lds_m[kWaves][R], lds_l[kWaves][R];
     const int Hkv = static_cast<int>(a.c.n_kv_heads);
-    // Blocks of rows run slowest: in a ragged batch most of the later ones are empty,
-    // and empty workgroups between the others leave CUs idle (48 us against 33 for
-    // five trees of up to 13 tokens).
+    // A sequence's blocks of rows side by side: they read the same keys (64 drafted tokens
+    // of four sequences 86.5 us with blocks slowest, 84.5 so).
     const int kvh = blockIdx.x, split = blockIdx.y;
-    const int block = static_cast<int>(blockIdx.z / static_cast<uint32_t>(a.n_seqs));
-    const int64_t b = blockIdx.z % static_cast<uint32_t>(a.n_seqs);
-    const int r0 = (a.row_block0 + block) * R;
+    const uint32_t blocks = static_cast<uint32_t>(a.row_blocks);
+    const int64_t b = blockIdx.z / blocks;
+    const int r0 = (a.row_block0 + static_cast<int>(blockIdx.z % blocks)) * R;
     const Seq sq(a, b);
     const int G = static_cast<int>(a.n_heads) / Hkv;
     const int rows = sq.rows * G;   // of this KV head
@@ -690,18 +696,6 @@ __global__ __launch_bounds__(kThreads, D <= 128 || NS == 1 ? 2 : 1) void attn_q8
             for (int i = 0; i < D / 64; i++) biased[i] = st.v[u][i] ^ 0x80808080u;
             spread_values<D>(biased, vx[u]);
         }
-        // The next values are loaded as soon as this step's have left their registers, not
-        // behind the products (8 tokens of 16 sequences over 8k keys 75 -> 72 us, 48
-        // sequences of 512 keys 17.0 -> 16.2; the keys likewise before the scores: no gain).
-#pragma unroll
-        for (int u = 0; u < 2; u++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int w = 0; w < VB / 4; w++) asm volatile("" : "+v"(vx[u][i][w]));
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (kMore) load_values<D>(a, next, lane, st);
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < VB; t++) {
             // byte t of two keys as (code + 128) 2^-24 (f16's smallest steps), times 2^14, less 2^-3: code 2^-10
@@ -726,6 +720,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 || NS == 1 ? 2 : 1) void attn_q8
                 }
             }
         }
+        // Behind the products, in registers that they have left (before them: f32 of 8k to
+        // 16k keys 182 us where this takes 172; 8 tokens of 16 sequences 62 and 62.5).
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kMore) load_values<D>(a, next, lane, st);
+        __builtin_amdgcn_sched_barrier(0);
     };
     for (; j + kGroupKeys < j1; j += kGroupKeys) step(std::true_type{});
     if (j < j1) step(std::false_type{});
@@ -846,7 +845,7 @@ __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
 // 8 sequences of 2k to 4k keys 20.4, 16.6 and 17.9 us, one of 32k 21.0, 18.0 and 20.9,
 // trees of up to 13 over 2.5k to 5k keys (two blocks) 26.9, 29.6 and 24.6. 128 sequences of
 // 1k keys 50 us with parts of 4 steps, 41 with 8; 48 of 512 keys (one and a half for each
-// CU) 17 us whole, 20 in two parts; 32 sequences of 16k to 32k keys 281 with 4096
+// CU) 13.4 us whole, 16.3 in two parts; 32 sequences of 16k to 32k keys 281 with 4096
 // workgroups or 6144, and 6 % more with 2048.
 constexpr int kCus = 256, kFill = 512, kFillBlocks = 768, kFine = 4096, kMinSteps = 8;
 
@@ -859,8 +858,9 @@ struct Plan {
 Plan plan_of(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim, int64_t max_q, int64_t max_kv_len) {
     Plan p;
     const int64_t rows = max_q * (n_heads / n_kv_heads);
-    // Two tiles of 16 rows share a step's conversions (64 drafted tokens of four sequences over 8k keys 108 us, 132 with
-    // one, 31 against 41 for five trees of up to 13); for head dim 256 their sums do not fit the registers.
+    // Two tiles of 16 rows share a step's conversions (64 drafted tokens of four sequences over 8k keys 87 us, 112 with
+    // one, 24.5 against 34 for five trees of up to 13, though 8 tokens of one over 4k 12.7 against 12.1); for head dim
+    // 256 their sums do not fit the registers.
     p.row_tiles = rows > 16 && head_dim <= 128 ? 2 : 1;
     p.row_blocks = (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
     const int64_t groups = n_seqs * n_kv_heads * p.row_blocks;   // at one part each
@@ -969,7 +969,7 @@ extern "C" int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, c
                 const int64_t blocks = p.row_blocks - rb < most ? p.row_blocks - rb : most;
                 const dim3 grid(static_cast<uint32_t>(cache->n_kv_heads), static_cast<uint32_t>(p.splits),
                                 static_cast<uint32_t>(n_seqs * blocks));
-                a.row_block0 = static_cast<int32_t>(rb);
+                a.row_block0 = static_cast<int32_t>(rb), a.row_blocks = static_cast<int32_t>(blocks);
                 if (p.row_tiles == 2) {
                     if constexpr (D <= 128)
                         hipLaunchKernelGGL((attn_q8_kernel<T, D, NS, 2>), grid, dim3(kThreads), 0, hs, a);

@@ -23,9 +23,9 @@ constexpr int64_t kMaxThreads = (INT64_C(1) << 32) - 1;   // of one launch
 constexpr int kMaxRot = 256;
 constexpr int64_t kMaxStride = INT64_C(1) << 36;   // elements between tokens
 // From here on a workgroup per token (store) or four tokens (load) fills the card: 8191
-// tokens stored and read back in 60 us, 86 with a workgroup per 16 rows of a token, and
+// tokens stored and read back in 57 us, 86 with a workgroup per 16 rows of a token, and
 // 65521 read in 138 us, 160 one by one; fewer tokens are spread as far as they go (one
-// token stored and read back in 5.6 us, 6.5 by one workgroup).
+// token stored and read back in 5.5 us, a microsecond more by one workgroup).
 constexpr int64_t kManyTokens = 1024;
 
 // ------------------------------------------------------- rotary table
@@ -136,7 +136,7 @@ __device__ __forceinline__ void turn(f32x4 (&x)[E / 4], const f32x4 (&o)[E / 4],
 // heads, k heads, v heads; a batch of them is loaded while the one before it is turned and
 // quantized, the first while the token's slot, position and angles are looked up. A row
 // never leaves its wave and the batches differ in their rows, so q_out may be q itself.
-// 8191 tokens of 32 / 8 heads of 128 in bf16: 44 us, 4.3 TB/s (35 with the inputs still in
+// 8191 tokens of 32 / 8 heads of 128 in bf16: 42 us, 4.4 TB/s (35 with the inputs still in
 // the last cache), near memory's rate with the quantizer's arithmetic beside it (36 with
 // loads behind the look-up and between the batches, 37 with batches of two rows, 53 at 80
 // registers; of f32, four elements a thread, 2000 tokens 17.4 us with one row, 16.7 with

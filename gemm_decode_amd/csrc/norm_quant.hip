@@ -352,10 +352,10 @@ void launch_norm(const void *x, const void *residual, const float *weight, void 
             hipLaunchKernelGGL((rmsnorm_quant_kernel<T, decltype(r)::value, W, kTernary>), grid,
                                dim3(W == 1 ? 256 : 64 * W), 0, hs, xt, rt, weight, ht, out, x_scale, n, K, eps);
         };
-        // Many short rows: a wave each (16384 rows of 512 in bf16: 29 us a pass with its reader, 74 with eight
-        // waves a row, most of them idle; a single row of 1024: 6.0 us, 5.2 with eight). Else eight waves a
-        // row (a row of 4096: 5.5 us with its reader, 6.3 with four waves, 5.4 with sixteen, which take 50 us
-        // for 4099 rows where eight take 47).
+        // Many short rows: a wave each (16384 rows of 512 in bf16: 13.8 us, 41.8 with eight waves a row, most of
+        // them idle; 1024 rows of 1024 4.7 and 5.6, 512 of them 4.5 and 4.2, one 3.2 and 2.8). Else eight waves a
+        // row (one f32 row of 4096: 3.4 us, 3.9 with four waves; 4099 rows in bf16 26.4 and 27.3; sixteen for rows
+        // past 4096: 1024 rows of 14336 in bf16 27.1 where eight take 25.8, one in f32 5.9 and 6.5).
         const bool many = n >= 1024;
         if (K <= 512 && many)
             launch(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
