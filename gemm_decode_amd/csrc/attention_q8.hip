@@ -471,13 +471,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 || NS == 1 ? 2 : 1) void attn_q8
     int j = j0 + kStep * wave;
     const int last = (j1 > 0 ? j1 - 1 : 0) / 16;
     const int64_t of_page = a.c.page_size * Hkv * D, of_head = a.c.page_size * kvh * D;
-    Place next = {};
     // Keys are loaded before values everywhere, and the scheduler is kept from mixing
     // the two: loads complete in order, and a wait for the keys must not include the
-    // values behind them.
-    // A wave without keys loads the last tile and does not use it: with as many loads on
-    // every path, the wait for the queries is for them alone.
-    next = place_of<D>(a, b, of_page, of_head, j / 16 < last ? j / 16 : last, last);
+    // values behind them. A wave without keys loads the last tile and does not use it:
+    // with as many loads on every path, the wait for the queries is for them alone.
+    Place next = place_of<D>(a, b, of_page, of_head, j / 16 < last ? j / 16 : last, last);
     load_keys<D>(a, next, lane, st);
     __builtin_amdgcn_sched_barrier(0);
     load_values<D>(a, next, lane, st);
