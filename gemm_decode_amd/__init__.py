@@ -646,11 +646,14 @@ def attn_decode_q8(q, cache: KVCacheQ8, page_table, kv_lens, q_start, tree_mask,
                 _attn_bytes.clear()
             _attn_bytes[sizes] = need
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        space = workspace.data_ptr()
+    else:
+        need, space = workspace.numel(), _on(i, workspace, torch.uint8, None, "workspace")
     _check(_lib.attn_decode_q8(ref, _on(i, q, q.dtype, n, "q"), _on(i, out, q.dtype, n, "out"), table, max_pages, lens,
                                None if q_start is None else _on(i, q_start, torch.int32, n_seqs + 1, "q_start"),
                                None if tree_mask is None else _on(i, tree_mask, torch.int64, n_q, "tree_mask"),
                                n_seqs, n_q, n_heads, max_q, max_kv_len, scale, softcap, dt,
-                               _on(i, workspace, torch.uint8, None, "workspace"), workspace.numel(), stream))
+                               space, need, stream))
 
 
 # ------------------------------------------------------------ measurement
