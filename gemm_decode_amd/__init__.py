@@ -606,6 +606,7 @@ def kv_q8_load(cache: KVCacheQ8, slots, k_out, v_out, n_tok: int):
 
 def attn_decode_q8_workspace_bytes(n_seqs: int, n_q: int, n_heads: int, n_kv_heads: int, head_dim: int, max_q: int,
                                    max_kv_len: int) -> int:
+    """Workspace bytes that serve this call and every one no larger in n_seqs, n_q, max_q and max_kv_len."""
     b = ctypes.c_size_t()
     _check(_lib.attn_decode_q8_workspace_bytes(n_seqs, n_q, n_heads, n_kv_heads, head_dim, max_q, max_kv_len,
                                                ctypes.byref(b)))

@@ -873,6 +873,39 @@ Plan plan_of(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads, int64_t head_d
     return p;
 }
 
+// Rows of partial sums that the workspace has to hold: an upper bound on n_q * n_heads *
+// splits of this call and of every call that is no larger in n_seqs, n_q, max_q and
+// max_kv_len (the same heads), and itself no smaller for a larger call, so that a
+// workspace made for the largest call serves the others. The plan's own product is not:
+// a call of more sequences or more keys may be cut into fewer parts. Two bounds, the
+// smaller one taken: every row in as many parts as the smallest batch is cut into, and as
+// many workgroups as any plan makes, each with the rows of its block. With g workgroups at
+// one part each, ceil(c / g) parts are at most c + g - 1 workgroups, for g < kCus where a
+// plan fills the CUs and for g < kFine where it cuts finer.
+int64_t part_rows(int64_t n_seqs, int64_t n_q, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim, int64_t max_q,
+                  int64_t max_kv_len) {
+    const int64_t rows = max_q * (n_heads / n_kv_heads), tall = head_dim <= 128 ? 32 : 16;   // of a KV head, of a block
+    const int64_t row_blocks = rows <= 16 ? 1 : (rows + tall - 1) / tall;
+    const int64_t groups = n_seqs * n_kv_heads * row_blocks;
+    const int64_t steps = (max_kv_len + kGroupKeys - 1) / kGroupKeys, fine = steps / kMinSteps;
+    const int64_t most = row_blocks > 1 ? kFillBlocks : kFill;
+    const int64_t fill1 = n_kv_heads < kCus ? (most + n_kv_heads - 1) / n_kv_heads : 1;   // one sequence, one block
+    const int64_t fine1 = (kFine + n_kv_heads - 1) / n_kv_heads;
+    int64_t parts = fine < fine1 ? fine : fine1;
+    parts = parts > fill1 ? parts : fill1;
+    parts = parts < steps ? parts : steps;
+    if (parts <= 1) return 0;
+    int64_t workgroups = most + (groups < kCus - 1 ? groups : kCus - 1) - 1;
+    if (fine > 1) {
+        const int64_t cut = kFine + (groups < kFine - 1 ? groups : kFine - 1) - 1;
+        const int64_t n = groups * fine < cut ? groups * fine : cut;
+        workgroups = workgroups > n ? workgroups : n;
+    }
+    workgroups = workgroups < groups * steps ? workgroups : groups * steps;
+    const int64_t by_parts = n_q * n_heads * parts, by_blocks = (rows < tall ? rows : tall) * workgroups;
+    return by_parts < by_blocks ? by_parts : by_blocks;
+}
+
 int check_sizes(const char *name, int64_t n_seqs, int64_t n_q, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim,
                 int64_t max_q, int64_t max_kv_len) {
     GD_REQUIRE(n_seqs >= 1 && n_q >= 1 && n_heads >= 1 && n_kv_heads >= 1 && max_q >= 1 && max_kv_len >= 1, GD_EINVAL,
@@ -897,9 +930,9 @@ extern "C" int attn_decode_q8_workspace_bytes(int64_t n_seqs, int64_t n_q, int64
     GD_REQUIRE(bytes, GD_EINVAL, "attn_decode_q8_workspace_bytes: null output pointer");
     int st = check_sizes("attn_decode_q8_workspace_bytes", n_seqs, n_q, n_heads, n_kv_heads, head_dim, max_q, max_kv_len);
     if (st) return st;
-    const Plan p = plan_of(n_seqs, n_heads, n_kv_heads, head_dim, max_q, max_kv_len);
     // a sum of head_dim values, a maximum and a denominator per row, head and part
-    *bytes = p.splits > 1 ? static_cast<size_t>(n_q * n_heads * p.splits * (head_dim + 2) * 4) : 16;
+    const int64_t rows = part_rows(n_seqs, n_q, n_heads, n_kv_heads, head_dim, max_q, max_kv_len);
+    *bytes = rows > 0 ? static_cast<size_t>(rows * (head_dim + 2) * 4) : 16;
     clear_error();
     return GD_OK;
 }

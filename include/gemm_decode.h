@@ -590,7 +590,8 @@ int kv_q8_load(const gd_kv_q8 *cache, const int64_t *slots, void *k_out, void *v
  *   max_kv_len  the longest kv_lens: sets the split of the keys, at most
  *               max_pages * page_size.
  *   workspace   device, attn_decode_q8_workspace_bytes(...) bytes, 16-byte
- *               aligned; calls that share it must be ordered.
+ *               aligned; one made for the largest call serves every smaller
+ *               one. Calls that share it must be ordered.
  * f32 inputs: within 1e-5 of the largest |v| seen (plus 2^-22 max|s|, as
  * attn_decode_splitk). f16 and bf16: the products run on operands rounded to
  * f16 (weights of the softmax included), sums in f32.
@@ -603,7 +604,10 @@ int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, const int32_
                    int64_t max_q, int64_t max_kv_len, float scale, float softcap, int32_t dtype,
                    void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes of such a call. Host only. Errors as its size checks. */
+/* Workspace bytes of such a call: enough for every call of the same head counts
+ * and head_dim that is no larger in n_seqs, n_q, max_q and max_kv_len, and never
+ * less for a larger call (a call itself may be cut into more parts than a larger
+ * one). Host only. Errors as its size checks. */
 int attn_decode_q8_workspace_bytes(int64_t n_seqs, int64_t n_q, int64_t n_heads, int64_t n_kv_heads,
                                    int64_t head_dim, int64_t max_q, int64_t max_kv_len, size_t *bytes);
 

@@ -177,3 +177,34 @@ def test_attention_workspace(gd):
         assert L.attn_decode_q8_workspace_bytes(*args, ctypes.byref(b)) == 0
         n_q, heads, dim, length = args[1], args[2], args[4], args[6]
         assert 16 <= b.value <= 16 + n_q * heads * (dim + 2) * 4 * -(-length // 64)
+
+
+def test_attention_workspace_of_the_largest_call_serves_the_smaller_ones(gd):
+    """Fewer sequences, rows, query tokens or keys never need more (a plan may cut a smaller call into more parts)."""
+    L, b = gd.lib(), ctypes.c_size_t()
+
+    def need(*args):
+        assert L.attn_decode_q8_workspace_bytes(*args, ctypes.byref(b)) == 0, args
+        return b.value
+    assert need(1, 1, 32, 8, 128, 1, 8192) <= need(1, 1, 32, 8, 128, 1, 8320)
+    assert need(31, 31, 32, 8, 128, 1, 1024) <= need(32, 32, 32, 8, 128, 1, 1024)
+    for heads, kv, dim in ((32, 8, 128), (8, 2, 64), (16, 1, 256), (40, 40, 128), (4096, 4096, 64)):
+        for seqs in (1, 3, 32, 300):
+            prev = 0
+            for length in range(1, 40000, 517):
+                now = need(seqs, seqs, heads, kv, dim, 1, length)
+                assert now >= prev, (heads, kv, dim, seqs, length)
+                prev = now
+        for length in (300, 1024, 8192, 1 << 20):
+            prev = 0
+            for seqs in list(range(1, 70)) + [100, 255, 256, 257, 511, 512, 513, 1000, 4095, 4096, 5000, 65535]:
+                now = need(seqs, seqs, heads, kv, dim, 1, length)
+                assert now >= prev, (heads, kv, dim, seqs, length)
+                prev = now
+            for seqs in (1, 5, 40):
+                prev = 0
+                for max_q in range(1, 65):
+                    now = need(seqs, seqs * max_q, heads, kv, dim, max_q, length)
+                    assert now >= prev, (heads, kv, dim, seqs, max_q, length)
+                    assert need(seqs, seqs * max_q - (max_q > 1), heads, kv, dim, max_q, length) <= now
+                    prev = now

@@ -406,3 +406,20 @@ def test_refusals(gd):
     c.page_table = dev(c.table.astype(np.int32))[:, :2].contiguous()
     with pytest.raises(gd.GemmDecodeError, match="GD_EINVAL"):
         c.run()
+
+
+def test_one_workspace_for_every_smaller_call(gd):
+    """A workspace made for a server's largest call takes every smaller one, and none writes past what it asks for itself."""
+    H, Hkv, D, B, max_q, max_len = 8, 2, 64, 12, 6, 2000
+    most = gd.attn_decode_q8_workspace_bytes(B, B * max_q, H, Hkv, D, max_q, max_len)
+    ws = torch.empty(most, dtype=torch.uint8, device="cuda")
+    for seqs, q, n in ((12, 6, 2000), (12, 6, 1000), (12, 1, 300), (1, 1, 2000), (1, 6, 1920), (3, 4, 129), (7, 5, 1100), (11, 1, 1999),
+                       (1, 1, 128), (2, 3, 40)):
+        c = Case(gd, [n] + [max(q, n - 7 * i) for i in range(1, seqs)], [q] * seqs, H, Hkv, D, 16, BF16, seed=n)
+        need = gd.attn_decode_q8_workspace_bytes(seqs, seqs * q, H, Hkv, D, q, n)
+        assert need <= most
+        ws.fill_(0xA5)
+        got = c.run(workspace=ws)
+        assert bool((ws[need:] == 0xA5).all())
+        c.check(got)
+        assert torch.equal(got, c.run())
