@@ -592,9 +592,14 @@ int kv_q8_load(const gd_kv_q8 *cache, const int64_t *slots, void *k_out, void *v
  *   workspace   device, attn_decode_q8_workspace_bytes(...) bytes, 16-byte
  *               aligned; one made for the largest call serves every smaller
  *               one. Calls that share it must be ordered.
- * f32 inputs: within 1e-5 of the largest |v| seen (plus 2^-22 max|s|, as
- * attn_decode_splitk). f16 and bf16: the products run on operands rounded to
- * f16 (weights of the softmax included), sums in f32.
+ * Accuracy, against the definition without roundings, with V the largest |v| of
+ * the sequence, S the largest scale * sum |q_i k_i| (the products' magnitudes: where
+ * they cancel, far above |s|) and n its keys:
+ *   f32        (1e-5 + 2^-28 n + 2^-19 S) V: q and the weights keep 22 bits, sums
+ *              are f32. With a softcap 2^-18 S.
+ *   f16, bf16  2^-10 V and half a step of the result more: the weights and the
+ *              values (code * scale) are rounded to f16 for their product, and q
+ *              loses what lies below 2^-25 of its row's largest value.
  * Requires n_heads % n_kv_heads == 0, max_q <= 64, n_q <= n_seqs * max_q,
  * n_heads <= 4096, n_seqs <= 65535, max_kv_len <= 2^30, finite scale,
  * 0 <= softcap <= 1e30. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE, GD_EHIP. */

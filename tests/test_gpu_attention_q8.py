@@ -423,3 +423,91 @@ def test_one_workspace_for_every_smaller_call(gd):
         assert bool((ws[need:] == 0xA5).all())
         c.check(got)
         assert torch.equal(got, c.run())
+
+
+def overwrite(c, which, codes, scales):
+    """Keys (0) or values (1) of every sequence of c as given: codes [len, D] and scales [len, D/32], the same in every head."""
+    planes = ((c.cache.k_codes, c.cache.k_scales), (c.cache.v_codes, c.cache.v_scales))[which]
+    for b, n in enumerate(c.lens):
+        g, p = dev(c.table[b, np.arange(n) // c.page]), dev(np.arange(n) % c.page)
+        planes[0][g, :, p] = dev(np.asarray(codes[:n], np.int8))[:, None]
+        planes[1][g, :, p] = dev(np.asarray(scales[:n], np.float16))[:, None]
+        x = np.asarray(codes[:n], np.float64) * np.repeat(np.asarray(scales[:n], np.float16).astype(np.float64), 32, -1)
+        (c.k, c.v)[which][b][:] = x
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_that_cancel(gd, D):
+    """Pairs of dims whose products nearly cancel: the bar goes by scale * sum |q k| (here some 10^5), which the 22
+    bits of q are parts of, and not by the scores."""
+    c = Case(gd, [300], [1], 4, 2, D, 16, seed=21, qscale=6e3)
+    rng = np.random.default_rng(2)
+    q = c.q.double().numpy()
+    q[..., 1::2] = q[..., 0::2] * (1 + rng.uniform(-1, 1, q[..., 0::2].shape) * 2.0 ** -15)
+    c.q = torch.from_numpy(q.astype(np.float32))
+    codes = rng.integers(-127, 128, (300, D))
+    codes[:, 1::2] = -codes[:, 0::2]
+    overwrite(c, 0, codes, rng.uniform(0.3, 1.0, (300, D // 32)) / 60)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("T", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_worst_roundings_to_f16(gd, T, D):
+    """Every weight but the first and every value lies just below the middle of two f16 numbers at the low end of a binade:
+    each is off by nearly 2^-11 of itself, both downwards, 2^-10 of the result in all; half a step of the result's type is
+    added. The sums of f32 add 1e-5, and the weights' scores (0 and one of 0.69) 2^-19."""
+    n = 200
+    c = Case(gd, [n], [1], 4, 2, D, 16, T, seed=3)
+    w = 0.5 * (1 + 0.98 * 2.0 ** -11)
+    low = lambda m: m / 2.0 ** np.floor(np.log2(m)) - 1          # over the binade's low end
+    best = max(((x * y, x, y) for x in range(1, 128) for y in range(1024, 2048) if low(x * y) < 2.0 ** -11),
+               key=lambda t: low(t[0]))
+    k = np.zeros((n, D), np.int8)
+    k[1:, 0] = -1
+    overwrite(c, 0, k, np.ones((n, D // 32)))
+    overwrite(c, 1, np.full((n, D), best[1]), np.full((n, D // 32), best[2] / 1024.0))
+    c.q = torch.ones_like(c.q)
+    scale = float(-np.log(w))
+    got, (want, _) = c.run(scale=scale).double().cpu().numpy(), c.want(scale=scale)
+    v = best[0] / 1024.0
+    assert np.allclose(want, v, rtol=1e-12)
+    bar = (2.0 ** -10 + 1e-5 + 2.0 ** -19 * scale) * v + torch.finfo(T).eps / 2 * v
+    assert np.abs(got - want).max() <= bar
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+@pytest.mark.parametrize("even", [False, True])
+def test_long_parts(gd, T, even):
+    """65536 keys in one part (512 sequences of 8 KV heads share one sequence's pages: a workgroup for each is enough). A
+    lane's sum of weights is 2048 roundings of at most 2^-24 each, and a sum of values three matrix products for each of a
+    wave's 512 steps, 1536: 3584 * 2^-24 is below 2^-28 per key. even: all weights but one are equal and all values too, so
+    that the roundings have one sign."""
+    B, Hkv, D, page, n = 512, 8, 64, 256, 65536
+    assert gd.attn_decode_q8_workspace_bytes(B, B, Hkv, Hkv, D, 1, n) < B * Hkv * (D + 2) * 4 * 2   # one part
+    rng = np.random.default_rng(31)
+    pages = n // page
+    codes = rng.integers(-127, 128, (2, pages, Hkv, page, D)).astype(np.int8)
+    scales = (rng.uniform(0.3, 1.0, (2, pages, Hkv, page, D // 32)) / 60).astype(np.float16)
+    q = torch.from_numpy(rng.standard_normal((1, Hkv, D)).astype(np.float32)).to(T)
+    if even:
+        codes[0], codes[1] = -10, 101
+        codes[0, 0, :, 0] = 0
+        scales[0], scales[1] = 0.01, 0.0101
+        q = torch.full_like(q, 1.0)
+    cache = gd.KVCacheQ8(dev(codes[0]), dev(scales[0]), dev(codes[1]), dev(scales[1]))
+    out = torch.empty(B, Hkv, D, dtype=T, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(B, 1)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    scale = 0.1875
+    gd.attn_decode_q8(q.cuda().expand(B, -1, -1).contiguous(), cache, table, lens, None, None, out, Hkv, 1, n, scale)
+    assert bool((out == out[:1]).all())
+    k, v = (np.repeat(scales[i].astype(np.float64), 32, -1) * codes[i] for i in range(2))
+    k, v = (x.transpose(1, 0, 2, 3).reshape(Hkv, n, D) for x in (k, v))
+    want, vmax, smax = layer.attention_rows(q.double().numpy(), k, v, np.ones((1, n), bool), scale)
+    err = np.abs(out[:1].double().cpu().numpy() - want)
+    bar = (1e-5 + 2.0 ** -28 * n + 2.0 ** -19 * smax) * vmax
+    if T != F32:
+        bar = bar + 2.0 ** -10 * vmax + torch.finfo(T).eps / 2 * np.abs(want)
+    print(T, even, "off by", err.max() / vmax)
+    assert np.all(err <= bar)
