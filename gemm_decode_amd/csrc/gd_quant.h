@@ -1,9 +1,10 @@
 // gd_quant.h -- device side of the activation quantization rule (absmax to
 // int8, stated in include/gemm_decode.h under "Activation quantization"),
 // as the norms with an 8-bit output and the 8-bit cache apply it: the factor
-// is 127 * (1 / absmax). (quantize.hip, for plain f32 activations, has it as
-// 127 / absmax, and its own text: the HBM traffic the benchmark reports for
-// it is tied to that file's bytes.)
+// is 127 * (1 / absmax), as torch evaluates `127 / tensor`, so that rows quantized by
+// such code are reproduced bit for bit. (quantize.hip, for plain f32 activations, has it
+// as 127 / absmax; the two lead to different codes only at exact halves. It has its own
+// text: the HBM traffic the benchmark reports for it is tied to that file's bytes.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -37,9 +38,10 @@ __device__ __forceinline__ double factor_of(double absmax) { return absmax > 0.0
 constexpr float kTieGuard = 6.4e-5f;   // 4x the f32 error bound above
 
 // f32(127 / a) and f32(a / 127) for a finite f32 a > 0, correctly rounded
-// f32 divisions. They equal the f64 quotients rounded to f32 (the rule's
-// order): an f32 midpoint is never within 2^-49 (relative) of either exact
-// quotient, far beyond f64's rounding, so rounding twice cannot differ.
+// f32 divisions. They equal the rule's f64 factor (two roundings) and quotient
+// (one) rounded to f32: an f32 midpoint is never within 2^-49 (relative) of
+// either exact quotient, beyond what f64 rounds off, so rounding again cannot
+// differ.
 __device__ __forceinline__ float recip127(float a) { return 127.0f / a; }
 __device__ __forceinline__ float scale_of(float a) { return a / 127.0f; }
 

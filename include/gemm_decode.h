@@ -424,12 +424,23 @@ int attn_decode_splitk_noalloc(const float *q, const float *k_cache, const float
  * The step between the residual stream and a product. With
  *   h = x + residual                (rounded to the stream's type)
  *   p = h * weight,  rstd = 1 / sqrt(mean over the row of h^2 + eps)
- * the norm is y = rstd * p, quantized by the rule above. rstd divides out of
- * y * (127 / max|y|), so the codes are Math.round(p * (127 * (1 / max|p|)))
+ * the norm is y = rstd * p, quantized as above but for the factor (below). rstd
+ * divides out of y * factor, so the codes are Math.round(p * (127 * (1 / max|p|)))
  * (each step rounded in f64, where p is exact) and the scale is max|p| * rstd
  * / 127, evaluated in f64 from left to right and rounded to f32. A group whose
  * products are all 0 gets scale 0 and zero codes. Sums are f64; inputs and h
  * must be finite.
+ *
+ * The factor. The norms and the cache write form it as 127 * (1 / absmax), each
+ * step rounded in f64, where q8_0_quantize and ternary_quantize_act form the
+ * quotient 127 / absmax: that is how torch evaluates `127 / tensor`, and rows
+ * quantized by such code are reproduced bit for bit. The two factors differ by at
+ * most 2^-52 of themselves, so a code of one value can differ between the entry
+ * points only where value * 127 / absmax is an exact half (for the norms, whose
+ * products have 48 bits, or within 2^-45 of one): it is then one of the two whole
+ * numbers beside the half, which are equally near. Scales are the same. f32 data
+ * hardly meet that; of random blocks of bf16 values about one in ninety has such
+ * a code.
  *
  * Element types of the entry points from here on that take a `dtype`: */
 #define GD_F32  0
@@ -474,10 +485,9 @@ int ternary_dequantize_act(const uint32_t *planes, const float *x_scale, void *y
  * ====================================================================
  * A pool of pages, each of page_size positions of every KV head. A row (one
  * position of one head) is head_dim int8 codes with an f16 scale per 32 dims,
- * quantized as q8_0_quantize does but for the factor, 127 * (1 / absmax) (a
- * code can differ only where it falls on an exact half); it stands for code *
- * scale. Position p of
- * page g of head h is row (g * n_kv_heads + h) * page_size + p of each plane;
+ * quantized as q8_0_quantize does but for the factor, which is the norms' (a code
+ * can differ by one, and only where it falls on an exact half); it stands for
+ * code * scale. Position p of page g of head h is row (g * n_kv_heads + h) * page_size + p of each plane;
  * slot s names position s % page_size of page s / page_size. A cache without
  * paging is a pool whose page b holds all of sequence b.
  * The struct is read on the host during the call; the planes are device

@@ -248,3 +248,31 @@ def test_refusals_launch_nothing(gd):
     with pytest.raises(ValueError):
         gd.rmsnorm_q8_0(x.t(), None, w, None, a, 2, 64, EPS)
     assert not a.any()
+
+
+@pytest.mark.parametrize("T", TYPES)
+def test_codes_beside_those_of_the_quantizer(gd, T):
+    """Rows of weight 1 against q8_0_quantize of the same values, and the cache's rows: other codes only at exact halves of a
+    step (which bf16 rows have), by one; the cache's scales are the quantizer's."""
+    n, K = 512, 1024
+    x = rows(n, K, T, 77)
+    x = torch.where(x.abs() < 2.0 ** -10, torch.full_like(x, 0.5), x)   # whole multiples of 2^-40, for exact arithmetic
+    blocks_of = lambda a: a.cpu().numpy().reshape(-1, 34)
+    plain = torch.empty(n * (K // 32) * 34, dtype=torch.uint8, device="cuda")
+    gd.q8_0_quantize(x.float().cuda(), plain, n, K)
+    plain = blocks_of(plain)
+    norm = blocks_of(run(gd, "q8_0", x.cuda(), None, torch.ones(K, device="cuda"), None, n, K))
+    cache = gd.kv_q8_alloc(n // 16, 16, K // 64, 64)
+    v = x.cuda().view(n, K // 64, 64)
+    gd.kv_q8_store(cache, v, v, torch.arange(n, device="cuda"), n)
+    stored = cache.v_codes.transpose(1, 2).reshape(-1, 32).cpu().numpy()
+    scales = cache.v_scales.transpose(1, 2).reshape(-1).cpu().numpy()
+    assert np.array_equal(scales, plain[:, :2].copy().view(np.float16)[:, 0])
+    values, want = x.double().numpy().reshape(-1, 32), plain[:, 2:].view(np.int8)
+    for got in (norm[:, 2:].view(np.int8), stored):
+        at = np.argwhere(got != want)
+        assert T != torch.bfloat16 or len(at)
+        for r, i in at:
+            val, top = (int(t * 2.0 ** 40) for t in (values[r, i], np.abs(values[r]).max()))
+            lower = min(int(got[r, i]), int(want[r, i]))
+            assert abs(int(got[r, i]) - int(want[r, i])) == 1 and 2 * 127 * val == (2 * lower + 1) * top

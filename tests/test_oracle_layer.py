@@ -86,3 +86,29 @@ def test_attention_rows_match_the_single_token_oracle():
     assert not none.any()
     flat, _, _ = layer.attention_rows(q * 1e9, k, v, sees, 0.5, cap=1e-9)
     assert np.allclose(flat[1, 0], v[0].mean(0), atol=1e-7)   # a cap of nothing: the mean
+
+
+def off_by_a_tie(values, a, b):
+    """The codes a and b of rows `values` [n, 32] (of up to 24 bits each) differ by one, upwards from the half that both lie
+    beside, in exact arithmetic; how many."""
+    at = np.argwhere(a != b)
+    for r, i in at:
+        v, top = int(values[r, i] * 2.0 ** 40), int(np.abs(values[r]).max() * 2.0 ** 40)
+        assert v * 2.0 ** -40 == values[r, i] and top * 2.0 ** -40 == np.abs(values[r]).max()
+        lower = min(int(a[r, i]), int(b[r, i]))
+        assert abs(int(a[r, i]) - int(b[r, i])) == 1 and 2 * 127 * v == (2 * lower + 1) * top
+    return len(at)
+
+
+def test_the_two_factors_differ_at_exact_halves_only():
+    """The cache's factor 127 * (1 / absmax) and the quantizers' 127 / absmax give one block other codes only where a value is
+    an exact half of a step; the scales are the same."""
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((20000, 32)).astype(np.float32)
+    x = np.where(np.abs(x) < 2.0 ** -10, np.float32(0.5), x)   # whole multiples of 2^-40, for exact arithmetic
+    coarse = (x.view(np.uint32) & 0xffff0000).view(np.float32)   # bf16 values
+    for values, ties in ((coarse, True), (x, False)):
+        codes, scale = layer.q8_rows(values)
+        want, s = oracle.quantize_absmax_int8(values)
+        assert np.array_equal(scale[:, 0], s.astype(np.float16))
+        assert (off_by_a_tie(values.astype(np.float64), codes, want) > 0) == ties
