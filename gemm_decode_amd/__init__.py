@@ -490,22 +490,28 @@ class KVCacheQ8:
     """A pool of pages of 8-bit keys and values (gd_kv_q8): codes int8
     [n_pages, n_kv_heads, page_size, head_dim] and scales float16
     [n_pages, n_kv_heads, page_size, head_dim/32] for keys and for values. The
-    handle checks the four tensors once and keeps them alive."""
+    handle checks the four tensors' shapes and types once and keeps them alive."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         import torch
         if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
             raise ValueError("k_codes must be [n_pages, n_kv_heads, page_size, head_dim]")
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_codes.shape
-        n = k_codes.numel()
-        codes = [_dev(t, torch.int8, n, name) for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes"))]
-        scales = [_dev(t, torch.float16, n // 32, name) for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales"))]
+        shape = k_codes.shape
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
+        scales = shape[:3] + (self.head_dim // 32,)
+        given = ((k_codes, "k_codes", torch.int8, shape), (k_scales, "k_scales", torch.float16, scales),
+                 (v_codes, "v_codes", torch.int8, shape), (v_scales, "v_scales", torch.float16, scales))
+        for t, name, _, want in given:   # a plane of another order would be misread
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.shape != want:
+                raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
+        planes = [_dev(t, dtype, None, name) for t, name, dtype, _ in given]
         self.device = k_codes.device
         if any(t.device != self.device for t in (k_scales, v_codes, v_scales)):
             raise ValueError("the cache's planes must be on one device")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self._c = _KVQ8(codes[0], scales[0], codes[1], scales[1], self.n_pages, self.page_size, self.n_kv_heads,
-                        self.head_dim)
+        self._c = _KVQ8(*planes, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim)
         self._ref = ctypes.addressof(self._c)
 
     def _on(self, index):

@@ -45,3 +45,25 @@ def test_binding_token_rows(gd):
         gd._token_rows(0, rows, torch.float32, 5, 384, "x")
     with pytest.raises(TypeError):
         gd._token_rows(-1, rows, torch.bfloat16, 5, 384, "x")
+
+
+def test_cache_planes_of_another_order_are_refused(gd):
+    """Planes with the right number of elements in another order of the axes, or in fewer axes (refused by shape, before the
+    device is asked for)."""
+    def planes():
+        codes = lambda: torch.zeros(3, 2, 32, 64, dtype=torch.int8)
+        scales = lambda: torch.zeros(3, 2, 32, 2, dtype=torch.float16)
+        return [codes(), scales(), codes(), scales()]
+    for i, name in ((1, "k_scales"), (2, "v_codes"), (3, "v_scales")):
+        for other in (lambda t: t.transpose(1, 2).contiguous(), lambda t: t.reshape(-1), lambda t: t.reshape(3, 2, 16, -1),
+                      lambda t: t[:2]):
+            p = planes()
+            p[i] = other(p[i])
+            with pytest.raises(ValueError, match=name + r" must be \["):
+                gd.KVCacheQ8(*p)
+        p = planes()
+        p[i] = None
+        with pytest.raises(TypeError, match=name):
+            gd.KVCacheQ8(*p)
+    with pytest.raises(ValueError, match="device"):
+        gd.KVCacheQ8(*planes())
