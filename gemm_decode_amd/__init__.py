@@ -439,6 +439,22 @@ def _on(index, t, dtype, numel, name):
     return p
 
 
+def _rows_on(index, t, dtype, n, heads, head_dim, name):
+    """_on of n rows of `heads` head rows: [n, heads, head_dim], or those with the leading or the last axes joined or split
+    up. Rows in another order of the axes, the heads first for instance, are refused (where their sizes tell)."""
+    try:
+        if (t.dtype == dtype and t.get_device() == index and t.is_contiguous()
+                and t.shape == (n, heads, head_dim)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p, s = _on(index, t, dtype, None, name), t.shape
+    if t.numel() != n * heads * head_dim or len(s) > 1 and s[-1] != heads * head_dim and (
+            s[-1] != head_dim or len(s) > 2 and s[-2] != heads):
+        raise ValueError(f"{name} must be [{n}, {heads}, {head_dim}], got {list(s)}")
+    return p
+
+
 def rmsnorm_q8_0(x, residual, weight, h_out, a_q8, n: int, K: int, eps: float):
     """h = x + residual, and the RMS norm of h times `weight` as q8_0 blocks
     (uint8 [n * K/32 * 34], what q1_q8_gemv reads). x, residual (or None) and
@@ -540,9 +556,10 @@ def rope_table(table, n_pos: int, rot_dim: int, base: float = 10000.0, scaling: 
                            None if scaling is None else ctypes.addressof(scaling), stream))
 
 
-def _token_rows(i, t, dtype, n_tok, width, name):
+def _token_rows(i, t, dtype, n_tok, width, name, head_dim=None):
     """(data_ptr, stride between tokens) of a tensor of n_tok rows of `width`
-    elements: [n_tok, width] or [n_tok, heads, head_dim], each row contiguous."""
+    elements: [n_tok, width] or [n_tok, heads, head_dim] (or the heads joined,
+    [n_tok, 1, width]), each row contiguous."""
     try:
         good = t.dtype == dtype and t.get_device() == i
     except AttributeError:
@@ -554,6 +571,8 @@ def _token_rows(i, t, dtype, n_tok, width, name):
     shape, strides = t.shape, t.stride()
     if len(shape) == 3:
         rows, inner = shape[1] * shape[2], strides[2] == 1 and (strides[1] == shape[2] or shape[1] == 1)
+        if head_dim is not None and shape[2] != head_dim and shape[1] != 1:
+            raise ValueError(f"{name} must be [{n_tok}, {width // head_dim}, {head_dim}], got {list(shape)}")
     elif len(shape) == 2:
         rows, inner = shape[1], strides[1] == 1
     else:
@@ -574,13 +593,13 @@ def kv_q8_store(cache: KVCacheQ8, k, v, slots, n_tok: int, q=None, q_out=None, n
     import torch
     dt, (i, stream) = _dtype(k, "k"), _current()
     ref, D = cache._on(i), cache.head_dim
-    kp, ks = _token_rows(i, k, k.dtype, n_tok, cache.n_kv_heads * D, "k")
-    vp, vs = _token_rows(i, v, k.dtype, n_tok, cache.n_kv_heads * D, "v")
+    kp, ks = _token_rows(i, k, k.dtype, n_tok, cache.n_kv_heads * D, "k", D)
+    vp, vs = _token_rows(i, v, k.dtype, n_tok, cache.n_kv_heads * D, "v", D)
     qp = qo = None
     qs = 0
     if n_heads:
-        qp, qs = _token_rows(i, q, k.dtype, n_tok, n_heads * D, "q")
-        qo = _on(i, q_out, k.dtype, n_tok * n_heads * D, "q_out")
+        qp, qs = _token_rows(i, q, k.dtype, n_tok, n_heads * D, "q", D)
+        qo = _rows_on(i, q_out, k.dtype, n_tok, n_heads, D, "q_out")
     elif q is not None or q_out is not None:
         raise ValueError("q and q_out need n_heads")
     rp = pp = None
@@ -604,10 +623,11 @@ def kv_q8_load(cache: KVCacheQ8, slots, k_out, v_out, n_tok: int):
     import torch
     one = v_out if k_out is None else k_out
     dt, (i, stream) = _dtype(one, "k_out" if k_out is not None else "v_out"), _current()
-    n = n_tok * cache.n_kv_heads * cache.head_dim
+    H, D = cache.n_kv_heads, cache.head_dim
     _check(_lib.kv_q8_load(cache._on(i), _on(i, slots, torch.int64, n_tok, "slots"),
-                           None if k_out is None else _on(i, k_out, one.dtype, n, "k_out"),
-                           None if v_out is None else _on(i, v_out, one.dtype, n, "v_out"), n_tok, dt, stream))
+                           None if k_out is None else _rows_on(i, k_out, one.dtype, n_tok, H, D, "k_out"),
+                           None if v_out is None else _rows_on(i, v_out, one.dtype, n_tok, H, D, "v_out"), n_tok, dt,
+                           stream))
 
 
 def attn_decode_q8_workspace_bytes(n_seqs: int, n_q: int, n_heads: int, n_kv_heads: int, head_dim: int, max_q: int,
@@ -635,7 +655,7 @@ def attn_decode_q8(q, cache: KVCacheQ8, page_table, kv_lens, q_start, tree_mask,
     n_q, rest = divmod(q.numel(), n_heads * D) if n_heads > 0 else (0, 1)
     if rest or n_q == 0:
         raise ValueError(f"q must be [n_q, {n_heads}, {D}], got {tuple(q.shape)}")
-    n = n_q * n_heads * D
+    qp, op = _rows_on(i, q, q.dtype, n_q, n_heads, D, "q"), _rows_on(i, out, q.dtype, n_q, n_heads, D, "out")
     table, max_pages = None, 1
     if page_table is not None:
         table = _on(i, page_table, torch.int32, None, "page_table")
@@ -656,7 +676,7 @@ def attn_decode_q8(q, cache: KVCacheQ8, page_table, kv_lens, q_start, tree_mask,
         space = workspace.data_ptr()
     else:
         need, space = workspace.numel(), _on(i, workspace, torch.uint8, None, "workspace")
-    _check(_lib.attn_decode_q8(ref, _on(i, q, q.dtype, n, "q"), _on(i, out, q.dtype, n, "out"), table, max_pages, lens,
+    _check(_lib.attn_decode_q8(ref, qp, op, table, max_pages, lens,
                                None if q_start is None else _on(i, q_start, torch.int32, n_seqs + 1, "q_start"),
                                None if tree_mask is None else _on(i, tree_mask, torch.int64, n_q, "tree_mask"),
                                n_seqs, n_q, n_heads, max_q, max_kv_len, scale, softcap, dt,

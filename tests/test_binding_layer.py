@@ -67,3 +67,20 @@ def test_cache_planes_of_another_order_are_refused(gd):
             gd.KVCacheQ8(*p)
     with pytest.raises(ValueError, match="device"):
         gd.KVCacheQ8(*planes())
+
+
+def test_rows_of_another_order_are_refused(gd):
+    """Rows with the heads first or the dims before the heads (on the CPU: the device index of a CPU tensor is -1); the axes that
+    say the same, joined or split, are taken."""
+    t = torch.zeros(5, 6, 64)
+    for same in (t, t.view(5, 384), t.view(30, 64), t.view(-1), t.view(1, 5, 6, 64), t.view(5, 1, 384)):
+        assert gd._rows_on(-1, same, torch.float32, 5, 6, 64, "x") == t.data_ptr()
+    for other in (t.view(6, 5, 64), t.view(5, 64, 6), t.view(64, 30), t.view(6, 320), t.view(5, 12, 32), t[:4].contiguous(),
+                  torch.zeros(4, 8, 60)):
+        with pytest.raises(ValueError, match="x must be"):
+            gd._rows_on(-1, other, torch.float32, 5, 6, 64, "x")
+    assert gd._token_rows(-1, t, torch.float32, 5, 384, "k", 64)[1] == 384
+    assert gd._token_rows(-1, t.view(5, 1, 384), torch.float32, 5, 384, "k", 64)[1] == 384
+    for other in (t.view(5, 64, 6), t.view(5, 12, 32), t.view(5, 3, 128)):
+        with pytest.raises(ValueError, match="k must be"):
+            gd._token_rows(-1, other, torch.float32, 5, 384, "k", 64)

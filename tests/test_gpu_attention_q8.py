@@ -511,3 +511,16 @@ def test_long_parts(gd, T, even):
         bar = bar + 2.0 ** -10 * vmax + torch.finfo(T).eps / 2 * np.abs(want)
     print(T, even, "off by", err.max() / vmax)
     assert np.all(err <= bar)
+
+
+def test_rows_of_another_order_are_refused(gd):
+    """Queries or outputs with the heads first have the right number of elements and would be read in the wrong order."""
+    c = Case(gd, [40, 40, 40], [1, 1, 1], 4, 2, 64, 16)
+    ref = c.run()
+    first = torch.empty(4, 3, 64, device="cuda")
+    with pytest.raises(ValueError, match="out must be"):
+        c.run(out=first)
+    assert torch.equal(c.run(out=torch.empty(3, 256, device="cuda")).view_as(ref), ref)
+    c.q = c.q.transpose(0, 1).contiguous()
+    with pytest.raises(ValueError, match="q must be"):
+        c.run(out=torch.empty(3, 4, 64, device="cuda"))
