@@ -971,6 +971,9 @@ extern "C" int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, c
     GD_REQUIRE(aligned(workspace, 16), GD_EALIGN, "attn_decode_q8: workspace must be 16-byte aligned");
     GD_REQUIRE(workspace_bytes >= need, GD_ERANGE, "attn_decode_q8: workspace of %zu bytes, %zu needed",
                workspace_bytes, need);
+    const int64_t row_bytes = n_q * n_heads * cache->head_dim * dtype_size(dtype);
+    GD_REQUIRE(!overlaps(q, row_bytes, row_bytes, 1, out, row_bytes), GD_EINVAL,
+               "attn_decode_q8: out must not overlap q");
     const Plan p = plan_of(n_seqs, n_heads, cache->n_kv_heads, cache->head_dim, max_q, max_kv_len);
     AttnArgs a;
     a.c = *cache;

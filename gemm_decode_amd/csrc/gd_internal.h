@@ -33,6 +33,16 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t *out) {
     return true;
 }
 
+// Whether one of n >= 1 ranges of `bytes` bytes at a, a + stride, ... meets the range of
+// other_bytes at b (stride >= bytes >= 1; null pointers meet nothing).
+inline bool overlaps(const void *a, int64_t stride, int64_t bytes, int64_t n, const void *b, int64_t other_bytes) {
+    if (!a || !b) return false;
+    // of b's start and end, from a on: the first range that ends behind b's start is the one to look at
+    const int64_t from = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    const int64_t first = from < bytes ? 0 : (from - bytes) / stride + 1;
+    return first < n && from + other_bytes > first * stride;
+}
+
 // The checks every entry point makes of an 8-bit cache's description.
 int check_kv_q8(const gd_kv_q8 *cache, const char *name);
 

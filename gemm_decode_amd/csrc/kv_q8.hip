@@ -424,6 +424,14 @@ extern "C" int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_strid
     GD_REQUIRE(aligned(k, 16) && aligned(v, 16) && (n_heads == 0 || (aligned(q, 16) && aligned(q_out, 16))) &&
                    aligned(slots, 8),
                GD_EALIGN, "kv_q8_store: q, k, v and q_out must be 16-byte aligned, slots 8-byte");
+    if (n_heads > 0) {
+        const int64_t size = dtype_size(dtype), out_bytes = n_tok * n_heads * D * size;
+        GD_REQUIRE(q_out == q || !overlaps(q, q_stride * size, n_heads * D * size, n_tok, q_out, out_bytes), GD_EINVAL,
+                   "kv_q8_store: q_out may be q itself, but not overlap it otherwise");
+        GD_REQUIRE(!overlaps(k, k_stride * size, Hkv * D * size, n_tok, q_out, out_bytes) &&
+                       !overlaps(v, v_stride * size, Hkv * D * size, n_tok, q_out, out_bytes),
+                   GD_EINVAL, "kv_q8_store: q_out must not overlap k or v");
+    }
     StoreArgs a;
     a.q = q, a.k = k, a.v = v, a.q_out = q_out;
     a.rope = reinterpret_cast<const f32x2 *>(rope);

@@ -339,6 +339,16 @@ int check_norm(const char *name, const void *x, const void *residual, const floa
     return GD_OK;
 }
 
+// After the other checks: h_out is x or residual, or apart from them.
+int check_in_place(const char *name, const void *x, const void *residual, const void *h_out, int64_t n, int64_t K,
+                   int32_t dtype) {
+    const int64_t bytes = n * K * dtype_size(dtype);   // below 2^55
+    GD_REQUIRE((h_out == x || !overlaps(x, bytes, bytes, 1, h_out, bytes)) &&
+                   (h_out == residual || !overlaps(residual, bytes, bytes, 1, h_out, bytes)),
+               GD_EINVAL, "%s: h_out may be x or residual itself, but not overlap them otherwise", name);
+    return GD_OK;
+}
+
 template <bool kTernary>
 void launch_norm(const void *x, const void *residual, const float *weight, void *h_out, void *out, float *x_scale,
                  int64_t n, int64_t K, float eps, int32_t dtype, hipStream_t hs) {
@@ -386,6 +396,8 @@ extern "C" int rmsnorm_q8_0(const void *x, const void *residual, const float *we
     if (st) return st;
     GD_REQUIRE(a_q8, GD_EINVAL, "rmsnorm_q8_0: null pointer");
     GD_REQUIRE(aligned(a_q8, 2), GD_EALIGN, "rmsnorm_q8_0: a_q8 must be 2-byte aligned");
+    st = check_in_place("rmsnorm_q8_0", x, residual, h_out, n, K, dtype);
+    if (st) return st;
     launch_norm<false>(x, residual, weight, h_out, a_q8, nullptr, n, K, eps, dtype, as_stream(stream));
     return check_launch("rmsnorm_q8_0");
 }
@@ -398,6 +410,8 @@ extern "C" int rmsnorm_ternary_act(const void *x, const void *residual, const fl
     GD_REQUIRE(planes && x_scale, GD_EINVAL, "rmsnorm_ternary_act: null pointer");
     GD_REQUIRE(aligned(planes, 4) && aligned(x_scale, 4), GD_EALIGN,
                "rmsnorm_ternary_act: planes and x_scale must be 4-byte aligned");
+    st = check_in_place("rmsnorm_ternary_act", x, residual, h_out, n, K, dtype);
+    if (st) return st;
     launch_norm<true>(x, residual, weight, h_out, planes, x_scale, n, K, eps, dtype, as_stream(stream));
     return check_launch("rmsnorm_ternary_act");
 }

@@ -544,8 +544,9 @@ int rope_table(float *table, int64_t n_pos, int64_t rot_dim, double base,
  *              Strides in elements, multiples of 16 bytes, at most 2^36. All values finite,
  *              below 65504 * 127 in k and v (the scales are f16).
  *   q_out      device dtype [n_tok][n_heads][head_dim]; may be q itself if
- *              q_stride is n_heads * head_dim. n_heads may be 0, with q and
- *              q_out NULL (only the cache is written).
+ *              q_stride is n_heads * head_dim or n_tok is 1, must not overlap q
+ *              otherwise, nor k or v. n_heads may be 0, with q and q_out NULL
+ *              (only the cache is written).
  *   rope       device f32 [n_pos][rot_dim/2][2] from rope_table, with
  *   positions  device int32 [n_tok]; both NULL: nothing is rotated (n_pos and
  *              rot_dim are then ignored). A token whose position is outside

@@ -208,3 +208,26 @@ def test_attention_workspace_of_the_largest_call_serves_the_smaller_ones(gd):
                     assert now >= prev, (heads, kv, dim, seqs, max_q, length)
                     assert need(seqs, seqs * max_q - (max_q > 1), heads, kv, dim, max_q, length) <= now
                     prev = now
+
+
+def test_outputs_that_overlap_inputs_are_refused(gd):
+    """Rows are read and written by workgroups in any order: an output on top of an input is refused unless it is one of the
+    documented in-place calls."""
+    L = gd.lib()
+    keep, ref = cache(gd)
+    for at in (0, 16, -16, 3 * 4 * 64 * 4 - 16):      # three rows of 4 heads of 64 in f32
+        assert attn(gd, ref, out=FAKE + at) == INVAL and "overlap" in L.gemm_decode_last_error().decode(), at
+    for at in (16, -16, 2 * 64 * 4 - 16):             # two rows of 64
+        for x, r in ((FAKE, None), (FAKE + (1 << 16), FAKE)):
+            assert L.rmsnorm_q8_0(x, r, FAKE, FAKE + at, FAKE, 2, 64, 1e-5, F32, None) == INVAL
+            assert L.rmsnorm_ternary_act(x, r, FAKE, FAKE + at, FAKE, FAKE, 2, 64, 1e-5, F32, None) == INVAL
+            assert "h_out" in L.gemm_decode_last_error().decode()
+    far, row = FAKE + (1 << 20), 2 * 64 * 4           # a token's two heads of 64 in f32: 512 bytes
+    for q, qs, qo in ((FAKE, 128, FAKE + 16), (FAKE, 128, FAKE - 16), (FAKE, 192, FAKE + row), (FAKE, 4096, FAKE + 2 * 4096 * 4),
+                      (FAKE, 4096, FAKE + row - 16), (FAKE, 4096, FAKE + 4096 * 4 - 3 * row + 16)):
+        assert store(gd, ref, q=q, qs=qs, qo=qo, k=far, v=far, ks=128, vs=128) == INVAL, (q, qs, qo)
+        assert "q_out" in L.gemm_decode_last_error().decode()
+    for name in ("k", "v"):
+        args = dict(q=FAKE, qo=FAKE + (1 << 16), k=far, v=far)
+        args[name] = FAKE + (1 << 16) + 3 * row - 16
+        assert store(gd, ref, **args) == INVAL and "k or v" in L.gemm_decode_last_error().decode()

@@ -272,3 +272,31 @@ def test_refusals(gd):
         gd.kv_q8_load(c, slots, None, None, 2)
     with pytest.raises(gd.GemmDecodeError, match="GD_ESHAPE"):
         gd.kv_q8_load(gd.kv_q8_alloc(2, 20, 1, 64), slots, k, k, 2)
+
+
+def test_outputs_beside_the_inputs(gd):
+    """q_out right behind q, between the rows of a wide projection, and (one token) at q inside a fused row: none of them
+    overlaps what is read."""
+    n, H, D = 2, 2, 64
+    rng = np.random.default_rng(12)
+    table = layer.rope_table(8, D, 10000.0).astype(np.float32)
+    pos, slots = np.array([3, 5], np.int32), dev(np.arange(n))
+    c = pool(gd, 1, 16, 1, D)
+    x = rng.standard_normal((n, H + 2, D)).astype(np.float32)
+    want = layer.rotate(x[:, :H], table, pos, False, fused=True)
+    buf = torch.full((n, 16, D), 7.0, device="cuda")         # a token's row, with room behind its heads
+    buf[:, :H + 2] = dev(x)
+    room = buf.view(-1)[(H + 2) * D:(H + 2) * D + n * H * D].view(n, H, D)
+    q, k, v = buf[:, :H], buf[:, H:H + 1], buf[:, H + 1:H + 2]
+    gd.kv_q8_store(c, k, v, slots, n, q=q, q_out=room, n_heads=H, rope=dev(table), positions=dev(pos))
+    assert np.array_equal(room.cpu().numpy(), want)
+    assert np.array_equal(buf[:, :H + 2].cpu().numpy(), x) and bool((buf.view(-1)[(H + 2 + n * H) * D:16 * D] == 7).all())
+    both = torch.cat([dev(x[:, :H]).view(-1), torch.zeros(n * H * D, device="cuda")]).view(2, n, H, D)
+    gd.kv_q8_store(c, k, v, slots, n, q=both[0], q_out=both[1], n_heads=H, rope=dev(table), positions=dev(pos))
+    assert np.array_equal(both.cpu().numpy(), np.stack([x[:, :H], want]))
+    one = dev(x[:1])
+    gd.kv_q8_store(c, one[:, H:H + 1], one[:, H + 1:], slots[:1], 1, q=one[:, :H], q_out=one[:, :H], n_heads=H, rope=dev(table),
+                   positions=dev(pos[:1]))
+    assert np.array_equal(one.cpu().numpy()[:, :H], want[:1]) and np.array_equal(one.cpu().numpy()[:, H:], x[:1, H:])
+    with pytest.raises(gd.GemmDecodeError, match="GD_EINVAL"):
+        gd.kv_q8_store(c, k, v, slots, n, q=both[0], q_out=both.view(-1)[64:64 + n * H * D].view(n, H, D), n_heads=H)
