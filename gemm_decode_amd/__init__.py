@@ -417,13 +417,23 @@ def _dtype(t, name):
         raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor") from None
 
 
+_device_and_stream = []   # how torch is asked for the current device and its stream
+
+
 def _current():
     """(index of the current device, torch's current stream on it)."""
-    import torch
-    if not torch.cuda.is_initialized():
-        torch.cuda.init()
-    i = torch._C._cuda_getDevice()
-    return i, torch._C._cuda_getCurrentRawStream(i)   # 0.1 us; a torch.cuda.Stream object takes 1.1
+    if not _device_and_stream:
+        import torch
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        # The calls below torch.cuda's: 0.1 us, where a torch.cuda.Stream object takes 1.1. They are not public: a torch
+        # without them is asked the public way.
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _device_and_stream[:] = device, stream
+    device, stream = _device_and_stream
+    i = device()
+    return i, stream(i)
 
 
 def _on(index, t, dtype, numel, name):

@@ -84,3 +84,21 @@ def test_rows_of_another_order_are_refused(gd):
     for other in (t.view(5, 64, 6), t.view(5, 12, 32), t.view(5, 3, 128)):
         with pytest.raises(ValueError, match="k must be"):
             gd._token_rows(-1, other, torch.float32, 5, 384, "k", 64)
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_current_device_and_stream_without_private_calls(gd, monkeypatch, private):
+    """The device and stream come from torch's public functions where the quick ones are not there."""
+    asked = []
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: asked.append("public") or 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda i: type("S", (), {"cuda_stream": 40 + i}))
+    for name, value in (("_cuda_getDevice", lambda: 5), ("_cuda_getCurrentRawStream", lambda i: 70 + i)):
+        if private:
+            monkeypatch.setattr(torch._C, name, value, raising=False)
+        else:
+            monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(gd, "_device_and_stream", [])
+    assert gd._current() == ((5, 75) if private else (3, 43))
+    assert gd._current() == ((5, 75) if private else (3, 43))   # asked anew, not kept
+    assert len(asked) == (0 if private else 2)
