@@ -80,7 +80,7 @@ struct AttnArgs {
     void *out;
     const int32_t *page_table, *kv_lens, *q_start;
     const uint64_t *tree;
-    int64_t max_pages, n_seqs, n_q, n_heads, max_q, max_kv_len;
+    int64_t max_pages, n_q, n_heads, max_q, max_kv_len;
     int64_t chunk;         // keys per part, a multiple of kGroupKeys
     int32_t splits;        // parts of the longest sequence
     int32_t row_block0, row_blocks;   // the launch's first block of 16 RT rows, and how many
@@ -978,7 +978,7 @@ extern "C" int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, c
     AttnArgs a;
     a.c = *cache;
     a.q = q, a.out = out, a.page_table = page_table, a.kv_lens = kv_lens, a.q_start = q_start, a.tree = tree_mask;
-    a.max_pages = max_pages, a.n_seqs = n_seqs, a.n_q = n_q, a.n_heads = n_heads, a.max_q = max_q;
+    a.max_pages = max_pages, a.n_q = n_q, a.n_heads = n_heads, a.max_q = max_q;
     a.max_kv_len = max_kv_len, a.scale = scale, a.softcap = softcap;
     a.chunk = p.chunk, a.splits = static_cast<int32_t>(p.splits);
     // 16-key tiles (fewer than 2^27) to pages by a multiplication: with 2^(L-1) < per <= 2^L and

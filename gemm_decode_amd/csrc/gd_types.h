@@ -36,12 +36,6 @@ __device__ __forceinline__ void store4(T *p, f32x4 v) {
     *reinterpret_cast<typename Vec4<T>::type *>(p) = __builtin_convertvector(v, typename Vec4<T>::type);
 }
 
-// v rounded to T and back.
-template <typename T>
-__device__ __forceinline__ f32x4 round_to(f32x4 v) {
-    return __builtin_convertvector(__builtin_convertvector(v, typename Vec4<T>::type), f32x4);
-}
-
 inline bool dtype_ok(int32_t dtype) { return dtype == GD_F32 || dtype == GD_F16 || dtype == GD_BF16; }
 inline int64_t dtype_size(int32_t dtype) { return dtype == GD_F32 ? 4 : 2; }
 

@@ -52,7 +52,7 @@ struct StoreArgs {
     const f32x2 *rope;
     const int32_t *positions;
     const int64_t *slots;
-    int64_t q_stride, k_stride, v_stride, n_pos, n_tok;
+    int64_t q_stride, k_stride, v_stride, n_pos;
     int32_t n_heads, rot, interleaved, page_shift;
     gd_kv_q8 c;
 };
@@ -436,7 +436,7 @@ extern "C" int kv_q8_store(const gd_kv_q8 *cache, const void *q, int64_t q_strid
     a.q = q, a.k = k, a.v = v, a.q_out = q_out;
     a.rope = reinterpret_cast<const f32x2 *>(rope);
     a.positions = positions, a.slots = slots;
-    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.n_pos = n_pos, a.n_tok = n_tok;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.n_pos = n_pos;
     a.n_heads = static_cast<int32_t>(n_heads), a.rot = static_cast<int32_t>(rot_dim), a.interleaved = interleaved != 0;
     a.page_shift = page_shift_of(cache->page_size);
     a.c = *cache;
