@@ -51,6 +51,7 @@
 // rounding and near a f16 result's. Sums, maxima and the softmax are f32. The
 // scales of the values are brought near f16's upper end by a power of two per
 // wave, which follows the largest scale seen.
+#include <cmath>
 #include <type_traits>
 
 #include "gd_internal.h"
@@ -86,7 +87,8 @@ struct AttnArgs {
     int32_t row_block0, row_blocks;   // the launch's first block of 16 RT rows, and how many
     uint32_t page_magic;   // tile / (page_size / 16) = tile * page_magic >> page_shift
     int32_t page_shift, page_tiles;   // page_size / 16
-    float scale, softcap;
+    float factor, softcap;   // factor 2^factor_exp: from q . k to a score over the cap, or times log2 e without a cap
+    int32_t factor_exp;
     float *part_o, *part_ml;
 };
 
@@ -493,7 +495,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 || NS == 1 ? 2 : 1) void attn_q8
         }
         mx = max_of_row<kPerRow>(mx);
         const int e = mx > 0.0f && mx <= 3.40282347e38f ? 14 - __builtin_amdgcn_frexp_expf(mx) : 0;
-        if (d0 == 0) lds_scale[row] = ldexpf(a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e, -e);
+        // Finite, so that a product of 0 stays a score of 0 (a larger factor would take any other past the cap).
+        if (d0 == 0) lds_scale[row] = fminf(fmaxf(ldexpf(a.factor, a.factor_exp - e), -3.40282347e38f), 3.40282347e38f);
         f16x2 hi[E / 2], lo[E / 2];
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
@@ -979,7 +982,12 @@ extern "C" int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, c
     a.c = *cache;
     a.q = q, a.out = out, a.page_table = page_table, a.kv_lens = kv_lens, a.q_start = q_start, a.tree = tree_mask;
     a.max_pages = max_pages, a.n_q = n_q, a.n_heads = n_heads, a.max_q = max_q;
-    a.max_kv_len = max_kv_len, a.scale = scale, a.softcap = softcap;
+    a.max_kv_len = max_kv_len, a.softcap = softcap;
+    // apart from its power of two: scale / softcap can pass f32's range where, times the queries', it does not
+    int factor_exp;
+    a.factor = static_cast<float>(std::frexp(
+        softcap > 0.0f ? static_cast<double>(scale) / softcap : static_cast<double>(scale) * kLog2e, &factor_exp));
+    a.factor_exp = factor_exp;
     a.chunk = p.chunk, a.splits = static_cast<int32_t>(p.splits);
     // 16-key tiles (fewer than 2^27) to pages by a multiplication: with 2^(L-1) < per <= 2^L and
     // magic = ceil(2^(31+L) / per), tile * (magic * per - 2^(31+L)) < 2^(27+L), so the quotient is exact.

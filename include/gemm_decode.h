@@ -582,7 +582,8 @@ int kv_q8_load(const gd_kv_q8 *cache, const int64_t *slots, void *k_out, void *v
  * its ancestors) or, without masks, if i <= t.
  *   s_j = scale * q . k_j, then softcap * tanh(s_j / softcap) if softcap > 0;
  *   out = sum over seen j of exp(s_j - max s) v_j / sum of exp(s_j - max s);
- * a row that sees no key gets zeros. A drafted key that no row of its sequence
+ * scores, without a softcap, lie within f32's range (|s_j| < 2^126). A row that
+ * sees no key gets zeros. A drafted key that no row of its sequence
  * sees need not be stored.
  *   q, out      device dtype [n_q][n_heads][head_dim], finite; head h reads KV
  *               head h / (n_heads / n_kv_heads). 16-byte aligned; out must not

@@ -524,3 +524,22 @@ def test_rows_of_another_order_are_refused(gd):
     c.q = c.q.transpose(0, 1).contiguous()
     with pytest.raises(ValueError, match="q must be"):
         c.run(out=torch.empty(3, 4, 64, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+@pytest.mark.parametrize("scale,cap,top", [(1.0, 1e-39, 0.0), (1.0, 1e-39, 1.0), (1.0, 1e-30, 1e30), (3e38, 0.0, 0.0), (-3e38, 1e-3, 0.0),
+                                           (3e38, 1e-3, 1e-3)])
+def test_factors_past_f32(gd, T, scale, cap, top):
+    """scale / softcap (or scale log2 e) past f32's range, with keys of zeros among the others: their scores are 0 and not
+    NaN, and a cap of next to nothing leaves the mean of the values."""
+    c = Case(gd, [90], [2], 4, 2, 64, 16, T, seed=14)
+    c.q = (c.q.double() / c.q.double().abs().max() * top).to(T)
+    codes = np.random.default_rng(3).integers(-127, 128, (90, 64))
+    codes[::3] = 0
+    overwrite(c, 0, codes, np.full((90, 2), 0.01))
+    got, (want, _) = c.run(scale=scale, cap=cap).double().cpu().numpy(), c.want(scale=scale, cap=cap)
+    vmax = np.abs(c.v[0]).max()
+    if cap != 1e-3:
+        mean = np.repeat(np.stack([c.v[0][:, :89].mean(1), c.v[0].mean(1)]), 2, axis=1)
+        assert np.allclose(want, mean, atol=1e-12)
+    assert np.abs(got - want).max() <= (1e-5 + (2.0 ** -10 + torch.finfo(T).eps / 2 if T != F32 else 0)) * vmax
