@@ -543,3 +543,43 @@ def test_factors_past_f32(gd, T, scale, cap, top):
         mean = np.repeat(np.stack([c.v[0][:, :89].mean(1), c.v[0].mean(1)]), 2, axis=1)
         assert np.allclose(want, mean, atol=1e-12)
     assert np.abs(got - want).max() <= (1e-5 + (2.0 ** -10 + torch.finfo(T).eps / 2 if T != F32 else 0)) * vmax
+
+
+@pytest.mark.parametrize("T", [F32, BF16])
+@pytest.mark.parametrize("n", [8200, 9001, 17000])
+@pytest.mark.parametrize("at", ["early", "late", "none"])
+def test_more_than_64_parts(gd, T, n, at):
+    """One sequence and KV head: 65, 71 and 133 parts, which the joining launch takes 64 at a time, the last batch partly
+    filled. One key's score is far above the others' in the first batch or in the last part, so that the sums before (or
+    behind) it are rescaled."""
+    H, D = 3, 128
+    c = Case(gd, [n], [1], H, 1, D, 16, T, seed=n)
+    assert gd.attn_decode_q8_workspace_bytes(1, 1, H, 1, D, 1, n) >= 65 * H * (D + 2) * 4
+    if at != "none":
+        rng = np.random.default_rng(1)
+        codes, scales = rng.integers(-127, 128, (n, D)), rng.uniform(0.3, 1.0, (n, D // 32)) / 60
+        j = 130 if at == "early" else n - 2
+        q0 = c.q[0, 0].double().numpy()
+        codes[j] = np.where(q0 > 0, 127, -127)
+        c.q = c.q[:, :1].expand(-1, H, -1).contiguous()
+        overwrite(c, 0, codes, scales)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_trees_in_f16(gd, D):
+    """Random trees of 64, 9 and 1 drafted tokens, capped and not, with rows that see nothing drafted or nothing at all."""
+    rng = np.random.default_rng(D + 1)
+    qs, lens, words = [64, 9, 1], [200, 9, 33], []
+    for t in qs:
+        seen = []
+        for i in range(t):
+            seen.append((seen[rng.integers(0, i)] if i else 0) | 1 << i)
+        words += seen
+    words[3] = words[64] = 0
+    words[5] = (1 << 64) - 1
+    c = Case(gd, lens, qs, 8, 2, D, 16, F16, seed=15, words=words)
+    got = c.run()
+    c.check(got)
+    assert not got[64].any()
+    c.check(c.run(cap=2.0), cap=2.0)
