@@ -414,9 +414,12 @@ __device__ __forceinline__ void add_scaled(float (&s)[4], f32x4 d, const float (
 }
 
 // NS = 2: operands in two f16 parts (f32 inputs), NS = 1: in one. A workgroup
-// serves RT tiles of 16 query rows.
+// serves RT tiles of 16 query rows. Waves a SIMD: one tile at head dims 64 and 128 is
+// held to three, which f32 at 128 reaches with 166 registers and is on the edge of (left
+// alone, it takes 181 or 165 with the text around it: 32 sequences of 8k to 16k keys 180
+// us with two waves, 172 with three; 4 rows of 16 sequences 56 and 59).
 template <typename T, int D, int NS, int RT>
-__global__ __launch_bounds__(kThreads, D <= 128 || NS == 1 ? 2 : 1) void attn_q8_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D <= 128 && RT == 1 ? 3 : D <= 128 || NS == 1 ? 2 : 1) void attn_q8_kernel(AttnArgs a) {
     constexpr int C = D / 32, VB = D / 16, R = 16 * RT;
     typedef f32x4 Joined[R][D / 4 + 1];   // a wave's sums, padded: 16 lanes write one column
     __shared__ union {
@@ -496,7 +499,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 || NS == 1 ? 2 : 1) void attn_q8
         mx = max_of_row<kPerRow>(mx);
         const int e = mx > 0.0f && mx <= 3.40282347e38f ? 14 - __builtin_amdgcn_frexp_expf(mx) : 0;
         // Finite, so that a product of 0 stays a score of 0 (a larger factor would take any other past the cap).
-        if (d0 == 0) lds_scale[row] = fminf(fmaxf(ldexpf(a.factor, a.factor_exp - e), -3.40282347e38f), 3.40282347e38f);
+        if (d0 == 0) lds_scale[row] = ldexpf(a.factor, a.factor_exp - e < 127 ? a.factor_exp - e : 127);
         f16x2 hi[E / 2], lo[E / 2];
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
