@@ -30,10 +30,11 @@
 // and are handed round by DPP.
 //
 // What bounds it. 32 sequences of 16k to 32k keys (32 / 8 heads, head dim 128, bf16,
-// 1.75 GB of cache): 280 us, 6.2 TB/s, 91 % of what a streaming read reaches; bound by
-// memory. Few keys (4096 of one sequence, f32: 6.6 us) are bound by the chain of
-// dependent loads before the first product, many rows (64 tokens of four sequences, 200
-// TFLOP/s) by vector instructions, some 590 for 32 keys and 32 rows.
+// 1.75 GB of cache): 285 us with the 5 of the joining launch, 6.1 TB/s, 89 % of what a
+// streaming read reaches; bound by memory. Few keys (4096 of one sequence, f32: 6.6 us, and
+// 3.8 for the joining launch) are bound by the chain of dependent loads before the first
+// product, many rows (64 tokens of four sequences, 210 TFLOP/s) by vector instructions,
+// some 590 for 32 keys and 32 rows.
 //
 // Waits. Loads complete in order and a wait counts those behind the one it is for, so a
 // wait is only as exact as that count is the same on every path: loads stand outside
@@ -782,7 +783,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 && RT == 1 ? 3 : D <= 128 || NS 
 
 // Joins the parts of one query row and head. A step takes 64 parts: lane i of every
 // wave holds part i's maximum and sum, wave w adds up the parts w, w + 4, ..., D/64
-// dims to a lane, all of them loaded before any is used. 4.7 us for 1024 rows of 16
+// dims to a lane, all of them loaded before any is used. 5.2 us for 1024 rows of 16
 // parts (8.5 MB), of which a launch is about 2: bound by its two loads in a chain.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
@@ -839,18 +840,25 @@ __global__ __launch_bounds__(kThreads) void attn_q8_merge_kernel(AttnArgs a) {
 }
 
 // Parts per sequence. While there is not a workgroup for every CU at one part each
-// (kCus), as many as give each CU the two that it holds (kFill), however short they get:
-// one that starts when another has ended costs a whole round more. A call with more rows
-// than a block is planned for half as many again (kFillBlocks), since the later blocks
-// are empty in sequences of fewer rows. Beyond that, parts of no fewer than kMinSteps
-// steps a wave, up to kFine workgroups in all: many of them even out the end of the
-// launch and sequences of different lengths, but each prepares its queries and joins its
-// waves anew. Measured (bf16, head dim 128, 32 / 8 heads), planned for 384, 512 and 768:
-// 8 sequences of 2k to 4k keys 20.4, 16.6 and 17.9 us, one of 32k 21.0, 18.0 and 20.9,
-// trees of up to 13 over 2.5k to 5k keys (two blocks) 26.9, 29.6 and 24.6. 128 sequences of
-// 1k keys 50 us with parts of 4 steps, 41 with 8; 48 of 512 keys (one and a half for each
-// CU) 13.4 us whole, 16.3 in two parts; 32 sequences of 16k to 32k keys 281 with 4096
-// workgroups or 6144, and 6 % more with 2048.
+// (kCus), parts are made for kFill workgroups, however short they get; a call with more
+// rows than a block for kFillBlocks, since the later blocks are empty in sequences of fewer
+// rows. (Parts are rounded up: 80 groups become 560.) Beyond that, parts of no fewer than
+// kMinSteps steps a wave, up to kFine workgroups in all: many of them even out the end of
+// the launch and sequences of different lengths, but each prepares its queries and joins
+// its waves anew.
+// kFill and kFillBlocks are what measured best on these shapes, not what a CU holds: of
+// one tile of rows that is four workgroups at head dim 64, three at 128, and two (f32: one)
+// at 256; of two tiles three and two. Measured (bf16, head dim 128, 32 / 8 heads), planned
+// for 384, 512 and 768: 8 sequences of 2k to 4k keys 20.4, 16.6 and 17.9 us, one of 32k 21.0,
+// 18.0 and 20.9, trees of up to 13 over 2.5k to 5k keys (two blocks) 26.9, 29.6 and 24.6.
+// Where they lose: two blocks that are both full are slower planned for 768 than for 512
+// (13 rows of each of three sequences of 5k keys 30.7 and 25.3 us, of five 43 and 42, 16 rows
+// of eight of 4k 52 and 44, 33 rows of two of 8k 57 and 54, 64 rows of one 45 and 39), and f32
+// at head dim 256 planned for 512 than for 256 (8 sequences of 2k to 4k keys 24.3 and 20.4 us,
+// one of 32k 27.9 and 21.9).
+// kMinSteps: 128 sequences of 1k keys 50 us with parts of 4 steps, 41 with 8; 48 of 512 keys
+// (one and a half for each CU) 13.4 us whole, 16.3 in two parts. kFine: 32 sequences of 16k
+// to 32k keys 281 with 4096 workgroups or 6144, and 6 % more with 2048.
 constexpr int kCus = 256, kFill = 512, kFillBlocks = 768, kFine = 4096, kMinSteps = 8;
 
 // How the work is cut: rows per workgroup, and keys per part.

@@ -146,10 +146,11 @@ __device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*
 // 256 W R elements are read once); what is past them is read again in the second pass,
 // from h_out if that is written (it may overwrite an input), each thread reading back its
 // own. A pair is one load of a 16-bit type, and four lanes make a block of 32 (one float4
-// a thread and eight lanes: 4099 rows of 4096 in bf16 30.5 us to q8_0 and 33.8 to planes,
-// where this takes 26.6 and 30.8). That is 4.5 TB/s, bound by memory with the row's sum
-// between its reads and its writes; one row: 3.3 us, bound by the chain load, sum,
-// barrier, codes, store.
+// a thread and eight lanes: 4099 rows of 4096 in bf16 3.9 us more to q8_0 and 3.0 to
+// planes). 4099 rows of 4096 in bf16: 27.8 us to q8_0, 4.3 TB/s, and 32.8 to planes with the
+// inputs in memory, 24.9 and 30.7 with them in the last cache; bound by memory with the
+// row's sum between its reads and its writes. One row: 3.2 us, bound by the chain load,
+// sum, barrier, codes, store.
 template <typename T, int R, int W, bool kTernary>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_quant_kernel(const T *x, const T *res, const float *__restrict__ weight,
                                                                T *h_out, void *__restrict__ out,
@@ -365,7 +366,8 @@ void launch_norm(const void *x, const void *residual, const float *weight, void 
         // Many short rows: a wave each (16384 rows of 512 in bf16: 13.8 us, 41.8 with eight waves a row, most of
         // them idle; 1024 rows of 1024 4.7 and 5.6, 512 of them 4.5 and 4.2, one 3.2 and 2.8). Else eight waves a
         // row (one f32 row of 4096: 3.4 us, 3.9 with four waves; 4099 rows in bf16 26.4 and 27.3; sixteen for rows
-        // past 4096: 1024 rows of 14336 in bf16 27.1 where eight take 25.8, one in f32 5.9 and 6.5).
+        // past 4096: 1024 rows of 14336 in bf16 27.1 where eight take 25.8, one in f32 5.9 and 6.5). Each pair of
+        // figures is of one run, inputs of three states in turn; single figures differ by 5 % from card to card.
         const bool many = n >= 1024;
         if (K <= 512 && many)
             launch(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});

@@ -541,8 +541,9 @@ int rope_table(float *table, int64_t n_pos, int64_t rot_dim, double base,
  *   q, k, v    device dtype, token t's heads at q + t * q_stride (n_heads head
  *              rows of head_dim), k + t * k_stride, v + t * v_stride
  *              (n_kv_heads): parts of one projection's row, for instance.
- *              Strides in elements, multiples of 16 bytes, at most 2^36. All values finite,
- *              below 65504 * 127 in k and v (the scales are f16).
+ *              Strides in elements, multiples of 16 bytes, at most 2^36. All values
+ *              finite, those of v and of the rotated k (a pair can grow by a factor
+ *              of sqrt 2, times the table's) below 65504 * 127: the scales are f16.
  *   q_out      device dtype [n_tok][n_heads][head_dim]; may be q itself if
  *              q_stride is n_heads * head_dim or n_tok is 1, must not overlap q
  *              otherwise, nor k or v. n_heads may be 0, with q and q_out NULL
