@@ -367,7 +367,7 @@ void launch_norm(const void *x, const void *residual, const float *weight, void 
         // them idle; 1024 rows of 1024 4.7 and 5.6, 512 of them 4.5 and 4.2, one 3.2 and 2.8). Else eight waves a
         // row (one f32 row of 4096: 3.4 us, 3.9 with four waves; 4099 rows in bf16 26.4 and 27.3; sixteen for rows
         // past 4096: 1024 rows of 14336 in bf16 27.1 where eight take 25.8, one in f32 5.9 and 6.5). Each pair of
-        // figures is of one run, inputs of three states in turn; single figures differ by 5 % from card to card.
+        // figures is of one run, inputs of two or three states in turn; single figures differ by 5 % from card to card.
         const bool many = n >= 1024;
         if (K <= 512 && many)
             launch(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
