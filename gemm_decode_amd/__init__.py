@@ -106,6 +106,14 @@ def _declare():
         "attn_decode_q8": [_P, _P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _F32, _F32, _I32, _P, _SZ,
                            _P],
         "attn_decode_q8_workspace_bytes": [_I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_SZ)],
+        "rmsnorm_sandwich_q8_0": [_P, _P, _P, _I64, _P, _P, _F32, _F32, _P, _P, _P, _I64, _I64, _F32, _I32, _P],
+        "rmsnorm_sandwich_ternary_act": [_P, _P, _P, _I64, _P, _P, _F32, _F32, _P, _P, _P, _P, _I64, _I64, _F32, _I32,
+                                         _P],
+        "q1_q8_linear": [_P, _P, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _SZ, _P],
+        "q1_q8_gated": [_P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I32, _P, _SZ, _P],
+        "q1_q8_linear_workspace_bytes": [_I64, _I64, ctypes.POINTER(_SZ)],
+        "token_logprobs": [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _F32, _F32, _I32, _P, _SZ, _P],
+        "token_logprobs_workspace_bytes": [_I64, _I64, _I64, ctypes.POINTER(_SZ)],
         "gemm_decode_fill": [_P, ctypes.c_size_t, ctypes.c_uint32, _P],
         "gemm_decode_stream_read": [_P, ctypes.c_size_t, ctypes.c_int32, _P, _I64, _P],
     }
@@ -493,6 +501,51 @@ def rmsnorm_ternary_act(x, residual, weight, h_out, planes, x_scale, n: int, K: 
                                     _on(i, x_scale, torch.float32, n, "x_scale"), n, K, eps, dt, stream))
 
 
+def _sandwich(i, x, post_weight, residual, weight, h_out, gate, gate_index, n, K):
+    """The arguments that the sandwich norms share, checked."""
+    import torch
+    rows, n_gates = n * K, 0
+    if gate is not None:
+        n_gates, rest = divmod(gate.numel(), K) if K > 0 else (0, 1)
+        if rest or n_gates == 0 or gate.shape[-1] != K:
+            raise ValueError(f"gate must be [n_gates, {K}], got {list(gate.shape)}")
+    return (_on(i, x, x.dtype, rows, "x"),
+            None if post_weight is None else _on(i, post_weight, torch.float32, K, "post_weight"),
+            None if gate is None else _on(i, gate, x.dtype, None, "gate"), n_gates,
+            None if gate_index is None else _on(i, gate_index, torch.int32, n, "gate_index"),
+            _on(i, residual, x.dtype, rows, "residual"), _on(i, weight, torch.float32, K, "weight"),
+            None if h_out is None else _on(i, h_out, x.dtype, rows, "h_out"))
+
+
+def rmsnorm_sandwich_q8_0(x, post_weight, residual, weight, h_out, a_q8, n: int, K: int, eps: float, gate=None,
+                          gate_index=None, residual_scale: float = 1.0, block_scale: float = 1.0):
+    """The norms behind and before a block: h = residual_scale * residual +
+    block_scale * gate * u, u the RMS norm of the block's output x times
+    post_weight (None: x itself), and the RMS norm of h times `weight` as q8_0
+    blocks. x, residual, h_out (or None; may be x or residual) are [n, K] of one
+    type, gate (or None) [n_gates, K] of the same; gate_index int32 [n] names each
+    row's gate (None: one gate for all rows, or one per row); weights float32 [K]."""
+    import torch
+    dt, (i, stream) = _dtype(x, "x"), _current()
+    xp, pp, gp, ng, ip, rp, wp, hp = _sandwich(i, x, post_weight, residual, weight, h_out, gate, gate_index, n, K)
+    _check(_lib.rmsnorm_sandwich_q8_0(xp, pp, gp, ng, ip, rp, residual_scale, block_scale, wp, hp,
+                                      _on(i, a_q8, torch.uint8, n * (K // 32) * 34 if K % 32 == 0 else None, "a_q8"),
+                                      n, K, eps, dt, stream))
+
+
+def rmsnorm_sandwich_ternary_act(x, post_weight, residual, weight, h_out, planes, x_scale, n: int, K: int, eps: float,
+                                 gate=None, gate_index=None, residual_scale: float = 1.0, block_scale: float = 1.0):
+    """rmsnorm_sandwich_q8_0 with one scale per row: int8 bit planes (int32
+    [n * 8 * K/32]) and scales (float32 [n])."""
+    import torch
+    dt, (i, stream) = _dtype(x, "x"), _current()
+    xp, pp, gp, ng, ip, rp, wp, hp = _sandwich(i, x, post_weight, residual, weight, h_out, gate, gate_index, n, K)
+    _check(_lib.rmsnorm_sandwich_ternary_act(
+        xp, pp, gp, ng, ip, rp, residual_scale, block_scale, wp, hp,
+        _on(i, planes, torch.int32, n * 8 * (K // 32) if K % 32 == 0 else None, "planes"),
+        _on(i, x_scale, torch.float32, n, "x_scale"), n, K, eps, dt, stream))
+
+
 def q8_0_dequantize(a_q8, y, n: int, K: int):
     """The values of q8_0 blocks: y [n, K] (float32, float16 or bfloat16)."""
     import torch
@@ -508,6 +561,89 @@ def ternary_dequantize_act(planes, x_scale, y, n: int, K: int):
     _check(_lib.ternary_dequantize_act(_on(i, planes, torch.int32, n * 8 * (K // 32) if K % 32 == 0 else None, "planes"),
                                        _on(i, x_scale, torch.float32, n, "x_scale"), _on(i, y, y.dtype, n * K, "y"),
                                        n, K, dt, stream))
+
+
+# ---------------------------------------------- products with an epilogue
+
+ACT_NONE, ACT_RELU, ACT_RELU2, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(6)
+
+_plane_bytes = {}    # of a weight by its sizes, and
+_linear_bytes = {}   # workspace bytes: pure functions, asked for at each launch
+
+
+def _kept(table, sizes, of):
+    """of(*sizes), kept in `table`."""
+    got = table.get(sizes)
+    if got is None:
+        got = of(*sizes)
+        if len(table) >= 4096:
+            table.clear()
+        table[sizes] = got
+    return got
+
+
+def q1_q8_linear_workspace_bytes(K: int, n_act: int) -> int:
+    """Workspace bytes of q1_q8_linear and q1_q8_gated (0 up to four columns)."""
+    b = ctypes.c_size_t()
+    _check(_lib.q1_q8_linear_workspace_bytes(K, n_act, ctypes.byref(b)))
+    return b.value
+
+
+def _linear(i, a_q8, y, y_q8, rows, K, n_act, residual, workspace):
+    """What q1_q8_linear and q1_q8_gated check alike: (a_q8, residual, y, y_q8, dtype, workspace tensor, its address and
+    bytes)."""
+    import torch
+    if y is None:
+        dtype, code = (torch.float32, 0) if residual is None else (residual.dtype, _dtype(residual, "residual"))
+    else:
+        dtype, code = y.dtype, _dtype(y, "y")
+    need = _kept(_linear_bytes, (K, n_act), q1_q8_linear_workspace_bytes)
+    space = None
+    if workspace is not None:
+        need, space = workspace.numel(), _on(i, workspace, torch.uint8, None, "workspace")
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=a_q8.device)
+        space = workspace.data_ptr()
+    return (_on(i, a_q8, torch.uint8, n_act * (K // 32) * 34, "a_q8"),
+            None if residual is None else _on(i, residual, dtype, n_act * rows, "residual"),
+            None if y is None else _on(i, y, dtype, n_act * rows, "y"),
+            None if y_q8 is None else _on(i, y_q8, torch.uint8, n_act * (rows // 32) * 34 if rows % 32 == 0 else None, "y_q8"),
+            code, workspace, space, need)
+
+
+def q1_q8_linear(bits_plane, scale_plane, a_q8, y, rows: int, K: int, n_act: int = 1, bias=None, act: int = ACT_NONE,
+                 residual=None, y_q8=None, workspace=None):
+    """y = act(W a + bias) + residual for Q1 planes of a [rows, K] weight and
+    n_act q8_0 columns: y and residual [n_act, rows] (float32, float16 or
+    bfloat16; y may be residual), bias float32 [rows], and the same values as
+    q8_0 blocks in y_q8 (uint8 [n_act * rows/32 * 34]) where that is given; y may
+    then be None. The workspace (uint8) is allocated here when one is needed and
+    not given."""
+    import torch
+    i, stream = _current()
+    bb, sb = _kept(_plane_bytes, (rows, K), q1_planes_bytes)
+    ap, rp, yp, qp, dt, workspace, space, need = _linear(i, a_q8, y, y_q8, rows, K, n_act, residual, workspace)
+    _check(_lib.q1_q8_linear(_on(i, bits_plane, torch.uint8, bb, "bits_plane"),
+                             _on(i, scale_plane, torch.uint8, sb, "scale_plane"), ap,
+                             None if bias is None else _on(i, bias, torch.float32, rows, "bias"), act, rp, yp, qp, rows, K,
+                             n_act, dt, space, need, stream))
+
+
+def q1_q8_gated(gate_bits, gate_scales, up_bits, up_scales, a_q8, y, rows: int, K: int, n_act: int = 1,
+                act: int = ACT_SILU, gate_bias=None, up_bias=None, y_q8=None, workspace=None):
+    """y = act(G a + gate_bias) * (U a + up_bias) for the Q1 planes of a gated
+    feed-forward block's two [rows, K] weights; y, y_q8 and the workspace as
+    q1_q8_linear's."""
+    import torch
+    i, stream = _current()
+    bb, sb = _kept(_plane_bytes, (rows, K), q1_planes_bytes)
+    ap, _, yp, qp, dt, workspace, space, need = _linear(i, a_q8, y, y_q8, rows, K, n_act, None, workspace)
+    _check(_lib.q1_q8_gated(_on(i, gate_bits, torch.uint8, bb, "gate_bits"),
+                            _on(i, gate_scales, torch.uint8, sb, "gate_scales"),
+                            _on(i, up_bits, torch.uint8, bb, "up_bits"), _on(i, up_scales, torch.uint8, sb, "up_scales"), ap,
+                            None if gate_bias is None else _on(i, gate_bias, torch.float32, rows, "gate_bias"),
+                            None if up_bias is None else _on(i, up_bias, torch.float32, rows, "up_bias"), act, yp, qp, rows,
+                            K, n_act, dt, space, need, stream))
 
 
 # ------------------------------------------------------------ 8-bit cache
@@ -691,6 +827,64 @@ def attn_decode_q8(q, cache: KVCacheQ8, page_table, kv_lens, q_start, tree_mask,
                                None if tree_mask is None else _on(i, tree_mask, torch.int64, n_q, "tree_mask"),
                                n_seqs, n_q, n_heads, max_q, max_kv_len, scale, softcap, dt,
                                space, need, stream))
+
+
+# -------------------------------------------------------- log probabilities
+
+_logprobs_bytes = {}   # workspace bytes by sizes
+
+
+def token_logprobs_workspace_bytes(n: int, V: int, k: int) -> int:
+    """Workspace bytes that serve this call and every one no larger in n, V and k."""
+    b = ctypes.c_size_t()
+    _check(_lib.token_logprobs_workspace_bytes(n, V, k, ctypes.byref(b)))
+    return b.value
+
+
+def token_logprobs(logits, tokens, logprobs, entropy, top_ids, top_logprobs, n: int, V: int, scale: float = 1.0,
+                   softcap: float = 0.0, workspace=None):
+    """Natural log probabilities of logits [n, V] (float32, float16 or bfloat16;
+    rows may be apart, as logits[:, :V] of a padded vocabulary), scaled (1 /
+    temperature) and capped: of tokens (int64 [n, n_given], -1: padding) into
+    logprobs (float32, the same shape), of each row's entropy (float32 [n]), and of the
+    k <= 64 largest logits (top_ids int64 [n, k], top_logprobs float32 [n, k]).
+    Pairs that are not asked for are None. The workspace (uint8) is allocated
+    here when one is needed and not given."""
+    import torch
+    dt, (i, stream) = _dtype(logits, "logits"), _current()
+    if logits.get_device() != i:
+        raise ValueError(f"logits is on {logits.device}, the current device is cuda:{i}")
+    shape = logits.shape
+    if len(shape) == 1 and n == 1 and shape[0] == V and logits.stride(0) == 1:
+        stride = V
+    elif len(shape) == 2 and shape[0] == n and shape[1] == V and (logits.stride(1) == 1 or V == 1):
+        stride = logits.stride(0) if n > 1 else V
+    else:
+        raise ValueError(f"logits must be [{n}, {V}] with contiguous rows, got {list(shape)}")
+
+    def of(a, b, first, second, names):
+        if (a is None) != (b is None):
+            raise ValueError(f"{names[0]} and {names[1]} come together")
+        if a is None:
+            return None, None, 0
+        if len(a.shape) not in (1, 2) or a.shape[0] != n or a.shape != b.shape:
+            raise ValueError(f"{names[0]} and {names[1]} must be [{n}, number each], got {list(a.shape)} and {list(b.shape)}")
+        if a.numel() == 0:
+            raise ValueError(f"{names[0]} is empty")
+        return _on(i, a, first, None, names[0]), _on(i, b, second, None, names[1]), a.numel() // n
+    tp, lp, n_given = of(tokens, logprobs, torch.int64, torch.float32, ("tokens", "logprobs"))
+    kp, kl, k = of(top_ids, top_logprobs, torch.int64, torch.float32, ("top_ids", "top_logprobs"))
+    space, need = None, 0
+    if workspace is not None:
+        need, space = workspace.numel(), _on(i, workspace, torch.uint8, None, "workspace")
+    else:
+        need = _kept(_logprobs_bytes, (n, V, k), token_logprobs_workspace_bytes)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+            space = workspace.data_ptr()
+    _check(_lib.token_logprobs(logits.data_ptr(), stride, tp, n_given, lp,
+                               None if entropy is None else _on(i, entropy, torch.float32, n, "entropy"), kp, kl, k, n, V,
+                               scale, softcap, dt, space, need, stream))
 
 
 # ------------------------------------------------------------ measurement

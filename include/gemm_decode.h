@@ -472,6 +472,35 @@ int rmsnorm_ternary_act(const void *x, const void *residual, const float *weight
                         uint32_t *planes, float *x_scale, int64_t n, int64_t K, float eps,
                         int32_t dtype, void *stream);
 
+/* Norms behind and before a block, with the block's gate and the residual scale:
+ * what stands between two blocks of a layer. With x the block's output,
+ *   u = x * rstd(x) * post_weight     (u = x without post_weight)
+ *   h = residual_scale * residual + block_scale * gate * u
+ * in f64, rounded to f32 and then to dtype, and the norm of h quantized as above.
+ * rstd(x) = 1 / sqrt(mean over the row of x^2 + eps), the same eps as h's.
+ *   x, residual  device dtype [n][K].
+ *   post_weight  device f32 [K] or NULL.
+ *   gate         device dtype [n_gates][K], or NULL (1; n_gates is ignored).
+ *   gate_index   device int32 [n], the gate of each row; a row whose index is
+ *                outside [0, n_gates) takes nothing of its block (h =
+ *                residual_scale * residual). NULL: needs n_gates = 1 (one for
+ *                all rows: a scale per channel) or n_gates = n (each row its own).
+ *   weight, h_out, a_q8, limits, errors  as rmsnorm_q8_0; h_out may be x or
+ *                residual itself, must not overlap them otherwise, nor gate.
+ * All pointers but gate_index (4) and a_q8 (2) 16-byte aligned; finite
+ * residual_scale and block_scale; n_gates < 2^23. */
+int rmsnorm_sandwich_q8_0(const void *x, const float *post_weight, const void *gate, int64_t n_gates,
+                          const int32_t *gate_index, const void *residual, float residual_scale,
+                          float block_scale, const float *weight, void *h_out, void *a_q8, int64_t n,
+                          int64_t K, float eps, int32_t dtype, void *stream);
+
+/* The same with one scale per row (planes and x_scale as rmsnorm_ternary_act). */
+int rmsnorm_sandwich_ternary_act(const void *x, const float *post_weight, const void *gate, int64_t n_gates,
+                                 const int32_t *gate_index, const void *residual, float residual_scale,
+                                 float block_scale, const float *weight, void *h_out, uint32_t *planes,
+                                 float *x_scale, int64_t n, int64_t K, float eps, int32_t dtype,
+                                 void *stream);
+
 /* The values that activations stand for: f32(code) * scale in f32, rounded
  * to dtype. y device dtype [n][K], 16-byte aligned. Requires K % 32 == 0 and
  * n * K < 2^34 - 1024. Errors: GD_EINVAL, GD_ESHAPE, GD_EALIGN, GD_ERANGE,
@@ -479,6 +508,65 @@ int rmsnorm_ternary_act(const void *x, const void *residual, const float *weight
 int q8_0_dequantize(const void *a_q8, void *y, int64_t n, int64_t K, int32_t dtype, void *stream);
 int ternary_dequantize_act(const uint32_t *planes, const float *x_scale, void *y, int64_t n, int64_t K,
                            int32_t dtype, void *stream);
+
+/* ====================================================================
+ * Q1_0 . q8_0 products with an epilogue
+ * ====================================================================
+ * The products of a layer together with what stands between them, for one
+ * decode token, a batch or a whole prompt. Weights and activations are those of
+ * q1_q8_gemv; the arithmetic is another one: every product d0 * d1 * code is
+ * exact, and sums are taken on the matrix cores in f32, in an order of their own
+ * (q1_q8_gemv keeps the stated order bit for bit, once per column). A sum t lies
+ * within (K/128 + 9) * 2^-23 * sum_k |W[r][k] a[c][k]| of the exact one. The bits
+ * of a column depend on K, rows and n_act, not on the other columns' values.
+ *
+ * Activation functions, within 2^-20 |t| of their value at t (RELU, RELU2: one
+ * rounding): */
+#define GD_ACT_NONE      0
+#define GD_ACT_RELU      1 /* max(t, 0)                                          */
+#define GD_ACT_RELU2     2 /* max(t, 0)^2                                        */
+#define GD_ACT_GELU      3 /* t * Phi(t), Phi the normal distribution's          */
+#define GD_ACT_GELU_TANH 4 /* t / (1 + exp(-2 sqrt(2/pi) (t + 0.044715 t^3)))    */
+#define GD_ACT_SILU      5 /* t / (1 + exp(-t))                                  */
+
+/* v[c][r] = act(sum_k W[r][k] a[c][k] + bias[r]) + residual[c][r], each step in
+ * f32; y = v rounded to dtype, y_q8 = v as q8_0 blocks (bit for bit what
+ * q8_0_quantize makes of v in f32), the next product's activations.
+ *   bits_plane, scale_plane  device Q1 planes of a rows x K weight (q1_repack).
+ *   a_q8       device, n_act*(K/32)*34 bytes of q8_0 blocks, 2-byte aligned.
+ *              A block whose scale is infinite or NaN makes its column's sums
+ *              NaN.
+ *   bias       device f32 [rows] or NULL.
+ *   act        a GD_ACT_ code.
+ *   residual   device dtype [n_act][rows] or NULL.
+ *   y          device dtype [n_act][rows], or NULL; may be residual itself, must
+ *              not overlap it otherwise.
+ *   y_q8       device, n_act*(rows/32)*34 bytes, 2-byte aligned, or NULL; needs
+ *              rows % 32 == 0 and finite v. One of y and y_q8 at least.
+ *   workspace  device, q1_q8_linear_workspace_bytes(K, n_act) bytes, 16-byte
+ *              aligned (NULL where that is 0); calls that share it must be
+ *              ordered.
+ * bias, residual and y are aligned to their element. Limits: rows <= 2^31 - 64,
+ * n_act <= 2^20, K <= 2^20. Errors: GD_EINVAL, GD_ESHAPE (K % 128, rows % 32),
+ * GD_EALIGN, GD_ERANGE (limits, workspace too small), GD_EHIP. */
+int q1_q8_linear(const void *bits_plane, const void *scale_plane, const void *a_q8, const float *bias,
+                 int32_t act, const void *residual, void *y, void *y_q8, int64_t rows, int64_t K,
+                 int64_t n_act, int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Both input products of a gated feed-forward block and what joins them:
+ * v[c][r] = act(sum_k G[r][k] a[c][k] + gate_bias[r]) * (sum_k U[r][k] a[c][k] +
+ * up_bias[r]), y and y_q8 as above. G and U are two rows x K weights. Limits,
+ * workspace and errors as q1_q8_linear. */
+int q1_q8_gated(const void *gate_bits, const void *gate_scales, const void *up_bits, const void *up_scales,
+                const void *a_q8, const float *gate_bias, const float *up_bias, int32_t act, void *y,
+                void *y_q8, int64_t rows, int64_t K, int64_t n_act, int32_t dtype, void *workspace,
+                size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of both: 0 up to four columns, else 100 * K per column, the
+ * columns rounded up to 32, over 32 (the activations as the matrix cores read
+ * them). Grows with n_act: one for the largest call serves every smaller one of
+ * the same K. Host only. Errors: GD_EINVAL, GD_ESHAPE, GD_ERANGE. */
+int q1_q8_linear_workspace_bytes(int64_t K, int64_t n_act, size_t *bytes);
 
 /* ====================================================================
  * 8-bit cache of keys and values
@@ -628,6 +716,45 @@ int attn_decode_q8(const gd_kv_q8 *cache, const void *q, void *out, const int32_
  * one). Host only. Errors as its size checks. */
 int attn_decode_q8_workspace_bytes(int64_t n_seqs, int64_t n_q, int64_t n_heads, int64_t n_kv_heads,
                                    int64_t head_dim, int64_t max_q, int64_t max_kv_len, size_t *bytes);
+
+/* ====================================================================
+ * Log probabilities
+ * ====================================================================
+ * What a server answers with beside a token: with
+ *   z_j = scale * x_j, or scale * softcap * tanh(x_j / softcap) if softcap > 0
+ *         (a logit of -infinity stays so: a banned token),
+ * the log probability of token j is lp_j = z_j - log(sum_i exp(z_i)), natural
+ * logarithms throughout, and the entropy -sum_j exp(lp_j) lp_j. The alternatives
+ * are the k largest logits x_j, larger ones first and of equal ones (0 and -0
+ * among them) the lower token first.
+ *   logits      device dtype, row i at logits + i * stride (in elements, stride >=
+ *               V; at most 2^40), aligned to the element: V and stride may be odd.
+ *   tokens      device int64 [n][n_given], the tokens asked for, in any order;
+ *               one outside [0, V) (-1: padding) gets 0. NULL if n_given is 0.
+ *   logprobs    device f32 [n][n_given] or NULL if n_given is 0.
+ *   entropy     device f32 [n] or NULL.
+ *   top_ids, top_logprobs  device int64 and f32 [n][k], both NULL if k is 0.
+ * A row with no token left (every logit -infinity) has entropy 0 and -infinity for
+ * its given tokens; alternatives that are not left are token -1 with -infinity.
+ * A row that holds a NaN or +infinity gives NaN for its entropy and log
+ * probabilities (0 for padding) and the tokens -1.
+ *   workspace   device, token_logprobs_workspace_bytes(...) bytes, 16-byte
+ *               aligned (NULL where that is 0); calls that share it must be
+ *               ordered.
+ * Accuracy: log probabilities and entropies within 2^-17 of their magnitude (of a
+ * confident token's as well, whose log probability is next to 0) plus 2^-100; with
+ * a softcap 2^-20 * scale * softcap more. One of n_given, k and entropy
+ * is asked for. Limits: 1 <= V <= 2^30, 1 <= n < 2^23, n_given <= 65536, k <= 64,
+ * n * n_given < 2^31, finite scale > 0, 0 <= softcap <= 1e30.
+ * Errors: GD_EINVAL, GD_EALIGN, GD_ERANGE, GD_EHIP. */
+int token_logprobs(const void *logits, int64_t stride, const int64_t *tokens, int64_t n_given,
+                   float *logprobs, float *entropy, int64_t *top_ids, float *top_logprobs, int64_t k,
+                   int64_t n, int64_t V, float scale, float softcap, int32_t dtype, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of such a call and of every one no larger in n, V and k. Host
+ * only. Errors: GD_EINVAL, GD_ERANGE. */
+int token_logprobs_workspace_bytes(int64_t n, int64_t V, int64_t k, size_t *bytes);
 
 /* ====================================================================
  * Measurement kernels  ("roofline.html": the FILL kernel writes a non-zero,

@@ -1,0 +1,217 @@
+"""GPU parity of the log probabilities against the f64 definition: values at the documented
+2^-17 of their magnitude (2^-20 scale softcap more under a cap), tokens exactly: larger logits
+first, of equal ones the lower token."""
+import numpy as np
+import pytest
+
+from oracle import answer
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def gd():
+    if not torch.cuda.is_available():
+        pytest.fail("a GPU test ran without a visible HIP device")
+    import gemm_decode_amd
+    return gemm_decode_amd
+
+
+def near(got, want, cap, scale):
+    got = got.cpu().numpy().astype(np.float64)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isneginf(got), np.isneginf(want))
+    ok = np.isfinite(want)
+    off = 2.0 ** -17 * np.abs(want[ok]) + 2.0 ** -100 + 2.0 ** -20 * scale * cap
+    assert (np.abs(got[ok] - want[ok]) <= off).all(), (got[ok] - want[ok], off)
+
+
+def run(gd, x, tokens, k, scale=1.0, cap=0.0, rows=None):
+    """One call on x [n, V] (a device tensor, its rows possibly apart), compared row by row (all, or `rows`)."""
+    n, V = x.shape
+    m = tokens.shape[1]
+    lp, ent = torch.full((n, m), 9.0, device="cuda"), torch.full((n + 8,), 9.0, device="cuda")
+    ids = torch.full((n * k + 8,), 9, dtype=torch.int64, device="cuda")
+    tops = torch.full((n * k + 8,), 9.0, device="cuda")
+    gd.token_logprobs(x, tokens if m else None, lp if m else None, ent[:n], ids[:n * k].view(n, k) if k else None,
+                      tops[:n * k].view(n, k) if k else None, n, V, scale=scale, softcap=cap)
+    assert bool((ent[n:] == 9).all()) and bool((ids[n * k:] == 9).all()) and bool((tops[n * k:] == 9).all())
+    xs, ts = x.float().cpu().numpy(), tokens.cpu().numpy()
+    for r in range(n) if rows is None else rows:
+        w_lp, w_ent, w_ids, w_tops = answer.logprobs(xs[r], ts[r], k, scale, cap)
+        assert np.array_equal(ids[r * k:(r + 1) * k].cpu().numpy(), w_ids), r
+        near(lp[r], w_lp, cap, scale)
+        near(ent[r:r + 1], np.array([w_ent]), cap, scale)
+        near(tops[r * k:(r + 1) * k], w_tops, cap, scale)
+    return lp, ent[:n], ids[:n * k], tops[:n * k]
+
+
+def given(n, V, m, seed):
+    g = torch.Generator().manual_seed(seed)
+    t = torch.randint(0, V, (n, m), generator=g)
+    if m:
+        t[0, 0] = V - 1
+        t[-1, -1] = -1
+        if m > 2:
+            t[0, 1] = t[0, 0]        # the same token twice
+            t[0, 2] = V              # one behind the vocabulary
+    return t.cuda()
+
+
+@pytest.mark.parametrize("V", [1, 2, 7, 63, 64, 65, 255, 1000, 2049, 8191, 8193, 16385, 50021, 131073])
+@pytest.mark.parametrize("T", list(TYPES))
+def test_lengths(gd, V, T):
+    for n, m, k in ((1, 1, 1), (3, 4, 64), (2, 1, 0), (5, 0, 5), (1, 0, 64)):
+        g = torch.Generator().manual_seed(V + n)
+        x = torch.randn(n, V, generator=g).mul(3).to(TYPES[T]).cuda()
+        run(gd, x, given(n, V, m, n), k)
+
+
+@pytest.mark.parametrize("n,V,k", [(300, 4099, 20), (520, 33000, 5), (1500, 513, 64), (2100, 50, 3), (40, 100003, 20)])
+def test_many_rows(gd, n, V, k):
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(n, V, generator=g).mul(2).to(torch.bfloat16).cuda()
+    run(gd, x, given(n, V, 1, 1), k, rows=[0, 1, n // 2, n - 1])
+
+
+@pytest.mark.parametrize("V,k", [(37, 64), (5000, 64), (70001, 20), (70001, 1)])
+@pytest.mark.parametrize("T", list(TYPES))
+def test_orders_that_are_hard_on_a_selection(gd, V, k, T):
+    """All alike, rising, falling, two values, one high run at the end, and zeros of both signs."""
+    i = torch.arange(V, dtype=torch.float32)
+    rows = torch.stack([torch.full((V,), 0.25), i / V * 8, -i / V * 8, (i % 2) * 3, torch.where(i > V - 40, 5.0, -1.0),
+                        torch.where(i % 3 == 0, -0.0, 0.0), (i * 7919 % 64) / 8, torch.where(i % 512 < 16, 4.0, 0.0)])
+    run(gd, rows.to(TYPES[T]).cuda(), given(8, V, 2, 3), k)
+
+
+@pytest.mark.parametrize("T", list(TYPES))
+@pytest.mark.parametrize("V", [70, 3001, 60007])
+def test_banned_and_bad_logits(gd, T, V):
+    """-infinity in most places, in all, in all but one; the type's lowest value as a mask, in all places too; NaN and infinities."""
+    T = TYPES[T]
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(12, V, generator=g).to(T)
+    low, inf = torch.finfo(T).min, float("inf")
+    x[0, torch.rand(V, generator=g) < 0.99] = -inf
+    x[1] = -inf
+    x[2] = -inf
+    x[2, V - 1] = -3.0
+    x[3, torch.rand(V, generator=g) < 0.9] = low
+    x[4] = low
+    x[5] = low
+    x[5, 3] = -inf
+    x[6, V // 2] = float("nan")
+    x[7, 0] = inf
+    x[8, 1], x[8, 2] = inf, -inf
+    x[9] = float("nan")
+    x[10] = torch.finfo(T).max
+    x[11, 5] = torch.finfo(T).max
+    tokens = given(12, V, 3, 5)
+    for cap, scale in ((0.0, 1.0), (30.0, 0.5)):
+        run(gd, x.cuda(), tokens, 20, scale, cap)
+
+
+@pytest.mark.parametrize("scale,cap", [(1.0, 0.0), (1.25, 0.0), (0.01, 0.0), (100.0, 0.0), (1.0, 30.0), (2.0, 5.0), (1.0, 1e30)])
+def test_scales_and_caps(gd, scale, cap):
+    for T in TYPES.values():
+        g = torch.Generator().manual_seed(11)
+        x = torch.randn(4, 20011, generator=g).mul(8).to(T).cuda()
+        run(gd, x, given(4, 20011, 3, 2), 10, scale, cap)
+
+
+def test_confident_rows(gd):
+    """A token ahead of the others by 10 to 80: its log probability and the entropy keep their digits next to 0."""
+    x = torch.zeros(8, 50000)
+    for r in range(8):
+        x[r, 777 * (r + 1)] = 10.0 * (r + 1)
+    tokens = torch.tensor([[777 * (r + 1), 5] for r in range(8)]).cuda()
+    run(gd, x.cuda(), tokens, 3)
+
+
+@pytest.mark.parametrize("T", list(TYPES))
+def test_rows_apart_and_unaligned(gd, T):
+    """A vocabulary padded with NaN behind each row, rows that start at every alignment, one token's row from the middle."""
+    T = TYPES[T]
+    g = torch.Generator().manual_seed(3)
+    for V, stride in ((5003, 5008), (5003, 5007), (64, 65), (8192, 8195), (9, 13)):
+        pool = torch.full((6 * stride + 16,), float("nan"), dtype=T)
+        for at in (0, 1, 3, 7):
+            whole = pool.clone()
+            rows = whole[at:at + 6 * stride].view(6, stride)[:, :V]
+            rows.copy_(torch.randn(6, V, generator=g).to(T))
+            d = whole.cuda()
+            view = d[at:at + 6 * stride].view(6, stride)[:, :V]
+            run(gd, view, given(6, V, 1, 1), 5)
+            run(gd, view[4:5], given(1, V, 1, 1), 5)
+
+
+def test_parts_that_are_asked_for(gd):
+    """Each output alone equals the one of the whole call, bit for bit."""
+    g = torch.Generator().manual_seed(8)
+    for n, V in ((1, 50000), (70, 9001)):
+        x, t = torch.randn(n, V, generator=g).cuda(), given(n, V, 2, 1)
+        lp, ent, ids, tops = run(gd, x, t, 7, rows=[0])
+        a, b = torch.empty_like(lp), torch.empty_like(ent)
+        gd.token_logprobs(x, t, a, None, None, None, n, V)
+        gd.token_logprobs(x, None, None, b, None, None, n, V)
+        c, d = torch.empty(n, 7, dtype=torch.int64, device="cuda"), torch.empty(n, 7, device="cuda")
+        gd.token_logprobs(x, None, None, None, c, d, n, V)
+        assert torch.equal(a, lp) and torch.equal(b, ent) and torch.equal(c.view(-1), ids) and torch.equal(d.view(-1), tops)
+
+
+def test_far_rows(gd):
+    """Rows past 2^32 bytes of logits."""
+    n, V = 36, 1 << 26
+    x = torch.empty(n, V, dtype=torch.bfloat16, device="cuda")
+    x.fill_(-2.0)
+    x[:, 12345] = 20.0
+    x[n - 1, V - 1] = 25.0
+    t = torch.tensor([[12345]] * (n - 1) + [[V - 1]]).cuda()
+    lp, ent = torch.empty(n, 1, device="cuda"), torch.empty(n, device="cuda")
+    ids, tops = torch.empty(n, 2, dtype=torch.int64, device="cuda"), torch.empty(n, 2, device="cuda")
+    gd.token_logprobs(x, t, lp, ent, ids, tops, n, V)
+    s = (V - 1) * np.exp(-22.0)
+    near(lp[0], np.array([-np.log1p(s)]), 0, 1)
+    assert ids[0].tolist() == [12345, 0] and ids[n - 1].tolist() == [V - 1, 12345]
+    s = (V - 2) * np.exp(-27.0) + np.exp(-5.0)
+    near(lp[n - 1], np.array([-np.log1p(s)]), 0, 1)
+
+
+def test_streams_and_graphs(gd):
+    """On the user's stream, and captured twice on one workspace, replayed in turns with eager calls between."""
+    g = torch.Generator().manual_seed(1)
+    sizes = [(2, 60000), (9, 30000)]
+    xs = [torch.randn(n, V, generator=g).cuda() for n, V in sizes]
+    ts = [given(n, V, 1, 2) for n, V in sizes]
+    need = max(gd.token_logprobs_workspace_bytes(n, V, 5) for n, V in sizes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+
+    def outs(n):
+        return (torch.zeros(n, 1, device="cuda"), torch.zeros(n, device="cuda"), torch.zeros(n, 5, dtype=torch.int64, device="cuda"),
+                torch.zeros(n, 5, device="cuda"))
+
+    def call(j, o):
+        gd.token_logprobs(xs[j], ts[j], *o, *sizes[j], workspace=ws)
+        return o
+    want = [call(j, outs(sizes[j][0])) for j in range(2)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = [call(j, outs(sizes[j][0])) for j in range(2)]
+    s.synchronize()
+    assert all(torch.equal(a, b) for o, w in zip(got, want) for a, b in zip(o, w))
+    kept, graphs = [outs(sizes[j][0]) for j in range(2)], []
+    for j in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(j, kept[j])
+        graphs.append(graph)
+    for i in range(6):
+        for o in kept:
+            for t in o:
+                t.zero_()
+        for j in ((0, 1) if i % 2 else (1, 0)):
+            graphs[j].replay()
+        assert all(torch.equal(a, b) for o, w in zip(kept, want) for a, b in zip(o, w)), i
+        assert all(torch.equal(a, b) for a, b in zip(call(0, outs(2)), want[0]))
