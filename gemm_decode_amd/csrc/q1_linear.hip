@@ -1,5 +1,7 @@
 // q1_linear.hip -- Q1_0 . q8_0 products with an epilogue: bias, activation, residual or the
 // product with a second weight's sums, and the output in the stream's type or as q8_0 blocks.
+#include <type_traits>
+
 #include "gd_internal.h"
 #include "gd_quant.h"
 #include "gd_types.h"
@@ -9,6 +11,9 @@ namespace {
 using namespace gd;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // One weight: its Q1 planes and the bias of its rows.
 struct Weight {
@@ -48,85 +53,555 @@ __device__ __forceinline__ float activate(float t, int32_t act) {
     }
 }
 
-// Max over the 32 lanes of a half wave.
-__device__ __forceinline__ float max32(float v) {
-    v = max8(v);
-    v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, false)));
-    return fmaxf(v, __shfl_xor(v, 16));
-}
-
-// The 8-bit code of v among 32 values whose largest magnitude is a, by the rule of
-// q8_0_quantize: in f32 where that gives what the f64 rule gives.
-__device__ __forceinline__ uint32_t code_of(float v, float a) {
+// Four codes, byte j that of v[j], among 32 values whose largest magnitude is a, by the rule
+// of q8_0_quantize: in f32 where that gives what the f64 rule gives.
+__device__ __forceinline__ uint32_t codes_of(f32x4 v, float a) {
     if (!(a > 0.0f)) return 0;
-    const float inv = recip127(a), t = v * inv;
-    int32_t q = static_cast<int32_t>(floorf(t + 0.5f));
-    if (!(inv <= 3.40282347e38f) || fabsf(__builtin_amdgcn_fractf(t) - 0.5f) < kTieGuard)
-        q = round_code(static_cast<double>(v) * (127.0 / static_cast<double>(a)));
-    return static_cast<uint32_t>(q) & 0xffu;
+    const float inv = recip127(a);
+    bool doubt = !(inv <= 3.40282347e38f);
+    int32_t q[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float t = v[j] * inv;
+        q[j] = static_cast<int32_t>(floorf(t + 0.5f));
+        doubt |= fabsf(__builtin_amdgcn_fractf(t) - 0.5f) < kTieGuard;
+    }
+    if (doubt) {   // rare
+        const double factor = 127.0 / static_cast<double>(a);
+#pragma unroll
+        for (int j = 0; j < 4; j++) q[j] = round_code(static_cast<double>(v[j]) * factor);
+    }
+    uint32_t packed = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) packed |= (static_cast<uint32_t>(q[j]) & 0xffu) << (8 * j);
+    return packed;
 }
 
-// One value of column c and row r; where q8_0 blocks are written, the 32 lanes of a half
-// wave hold the 32 rows of one block (r % 32 = lane % 32) and all of them call this.
+// Four elements at p (aligned to one), `count` of them there.
 template <typename T>
-__device__ __forceinline__ void finish(const Epilogue &e, float v, int64_t c, int64_t r, bool live) {
+__device__ __forceinline__ f32x4 load_some(const T *p, int count) {
+    typedef T Vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    if (count >= 4) return __builtin_convertvector(*reinterpret_cast<const Vec *>(p), f32x4);
+    f32x4 v = {};
+#pragma unroll
+    for (int j = 0; j < 3; j++)
+        if (j < count) v[j] = static_cast<float>(p[j]);
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T *p, f32x4 v, int count) {
+    typedef T Vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    if (count >= 4) {
+        *reinterpret_cast<Vec *>(p) = __builtin_convertvector(v, Vec);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 3; j++)
+        if (j < count) p[j] = static_cast<T>(v[j]);
+}
+
+// What becomes of the sums v (and u, the second weight's) of rows r .. r + 3, r % 4 = 0, and
+// column c. Where q8_0 blocks are written, eight neighbouring lanes hold the 32 rows of one
+// (r / 4 % 8 = lane % 8) and all of them call this.
+template <typename T, int S>
+__device__ __forceinline__ void finish(const Weight &w0, const Weight &w1, const Epilogue &e, f32x4 v, f32x4 u, int64_t c, int64_t r) {
+    const int64_t rest = c < e.n ? e.rows - r : 0;
+    const int count = rest >= 4 ? 4 : rest > 0 ? static_cast<int>(rest) : 0;
+    if (w0.bias) v += load_some(w0.bias + r, count);
+    if (S == 2 && w1.bias) u += load_some(w1.bias + r, count);
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = activate(v[j], e.act);
+    if (S == 2) v *= u;
     const int64_t at = c * e.rows + r;
-    if (e.residual && live) v += static_cast<float>(static_cast<const T *>(e.residual)[at]);
-    if (e.y && live) static_cast<T *>(e.y)[at] = static_cast<T>(v);
+    if (e.residual) v += load_some(static_cast<const T *>(e.residual) + at, count);
+    if (e.y) store_some(static_cast<T *>(e.y) + at, v, count);
     if (e.y_q8) {
-        const float a = max32(live ? fabsf(v) : 0.0f);
-        const uint32_t q = code_of(v, a);
-        if (live) {
+        const float a = max8(absmax4(float4{v[0], v[1], v[2], v[3]}));
+        const uint32_t q = codes_of(v, a);
+        if (count) {
             uint16_t *o = e.y_q8 + at / 32 * 17;   // 34 bytes = 17 halves
-            reinterpret_cast<uint8_t *>(o + 1)[r % 32] = static_cast<uint8_t>(q);
-            if (r % 32 == 0) o[0] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(a > 0.0f ? scale_of(a) : 0.0f));
+            const int k8 = static_cast<int>(r / 4 % 8);
+            typedef uint32_t Word __attribute__((aligned(2)));
+            *reinterpret_cast<Word *>(o + 1 + 2 * k8) = q;
+            if (k8 == 0) o[0] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(a > 0.0f ? scale_of(a) : 0.0f));
         }
     }
 }
 
-// The sum of one row and one column.
-__device__ float sum_of(const Weight &w, const uint16_t *a, int64_t r, int64_t K) {
-    const int64_t nb = K / 128, nb8 = (nb + 7) / 8;
-    float acc = 0.0f;
-    for (int64_t i = 0; i < nb; i++) {
-        const u32x2 lo = w.bits[((r / 64 * nb + i) * 2 + 0) * 64 + r % 64], hi = w.bits[((r / 64 * nb + i) * 2 + 1) * 64 + r % 64];
-        float t = 0.0f;
-        for (int k = 0; k < 4; k++) {
-            const uint16_t *b = a + (4 * i + k) * 17;
-            const int8_t *q = reinterpret_cast<const int8_t *>(b + 1);
-            int s = 0;
-            for (int j = 0; j < 32; j++) {
-                const uint32_t word = j < 16 ? lo[k / 2] : hi[k / 2];
-                const int bit = (8 * (j / 4 % 4) + 2 + 4 * (k % 2) + j % 4) % 32;
-                s += word >> bit & 1 ? q[j] : -q[j];
+// ------------------------------------------------------------- operands
+// The matrix instructions take 6-bit floats (e2m3) for the activations and 4-bit ones
+// (e2m1) for the weights, 32 of a lane with a power of two for all of them. A weight is its
+// sign, +1 or -1. An activation d1 q, d1 = m 2^e an f16 value with |m| < 2^11, is the whole
+// number m q, |m q| < 2^18, times 2^e: four digits to the base 32, each in [-16, 16], which
+// e2m3 holds exactly (as that many eighths, and the code of n eighths is n for n <= 16).
+// So four instructions multiply exactly, and their sums round in f32 alone; d0 is
+// multiplied to the sum over a weight block's 128 elements.
+//
+// The 32 elements of a sub-block stand in the order that the plane words give up with the
+// fewest steps: place 8 j + 2 jj + h holds element 16 h + 4 jj + j.
+constexpr uint32_t kBias = 0x84210u;   // 16 in each digit: keeps m q + bias positive
+constexpr int kFp6 = 2, kFp4 = 4;      // operand formats
+constexpr int kOne = 0x7f7f7f7f;       // scales of 1
+
+// Byte p: the e2m3 code of digit p of q m.
+__device__ __forceinline__ uint32_t digit_codes(int32_t q, int32_t m) {
+    const uint32_t u = static_cast<uint32_t>(__mul24(q, m)) + kBias;   // digits + 16, five bits each
+    uint32_t t = (u & 0x3ffu) | (u << 6 & ~0x3ffu);
+    t = ((t & 0x001f001fu) | (t << 3 & ~0x001f001fu)) & 0x1f1f1f1fu;   // a byte each
+    const uint32_t minus = ~t & 0x10101010u, one = minus >> 4;         // digits below 0
+    return ((((t & 0x0f0f0f0fu) ^ (minus - one)) + one) | minus << 1);   // 16 - d there, d elsewhere; the sign bit
+}
+
+// Bits 6 k: byte k of x, six bits of it.
+__device__ __forceinline__ uint32_t pack6(uint32_t x) {
+    const uint32_t t = (x & 0x003f003fu) | (x >> 2 & ~0x003f003fu);
+    return (t & 0xfffu) | (t >> 4 & 0xfff000u);
+}
+
+// Places 8 j .. 8 j + 7 of a sub-block's digits p: r[0][p] and r[1][p] hold four each, 24
+// bits. d: the sub-block's codes as eight words.
+__device__ __forceinline__ void digits8(const uint32_t *d, int j, int32_t m, uint32_t r[2][4]) {
+#pragma unroll
+    for (int a = 0; a < 2; a++) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t word = d[2 * a + (i >> 1) + 4 * (i & 1)];
+            w[i] = digit_codes(static_cast<int32_t>(word << (24 - 8 * j)) >> 24, m);
+        }
+        const uint32_t lo0 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), lo1 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+        const uint32_t hi0 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u), hi1 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+        r[a][0] = pack6(__builtin_amdgcn_perm(lo1, lo0, 0x05040100u));
+        r[a][1] = pack6(__builtin_amdgcn_perm(lo1, lo0, 0x07060302u));
+        r[a][2] = pack6(__builtin_amdgcn_perm(hi1, hi0, 0x05040100u));
+        r[a][3] = pack6(__builtin_amdgcn_perm(hi1, hi0, 0x07060302u));
+    }
+}
+
+// m of an f16 scale d1 = m 2^(E - 25), and the powers of two of its four digits (biased, a
+// byte each; NaN for an infinity or a NaN).
+struct Scale {
+    int32_t m;
+    uint32_t powers;
+    __device__ __forceinline__ explicit Scale(uint32_t h) {
+        const uint32_t e = h >> 10 & 31u;
+        m = static_cast<int32_t>((h & 0x3ffu) | (e ? 0x400u : 0u));
+        if (h & 0x8000u) m = -m;
+        powers = e == 31u ? 0xffffffffu : 0x0f0a0500u + (105u + (e ? e : 1u)) * 0x01010101u;
+    }
+};
+
+// A q8_0 block's codes as words, and its scale (34 bytes, 2-byte aligned).
+__device__ __forceinline__ uint32_t load_block(const uint16_t *b, uint32_t d[8]) {
+    typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+    const Words lo = *reinterpret_cast<const Words *>(b + 1), hi = *reinterpret_cast<const Words *>(b + 9);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        d[i] = lo[i];
+        d[4 + i] = hi[i];
+    }
+    return b[0];
+}
+
+// The 32 signs of a lane's sub-block as e2m1 codes, from its words of the two halves (which
+// hold those of the neighbouring sub-block as well: odd says which of the two).
+struct Signs {
+    uint32_t lo, hi;   // rotations
+    __device__ __forceinline__ explicit Signs(int odd) : lo(2 + 4 * odd), hi((30 + 4 * odd) & 31) {}
+    __device__ __forceinline__ i32x8 operator()(uint32_t half0, uint32_t half1) const {
+        const uint32_t a = __builtin_amdgcn_alignbit(half0, half0, lo), b = __builtin_amdgcn_alignbit(half1, half1, hi);
+        const uint32_t y = (a & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);   // nibble 2 jj + h: the signs of j = 0..3
+        i32x8 v = {};
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = static_cast<int>((~(y << (3 - j)) & 0x88888888u) | 0x22222222u);
+        return v;
+    }
+};
+
+__device__ __forceinline__ i32x8 frag(u32x4 lo, u32x2 hi) {
+    return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]), static_cast<int>(lo[3]),
+                 static_cast<int>(hi[0]), static_cast<int>(hi[1]), 0, 0};
+}
+
+// ------------------------------------------------- up to four columns
+// The rows of a 16 x 16 x 128 instruction are the digits of the columns (row 4 c + p: digit p
+// of column c), its columns 16 weight rows, so that a lane's four results are the digits'
+// sums of one row and column, and one instruction takes a weight block of 16 rows.
+//
+// A workgroup of eight waves holds the digits of `kBlocks` blocks in LDS and takes 16-row
+// tiles of the weights, KW waves sharing a tile by its K.
+constexpr int kFew = 512;
+template <int C>
+constexpr int kBlocks = 128 / C;
+
+struct FewShape {
+    int64_t nb;        // blocks of a row
+    int kw, tiles;     // waves along K; 16-row tiles a wave takes (at most 4)
+};
+
+template <typename T, int C, int S>
+__global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, const uint16_t *__restrict__ a_q8, Epilogue e,
+                                                         FewShape f) {
+    constexpr int kQuads = C == 1 ? 4 : 2;   // of blocks, a wave's of a chunk at most
+    __shared__ __attribute__((aligned(16))) uint16_t digits[kBlocks<C> * 4 * 4 * C * 12];
+    __shared__ uint32_t powers[kBlocks<C> * 4 * C];
+    __shared__ __attribute__((aligned(16))) float red[8 * 4 * S * 64];
+    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int g = lane / 16, n16 = lane % 16, n = static_cast<int>(e.n);
+    const int kpart = wave % f.kw, ipart = wave / f.kw, groups = 8 / f.kw;
+    const int64_t nb = f.nb, nb8 = (nb + 7) / 8;
+    const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * f.tiles * groups, last = (e.rows + 15) / 16 - 1;
+    const int row_a = n16 / 4 < n ? n16 : n16 % 4;   // rows of no column repeat another's
+    const Signs signs(g & 1);
+    float acc[4 * S];
+#pragma unroll
+    for (int i = 0; i < 4 * S; i++) acc[i] = 0.0f;
+    for (int64_t b0 = 0; b0 < nb; b0 += kBlocks<C>) {
+        const int blocks = static_cast<int>(nb - b0 < kBlocks<C> ? nb - b0 : kBlocks<C>);
+        if (b0) __syncthreads();
+        // Digits: a thread takes eight elements of a sub-block at a time.
+        for (int i = tid; i < blocks * 16 * n; i += kFew) {
+            const int j = i % 4, sub = i / 4 % (blocks * 4), c = i / 4 / (blocks * 4);
+            uint32_t d[8], r[2][4];
+            const Scale s(load_block(a_q8 + ((c * nb + b0) * 4 + sub) * 17, d));
+            digits8(d, j, s.m, r);
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                uint16_t *o = digits + ((sub * C + c) * 4 + p) * 12 + 3 * j;
+                o[0] = static_cast<uint16_t>(r[0][p]);
+                o[1] = static_cast<uint16_t>(r[0][p] >> 16 | r[1][p] << 8);
+                o[2] = static_cast<uint16_t>(r[1][p] >> 8);
             }
-            const float d = f16_value(b[0]);
-            t = fmaf(fabsf(d) <= 65504.0f ? d : __builtin_nanf(""), static_cast<float>(s), t);
+            if (j == 0) powers[sub * C + c] = s.powers;
         }
-        acc = fmaf(f16_value(w.scales[(r / 64 * nb8 + i / 8) * 512 + r % 64 * 8 + i % 8]), t, acc);
+        __syncthreads();
+#pragma unroll
+        for (int it = 0; it < 4; it++) {
+            if (it >= f.tiles) break;
+            int64_t tile = tile0 + it * groups + ipart;
+            tile = tile <= last ? tile : last;
+            const int64_t t64 = tile / 4;
+            const int in64 = static_cast<int>(tile % 4) * 16 + n16;
+#pragma unroll
+            for (int s = 0; s < S; s++) {
+                const Weight &w = s ? w1 : w0;
+                float sum = acc[it * S + s];
+#pragma unroll
+                for (int qi = 0; qi < kQuads; qi++) {
+                    const int q = kpart + qi * f.kw;
+                    if (4 * q >= blocks) break;
+                    const int64_t i0 = b0 + 4 * q;
+                    const u32x2 d0 = *reinterpret_cast<const u32x2 *>(w.scales + (t64 * nb8 + i0 / 8) * 512 + in64 * 8 + i0 % 8);
+#pragma unroll
+                    for (int b = 0; b < 4; b += 2) {
+                        if (4 * q + b >= blocks) break;
+                        int64_t i = i0 + b + (g >> 1);
+                        i = i < nb ? i : nb - 1;
+                        const u32x2 word = w.bits[((t64 * nb + i) * 2 + (g & 1)) * 64 + in64];
+                        // Words 0 and 1 of both halves of both blocks to the lanes of their sub-blocks.
+                        const auto x = __builtin_amdgcn_permlane32_swap(word[0], word[1], false, false);
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            if (4 * q + b + k >= blocks) break;
+                            const auto h = __builtin_amdgcn_permlane16_swap(x[k], x[k], false, false);
+                            const int at = ((4 * q + b + k) * 4 + g) * C;
+                            const u32x2 *dig = reinterpret_cast<const u32x2 *>(digits + (at * 4 + row_a) * 12);
+                            const u32x2 f0 = dig[0], f1 = dig[1], f2 = dig[2];
+                            const int power = static_cast<int>(powers[at + row_a / 4] >> (8 * (row_a & 3)));
+                            const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                frag(u32x4{f0[0], f0[1], f1[0], f1[1]}, f2), signs(h[0], h[1]), f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp6,
+                                kFp4, 0, power, 0, kOne);
+                            const float d = f16_value(static_cast<uint16_t>(d0[(b + k) / 2] >> (16 * ((b + k) & 1))));
+                            sum = fmaf(d, (t[0] + t[1]) + (t[2] + t[3]), sum);
+                        }
+                    }
+                }
+                acc[it * S + s] = sum;
+            }
+        }
     }
-    return acc;
+    const int tw = f.tiles * groups;   // the workgroup's tiles
+#pragma unroll
+    for (int it = 0; it < 4; it++)
+#pragma unroll
+        for (int s = 0; s < S; s++)
+            if (it < f.tiles) red[((kpart * tw + it * groups + ipart) * S + s) * 64 + lane] = acc[it * S + s];
+    __syncthreads();
+    for (int i = tid; i < n * 4 * tw; i += kFew) {   // eight lanes together hold 32 rows where blocks are written (tw even)
+        const int c = i / (4 * tw), quad = i % (4 * tw);
+        f32x4 v[2] = {};
+        for (int k = 0; k < f.kw; k++)
+#pragma unroll
+            for (int s = 0; s < S; s++)
+                v[s] += *reinterpret_cast<const f32x4 *>(red + ((k * tw + quad / 4) * S + s) * 64 + c * 16 + quad % 4 * 4);
+        finish<T, S>(w0, w1, e, v[0], v[1], c, tile0 * 16 + 4 * quad);
+    }
 }
 
-// Plain: a thread per row and column.
-template <typename T, bool kGated>
-__global__ __launch_bounds__(256) void q1_linear_plain_kernel(Weight g, Weight u, const uint16_t *a_q8, Epilogue e, int64_t K) {
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
-    const int64_t c = static_cast<int64_t>(blockIdx.y) * 8 + threadIdx.x / 32;
-    const bool live = r < e.rows && c < e.n;
-    float v = 0.0f;
-    if (live) {
-        const uint16_t *a = a_q8 + c * (K / 32) * 17;
-        v = sum_of(g, a, r, K);
-        if (g.bias) v += g.bias[r];
-        v = activate(v, e.act);
-        if (kGated) {
-            float up = sum_of(u, a, r, K);
-            if (u.bias) up += u.bias[r];
-            v *= up;
+// ------------------------------------------------------- more columns
+// The activations as operands of 32 x 32 x 64 instructions: for each 32 columns and 64
+// elements (a step) a fragment of 1536 bytes per digit (16 bytes of each lane, then 8), and
+// behind all of them a word of each lane with the digits' powers of two.
+constexpr int64_t kStepBytes = 4 * 1536;
+constexpr int kStepHalves = 2;   // sub-blocks of a step: the two halves of a wave
+
+__global__ __launch_bounds__(256) void q1_digits_kernel(const uint16_t *__restrict__ a_q8, uint8_t *__restrict__ out, int64_t n,
+                                                        int64_t steps) {
+    const int lane = threadIdx.x % 64;
+    const int64_t step = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64, tile = blockIdx.y;
+    if (step >= steps) return;
+    const int64_t c = tile * 32 + lane % 32;
+    uint32_t d[8] = {}, h = 0;
+    if (c < n) h = load_block(a_q8 + ((c * steps + step) * kStepHalves + lane / 32) * 17, d);
+    const Scale s(h);
+    uint32_t r[8][4];   // by places 4 k .. 4 k + 3
+#pragma unroll
+    for (int j = 0; j < 4; j++) digits8(d, j, s.m, r + 2 * j);
+    uint8_t *o = out + (tile * steps + step) * kStepBytes;
+#pragma unroll
+    for (int p = 0; p < 4; p++, o += 1536) {
+        uint32_t w[6];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            w[3 * k] = r[4 * k][p] | r[4 * k + 1][p] << 24;
+            w[3 * k + 1] = r[4 * k + 1][p] >> 8 | r[4 * k + 2][p] << 16;
+            w[3 * k + 2] = r[4 * k + 2][p] >> 16 | r[4 * k + 3][p] << 8;
+        }
+        reinterpret_cast<u32x4 *>(o)[lane] = u32x4{w[0], w[1], w[2], w[3]};
+        reinterpret_cast<u32x2 *>(o + 1024)[lane] = u32x2{w[4], w[5]};
+    }
+    reinterpret_cast<uint32_t *>(out + gridDim.y * steps * kStepBytes)[(tile * steps + step) * 64 + lane] = s.powers;
+}
+
+struct ManyShape {
+    int64_t nb, col_tiles, row_tiles;   // blocks of a row, tiles of 32 columns, of 32 rows
+    int64_t col_groups, row_groups;     // of a workgroup's tiles
+};
+
+// t += the products of one digit. (The builtin takes the digit's byte as an immediate.)
+template <int P>
+__device__ __forceinline__ f32x16 mma(i32x8 a, i32x8 b, f32x16 t, uint32_t powers) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, t, kFp6, kFp4, P, static_cast<int>(powers), 0, kOne);
+}
+
+// A wave's sums are TM tiles of 32 columns by NT = TN S tiles of 32 weight rows, TN of each
+// of the S weights. KS = 1: WN waves side by side along the rows share the columns' digits
+// through LDS, loaded a block ahead. KS > 1: the waves share one set of sums by K and load
+// digits into registers.
+template <typename T, int TM, int TN, int S, int KS, int WN>
+__global__ __launch_bounds__(64 * KS * WN, 2) void q1_many_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits,
+                                                                  Epilogue e, ManyShape f) {
+    constexpr int NT = TN * S, kWaves = KS * WN;
+    constexpr int kChunks = KS == 1 ? 2 * TM * 6 : 0, kOwn = kChunks / kWaves;   // KiB of digits of a block of 128; a wave's
+    static_assert(KS == 1 || WN == 1, "waves along K or along the rows");
+    static_assert(kChunks % kWaves == 0, "whole chunks a wave");
+    constexpr int kTile = 32 * 36;   // floats of a tile of sums in LDS, a column's rows 36 apart
+    constexpr int kSums = kWaves * (KS == 1 ? S : TM * NT) * kTile * 4;
+    constexpr int kLds = kSums > 2 * kChunks * 1024 ? kSums : 2 * kChunks * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int g = lane / 32, n32 = lane % 32;
+    const int64_t steps = 2 * f.nb, nb = f.nb, nb8 = (nb + 7) / 8;
+    // Workgroups with consecutive numbers go to the 8 dies in turn: each die takes a run of row groups.
+    const int64_t total = f.col_groups * f.row_groups, id = blockIdx.x;
+    const int64_t per = (total + 7) / 8, at = id % 8 * per + id / 8;
+    if (at >= total) return;
+    const int64_t col0 = at % f.col_groups * TM, row0 = (at / f.col_groups * WN + (KS == 1 ? wave : 0)) * TN;
+    int64_t b = 0, end = nb;
+    if (KS > 1) {
+        const int64_t share = (nb + KS - 1) / KS;
+        b = wave * share < nb ? wave * share : nb;
+        end = b + share < nb ? b + share : nb;
+    }
+    // Where the wave reads next; a block on, each moves by a constant.
+    const uint8_t *frags[TM];        // a tile's fragments (KS > 1)
+    const uint8_t *chunk[kOwn + 1];  // the wave's share of what goes to LDS
+    const uint32_t *powers[TM];
+    const u32x2 *bits[NT];
+    const uint16_t *scales[NT];
+#pragma unroll
+    for (int m = 0; m < TM; m++) {
+        const int64_t tile = col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1;
+        frags[m] = digits + (tile * steps + 2 * b) * kStepBytes + lane * 16;
+        powers[m] = reinterpret_cast<const uint32_t *>(digits + f.col_tiles * steps * kStepBytes) + (tile * steps + 2 * b) * 64 + lane;
+    }
+#pragma unroll
+    for (int k = 0; k < kOwn; k++) {
+        const int c = wave * kOwn + k, s = c / 6 % 2, m = c / 12;   // LDS holds a tile's two steps together
+        const int64_t tile = col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1;
+        chunk[k] = digits + (tile * steps + s) * kStepBytes + c % 6 * 1024 + lane * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
+        const Weight &w = i / TN ? w1 : w0;
+        int64_t rt = row0 + i % TN;
+        rt = rt < f.row_tiles ? rt : f.row_tiles - 1;
+        const int64_t in64 = rt % 2 * 32 + n32;
+        bits[i] = w.bits + rt / 2 * nb * 128 + b * 128 + g * 64 + in64;
+        scales[i] = w.scales + rt / 2 * nb8 * 512 + in64 * 8;
+    }
+    const Signs signs(g);
+    f32x16 acc[TM][NT];
+#pragma unroll
+    for (int m = 0; m < TM; m++)
+#pragma unroll
+        for (int i = 0; i < NT; i++) acc[m][i] = f32x16{};
+    // A block's loads to registers.
+    struct Loads {
+        u32x2 bits[NT];
+        uint16_t scales[NT];
+        uint32_t powers[TM][2];
+        u32x4 lo[KS > 1 ? TM : 1][2][4];
+        u32x2 hi[KS > 1 ? TM : 1][2][4];
+    };
+    const auto load = [&](int64_t i) {
+        Loads l;
+#pragma unroll
+        for (int k = 0; k < NT; k++) {
+            l.bits[k] = *bits[k];
+            bits[k] += 128;
+            l.scales[k] = scales[k][i / 8 * 512 + i % 8];
+        }
+#pragma unroll
+        for (int m = 0; m < TM; m++) {
+#pragma unroll
+            for (int s = 0; s < 2; s++) {
+                l.powers[m][s] = powers[m][64 * s];
+                if constexpr (KS > 1) {
+#pragma unroll
+                    for (int p = 0; p < 4; p++) {
+                        const uint8_t *src = frags[m] + s * kStepBytes + 1536 * p;
+                        l.lo[m][s][p] = *reinterpret_cast<const u32x4 *>(src);
+                        l.hi[m][s][p] = *reinterpret_cast<const u32x2 *>(src + 1024 - lane * 8);
+                    }
+                }
+            }
+            powers[m] += 128;
+            frags[m] += 2 * kStepBytes;
+        }
+        return l;
+    };
+    const auto stage = [&](int buffer) {   // a block's digits to LDS
+#pragma unroll
+        for (int k = 0; k < kOwn; k++) {
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)chunk[k],
+                                             (__attribute__((address_space(3))) uint32_t *)(lds + (buffer * kChunks + wave * kOwn + k) * 1024),
+                                             16, 0, 0);
+            chunk[k] += 2 * kStepBytes;
+        }
+    };
+    const auto compute = [&](const Loads &l, int buffer) {
+        const uint8_t *lo = lds + (buffer * kChunks * 1024 + lane * 16), *hi = lds + (buffer * kChunks * 1024 + 1024 + lane * 8);
+        f32x16 t[TM][NT];
+#pragma unroll
+        for (int m = 0; m < TM; m++)
+#pragma unroll
+            for (int i = 0; i < NT; i++) t[m][i] = f32x16{};
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            i32x8 a[TM][4], w[NT];
+#pragma unroll
+            for (int m = 0; m < TM; m++)
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    if constexpr (KS > 1) {
+                        a[m][p] = frag(l.lo[m][s][p], l.hi[m][s][p]);
+                    } else {
+                        const int at = (m * 2 + s) * 6144 + 1536 * p;
+                        a[m][p] = frag(*reinterpret_cast<const u32x4 *>(lo + at), *reinterpret_cast<const u32x2 *>(hi + at));
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < NT; i++) {   // both halves' words of this step's sub-blocks to both halves of the wave
+                const auto h = __builtin_amdgcn_permlane32_swap(l.bits[i][s], l.bits[i][s], false, false);
+                w[i] = signs(h[0], h[1]);
+            }
+            const auto digit = [&](auto p) {
+#pragma unroll
+                for (int m = 0; m < TM; m++)
+#pragma unroll
+                    for (int i = 0; i < NT; i++) t[m][i] = mma<decltype(p)::value>(a[m][decltype(p)::value], w[i], t[m][i], l.powers[m][s]);
+            };
+            digit(std::integral_constant<int, 0>{});
+            digit(std::integral_constant<int, 1>{});
+            digit(std::integral_constant<int, 2>{});
+            digit(std::integral_constant<int, 3>{});
+        }
+#pragma unroll
+        for (int m = 0; m < TM; m++)
+#pragma unroll
+            for (int i = 0; i < NT; i++) {
+                const float d0 = f16_value(l.scales[i]);
+#pragma unroll
+                for (int k = 0; k < 16; k++) acc[m][i][k] = fmaf(d0, t[m][i][k], acc[m][i][k]);
+            }
+    };
+    if constexpr (KS == 1) {
+        stage(0);
+        Loads l = load(0);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        for (; b + 1 < end; b++) {
+            const int buffer = static_cast<int>(b & 1);
+            stage(buffer ^ 1);
+            const Loads ahead = load(b + 1);
+            compute(l, buffer);
+            l = ahead;
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+        }
+        compute(l, static_cast<int>(b & 1));
+        __syncthreads();
+    } else if (b < end) {
+        Loads l = load(b);
+        for (; b + 1 < end; b++) {
+            const Loads ahead = load(b + 1);
+            compute(l, 0);
+            l = ahead;
+        }
+        compute(l, 0);
+    }
+    // Sums go through LDS, so that a lane has four rows of a column: value k of a lane is
+    // column 8 (k / 4) + 4 g + k % 4 of its tile and row n32 of the other.
+    float *sums = reinterpret_cast<float *>(lds);
+    const auto put = [&](const f32x16 &v, float *to) {
+#pragma unroll
+        for (int k = 0; k < 16; k++) to[(8 * (k / 4) + 4 * g + k % 4) * 36 + n32] = v[k];
+    };
+    const int from = lane / 8 * 36 + lane % 8 * 4;   // the lane's four of each eight columns
+    if constexpr (KS == 1) {
+        float *own = sums + wave * S * kTile;
+#pragma unroll
+        for (int m = 0; m < TM; m++)
+#pragma unroll
+            for (int i = 0; i < TN; i++) {
+#pragma unroll
+                for (int s = 0; s < S; s++) put(acc[m][s * TN + i], own + s * kTile);
+                __builtin_amdgcn_wave_barrier();   // a wave's own tile: its LDS accesses stay in order
+#pragma unroll 1
+                for (int q = 0; q < 4; q++)
+                    finish<T, S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * 36),
+                                 *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + from + q * 8 * 36),
+                                 (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
+                __builtin_amdgcn_wave_barrier();
+            }
+    } else {
+#pragma unroll
+        for (int m = 0; m < TM; m++)
+#pragma unroll
+            for (int i = 0; i < NT; i++) put(acc[m][i], sums + (wave * TM * NT + m * NT + i) * kTile);
+        __syncthreads();
+        for (int j = wave; j < TM * TN * 4; j += KS) {   // eight columns of a tile at a time
+            const int q = j % 4, i = j / 4 % TN, m = j / 4 / TN;
+            f32x4 v[2] = {};
+#pragma unroll
+            for (int k = 0; k < KS; k++)
+#pragma unroll
+                for (int s = 0; s < S; s++)
+                    v[s] += *reinterpret_cast<const f32x4 *>(sums + (k * TM * NT + m * NT + s * TN + i) * kTile + from + q * 8 * 36);
+            finish<T, S>(w0, w1, e, v[0], v[1], (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
         }
     }
-    finish<T>(e, v, c, r, live);
 }
 
 constexpr int64_t kMaxK = INT64_C(1) << 20, kMaxColumns = INT64_C(1) << 20;
@@ -179,13 +654,57 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
     return GD_OK;
 }
 
-template <bool kGated>
-void run(const Weight &g, const Weight &u, const void *a_q8, const Epilogue &e, int64_t K, int32_t dtype, hipStream_t hs) {
+template <typename T, int S>
+void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, hipStream_t hs) {
+    FewShape f = {K / 128, 1, 1};
+    while (f.kw < 8 && 8 * f.kw <= f.nb) f.kw *= 2;   // four blocks a wave at least
+    const int64_t tiles = (e.rows + 15) / 16, groups = 8 / f.kw;
+    while (f.tiles < 4 && ((e.y_q8 && f.tiles * groups < 2) || tiles / (2 * f.tiles * groups) >= 256)) f.tiles *= 2;
+    const dim3 grid(static_cast<uint32_t>((tiles + f.tiles * groups - 1) / (f.tiles * groups)));
+    const auto go = [&](auto c) {
+        hipLaunchKernelGGL((q1_few_kernel<T, decltype(c)::value, S>), grid, dim3(kFew), 0, hs, w0, w1, a_q8, e, f);
+    };
+    if (e.n == 1)
+        go(std::integral_constant<int, 1>{});
+    else if (e.n == 2)
+        go(std::integral_constant<int, 2>{});
+    else
+        go(std::integral_constant<int, 4>{});
+}
+
+template <typename T, int S>
+void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, uint8_t *workspace,
+              hipStream_t hs) {
+    ManyShape f = {K / 128, (e.n + 31) / 32, (e.rows + 31) / 32, 0, 0};
+    hipLaunchKernelGGL(q1_digits_kernel, dim3(static_cast<uint32_t>((2 * f.nb + 3) / 4), static_cast<uint32_t>(f.col_tiles)), dim3(256),
+                       0, hs, a_q8, workspace, e.n, 2 * f.nb);
+    const auto go = [&](auto tm, auto tn, auto ks, auto wn) {
+        constexpr int TM = decltype(tm)::value, TN = decltype(tn)::value, KS = decltype(ks)::value, WN = decltype(wn)::value;
+        f.col_groups = (f.col_tiles + TM - 1) / TM;
+        f.row_groups = (f.row_tiles + TN * WN - 1) / (TN * WN);
+        const int64_t grid = (f.col_groups * f.row_groups + 7) / 8 * 8;
+        hipLaunchKernelGGL((q1_many_kernel<T, TM, TN, S, KS, WN>), dim3(static_cast<uint32_t>(grid)), dim3(64 * KS * WN), 0, hs, w0, w1,
+                           workspace, e, f);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Eight = std::integral_constant<int, 8>;
+    if ((f.col_tiles + 1) / 2 * ((f.row_tiles + 16 / S - 1) / (16 / S)) >= 128)
+        go(Two{}, std::integral_constant<int, 2 / S>{}, One{}, Eight{});
+    else
+        go(One{}, One{}, Eight{}, One{});
+}
+
+template <int S>
+void run(const Weight &w0, const Weight &w1, const void *a_q8, const Epilogue &e, int64_t K, int32_t dtype, void *workspace,
+         hipStream_t hs) {
     dispatch_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        const dim3 grid(static_cast<uint32_t>((e.rows + 31) / 32), static_cast<uint32_t>((e.n + 7) / 8));
-        hipLaunchKernelGGL((q1_linear_plain_kernel<T, kGated>), grid, dim3(256), 0, hs, g, u,
-                           static_cast<const uint16_t *>(a_q8), e, K);
+        const uint16_t *a = static_cast<const uint16_t *>(a_q8);
+        if (e.n <= kFewColumns)
+            run_few<T, S>(w0, w1, a, e, K, hs);
+        else
+            run_many<T, S>(w0, w1, a, e, K, static_cast<uint8_t *>(workspace), hs);
     });
 }
 
@@ -207,7 +726,7 @@ extern "C" int q1_q8_linear(const void *bits_plane, const void *scale_plane, con
     const Epilogue e = {residual, y, static_cast<uint16_t *>(y_q8), rows, n_act, act};
     const int st = check("q1_q8_linear", &w, 1, a_q8, e, K, dtype, workspace, workspace_bytes);
     if (st) return st;
-    run<false>(w, w, a_q8, e, K, dtype, as_stream(stream));
+    run<1>(w, w, a_q8, e, K, dtype, workspace, as_stream(stream));
     return check_launch("q1_q8_linear");
 }
 
@@ -220,6 +739,6 @@ extern "C" int q1_q8_gated(const void *gate_bits, const void *gate_scales, const
     const Epilogue e = {nullptr, y, static_cast<uint16_t *>(y_q8), rows, n_act, act};
     const int st = check("q1_q8_gated", w, 2, a_q8, e, K, dtype, workspace, workspace_bytes);
     if (st) return st;
-    run<true>(w[0], w[1], a_q8, e, K, dtype, as_stream(stream));
+    run<2>(w[0], w[1], a_q8, e, K, dtype, workspace, as_stream(stream));
     return check_launch("q1_q8_gated");
 }

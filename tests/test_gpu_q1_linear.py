@@ -84,7 +84,7 @@ def within(got, want, off, T):
 SHAPES = [(1, 128, 1), (16, 256, 1), (33, 640, 1), (70, 1024, 1), (4096, 4096, 1), (130, 14336, 1), (257, 2176, 2),
           (64, 512, 3), (96, 384, 4), (50, 128, 4), (40, 16512, 1), (17, 33024, 3),
           (1, 128, 5), (31, 128, 7), (65, 384, 16), (127, 640, 31), (128, 1024, 32), (129, 896, 33), (600, 2560, 37),
-          (515, 1152, 64), (200, 256, 65), (1030, 512, 130), (2085, 640, 300), (64, 14336, 13), (96, 33024, 9)]
+          (515, 1152, 64), (200, 256, 65), (1030, 512, 130), (2085, 640, 300), (4200, 256, 1000), (64, 14336, 13), (96, 33024, 9)]
 
 
 @pytest.mark.parametrize("rows,K,n", SHAPES)
@@ -121,7 +121,7 @@ def test_gated(gd, rows, K, n):
 
 
 @pytest.mark.parametrize("rows,K,n", [(32, 128, 1), (64, 640, 2), (4096, 1024, 1), (96, 384, 4), (32, 2176, 5),
-                                      (160, 896, 33), (512, 256, 64), (1056, 640, 130)])
+                                      (160, 896, 33), (512, 256, 64), (1056, 640, 130), (4192, 128, 1000)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_q8_output_is_the_quantized_f32_output(gd, rows, K, n, gated):
     """The blocks are those of the rule on v in f32, with and without y beside them, in any type; a row of zeros among them."""
