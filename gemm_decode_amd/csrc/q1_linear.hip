@@ -384,52 +384,212 @@ __device__ __forceinline__ f32x16 mma(i32x8 a, i32x8 b, f32x16 t, uint32_t power
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, t, kFp6, kFp4, P, static_cast<int>(powers), 0, kOne);
 }
 
-// A wave's sums are TM tiles of 32 columns by NT = TN S tiles of 32 weight rows, TN of each
-// of the S weights. KS = 1: WN waves side by side along the rows share the columns' digits
-// through LDS, loaded a block ahead. KS > 1: the waves share one set of sums by K and load
-// digits into registers.
-template <typename T, int TM, int TN, int S, int KS, int WN>
-__global__ __launch_bounds__(64 * KS * WN, 2) void q1_many_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits,
-                                                                  Epilogue e, ManyShape f) {
-    constexpr int NT = TN * S, kWaves = KS * WN;
-    constexpr int kChunks = KS == 1 ? 2 * TM * 6 : 0, kOwn = kChunks / kWaves;   // KiB of digits of a block of 128; a wave's
-    static_assert(KS == 1 || WN == 1, "waves along K or along the rows");
-    static_assert(kChunks % kWaves == 0, "whole chunks a wave");
-    constexpr int kTile = 32 * 36;   // floats of a tile of sums in LDS, a column's rows 36 apart
-    constexpr int kSums = kWaves * (KS == 1 ? S : TM * NT) * kTile * 4;
-    constexpr int kLds = kSums > 2 * kChunks * 1024 ? kSums : 2 * kChunks * 1024;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+// One step of TM x NT tiles: t[m][i] += a[m] w[i], the four digits one after the other so that
+// TM NT instructions stand between two on the same sums.
+template <int TM, int NT>
+__device__ __forceinline__ void step(f32x16 (&t)[TM][NT], const i32x8 (&a)[TM][4], const i32x8 (&w)[NT], const uint32_t (&powers)[TM]) {
+    const auto digit = [&](auto p) {
+#pragma unroll
+        for (int m = 0; m < TM; m++)
+#pragma unroll
+            for (int i = 0; i < NT; i++) t[m][i] = mma<decltype(p)::value>(a[m][decltype(p)::value], w[i], t[m][i], powers[m]);
+    };
+    digit(std::integral_constant<int, 0>{});
+    digit(std::integral_constant<int, 1>{});
+    digit(std::integral_constant<int, 2>{});
+    digit(std::integral_constant<int, 3>{});
+}
+
+// acc += d0 t, d0 of the lane's weight row.
+template <int TM, int NT>
+__device__ __forceinline__ void fold(f32x16 (&acc)[TM][NT], const f32x16 (&t)[TM][NT], const uint16_t (&d0)[NT]) {
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
+        const float d = f16_value(d0[i]);
+#pragma unroll
+        for (int m = 0; m < TM; m++)
+#pragma unroll
+            for (int k = 0; k < 16; k++) acc[m][i][k] = fmaf(d, t[m][i][k], acc[m][i][k]);
+    }
+}
+
+// A tile's sums to LDS, a column's rows kPitch apart: value k of a lane is column 8 (k / 4) +
+// 4 g + k % 4 of its tile and row n32 of the other. From there a lane takes four rows of a
+// column at a time: column lane / 8 of each eight, rows 4 (lane % 8) on.
+constexpr int kPitch = 36, kTile = 32 * kPitch;
+__device__ __forceinline__ void put_tile(const f32x16 &v, float *to, int g, int n32) {
+#pragma unroll
+    for (int k = 0; k < 16; k++) to[(8 * (k / 4) + 4 * g + k % 4) * kPitch + n32] = v[k];
+}
+
+// Workgroups with consecutive numbers go to the eight dies in turn: each die takes a run of
+// row groups with all their column groups, so that a weight is read by one die.
+__device__ __forceinline__ bool place(const ManyShape &f, int64_t &col_group, int64_t &row_group) {
+    const int64_t total = f.col_groups * f.row_groups, id = blockIdx.x, per = (total + 7) / 8, at = id % 8 * per + id / 8;
+    col_group = at % f.col_groups;
+    row_group = at / f.col_groups;
+    return at < total;
+}
+
+// 64 lanes times 16 (or 4) bytes from the lanes' addresses to LDS at `to` on. The compiler
+// does not see these loads: who reads what they bring waits with arrive().
+__device__ __forceinline__ void lds_load16(const void *from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load4(const void *from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+}
+
+// Prompts: eight waves side by side along the rows share the digits of TM tiles of 32 columns,
+// each with NT = TN S tiles of 32 weight rows of its own (TN of each of the S weights). All
+// that a block of 128 needs comes through LDS, loaded kAhead blocks before: a shorter lead
+// leaves the waves waiting for memory 43 % of their time.
+template <typename T, int TM, int TN, int S>
+__global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
+                                                         ManyShape f) {
+    constexpr int NT = TN * S, kWaves = 8, kAhead = 3, kBuffers = kAhead + 1;
+    // A buffer: the tiles' digits, each wave's signs and scales, the powers of two (twice).
+    constexpr int kDigits = TM * 2 * kStepBytes, kSigns = kDigits + 0, kScales = kSigns + kWaves * NT * 512,
+                  kPowers = kScales + kWaves * NT * 128, kBuffer = kPowers + kWaves * 256;
+    constexpr int kOwn = kDigits / 1024 / kWaves, kIssued = kOwn + NT / 2 + NT / 2 + 1;   // loads of a wave and block
+    static_assert(kDigits % (1024 * kWaves) == 0 && NT == 2 && TM == 2, "the shares of a wave");
+    constexpr int kSums = kWaves * S * kTile * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kBuffers * kBuffer > kSums ? kBuffers * kBuffer : kSums];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 32, n32 = lane % 32;
-    const int64_t steps = 2 * f.nb, nb = f.nb, nb8 = (nb + 7) / 8;
-    // Workgroups with consecutive numbers go to the 8 dies in turn: each die takes a run of row groups.
-    const int64_t total = f.col_groups * f.row_groups, id = blockIdx.x;
-    const int64_t per = (total + 7) / 8, at = id % 8 * per + id / 8;
-    if (at >= total) return;
-    const int64_t col0 = at % f.col_groups * TM, row0 = (at / f.col_groups * WN + (KS == 1 ? wave : 0)) * TN;
-    int64_t b = 0, end = nb;
-    if (KS > 1) {
-        const int64_t share = (nb + KS - 1) / KS;
-        b = wave * share < nb ? wave * share : nb;
-        end = b + share < nb ? b + share : nb;
+    const int64_t nb = f.nb, nb8 = (nb + 7) / 8, steps = 2 * nb;
+    int64_t col0, row0;
+    if (!place(f, col0, row0)) return;
+    col0 *= TM;
+    row0 = (row0 * kWaves + wave) * TN;
+    // Where the wave reads next.
+    const uint8_t *chunk[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn; k++) {
+        const int c = wave * kOwn + k, m = c / 12;   // a tile's two steps lie together: 12 KiB
+        const int64_t tile = col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1;
+        chunk[k] = digits + tile * steps * kStepBytes + c % 12 * 1024 + lane * 16;
     }
-    // Where the wave reads next; a block on, each moves by a constant.
-    const uint8_t *frags[TM];        // a tile's fragments (KS > 1)
-    const uint8_t *chunk[kOwn + 1];  // the wave's share of what goes to LDS
+    const int pm = wave / 2 % 2;   // the powers of one tile and step
+    const uint8_t *power = digits + f.col_tiles * steps * kStepBytes +
+                           ((col0 + pm < f.col_tiles ? col0 + pm : f.col_tiles - 1) * steps + wave % 2) * 256 + lane * 4;
+    // Signs: 16 bytes a lane, of tile lane / 32 the two rows 2 (lane % 16) of half lane / 16 % 2.
+    // Scales: of tile lane / 32 row lane % 32, those of a block and its neighbour.
+    const int which = lane / 32;
+    const Weight &w = S == 2 && which ? w1 : w0;
+    int64_t rt = row0 + (S == 2 ? 0 : which);
+    rt = rt < f.row_tiles ? rt : f.row_tiles - 1;
+    const uint8_t *sign = reinterpret_cast<const uint8_t *>(w.bits + rt / 2 * nb * 128 + lane / 16 % 2 * 64 + rt % 2 * 32 + lane % 16 * 2);
+    const uint16_t *scale = w.scales + rt / 2 * nb8 * 512 + (rt % 2 * 32 + n32) * 8;
+    const uint32_t base = __builtin_amdgcn_readfirstlane(
+        static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds)));
+    const auto stage = [&](int64_t i, uint32_t buffer) {   // block i; past the end the last one again, into a buffer not read
+        const int64_t b = i < nb ? i : nb - 1;
+        const uint32_t to = base + buffer * kBuffer;
+#pragma unroll
+        for (int k = 0; k < kOwn; k++) lds_load16(chunk[k] + b * 2 * kStepBytes, to + (wave * kOwn + k) * 1024);
+        lds_load16(sign + b * 1024, to + kSigns + wave * 1024);
+        lds_load4(scale + b / 8 * 512 + b % 8 / 2 * 2, to + kScales + wave * 256);
+        lds_load4(power + b * 512, to + kPowers + wave * 256);
+    };
+    const auto arrive = [&] {   // all but the loads of the kAhead - 1 newest blocks, in every wave
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kAhead - 1) * kIssued) : "memory");
+    };
+    const Signs signs(g);
+    f32x16 acc[TM][NT];
+#pragma unroll
+    for (int m = 0; m < TM; m++)
+#pragma unroll
+        for (int i = 0; i < NT; i++) acc[m][i] = f32x16{};
+#pragma unroll
+    for (int k = 0; k < kAhead; k++) stage(k, k);
+    arrive();
+    uint32_t buffer = 0;
+    for (int64_t b = 0; b < nb; b++) {
+        stage(b + kAhead, (buffer + kAhead) % kBuffers);
+        const uint8_t *in = lds + buffer * kBuffer;
+        const uint8_t *lo = in + lane * 16, *hi = in + (1024 + lane * 8), *sg = in + (kSigns + wave * 1024 + g * 256 + n32 * 8),
+                      *sc = in + (kScales + wave * 256 + n32 * 4 + (b & 1) * 2), *po = in + (kPowers + lane * 4);
+        f32x16 t[TM][NT];
+        u32x2 word[NT];
+        uint16_t d0[NT];
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+            word[i] = *reinterpret_cast<const u32x2 *>(sg + i * 512);
+            d0[i] = *reinterpret_cast<const uint16_t *>(sc + i * 128);
+#pragma unroll
+            for (int m = 0; m < TM; m++) t[m][i] = f32x16{};
+        }
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            i32x8 a[TM][4], x[NT];
+            uint32_t powers[TM];
+#pragma unroll
+            for (int m = 0; m < TM; m++) {
+                powers[m] = *reinterpret_cast<const uint32_t *>(po + (m * 2 + s) * 256);
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    const int at = (m * 2 + s) * static_cast<int>(kStepBytes) + 1536 * p;
+                    a[m][p] = frag(*reinterpret_cast<const u32x4 *>(lo + at), *reinterpret_cast<const u32x2 *>(hi + at));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NT; i++) {   // both halves' words of this step's sub-blocks to both halves of the wave
+                const auto h = __builtin_amdgcn_permlane32_swap(word[i][s], word[i][s], false, false);
+                x[i] = signs(h[0], h[1]);
+            }
+            step(t, a, x, powers);
+        }
+        fold(acc, t, d0);
+        arrive();
+        buffer = (buffer + 1) % kBuffers;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    float *own = reinterpret_cast<float *>(lds) + wave * S * kTile;   // a wave's own: its LDS accesses stay in order
+    const int from = lane / 8 * kPitch + lane % 8 * 4;
+#pragma unroll
+    for (int m = 0; m < TM; m++)
+#pragma unroll
+        for (int i = 0; i < TN; i++) {
+#pragma unroll
+            for (int s = 0; s < S; s++) put_tile(acc[m][s * TN + i], own + s * kTile, g, n32);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+            for (int q = 0; q < 4; q++)
+                finish<T, S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * kPitch),
+                             *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + from + q * 8 * kPitch),
+                             (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
+            __builtin_amdgcn_wave_barrier();
+        }
+}
+
+// Batches: KS waves share the sums of TM tiles of 32 columns and NT = TN S tiles of 32 weight
+// rows by K, each loading its digits to registers a block ahead.
+template <typename T, int TM, int TN, int S, int KS>
+__global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
+                                                              ManyShape f) {
+    constexpr int NT = TN * S;
+    __shared__ __attribute__((aligned(16))) float sums[KS * TM * NT * kTile];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int g = lane / 32, n32 = lane % 32;
+    const int64_t nb = f.nb, nb8 = (nb + 7) / 8, steps = 2 * nb;
+    int64_t col0, row0;
+    if (!place(f, col0, row0)) return;
+    col0 *= TM;
+    row0 *= TN;
+    const int64_t share = (nb + KS - 1) / KS;
+    int64_t b = wave * share < nb ? wave * share : nb;
+    const int64_t end = b + share < nb ? b + share : nb;
+    const uint8_t *frags[TM];
     const uint32_t *powers[TM];
     const u32x2 *bits[NT];
     const uint16_t *scales[NT];
 #pragma unroll
     for (int m = 0; m < TM; m++) {
         const int64_t tile = col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1;
-        frags[m] = digits + (tile * steps + 2 * b) * kStepBytes + lane * 16;
-        powers[m] = reinterpret_cast<const uint32_t *>(digits + f.col_tiles * steps * kStepBytes) + (tile * steps + 2 * b) * 64 + lane;
-    }
-#pragma unroll
-    for (int k = 0; k < kOwn; k++) {
-        const int c = wave * kOwn + k, s = c / 6 % 2, m = c / 12;   // LDS holds a tile's two steps together
-        const int64_t tile = col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1;
-        chunk[k] = digits + (tile * steps + s) * kStepBytes + c % 6 * 1024 + lane * 16;
+        frags[m] = digits + tile * steps * kStepBytes + lane * 16;
+        powers[m] = reinterpret_cast<const uint32_t *>(digits + f.col_tiles * steps * kStepBytes) + tile * steps * 64 + lane;
     }
 #pragma unroll
     for (int i = 0; i < NT; i++) {
@@ -437,7 +597,7 @@ __global__ __launch_bounds__(64 * KS * WN, 2) void q1_many_kernel(Weight w0, Wei
         int64_t rt = row0 + i % TN;
         rt = rt < f.row_tiles ? rt : f.row_tiles - 1;
         const int64_t in64 = rt % 2 * 32 + n32;
-        bits[i] = w.bits + rt / 2 * nb * 128 + b * 128 + g * 64 + in64;
+        bits[i] = w.bits + rt / 2 * nb * 128 + g * 64 + in64;
         scales[i] = w.scales + rt / 2 * nb8 * 512 + in64 * 8;
     }
     const Signs signs(g);
@@ -446,161 +606,76 @@ __global__ __launch_bounds__(64 * KS * WN, 2) void q1_many_kernel(Weight w0, Wei
     for (int m = 0; m < TM; m++)
 #pragma unroll
         for (int i = 0; i < NT; i++) acc[m][i] = f32x16{};
-    // A block's loads to registers.
     struct Loads {
         u32x2 bits[NT];
         uint16_t scales[NT];
-        uint32_t powers[TM][2];
-        u32x4 lo[KS > 1 ? TM : 1][2][4];
-        u32x2 hi[KS > 1 ? TM : 1][2][4];
+        uint32_t powers[2][TM];
+        u32x4 lo[TM][2][4];
+        u32x2 hi[TM][2][4];
     };
     const auto load = [&](int64_t i) {
         Loads l;
 #pragma unroll
         for (int k = 0; k < NT; k++) {
-            l.bits[k] = *bits[k];
-            bits[k] += 128;
+            l.bits[k] = bits[k][i * 128];
             l.scales[k] = scales[k][i / 8 * 512 + i % 8];
         }
 #pragma unroll
-        for (int m = 0; m < TM; m++) {
-#pragma unroll
-            for (int s = 0; s < 2; s++) {
-                l.powers[m][s] = powers[m][64 * s];
-                if constexpr (KS > 1) {
-#pragma unroll
-                    for (int p = 0; p < 4; p++) {
-                        const uint8_t *src = frags[m] + s * kStepBytes + 1536 * p;
-                        l.lo[m][s][p] = *reinterpret_cast<const u32x4 *>(src);
-                        l.hi[m][s][p] = *reinterpret_cast<const u32x2 *>(src + 1024 - lane * 8);
-                    }
-                }
-            }
-            powers[m] += 128;
-            frags[m] += 2 * kStepBytes;
-        }
-        return l;
-    };
-    const auto stage = [&](int buffer) {   // a block's digits to LDS
-#pragma unroll
-        for (int k = 0; k < kOwn; k++) {
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)chunk[k],
-                                             (__attribute__((address_space(3))) uint32_t *)(lds + (buffer * kChunks + wave * kOwn + k) * 1024),
-                                             16, 0, 0);
-            chunk[k] += 2 * kStepBytes;
-        }
-    };
-    const auto compute = [&](const Loads &l, int buffer) {
-        const uint8_t *lo = lds + (buffer * kChunks * 1024 + lane * 16), *hi = lds + (buffer * kChunks * 1024 + 1024 + lane * 8);
-        f32x16 t[TM][NT];
-#pragma unroll
         for (int m = 0; m < TM; m++)
 #pragma unroll
-            for (int i = 0; i < NT; i++) t[m][i] = f32x16{};
+            for (int s = 0; s < 2; s++) {
+                l.powers[s][m] = powers[m][(2 * i + s) * 64];
 #pragma unroll
-        for (int s = 0; s < 2; s++) {
-            i32x8 a[TM][4], w[NT];
+                for (int p = 0; p < 4; p++) {
+                    const uint8_t *src = frags[m] + (2 * i + s) * kStepBytes + 1536 * p;
+                    l.lo[m][s][p] = *reinterpret_cast<const u32x4 *>(src);
+                    l.hi[m][s][p] = *reinterpret_cast<const u32x2 *>(src + 1024 - lane * 8);
+                }
+            }
+        return l;
+    };
+    if (b < end) {
+        Loads l = load(b);
+        for (; b < end; b++) {
+            const Loads ahead = load(b + 1 < end ? b + 1 : b);
+            f32x16 t[TM][NT];
 #pragma unroll
             for (int m = 0; m < TM; m++)
 #pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    if constexpr (KS > 1) {
-                        a[m][p] = frag(l.lo[m][s][p], l.hi[m][s][p]);
-                    } else {
-                        const int at = (m * 2 + s) * 6144 + 1536 * p;
-                        a[m][p] = frag(*reinterpret_cast<const u32x4 *>(lo + at), *reinterpret_cast<const u32x2 *>(hi + at));
-                    }
-                }
+                for (int i = 0; i < NT; i++) t[m][i] = f32x16{};
 #pragma unroll
-            for (int i = 0; i < NT; i++) {   // both halves' words of this step's sub-blocks to both halves of the wave
-                const auto h = __builtin_amdgcn_permlane32_swap(l.bits[i][s], l.bits[i][s], false, false);
-                w[i] = signs(h[0], h[1]);
-            }
-            const auto digit = [&](auto p) {
+            for (int s = 0; s < 2; s++) {
+                i32x8 a[TM][4], x[NT];
 #pragma unroll
                 for (int m = 0; m < TM; m++)
 #pragma unroll
-                    for (int i = 0; i < NT; i++) t[m][i] = mma<decltype(p)::value>(a[m][decltype(p)::value], w[i], t[m][i], l.powers[m][s]);
-            };
-            digit(std::integral_constant<int, 0>{});
-            digit(std::integral_constant<int, 1>{});
-            digit(std::integral_constant<int, 2>{});
-            digit(std::integral_constant<int, 3>{});
-        }
+                    for (int p = 0; p < 4; p++) a[m][p] = frag(l.lo[m][s][p], l.hi[m][s][p]);
 #pragma unroll
-        for (int m = 0; m < TM; m++)
-#pragma unroll
-            for (int i = 0; i < NT; i++) {
-                const float d0 = f16_value(l.scales[i]);
-#pragma unroll
-                for (int k = 0; k < 16; k++) acc[m][i][k] = fmaf(d0, t[m][i][k], acc[m][i][k]);
+                for (int i = 0; i < NT; i++) {
+                    const auto h = __builtin_amdgcn_permlane32_swap(l.bits[i][s], l.bits[i][s], false, false);
+                    x[i] = signs(h[0], h[1]);
+                }
+                step(t, a, x, l.powers[s]);
             }
-    };
-    if constexpr (KS == 1) {
-        stage(0);
-        Loads l = load(0);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        for (; b + 1 < end; b++) {
-            const int buffer = static_cast<int>(b & 1);
-            stage(buffer ^ 1);
-            const Loads ahead = load(b + 1);
-            compute(l, buffer);
-            l = ahead;
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-        }
-        compute(l, static_cast<int>(b & 1));
-        __syncthreads();
-    } else if (b < end) {
-        Loads l = load(b);
-        for (; b + 1 < end; b++) {
-            const Loads ahead = load(b + 1);
-            compute(l, 0);
+            fold(acc, t, l.scales);
             l = ahead;
         }
-        compute(l, 0);
     }
-    // Sums go through LDS, so that a lane has four rows of a column: value k of a lane is
-    // column 8 (k / 4) + 4 g + k % 4 of its tile and row n32 of the other.
-    float *sums = reinterpret_cast<float *>(lds);
-    const auto put = [&](const f32x16 &v, float *to) {
 #pragma unroll
-        for (int k = 0; k < 16; k++) to[(8 * (k / 4) + 4 * g + k % 4) * 36 + n32] = v[k];
-    };
-    const int from = lane / 8 * 36 + lane % 8 * 4;   // the lane's four of each eight columns
-    if constexpr (KS == 1) {
-        float *own = sums + wave * S * kTile;
+    for (int m = 0; m < TM; m++)
 #pragma unroll
-        for (int m = 0; m < TM; m++)
+        for (int i = 0; i < NT; i++) put_tile(acc[m][i], sums + (wave * TM * NT + m * NT + i) * kTile, g, n32);
+    __syncthreads();
+    const int from = lane / 8 * kPitch + lane % 8 * 4;
+    for (int j = wave; j < TM * TN * 4; j += KS) {   // eight columns of a tile at a time
+        const int q = j % 4, i = j / 4 % TN, m = j / 4 / TN;
+        f32x4 v[2] = {};
 #pragma unroll
-            for (int i = 0; i < TN; i++) {
+        for (int k = 0; k < KS; k++)
 #pragma unroll
-                for (int s = 0; s < S; s++) put(acc[m][s * TN + i], own + s * kTile);
-                __builtin_amdgcn_wave_barrier();   // a wave's own tile: its LDS accesses stay in order
-#pragma unroll 1
-                for (int q = 0; q < 4; q++)
-                    finish<T, S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * 36),
-                                 *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + from + q * 8 * 36),
-                                 (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
-                __builtin_amdgcn_wave_barrier();
-            }
-    } else {
-#pragma unroll
-        for (int m = 0; m < TM; m++)
-#pragma unroll
-            for (int i = 0; i < NT; i++) put(acc[m][i], sums + (wave * TM * NT + m * NT + i) * kTile);
-        __syncthreads();
-        for (int j = wave; j < TM * TN * 4; j += KS) {   // eight columns of a tile at a time
-            const int q = j % 4, i = j / 4 % TN, m = j / 4 / TN;
-            f32x4 v[2] = {};
-#pragma unroll
-            for (int k = 0; k < KS; k++)
-#pragma unroll
-                for (int s = 0; s < S; s++)
-                    v[s] += *reinterpret_cast<const f32x4 *>(sums + (k * TM * NT + m * NT + s * TN + i) * kTile + from + q * 8 * 36);
-            finish<T, S>(w0, w1, e, v[0], v[1], (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
-        }
+            for (int s = 0; s < S; s++)
+                v[s] += *reinterpret_cast<const f32x4 *>(sums + (k * TM * NT + m * NT + s * TN + i) * kTile + from + q * 8 * kPitch);
+        finish<T, S>(w0, w1, e, v[0], v[1], (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
     }
 }
 
@@ -678,21 +753,20 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
     ManyShape f = {K / 128, (e.n + 31) / 32, (e.rows + 31) / 32, 0, 0};
     hipLaunchKernelGGL(q1_digits_kernel, dim3(static_cast<uint32_t>((2 * f.nb + 3) / 4), static_cast<uint32_t>(f.col_tiles)), dim3(256),
                        0, hs, a_q8, workspace, e.n, 2 * f.nb);
-    const auto go = [&](auto tm, auto tn, auto ks, auto wn) {
-        constexpr int TM = decltype(tm)::value, TN = decltype(tn)::value, KS = decltype(ks)::value, WN = decltype(wn)::value;
-        f.col_groups = (f.col_tiles + TM - 1) / TM;
-        f.row_groups = (f.row_tiles + TN * WN - 1) / (TN * WN);
-        const int64_t grid = (f.col_groups * f.row_groups + 7) / 8 * 8;
-        hipLaunchKernelGGL((q1_many_kernel<T, TM, TN, S, KS, WN>), dim3(static_cast<uint32_t>(grid)), dim3(64 * KS * WN), 0, hs, w0, w1,
-                           workspace, e, f);
+    const auto groups = [&](int64_t col, int64_t row) {   // of so many tiles; the grid
+        f.col_groups = (f.col_tiles + col - 1) / col;
+        f.row_groups = (f.row_tiles + row - 1) / row;
+        return f.col_groups * f.row_groups;
     };
-    using One = std::integral_constant<int, 1>;
-    using Two = std::integral_constant<int, 2>;
-    using Eight = std::integral_constant<int, 8>;
-    if ((f.col_tiles + 1) / 2 * ((f.row_tiles + 16 / S - 1) / (16 / S)) >= 128)
-        go(Two{}, std::integral_constant<int, 2 / S>{}, One{}, Eight{});
-    else
-        go(One{}, One{}, Eight{}, One{});
+    const auto grid = [](int64_t g) { return dim3(static_cast<uint32_t>((g + 7) / 8 * 8)); };
+    constexpr int TN = 2 / S;
+    const int64_t wide = groups(2, 8 * TN);
+    if (wide >= 128) {
+        hipLaunchKernelGGL((q1_wide_kernel<T, 2, TN, S>), grid(wide), dim3(512), 0, hs, w0, w1, workspace, e, f);
+    } else {
+        const int64_t split = groups(1, 1);
+        hipLaunchKernelGGL((q1_split_kernel<T, 1, 1, S, 8>), grid(split), dim3(512), 0, hs, w0, w1, workspace, e, f);
+    }
 }
 
 template <int S>
