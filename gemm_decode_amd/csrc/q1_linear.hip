@@ -440,128 +440,189 @@ __device__ __forceinline__ void lds_load4(const void *from, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory", "m0");
 }
 
-// Prompts: eight waves side by side along the rows share the digits of TM tiles of 32 columns,
-// each with NT = TN S tiles of 32 weight rows of its own (TN of each of the S weights). All
-// that a block of 128 needs comes through LDS, loaded kAhead blocks before: a shorter lead
-// leaves the waves waiting for memory 43 % of their time.
-template <typename T, int TM, int TN, int S>
+// Prompts: eight waves, two along the columns (a tile of 32 each) and four along the rows
+// (NT = TN S tiles of 32, TN of each of the S weights), take what a block of 128 needs from
+// LDS, loaded kBuffers blocks before it is used. A wave has the digits of a step in registers,
+// reads the next step's, and goes through its tiles, four instructions on the same sums each.
+template <typename T, int TN, int S>
 __global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
                                                          ManyShape f) {
-    constexpr int NT = TN * S, kWaves = 8, kAhead = 3, kBuffers = kAhead + 1;
-    // A buffer: the tiles' digits, each wave's signs and scales, the powers of two (twice).
-    constexpr int kDigits = TM * 2 * kStepBytes, kSigns = kDigits + 0, kScales = kSigns + kWaves * NT * 512,
-                  kPowers = kScales + kWaves * NT * 128, kBuffer = kPowers + kWaves * 256;
-    constexpr int kOwn = kDigits / 1024 / kWaves, kIssued = kOwn + NT / 2 + NT / 2 + 1;   // loads of a wave and block
-    static_assert(kDigits % (1024 * kWaves) == 0 && NT == 2 && TM == 2, "the shares of a wave");
-    constexpr int kSums = kWaves * S * kTile * 4;
+    constexpr int NT = TN * S, kBuffers = 4;
+    static_assert(NT == 4, "the waves' shares of the loads");
+    // A buffer: two column tiles' digits, four waves' signs and scales, the powers of two (and again).
+    constexpr int kDigits = 2 * 2 * kStepBytes, kSigns = kDigits, kScales = kSigns + 4 * NT * 512, kPowers = kScales + 4 * NT * 128,
+                  kBuffer = kPowers + 8 * 256;
+    constexpr int kIssued = 3 + 1 + 1 + 1;   // loads of a wave and block
+    constexpr int kSums = 8 * S * kTile * 4;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kBuffers * kBuffer > kSums ? kBuffers * kBuffer : kSums];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int g = lane / 32, n32 = lane % 32;
+    const int g = lane / 32, n32 = lane % 32, wm = wave / 4, wn = wave % 4;
     const int64_t nb = f.nb, nb8 = (nb + 7) / 8, steps = 2 * nb;
     int64_t col0, row0;
     if (!place(f, col0, row0)) return;
-    col0 *= TM;
-    row0 = (row0 * kWaves + wave) * TN;
-    // Where the wave reads next.
-    const uint8_t *chunk[kOwn];
-#pragma unroll
-    for (int k = 0; k < kOwn; k++) {
-        const int c = wave * kOwn + k, m = c / 12;   // a tile's two steps lie together: 12 KiB
-        const int64_t tile = col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1;
-        chunk[k] = digits + tile * steps * kStepBytes + c % 12 * 1024 + lane * 16;
-    }
-    const int pm = wave / 2 % 2;   // the powers of one tile and step
-    const uint8_t *power = digits + f.col_tiles * steps * kStepBytes +
-                           ((col0 + pm < f.col_tiles ? col0 + pm : f.col_tiles - 1) * steps + wave % 2) * 256 + lane * 4;
-    // Signs: 16 bytes a lane, of tile lane / 32 the two rows 2 (lane % 16) of half lane / 16 % 2.
-    // Scales: of tile lane / 32 row lane % 32, those of a block and its neighbour.
-    const int which = lane / 32;
-    const Weight &w = S == 2 && which ? w1 : w0;
-    int64_t rt = row0 + (S == 2 ? 0 : which);
+    col0 *= 2;
+    row0 = (row0 * 4 + wn) * TN;
+    const auto col_tile = [&](int m) { return col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1; };
+    // Where the wave reads next: three of the 24 KiB of digits (a tile's two steps lie together),
+    const uint8_t *chunk = digits + col_tile(wm) * steps * kStepBytes + wn * 3072 + lane * 16;
+    // the powers of one tile and step,
+    const uint8_t *power = digits + f.col_tiles * steps * kStepBytes + (col_tile(wn / 2) * steps + wn % 2) * 256 + lane * 4;
+    // the signs and scales of two of the four tiles of its rows: signs 16 bytes a lane, the rows
+    // 2 (lane % 16) and one more of half lane / 16 % 2, scales those of a block and its neighbour.
+    const int which = wm * 2 + lane / 32;
+    const Weight &w = which >= TN ? w1 : w0;
+    int64_t rt = row0 + which % TN;
     rt = rt < f.row_tiles ? rt : f.row_tiles - 1;
     const uint8_t *sign = reinterpret_cast<const uint8_t *>(w.bits + rt / 2 * nb * 128 + lane / 16 % 2 * 64 + rt % 2 * 32 + lane % 16 * 2);
     const uint16_t *scale = w.scales + rt / 2 * nb8 * 512 + (rt % 2 * 32 + n32) * 8;
     const uint32_t base = __builtin_amdgcn_readfirstlane(
         static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds)));
-    const auto stage = [&](int64_t i, uint32_t buffer) {   // block i; past the end the last one again, into a buffer not read
+    // One of the kIssued loads of block i; past the end the last block's again, into a buffer not read.
+    const auto stage = [&](int64_t i, uint32_t buffer, int part) {
         const int64_t b = i < nb ? i : nb - 1;
         const uint32_t to = base + buffer * kBuffer;
-#pragma unroll
-        for (int k = 0; k < kOwn; k++) lds_load16(chunk[k] + b * 2 * kStepBytes, to + (wave * kOwn + k) * 1024);
-        lds_load16(sign + b * 1024, to + kSigns + wave * 1024);
-        lds_load4(scale + b / 8 * 512 + b % 8 / 2 * 2, to + kScales + wave * 256);
-        lds_load4(power + b * 512, to + kPowers + wave * 256);
+        if (part < 3)
+            lds_load16(chunk + b * 2 * kStepBytes + part * 1024, to + (wave * 3 + part) * 1024);
+        else if (part == 3)
+            lds_load16(sign + b * 1024, to + kSigns + wn * 2048 + wm * 1024);
+        else if (part == 4)
+            lds_load4(scale + b / 8 * 512 + b % 8 / 2 * 2, to + kScales + wn * 512 + wm * 256);
+        else
+            lds_load4(power + b * 512, to + kPowers + wave * 256);
     };
-    const auto arrive = [&] {   // all but the loads of the kAhead - 1 newest blocks, in every wave
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kAhead - 1) * kIssued) : "memory");
+    const auto arrive = [&](auto behind) {   // all but the loads of so many newer blocks, in every wave
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(behind)::value * kIssued) : "memory");
     };
-    const Signs signs(g);
-    f32x16 acc[TM][NT];
-#pragma unroll
-    for (int m = 0; m < TM; m++)
-#pragma unroll
-        for (int i = 0; i < NT; i++) acc[m][i] = f32x16{};
-#pragma unroll
-    for (int k = 0; k < kAhead; k++) stage(k, k);
-    arrive();
-    uint32_t buffer = 0;
-    for (int64_t b = 0; b < nb; b++) {
-        stage(b + kAhead, (buffer + kAhead) % kBuffers);
+    // What a wave has of a step in registers: digits, their powers, the words of both halves.
+    struct Step {
+        i32x8 a[4];
+        uint32_t powers, half0[NT], half1[NT];
+    };
+    const auto read = [&](uint32_t buffer, int s) {
         const uint8_t *in = lds + buffer * kBuffer;
-        const uint8_t *lo = in + lane * 16, *hi = in + (1024 + lane * 8), *sg = in + (kSigns + wave * 1024 + g * 256 + n32 * 8),
-                      *sc = in + (kScales + wave * 256 + n32 * 4 + (b & 1) * 2), *po = in + (kPowers + lane * 4);
-        f32x16 t[TM][NT];
-        u32x2 word[NT];
-        uint16_t d0[NT];
+        const uint8_t *lo = in + (wm * 12288 + lane * 16), *hi = in + (wm * 12288 + 1024 + lane * 8),
+                      *sg = in + (kSigns + wn * 2048 + n32 * 8), *po = in + (kPowers + wm * 512 + lane * 4);
+        Step k;
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+            const int at = s * static_cast<int>(kStepBytes) + 1536 * p;
+            // (volatile: not two of them in one instruction, whose results would have to be moved)
+            const u32x2 h = *(const volatile __attribute__((address_space(3))) u32x2 *)(hi + at);
+            k.a[p] = frag(*reinterpret_cast<const u32x4 *>(lo + at), h);
+        }
+        k.powers = *reinterpret_cast<const uint32_t *>(po + s * 256);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
-            word[i] = *reinterpret_cast<const u32x2 *>(sg + i * 512);
-            d0[i] = *reinterpret_cast<const uint16_t *>(sc + i * 128);
-#pragma unroll
-            for (int m = 0; m < TM; m++) t[m][i] = f32x16{};
+            k.half0[i] = *reinterpret_cast<const uint32_t *>(sg + i * 512 + s * 4);
+            k.half1[i] = *reinterpret_cast<const uint32_t *>(sg + i * 512 + s * 4 + 256);
         }
+        return k;
+    };
+    const Signs signs(g);
+    f32x16 acc[NT], t[NT];
+    float d0[NT], before[NT];   // scales of this block and of the one before it
 #pragma unroll
-        for (int s = 0; s < 2; s++) {
-            i32x8 a[TM][4], x[NT];
-            uint32_t powers[TM];
+    for (int i = 0; i < NT; i++) {
+        acc[i] = t[i] = f32x16{};
+        before[i] = 0.0f;
+    }
+    // acc += d0 t, values k .. k + 7 of a tile
+    const auto fold8 = [&](int i, int k, float d) {
 #pragma unroll
-            for (int m = 0; m < TM; m++) {
-                powers[m] = *reinterpret_cast<const uint32_t *>(po + (m * 2 + s) * 256);
+        for (int j = k; j < k + 8; j++) acc[i][j] = fmaf(d, t[i][j], acc[i][j]);
+    };
+    // Four instructions of tile i with `vector` others spread between them: a matrix instruction
+    // hides up to five or six of those, whichever wave they are of, but not a run of them.
+    const auto multiply = [&](const Step &k, int i, const i32x8 &x) {
+        t[i] = mma<0>(k.a[0], x, t[i], k.powers);
+        t[i] = mma<1>(k.a[1], x, t[i], k.powers);
+        t[i] = mma<2>(k.a[2], x, t[i], k.powers);
+        t[i] = mma<3>(k.a[3], x, t[i], k.powers);
+    };
+    const auto spread = [](auto vector) {
 #pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    const int at = (m * 2 + s) * static_cast<int>(kStepBytes) + 1536 * p;
-                    a[m][p] = frag(*reinterpret_cast<const u32x4 *>(lo + at), *reinterpret_cast<const u32x2 *>(hi + at));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NT; i++) {   // both halves' words of this step's sub-blocks to both halves of the wave
-                const auto h = __builtin_amdgcn_permlane32_swap(word[i][s], word[i][s], false, false);
-                x[i] = signs(h[0], h[1]);
-            }
-            step(t, a, x, powers);
+        for (int i = 0; i < 4; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, decltype(vector)::value, 0);
         }
-        fold(acc, t, d0);
-        arrive();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using Few = std::integral_constant<int, 4>;
+    using More = std::integral_constant<int, 7>;
+#pragma unroll
+    for (int k = 0; k < kBuffers; k++)
+#pragma unroll
+        for (int part = 0; part < kIssued; part++) stage(k, k, part);
+    arrive(std::integral_constant<int, kBuffers - 1>{});
+    Step first = read(0, 0);
+    i32x8 x = signs(first.half0[0], first.half1[0]);
+    uint32_t buffer = 0;
+    for (int64_t b = 0; b < nb; b++) {
+        const Step second = read(buffer, 1);
+        const uint8_t *sc = lds + buffer * kBuffer + (kScales + wn * 512 + n32 * 4 + (b & 1) * 2);
+#pragma unroll
+        for (int i = 0; i < NT; i++) d0[i] = f16_value(*reinterpret_cast<const uint16_t *>(sc + i * 128));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < NT; i++) {   // the first step, with what is left of the block before it
+            if (i < 2) {
+                fold8(2 + i, 0, before[2 + i]);
+                fold8(2 + i, 8, before[2 + i]);
+            }
+            const i32x8 next = i + 1 < NT ? signs(first.half0[(i + 1) % NT], first.half1[(i + 1) % NT]) : signs(second.half0[0], second.half1[0]);
+            t[i] = f32x16{};
+            multiply(first, i, x);
+            x = next;
+            if (i < 2)
+                spread(More{});
+            else
+                spread(Few{});
+        }
+        arrive(std::integral_constant<int, kBuffers - 2>{});   // the next block; and nobody reads this one any more
+        const uint32_t free = buffer;
         buffer = (buffer + 1) % kBuffers;
+        first = read(buffer, 0);
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+            stage(b + kBuffers, free, i);
+            if (i == 2) stage(b + kBuffers, free, 4);
+            if (i == 3) stage(b + kBuffers, free, 5);
+            if (i >= 2) {
+                fold8(i - 2, 0, d0[i - 2]);
+                fold8(i - 2, 8, d0[i - 2]);
+            }
+            const i32x8 next = i + 1 < NT ? signs(second.half0[(i + 1) % NT], second.half1[(i + 1) % NT]) : signs(first.half0[0], first.half1[0]);
+            multiply(second, i, x);
+            x = next;
+            if (i >= 2)
+                spread(More{});
+            else
+                spread(Few{});
+        }
+#pragma unroll
+        for (int i = 0; i < NT; i++) before[i] = d0[i];
+    }
+#pragma unroll
+    for (int i = 2; i < NT; i++) {
+        fold8(i, 0, before[i]);
+        fold8(i, 8, before[i]);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     float *own = reinterpret_cast<float *>(lds) + wave * S * kTile;   // a wave's own: its LDS accesses stay in order
     const int from = lane / 8 * kPitch + lane % 8 * 4;
 #pragma unroll
-    for (int m = 0; m < TM; m++)
+    for (int i = 0; i < TN; i++) {
 #pragma unroll
-        for (int i = 0; i < TN; i++) {
-#pragma unroll
-            for (int s = 0; s < S; s++) put_tile(acc[m][s * TN + i], own + s * kTile, g, n32);
-            __builtin_amdgcn_wave_barrier();
+        for (int s = 0; s < S; s++) put_tile(acc[s * TN + i], own + s * kTile, g, n32);
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-            for (int q = 0; q < 4; q++)
-                finish<T, S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * kPitch),
-                             *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + from + q * 8 * kPitch),
-                             (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
-            __builtin_amdgcn_wave_barrier();
-        }
+        for (int q = 0; q < 4; q++)
+            finish<T, S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * kPitch),
+                         *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + from + q * 8 * kPitch),
+                         (col0 + wm) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // Batches: KS waves share the sums of TM tiles of 32 columns and NT = TN S tiles of 32 weight
@@ -759,10 +820,10 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
         return f.col_groups * f.row_groups;
     };
     const auto grid = [](int64_t g) { return dim3(static_cast<uint32_t>((g + 7) / 8 * 8)); };
-    constexpr int TN = 2 / S;
-    const int64_t wide = groups(2, 8 * TN);
+    constexpr int TN = 4 / S;
+    const int64_t wide = groups(2, 4 * TN);
     if (wide >= 128) {
-        hipLaunchKernelGGL((q1_wide_kernel<T, 2, TN, S>), grid(wide), dim3(512), 0, hs, w0, w1, workspace, e, f);
+        hipLaunchKernelGGL((q1_wide_kernel<T, TN, S>), grid(wide), dim3(512), 0, hs, w0, w1, workspace, e, f);
     } else {
         const int64_t split = groups(1, 1);
         hipLaunchKernelGGL((q1_split_kernel<T, 1, 1, S, 8>), grid(split), dim3(512), 0, hs, w0, w1, workspace, e, f);
