@@ -431,13 +431,20 @@ __device__ __forceinline__ bool place(const ManyShape &f, int64_t &col_group, in
     return at < total;
 }
 
-// 64 lanes times 16 (or 4) bytes from the lanes' addresses to LDS at `to` on. The compiler
-// does not see these loads: who reads what they bring waits with arrive().
-__device__ __forceinline__ void lds_load16(const void *from, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+// Loads of 16 (or 4) bytes a lane from base + `at` (per lane) to LDS, lane after lane from `to`
+// on: N of them, 1 KiB apart on both sides. The compiler does not see these loads: who reads
+// what they bring waits for them first.
+template <int N>
+__device__ __forceinline__ void lds_load16(const void *base, uint32_t at, uint32_t to) {
+    static_assert(N == 1 || N == 3, "as written");
+    if constexpr (N == 1)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(at), "s"(base) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024\n\t"
+                     "global_load_lds_dwordx4 %1, %2 offset:2048" ::"s"(to), "v"(at), "s"(base) : "memory", "m0");
 }
-__device__ __forceinline__ void lds_load4(const void *from, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+__device__ __forceinline__ void lds_load4(const void *base, uint32_t at, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(at), "s"(base) : "memory", "m0");
 }
 
 // Prompts: eight waves, two along the columns (a tile of 32 each) and four along the rows
@@ -463,32 +470,36 @@ __global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     col0 *= 2;
     row0 = (row0 * 4 + wn) * TN;
     const auto col_tile = [&](int m) { return col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1; };
-    // Where the wave reads next: three of the 24 KiB of digits (a tile's two steps lie together),
-    const uint8_t *chunk = digits + col_tile(wm) * steps * kStepBytes + wn * 3072 + lane * 16;
-    // the powers of one tile and step,
-    const uint8_t *power = digits + f.col_tiles * steps * kStepBytes + (col_tile(wn / 2) * steps + wn % 2) * 256 + lane * 4;
-    // the signs and scales of two of the four tiles of its rows: signs 16 bytes a lane, the rows
-    // 2 (lane % 16) and one more of half lane / 16 % 2, scales those of a block and its neighbour.
-    const int which = wm * 2 + lane / 32;
+    // Where a block lies for the wave: three of the 24 KiB of digits (a tile's two steps are
+    // together), the powers of one tile and step, the signs and scales of two of its rows' four
+    // tiles. Signs 16 bytes a lane, the rows 2 (lane % 16) and one more of half lane / 16 % 2;
+    // scales those of a block and its neighbour.
+    const uint8_t *chunk = digits + col_tile(wm) * steps * kStepBytes + wn * 3072;
+    const uint8_t *power = digits + f.col_tiles * steps * kStepBytes + (col_tile(wn / 2) * steps + wn % 2) * 256;
+    const int which = wm * 2;   // and the one behind it: of the same weight
     const Weight &w = which >= TN ? w1 : w0;
-    int64_t rt = row0 + which % TN;
-    rt = rt < f.row_tiles ? rt : f.row_tiles - 1;
-    const uint8_t *sign = reinterpret_cast<const uint8_t *>(w.bits + rt / 2 * nb * 128 + lane / 16 % 2 * 64 + rt % 2 * 32 + lane % 16 * 2);
-    const uint16_t *scale = w.scales + rt / 2 * nb8 * 512 + (rt % 2 * 32 + n32) * 8;
+    const auto row_tile = [&](int i) { return row0 + i < f.row_tiles ? row0 + i : f.row_tiles - 1; };
+    const int64_t ra = row_tile(which % TN), rb = row_tile(which % TN + 1);
+    const uint8_t *sign = reinterpret_cast<const uint8_t *>(w.bits + ra / 2 * nb * 128 + ra % 2 * 32);
+    const uint8_t *scale = reinterpret_cast<const uint8_t *>(w.scales + ra / 2 * nb8 * 512 + ra % 2 * 256);
+    const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+    const uint32_t sign_at = g * static_cast<uint32_t>((rb / 2 - ra / 2) * nb * 1024 + (rb % 2 - ra % 2) * 256) + lane / 16 % 2 * 512 + lane % 16 * 16;
+    const uint32_t scale_at = g * static_cast<uint32_t>((rb / 2 - ra / 2) * nb8 * 1024 + (rb % 2 - ra % 2) * 512) + n32 * 16;
     const uint32_t base = __builtin_amdgcn_readfirstlane(
         static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds)));
-    // One of the kIssued loads of block i; past the end the last block's again, into a buffer not read.
-    const auto stage = [&](int64_t i, uint32_t buffer, int part) {
-        const int64_t b = i < nb ? i : nb - 1;
-        const uint32_t to = base + buffer * kBuffer;
-        if (part < 3)
-            lds_load16(chunk + b * 2 * kStepBytes + part * 1024, to + (wave * 3 + part) * 1024);
-        else if (part == 3)
-            lds_load16(sign + b * 1024, to + kSigns + wn * 2048 + wm * 1024);
-        else if (part == 4)
-            lds_load4(scale + b / 8 * 512 + b % 8 / 2 * 2, to + kScales + wn * 512 + wm * 256);
+    const int blocks = static_cast<int>(nb);
+    // The kIssued loads of block i, one group of them after the other; past the end the last
+    // block's again, into a buffer not read.
+    const auto stage = [&](int i, uint32_t to, int part) {
+        const uint32_t b = i < blocks ? i : blocks - 1;
+        if (part == 0)
+            lds_load16<3>(chunk + b * static_cast<uint32_t>(2 * kStepBytes), lane16, to + wave * 3072);
+        else if (part == 1)
+            lds_load16<1>(sign + b * 1024u, sign_at, to + kSigns + wn * 2048 + wm * 1024);
+        else if (part == 2)
+            lds_load4(scale + (b / 8 * 1024u + b % 8 / 2 * 4), scale_at, to + kScales + wn * 512 + wm * 256);
         else
-            lds_load4(power + b * 512, to + kPowers + wave * 256);
+            lds_load4(power + b * 512u, lane4, to + kPowers + wave * 256);
     };
     const auto arrive = [&](auto behind) {   // all but the loads of so many newer blocks, in every wave
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(behind)::value * kIssued) : "memory");
@@ -498,8 +509,8 @@ __global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, c
         i32x8 a[4];
         uint32_t powers, half0[NT], half1[NT];
     };
-    const auto read = [&](uint32_t buffer, int s) {
-        const uint8_t *in = lds + buffer * kBuffer;
+    const auto read = [&](uint32_t at, int s) {   // at: the buffer's place
+        const uint8_t *in = lds + at;
         const uint8_t *lo = in + (wm * 12288 + lane * 16), *hi = in + (wm * 12288 + 1024 + lane * 8),
                       *sg = in + (kSigns + wn * 2048 + n32 * 8), *po = in + (kPowers + wm * 512 + lane * 4);
         Step k;
@@ -552,14 +563,14 @@ __global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, c
 #pragma unroll
     for (int k = 0; k < kBuffers; k++)
 #pragma unroll
-        for (int part = 0; part < kIssued; part++) stage(k, k, part);
+        for (int part = 0; part < 4; part++) stage(k, base + k * kBuffer, part);
     arrive(std::integral_constant<int, kBuffers - 1>{});
     Step first = read(0, 0);
     i32x8 x = signs(first.half0[0], first.half1[0]);
-    uint32_t buffer = 0;
-    for (int64_t b = 0; b < nb; b++) {
-        const Step second = read(buffer, 1);
-        const uint8_t *sc = lds + buffer * kBuffer + (kScales + wn * 512 + n32 * 4 + (b & 1) * 2);
+    uint32_t at = 0;
+    for (int b = 0; b < blocks; b++) {
+        const Step second = read(at, 1);
+        const uint8_t *sc = lds + at + (kScales + wn * 512 + n32 * 4 + (b & 1) * 2);
 #pragma unroll
         for (int i = 0; i < NT; i++) d0[i] = f16_value(*reinterpret_cast<const uint16_t *>(sc + i * 128));
         __builtin_amdgcn_sched_barrier(0);
@@ -579,14 +590,12 @@ __global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, c
                 spread(Few{});
         }
         arrive(std::integral_constant<int, kBuffers - 2>{});   // the next block; and nobody reads this one any more
-        const uint32_t free = buffer;
-        buffer = (buffer + 1) % kBuffers;
-        first = read(buffer, 0);
+        const uint32_t to = base + at;
+        at = at == (kBuffers - 1) * kBuffer ? 0 : at + kBuffer;
+        first = read(at, 0);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
-            stage(b + kBuffers, free, i);
-            if (i == 2) stage(b + kBuffers, free, 4);
-            if (i == 3) stage(b + kBuffers, free, 5);
+            stage(b + kBuffers, to, i);
             if (i >= 2) {
                 fold8(i - 2, 0, d0[i - 2]);
                 fold8(i - 2, 8, d0[i - 2]);
