@@ -447,59 +447,61 @@ __device__ __forceinline__ void lds_load4(const void *base, uint32_t at, uint32_
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(at), "s"(base) : "memory", "m0");
 }
 
-// Prompts: eight waves, two along the columns (a tile of 32 each) and four along the rows
-// (NT = TN S tiles of 32, TN of each of the S weights), take what a block of 128 needs from
-// LDS, loaded kBuffers blocks before it is used. A wave has the digits of a step in registers,
-// reads the next step's, and goes through its tiles, four instructions on the same sums each.
+// Prompts: four waves side by side along the rows (each NT = TN S tiles of 32, TN of each of the
+// S weights) share a tile of 32 columns and take what a block of 128 needs from LDS, loaded
+// kBuffers blocks before it is used. A wave has the digits of a step in registers, reads the
+// next step's, and goes through its tiles, four instructions on the same sums each. Two
+// workgroups on a CU, so that one wave of a SIMD works while the other one waits for its own.
 template <typename T, int TN, int S>
-__global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
+__global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
                                                          ManyShape f) {
-    constexpr int NT = TN * S, kBuffers = 4;
+    constexpr int NT = TN * S, kWaves = 4, kBuffers = 3;
     static_assert(NT == 4, "the waves' shares of the loads");
-    // A buffer: two column tiles' digits, four waves' signs and scales, the powers of two (and again).
-    constexpr int kDigits = 2 * 2 * kStepBytes, kSigns = kDigits, kScales = kSigns + 4 * NT * 512, kPowers = kScales + 4 * NT * 128,
-                  kBuffer = kPowers + 8 * 256;
-    constexpr int kIssued = 3 + 1 + 1 + 1;   // loads of a wave and block
-    constexpr int kSums = 8 * S * kTile * 4;
+    // A buffer: the column tile's digits, the waves' signs and scales, the powers of two (twice).
+    constexpr int kSigns = 2 * kStepBytes, kScales = kSigns + kWaves * NT * 512, kPowers = kScales + kWaves * NT * 128,
+                  kBuffer = kPowers + kWaves * 256;
+    constexpr int kIssued = 3 + 2 + 2 + 1;   // loads of a wave and block
+    constexpr int kSums = kWaves * S * kTile * 4;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kBuffers * kBuffer > kSums ? kBuffers * kBuffer : kSums];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int g = lane / 32, n32 = lane % 32, wm = wave / 4, wn = wave % 4;
+    const int g = lane / 32, n32 = lane % 32;
     const int64_t nb = f.nb, nb8 = (nb + 7) / 8, steps = 2 * nb;
-    int64_t col0, row0;
-    if (!place(f, col0, row0)) return;
-    col0 *= 2;
-    row0 = (row0 * 4 + wn) * TN;
-    const auto col_tile = [&](int m) { return col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1; };
-    // Where a block lies for the wave: three of the 24 KiB of digits (a tile's two steps are
-    // together), the powers of one tile and step, the signs and scales of two of its rows' four
-    // tiles. Signs 16 bytes a lane, the rows 2 (lane % 16) and one more of half lane / 16 % 2;
-    // scales those of a block and its neighbour.
-    const uint8_t *chunk = digits + col_tile(wm) * steps * kStepBytes + wn * 3072;
-    const uint8_t *power = digits + f.col_tiles * steps * kStepBytes + (col_tile(wn / 2) * steps + wn % 2) * 256;
-    const int which = wm * 2;   // and the one behind it: of the same weight
-    const Weight &w = which >= TN ? w1 : w0;
-    const auto row_tile = [&](int i) { return row0 + i < f.row_tiles ? row0 + i : f.row_tiles - 1; };
-    const int64_t ra = row_tile(which % TN), rb = row_tile(which % TN + 1);
-    const uint8_t *sign = reinterpret_cast<const uint8_t *>(w.bits + ra / 2 * nb * 128 + ra % 2 * 32);
-    const uint8_t *scale = reinterpret_cast<const uint8_t *>(w.scales + ra / 2 * nb8 * 512 + ra % 2 * 256);
+    int64_t col, row0;
+    if (!place(f, col, row0)) return;
+    row0 = (row0 * kWaves + wave) * TN;
+    // Where a block lies for the wave: three of the 12 KiB of digits (two steps are together), the
+    // powers of one step, the signs and scales of its tiles, two at a time. Signs 16 bytes a
+    // lane, the rows 2 (lane % 16) and one more of half lane / 16 % 2; scales those of a block
+    // and its neighbour.
+    const uint8_t *chunk = digits + col * steps * kStepBytes + wave * 3072;
+    const uint8_t *power = digits + (f.col_tiles * steps * kStepBytes + (col * steps + wave % 2) * 256);
+    const uint8_t *sign[2], *scale[2];
+    uint32_t sign_at[2], scale_at[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const Weight &w = 2 * i >= TN ? w1 : w0;
+        const int64_t last = f.row_tiles - 1, ra = row0 + 2 * i % TN < last ? row0 + 2 * i % TN : last, rb = ra < last ? ra + 1 : last;
+        sign[i] = reinterpret_cast<const uint8_t *>(w.bits + ra / 2 * nb * 128 + ra % 2 * 32);
+        scale[i] = reinterpret_cast<const uint8_t *>(w.scales + ra / 2 * nb8 * 512 + ra % 2 * 256);
+        sign_at[i] = g * static_cast<uint32_t>((rb / 2 - ra / 2) * nb * 1024 + (rb % 2 - ra % 2) * 256) + lane / 16 % 2 * 512 + lane % 16 * 16;
+        scale_at[i] = g * static_cast<uint32_t>((rb / 2 - ra / 2) * nb8 * 1024 + (rb % 2 - ra % 2) * 512) + n32 * 16;
+    }
     const uint32_t lane16 = lane * 16, lane4 = lane * 4;
-    const uint32_t sign_at = g * static_cast<uint32_t>((rb / 2 - ra / 2) * nb * 1024 + (rb % 2 - ra % 2) * 256) + lane / 16 % 2 * 512 + lane % 16 * 16;
-    const uint32_t scale_at = g * static_cast<uint32_t>((rb / 2 - ra / 2) * nb8 * 1024 + (rb % 2 - ra % 2) * 512) + n32 * 16;
     const uint32_t base = __builtin_amdgcn_readfirstlane(
         static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds)));
     const int blocks = static_cast<int>(nb);
-    // The kIssued loads of block i, one group of them after the other; past the end the last
+    // The kIssued loads of block i, two of them in each part but the first; past the end the last
     // block's again, into a buffer not read.
     const auto stage = [&](int i, uint32_t to, int part) {
         const uint32_t b = i < blocks ? i : blocks - 1;
-        if (part == 0)
+        if (part == 0) {
             lds_load16<3>(chunk + b * static_cast<uint32_t>(2 * kStepBytes), lane16, to + wave * 3072);
-        else if (part == 1)
-            lds_load16<1>(sign + b * 1024u, sign_at, to + kSigns + wn * 2048 + wm * 1024);
-        else if (part == 2)
-            lds_load4(scale + (b / 8 * 1024u + b % 8 / 2 * 4), scale_at, to + kScales + wn * 512 + wm * 256);
-        else
+        } else if (part == 1) {
             lds_load4(power + b * 512u, lane4, to + kPowers + wave * 256);
+        } else {
+            lds_load16<1>(sign[part - 2] + b * 1024u, sign_at[part - 2], to + kSigns + wave * 2048 + (part - 2) * 1024);
+            lds_load4(scale[part - 2] + (b / 8 * 1024u + b % 8 / 2 * 4), scale_at[part - 2], to + kScales + wave * 512 + (part - 2) * 256);
+        }
     };
     const auto arrive = [&](auto behind) {   // all but the loads of so many newer blocks, in every wave
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(behind)::value * kIssued) : "memory");
@@ -511,8 +513,8 @@ __global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     };
     const auto read = [&](uint32_t at, int s) {   // at: the buffer's place
         const uint8_t *in = lds + at;
-        const uint8_t *lo = in + (wm * 12288 + lane * 16), *hi = in + (wm * 12288 + 1024 + lane * 8),
-                      *sg = in + (kSigns + wn * 2048 + n32 * 8), *po = in + (kPowers + wm * 512 + lane * 4);
+        const uint8_t *lo = in + lane * 16, *hi = in + (1024 + lane * 8), *sg = in + (kSigns + wave * 2048 + n32 * 8),
+                      *po = in + (kPowers + lane * 4);
         Step k;
 #pragma unroll
         for (int p = 0; p < 4; p++) {
@@ -570,7 +572,7 @@ __global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     uint32_t at = 0;
     for (int b = 0; b < blocks; b++) {
         const Step second = read(at, 1);
-        const uint8_t *sc = lds + at + (kScales + wn * 512 + n32 * 4 + (b & 1) * 2);
+        const uint8_t *sc = lds + at + (kScales + wave * 512 + n32 * 4 + (b & 1) * 2);
 #pragma unroll
         for (int i = 0; i < NT; i++) d0[i] = f16_value(*reinterpret_cast<const uint16_t *>(sc + i * 128));
         __builtin_amdgcn_sched_barrier(0);
@@ -629,7 +631,7 @@ __global__ __launch_bounds__(512, 2) void q1_wide_kernel(Weight w0, Weight w1, c
         for (int q = 0; q < 4; q++)
             finish<T, S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * kPitch),
                          *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + from + q * 8 * kPitch),
-                         (col0 + wm) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
+                         col * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
         __builtin_amdgcn_wave_barrier();
     }
 }
@@ -830,9 +832,9 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
     };
     const auto grid = [](int64_t g) { return dim3(static_cast<uint32_t>((g + 7) / 8 * 8)); };
     constexpr int TN = 4 / S;
-    const int64_t wide = groups(2, 4 * TN);
-    if (wide >= 128) {
-        hipLaunchKernelGGL((q1_wide_kernel<T, TN, S>), grid(wide), dim3(512), 0, hs, w0, w1, workspace, e, f);
+    const int64_t wide = groups(1, 4 * TN);
+    if (wide >= 256) {
+        hipLaunchKernelGGL((q1_wide_kernel<T, TN, S>), grid(wide), dim3(256), 0, hs, w0, w1, workspace, e, f);
     } else {
         const int64_t split = groups(1, 1);
         hipLaunchKernelGGL((q1_split_kernel<T, 1, 1, S, 8>), grid(split), dim3(512), 0, hs, w0, w1, workspace, e, f);
