@@ -28,7 +28,7 @@ struct Epilogue {
     void *y;
     uint16_t *y_q8;
     int64_t rows, n;
-    int32_t act;
+    int32_t act, dtype;   // GD_ACT_, GD_F32 .. of residual and y
 };
 
 __device__ __forceinline__ float f16_value(uint16_t h) { return static_cast<float>(__builtin_bit_cast(_Float16, h)); }
@@ -103,7 +103,7 @@ __device__ __forceinline__ void store_some(T *p, f32x4 v, int count) {
 // What becomes of the sums v (and u, the second weight's) of rows r .. r + 3, r % 4 = 0, and
 // column c. Where q8_0 blocks are written, eight neighbouring lanes hold the 32 rows of one
 // (r / 4 % 8 = lane % 8) and all of them call this.
-template <typename T, int S>
+template <int S>
 __device__ __forceinline__ void finish(const Weight &w0, const Weight &w1, const Epilogue &e, f32x4 v, f32x4 u, int64_t c, int64_t r) {
     const int64_t rest = c < e.n ? e.rows - r : 0;
     const int count = rest >= 4 ? 4 : rest > 0 ? static_cast<int>(rest) : 0;
@@ -113,8 +113,17 @@ __device__ __forceinline__ void finish(const Weight &w0, const Weight &w1, const
     for (int j = 0; j < 4; j++) v[j] = activate(v[j], e.act);
     if (S == 2) v *= u;
     const int64_t at = c * e.rows + r;
-    if (e.residual) v += load_some(static_cast<const T *>(e.residual) + at, count);
-    if (e.y) store_some(static_cast<T *>(e.y) + at, v, count);
+    const auto outer = [&](auto one) {
+        using T = decltype(one);
+        if (e.residual) v += load_some(static_cast<const T *>(e.residual) + at, count);
+        if (e.y) store_some(static_cast<T *>(e.y) + at, v, count);
+    };
+    if (e.dtype == GD_F32)
+        outer(float{});
+    else if (e.dtype == GD_F16)
+        outer(_Float16{});
+    else
+        outer(__bf16{});
     if (e.y_q8) {
         const float a = max8(absmax4(float4{v[0], v[1], v[2], v[3]}));
         const uint32_t q = codes_of(v, a);
@@ -228,42 +237,71 @@ __device__ __forceinline__ i32x8 frag(u32x4 lo, u32x2 hi) {
 // of column c), its columns 16 weight rows, so that a lane's four results are the digits'
 // sums of one row and column, and one instruction takes a weight block of 16 rows.
 //
-// A workgroup of eight waves holds the digits of `kBlocks` blocks in LDS and takes 16-row
-// tiles of the weights, KW waves sharing a tile by its K.
+// A workgroup of eight waves holds the digits of kBlocks blocks in LDS and takes 16-row tiles
+// of the weights, kw waves sharing a tile by its K in quads of blocks. A wave's loads of its
+// TILES tiles and Q quads all go out before the digits are worked out: the call is as long
+// as a few memory latencies, and this hides the digits behind one.
 constexpr int kFew = 512;
 template <int C>
 constexpr int kBlocks = 128 / C;
 
 struct FewShape {
-    int64_t nb;        // blocks of a row
-    int kw, tiles;     // waves along K; 16-row tiles a wave takes (at most 4)
+    int64_t nb;   // blocks of a row
+    int kw;       // waves along K: 1, 2, 4 or 8
 };
 
-template <typename T, int C, int S>
+template <int C, int S, int TILES, int Q>
 __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, const uint16_t *__restrict__ a_q8, Epilogue e,
                                                          FewShape f) {
-    constexpr int kQuads = C == 1 ? 4 : 2;   // of blocks, a wave's of a chunk at most
+    constexpr int N = TILES * S;   // a wave's tiles of both weights
     __shared__ __attribute__((aligned(16))) uint16_t digits[kBlocks<C> * 4 * 4 * C * 12];
     __shared__ uint32_t powers[kBlocks<C> * 4 * C];
-    __shared__ __attribute__((aligned(16))) float red[8 * 4 * S * 64];
+    __shared__ __attribute__((aligned(16))) float red[8 * N * 64];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int g = lane / 16, n16 = lane % 16, n = static_cast<int>(e.n);
     const int kpart = wave % f.kw, ipart = wave / f.kw, groups = 8 / f.kw;
-    const int64_t nb = f.nb, nb8 = (nb + 7) / 8;
-    const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * f.tiles * groups, last = (e.rows + 15) / 16 - 1;
+    const int nb = static_cast<int>(f.nb), nb8 = (nb + 7) / 8;
+    const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * TILES * groups, last = (e.rows + 15) / 16 - 1;
     const int row_a = n16 / 4 < n ? n16 : n16 % 4;   // rows of no column repeat another's
     const Signs signs(g & 1);
-    float acc[4 * S];
+    const u32x2 *bits[N];
+    const uint16_t *scales[N];
 #pragma unroll
-    for (int i = 0; i < 4 * S; i++) acc[i] = 0.0f;
-    for (int64_t b0 = 0; b0 < nb; b0 += kBlocks<C>) {
-        const int blocks = static_cast<int>(nb - b0 < kBlocks<C> ? nb - b0 : kBlocks<C>);
+    for (int i = 0; i < N; i++) {
+        const Weight &w = i / TILES ? w1 : w0;
+        int64_t tile = tile0 + i % TILES * groups + ipart;
+        tile = tile <= last ? tile : last;
+        const int in64 = static_cast<int>(tile % 4) * 16 + n16;
+        bits[i] = w.bits + tile / 4 * nb * 128 + (g & 1) * 64 + in64;
+        scales[i] = w.scales + tile / 4 * nb8 * 512 + in64 * 8;
+    }
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) acc[i] = 0.0f;
+    for (int b0 = 0; b0 < nb; b0 += kBlocks<C>) {
+        const int blocks = nb - b0 < kBlocks<C> ? nb - b0 : kBlocks<C>;
+        u32x2 word[Q][N][2], d0[Q][N];
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+            int i0 = 4 * (kpart + q * f.kw);
+            i0 = b0 + (i0 < blocks ? i0 : 0);   // past the end: loaded, not used
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+#pragma unroll
+                for (int k = 0; k < 2; k++) {   // block i0 + 2 k + g / 2, half g % 2
+                    const int b = i0 + 2 * k + (g >> 1);
+                    word[q][i][k] = __builtin_nontemporal_load(bits[i] + static_cast<int64_t>(b < nb ? b : nb - 1) * 128);
+                }
+                d0[q][i] = *reinterpret_cast<const u32x2 *>(scales[i] + i0 / 8 * 512 + i0 % 8);
+            }
+        }
         if (b0) __syncthreads();
         // Digits: a thread takes eight elements of a sub-block at a time.
-        for (int i = tid; i < blocks * 16 * n; i += kFew) {
-            const int j = i % 4, sub = i / 4 % (blocks * 4), c = i / 4 / (blocks * 4);
+        const int subs = blocks * 4;
+        for (int i = tid; i < subs * 4 * n; i += kFew) {
+            const int j = i % 4, c = i / 4 / subs, sub = i / 4 - c * subs;
             uint32_t d[8], r[2][4];
-            const Scale s(load_block(a_q8 + ((c * nb + b0) * 4 + sub) * 17, d));
+            const Scale s(load_block(a_q8 + ((static_cast<int64_t>(c) * nb + b0) * 4 + sub) * 17, d));
             digits8(d, j, s.m, r);
 #pragma unroll
             for (int p = 0; p < 4; p++) {
@@ -276,56 +314,39 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
         }
         __syncthreads();
 #pragma unroll
-        for (int it = 0; it < 4; it++) {
-            if (it >= f.tiles) break;
-            int64_t tile = tile0 + it * groups + ipart;
-            tile = tile <= last ? tile : last;
-            const int64_t t64 = tile / 4;
-            const int in64 = static_cast<int>(tile % 4) * 16 + n16;
+        for (int q = 0; q < Q; q++) {
+            const int i0 = 4 * (kpart + q * f.kw);
+            uint32_t x[2][N];   // words 0 and 1 of both halves of a block to the lanes of their sub-blocks
 #pragma unroll
-            for (int s = 0; s < S; s++) {
-                const Weight &w = s ? w1 : w0;
-                float sum = acc[it * S + s];
+            for (int k = 0; k < 4; k++) {
+                if (i0 + k >= blocks) break;
+                if (k % 2 == 0) {
 #pragma unroll
-                for (int qi = 0; qi < kQuads; qi++) {
-                    const int q = kpart + qi * f.kw;
-                    if (4 * q >= blocks) break;
-                    const int64_t i0 = b0 + 4 * q;
-                    const u32x2 d0 = *reinterpret_cast<const u32x2 *>(w.scales + (t64 * nb8 + i0 / 8) * 512 + in64 * 8 + i0 % 8);
-#pragma unroll
-                    for (int b = 0; b < 4; b += 2) {
-                        if (4 * q + b >= blocks) break;
-                        int64_t i = i0 + b + (g >> 1);
-                        i = i < nb ? i : nb - 1;
-                        const u32x2 word = w.bits[((t64 * nb + i) * 2 + (g & 1)) * 64 + in64];
-                        // Words 0 and 1 of both halves of both blocks to the lanes of their sub-blocks.
-                        const auto x = __builtin_amdgcn_permlane32_swap(word[0], word[1], false, false);
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            if (4 * q + b + k >= blocks) break;
-                            const auto h = __builtin_amdgcn_permlane16_swap(x[k], x[k], false, false);
-                            const int at = ((4 * q + b + k) * 4 + g) * C;
-                            const u32x2 *dig = reinterpret_cast<const u32x2 *>(digits + (at * 4 + row_a) * 12);
-                            const u32x2 f0 = dig[0], f1 = dig[1], f2 = dig[2];
-                            const int power = static_cast<int>(powers[at + row_a / 4] >> (8 * (row_a & 3)));
-                            const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                frag(u32x4{f0[0], f0[1], f1[0], f1[1]}, f2), signs(h[0], h[1]), f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp6,
-                                kFp4, 0, power, 0, kOne);
-                            const float d = f16_value(static_cast<uint16_t>(d0[(b + k) / 2] >> (16 * ((b + k) & 1))));
-                            sum = fmaf(d, (t[0] + t[1]) + (t[2] + t[3]), sum);
-                        }
+                    for (int i = 0; i < N; i++) {
+                        const auto two = __builtin_amdgcn_permlane32_swap(word[q][i][k / 2][0], word[q][i][k / 2][1], false, false);
+                        x[0][i] = two[0];
+                        x[1][i] = two[1];
                     }
                 }
-                acc[it * S + s] = sum;
+                const int at = ((i0 + k) * 4 + g) * C;
+                const u32x2 *dig = reinterpret_cast<const u32x2 *>(digits + (at * 4 + row_a) * 12);
+                const u32x2 f0 = dig[0], f1 = dig[1], f2 = dig[2];
+                const i32x8 a = frag(u32x4{f0[0], f0[1], f1[0], f1[1]}, f2);
+                const int power = static_cast<int>(powers[at + row_a / 4] >> (8 * (row_a & 3)));
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    const auto h = __builtin_amdgcn_permlane16_swap(x[k % 2][i], x[k % 2][i], false, false);
+                    const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, signs(h[0], h[1]), f32x4{0.0f, 0.0f, 0.0f, 0.0f},
+                                                                                     kFp6, kFp4, 0, power, 0, kOne);
+                    const float d = f16_value(static_cast<uint16_t>(d0[q][i][k / 2] >> (16 * (k & 1))));
+                    acc[i] = fmaf(d, (t[0] + t[1]) + (t[2] + t[3]), acc[i]);
+                }
             }
         }
     }
-    const int tw = f.tiles * groups;   // the workgroup's tiles
+    const int tw = TILES * groups;   // the workgroup's tiles
 #pragma unroll
-    for (int it = 0; it < 4; it++)
-#pragma unroll
-        for (int s = 0; s < S; s++)
-            if (it < f.tiles) red[((kpart * tw + it * groups + ipart) * S + s) * 64 + lane] = acc[it * S + s];
+    for (int i = 0; i < N; i++) red[((kpart * tw + i % TILES * groups + ipart) * S + i / TILES) * 64 + lane] = acc[i];
     __syncthreads();
     for (int i = tid; i < n * 4 * tw; i += kFew) {   // eight lanes together hold 32 rows where blocks are written (tw even)
         const int c = i / (4 * tw), quad = i % (4 * tw);
@@ -334,7 +355,7 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
 #pragma unroll
             for (int s = 0; s < S; s++)
                 v[s] += *reinterpret_cast<const f32x4 *>(red + ((k * tw + quad / 4) * S + s) * 64 + c * 16 + quad % 4 * 4);
-        finish<T, S>(w0, w1, e, v[0], v[1], c, tile0 * 16 + 4 * quad);
+        finish<S>(w0, w1, e, v[0], v[1], c, tile0 * 16 + 4 * quad);
     }
 }
 
@@ -452,7 +473,7 @@ __device__ __forceinline__ void lds_load4(const void *base, uint32_t at, uint32_
 // kBuffers blocks before it is used. A wave has the digits of a step in registers, reads the
 // next step's, and goes through its tiles, four instructions on the same sums each. Two
 // workgroups on a CU, so that one wave of a SIMD works while the other one waits for its own.
-template <typename T, int TN, int S>
+template <int TN, int S>
 __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
                                                          ManyShape f) {
     constexpr int NT = TN * S, kWaves = 4, kBuffers = 3;
@@ -629,7 +650,7 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
         for (int q = 0; q < 4; q++)
-            finish<T, S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * kPitch),
+            finish<S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * kPitch),
                          *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + from + q * 8 * kPitch),
                          col * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
         __builtin_amdgcn_wave_barrier();
@@ -638,7 +659,7 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
 
 // Batches: KS waves share the sums of TM tiles of 32 columns and NT = TN S tiles of 32 weight
 // rows by K, each loading its digits to registers a block ahead.
-template <typename T, int TM, int TN, int S, int KS>
+template <int TM, int TN, int S, int KS>
 __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
                                                               ManyShape f) {
     constexpr int NT = TN * S;
@@ -747,7 +768,7 @@ __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight 
 #pragma unroll
             for (int s = 0; s < S; s++)
                 v[s] += *reinterpret_cast<const f32x4 *>(sums + (k * TM * NT + m * NT + s * TN + i) * kTile + from + q * 8 * kPitch);
-        finish<T, S>(w0, w1, e, v[0], v[1], (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
+        finish<S>(w0, w1, e, v[0], v[1], (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
     }
 }
 
@@ -801,25 +822,42 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
     return GD_OK;
 }
 
-template <typename T, int S>
+template <int C, int S>
 void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, hipStream_t hs) {
-    FewShape f = {K / 128, 1, 1};
-    while (f.kw < 8 && 8 * f.kw <= f.nb) f.kw *= 2;   // four blocks a wave at least
-    const int64_t tiles = (e.rows + 15) / 16, groups = 8 / f.kw;
-    while (f.tiles < 4 && ((e.y_q8 && f.tiles * groups < 2) || tiles / (2 * f.tiles * groups) >= 256)) f.tiles *= 2;
-    const dim3 grid(static_cast<uint32_t>((tiles + f.tiles * groups - 1) / (f.tiles * groups)));
-    const auto go = [&](auto c) {
-        hipLaunchKernelGGL((q1_few_kernel<T, decltype(c)::value, S>), grid, dim3(kFew), 0, hs, w0, w1, a_q8, e, f);
+    FewShape f = {K / 128, 1};
+    const int64_t chunk = f.nb < kBlocks<C> ? f.nb : kBlocks<C>, quads = (chunk + 3) / 4, tiles = (e.rows + 15) / 16;
+    while (f.kw < 8 && f.kw < quads) f.kw *= 2;
+    const auto go = [&](auto tiles_, auto q) {
+        constexpr int TILES = decltype(tiles_)::value, Q = decltype(q)::value;
+        const int64_t per = TILES * (8 / f.kw);
+        hipLaunchKernelGGL((q1_few_kernel<C, S, TILES, Q>), dim3(static_cast<uint32_t>((tiles + per - 1) / per)), dim3(kFew), 0, hs, w0, w1,
+                           a_q8, e, f);
     };
-    if (e.n == 1)
-        go(std::integral_constant<int, 1>{});
-    else if (e.n == 2)
-        go(std::integral_constant<int, 2>{});
-    else
-        go(std::integral_constant<int, 4>{});
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Four = std::integral_constant<int, 4>;
+    const int64_t full = tiles * f.kw / 8;   // workgroups with a tile a wave
+    if (quads <= f.kw) {
+        if (full >= 4 * 224)
+            go(Four{}, One{});
+        else if (full >= 2 * 224 || (e.y_q8 && f.kw == 8))
+            go(Two{}, One{});
+        else
+            go(One{}, One{});
+    } else if constexpr (C <= 2) {
+        if (C == 1 && quads > 2 * f.kw && !e.y_q8) {
+            if constexpr (C == 1) go(One{}, Four{});
+        } else if (quads > 2 * f.kw) {
+            if constexpr (C == 1) go(Two{}, Four{});
+        } else if (full >= 2 * 224 || e.y_q8) {
+            go(Two{}, Two{});
+        } else {
+            go(One{}, Two{});
+        }
+    }
 }
 
-template <typename T, int S>
+template <int S>
 void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, uint8_t *workspace,
               hipStream_t hs) {
     ManyShape f = {K / 128, (e.n + 31) / 32, (e.rows + 31) / 32, 0, 0};
@@ -834,24 +872,24 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
     constexpr int TN = 4 / S;
     const int64_t wide = groups(1, 4 * TN);
     if (wide >= 256) {
-        hipLaunchKernelGGL((q1_wide_kernel<T, TN, S>), grid(wide), dim3(256), 0, hs, w0, w1, workspace, e, f);
+        hipLaunchKernelGGL((q1_wide_kernel<TN, S>), grid(wide), dim3(256), 0, hs, w0, w1, workspace, e, f);
     } else {
         const int64_t split = groups(1, 1);
-        hipLaunchKernelGGL((q1_split_kernel<T, 1, 1, S, 8>), grid(split), dim3(512), 0, hs, w0, w1, workspace, e, f);
+        hipLaunchKernelGGL((q1_split_kernel<1, 1, S, 8>), grid(split), dim3(512), 0, hs, w0, w1, workspace, e, f);
     }
 }
 
 template <int S>
-void run(const Weight &w0, const Weight &w1, const void *a_q8, const Epilogue &e, int64_t K, int32_t dtype, void *workspace,
-         hipStream_t hs) {
-    dispatch_dtype(dtype, [&](auto t) {
-        using T = decltype(t);
-        const uint16_t *a = static_cast<const uint16_t *>(a_q8);
-        if (e.n <= kFewColumns)
-            run_few<T, S>(w0, w1, a, e, K, hs);
-        else
-            run_many<T, S>(w0, w1, a, e, K, static_cast<uint8_t *>(workspace), hs);
-    });
+void run(const Weight &w0, const Weight &w1, const void *a_q8, const Epilogue &e, int64_t K, void *workspace, hipStream_t hs) {
+    const uint16_t *a = static_cast<const uint16_t *>(a_q8);
+    if (e.n == 1)
+        run_few<1, S>(w0, w1, a, e, K, hs);
+    else if (e.n == 2)
+        run_few<2, S>(w0, w1, a, e, K, hs);
+    else if (e.n <= kFewColumns)
+        run_few<4, S>(w0, w1, a, e, K, hs);
+    else
+        run_many<S>(w0, w1, a, e, K, static_cast<uint8_t *>(workspace), hs);
 }
 
 }  // namespace
@@ -869,10 +907,10 @@ extern "C" int q1_q8_linear(const void *bits_plane, const void *scale_plane, con
                             int32_t act, const void *residual, void *y, void *y_q8, int64_t rows, int64_t K,
                             int64_t n_act, int32_t dtype, void *workspace, size_t workspace_bytes, void *stream) {
     const Weight w = {static_cast<const u32x2 *>(bits_plane), static_cast<const uint16_t *>(scale_plane), bias};
-    const Epilogue e = {residual, y, static_cast<uint16_t *>(y_q8), rows, n_act, act};
+    const Epilogue e = {residual, y, static_cast<uint16_t *>(y_q8), rows, n_act, act, dtype};
     const int st = check("q1_q8_linear", &w, 1, a_q8, e, K, dtype, workspace, workspace_bytes);
     if (st) return st;
-    run<1>(w, w, a_q8, e, K, dtype, workspace, as_stream(stream));
+    run<1>(w, w, a_q8, e, K, workspace, as_stream(stream));
     return check_launch("q1_q8_linear");
 }
 
@@ -882,9 +920,9 @@ extern "C" int q1_q8_gated(const void *gate_bits, const void *gate_scales, const
                            size_t workspace_bytes, void *stream) {
     const Weight w[2] = {{static_cast<const u32x2 *>(gate_bits), static_cast<const uint16_t *>(gate_scales), gate_bias},
                          {static_cast<const u32x2 *>(up_bits), static_cast<const uint16_t *>(up_scales), up_bias}};
-    const Epilogue e = {nullptr, y, static_cast<uint16_t *>(y_q8), rows, n_act, act};
+    const Epilogue e = {nullptr, y, static_cast<uint16_t *>(y_q8), rows, n_act, act, dtype};
     const int st = check("q1_q8_gated", w, 2, a_q8, e, K, dtype, workspace, workspace_bytes);
     if (st) return st;
-    run<2>(w[0], w[1], a_q8, e, K, dtype, workspace, as_stream(stream));
+    run<2>(w[0], w[1], a_q8, e, K, workspace, as_stream(stream));
     return check_launch("q1_q8_gated");
 }
