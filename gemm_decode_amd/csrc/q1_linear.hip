@@ -233,9 +233,12 @@ __device__ __forceinline__ i32x8 frag(u32x4 lo, u32x2 hi) {
 }
 
 // ------------------------------------------------- up to four columns
-// The rows of a 16 x 16 x 128 instruction are the digits of the columns (row 4 c + p: digit p
-// of column c), its columns 16 weight rows, so that a lane's four results are the digits'
-// sums of one row and column, and one instruction takes a weight block of 16 rows.
+// For few columns the digits are those of the codes alone, q = 16 h + l with l in [0, 16) and h
+// in [-8, 8), which takes a quarter of the work, and d1 is multiplied to the sums. A 16 x 16 x
+// 128 instruction takes a block of 16 weight rows; its other 16 rows are, for each of the four
+// sub-blocks, l and h of two columns, zero outside that sub-block. So a lane's four results
+// are the whole sums of one sub-block, one weight row and two columns, and acc += (d0 d1)
+// (l + h) rounds once (d0 d1 has 22 bits).
 //
 // A workgroup of eight waves holds the digits of kBlocks blocks in LDS and takes 16-row tiles
 // of the weights, kw waves sharing a tile by its K in quads of blocks. A wave's loads of its
@@ -243,26 +246,50 @@ __device__ __forceinline__ i32x8 frag(u32x4 lo, u32x2 hi) {
 // as a few memory latencies, and this hides the digits behind one.
 constexpr int kFew = 512;
 template <int C>
-constexpr int kBlocks = 128 / C;
+constexpr int kBlocks = C == 4 ? 64 : 128;
 
 struct FewShape {
     int64_t nb;   // blocks of a row
     int kw;       // waves along K: 1, 2, 4 or 8
 };
 
+// Half of a sub-block, its places 16 part .. 16 part + 15, as the three words each of l and h.
+__device__ __forceinline__ void code_digits(const uint32_t d[8], int part, uint32_t l[3], uint32_t h[3]) {
+    const uint32_t sel = part ? 0x07030602u : 0x05010400u;
+    uint32_t rl[4], rh[4];
+#pragma unroll
+    for (int a = 0; a < 2; a++) {
+        const uint32_t x = __builtin_amdgcn_perm(d[4 + 2 * a], d[2 * a], sel), y = __builtin_amdgcn_perm(d[5 + 2 * a], d[2 * a + 1], sel);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const uint32_t w = __builtin_amdgcn_perm(y, x, j ? 0x07060302u : 0x05040100u);   // four codes
+            const uint32_t n = w >> 4 & 0x0f0f0f0fu, minus = n & 0x08080808u, one = minus >> 3;
+            rl[2 * j + a] = pack6(w & 0x0f0f0f0fu);
+            rh[2 * j + a] = pack6(((n ^ ((minus << 1) - one)) + one) | minus << 2);   // magnitude and sign
+        }
+    }
+    const auto words = [](const uint32_t r[4], uint32_t w[3]) {
+        w[0] = r[0] | r[1] << 24;
+        w[1] = r[1] >> 8 | r[2] << 16;
+        w[2] = r[2] >> 16 | r[3] << 8;
+    };
+    words(rl, l);
+    words(rh, h);
+}
+
 template <int C, int S, int TILES, int Q>
 __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, const uint16_t *__restrict__ a_q8, Epilogue e,
                                                          FewShape f) {
     constexpr int N = TILES * S;   // a wave's tiles of both weights
-    __shared__ __attribute__((aligned(16))) uint16_t digits[kBlocks<C> * 4 * 4 * C * 12];
-    __shared__ uint32_t powers[kBlocks<C> * 4 * C];
+    constexpr int kRow = 6;        // words of a row of digits
+    __shared__ __attribute__((aligned(16))) uint32_t digits[kBlocks<C> * 4 * C * 2 * kRow + 8];   // and a row of zeros
+    __shared__ __attribute__((aligned(16))) float d1[kBlocks<C> * 4 * C];
     __shared__ __attribute__((aligned(16))) float red[8 * N * 64];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int g = lane / 16, n16 = lane % 16, n = static_cast<int>(e.n);
     const int kpart = wave % f.kw, ipart = wave / f.kw, groups = 8 / f.kw;
     const int nb = static_cast<int>(f.nb), nb8 = (nb + 7) / 8;
     const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * TILES * groups, last = (e.rows + 15) / 16 - 1;
-    const int row_a = n16 / 4 < n ? n16 : n16 % 4;   // rows of no column repeat another's
     const Signs signs(g & 1);
     const u32x2 *bits[N];
     const uint16_t *scales[N];
@@ -275,11 +302,36 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
         bits[i] = w.bits + tile / 4 * nb * 128 + (g & 1) * 64 + in64;
         scales[i] = w.scales + tile / 4 * nb8 * 512 + in64 * 8;
     }
-    float acc[N];
+    // The lane's row of an instruction: of columns 2 m and 2 m + 1, digit n16 % 2 of column
+    // 2 m + n16 / 2 % 2, where n16 / 4 is its sub-block.
+    const int power = n16 % 2 ? 134 : 130;   // 2^7 and 2^3: e2m3 codes are eighths
+    int row[(C + 1) / 2], stride[(C + 1) / 2];
 #pragma unroll
-    for (int i = 0; i < N; i++) acc[i] = 0.0f;
+    for (int m = 0; m < (C + 1) / 2; m++) {
+        const int c = 2 * m + n16 / 2 % 2;
+        const bool mine = n16 / 4 == g && c < n;
+        row[m] = mine ? ((g * C + c) * 2 + n16 % 2) * kRow : kBlocks<C> * 4 * C * 2 * kRow;
+        stride[m] = mine ? 4 * C * 2 * kRow : 0;
+    }
+    if (tid < 8) digits[kBlocks<C> * 4 * C * 2 * kRow + tid] = 0;
+    float acc[N][C];
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int c = 0; c < C; c++) acc[i][c] = 0.0f;
     for (int b0 = 0; b0 < nb; b0 += kBlocks<C>) {
         const int blocks = nb - b0 < kBlocks<C> ? nb - b0 : kBlocks<C>;
+        // Half sub-blocks, one to a thread at a time; the first two loads go out before the weights'.
+        const int subs = blocks * 4, halves = subs * 2 * n;
+        uint32_t d[2][8], scale[2];
+        const auto fetch = [&](int i, int slot) {
+            if (i < halves) {
+                const int c = i / 2 / subs, sub = i / 2 - c * subs;
+                scale[slot] = load_block(a_q8 + ((static_cast<int64_t>(c) * nb + b0) * 4 + sub) * 17, d[slot]);
+            }
+        };
+        fetch(tid, 0);
+        fetch(tid + kFew, 1);
         u32x2 word[Q][N][2], d0[Q][N];
 #pragma unroll
         for (int q = 0; q < Q; q++) {
@@ -296,21 +348,25 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
             }
         }
         if (b0) __syncthreads();
-        // Digits: a thread takes eight elements of a sub-block at a time.
-        const int subs = blocks * 4;
-        for (int i = tid; i < subs * 4 * n; i += kFew) {
-            const int j = i % 4, c = i / 4 / subs, sub = i / 4 - c * subs;
-            uint32_t d[8], r[2][4];
-            const Scale s(load_block(a_q8 + ((static_cast<int64_t>(c) * nb + b0) * 4 + sub) * 17, d));
-            digits8(d, j, s.m, r);
+        for (int i = tid; i < halves; i += 2 * kFew) {
 #pragma unroll
-            for (int p = 0; p < 4; p++) {
-                uint16_t *o = digits + ((sub * C + c) * 4 + p) * 12 + 3 * j;
-                o[0] = static_cast<uint16_t>(r[0][p]);
-                o[1] = static_cast<uint16_t>(r[0][p] >> 16 | r[1][p] << 8);
-                o[2] = static_cast<uint16_t>(r[1][p] >> 8);
+            for (int slot = 0; slot < 2; slot++) {
+                const int at = i + slot * kFew;
+                if (at < halves) {
+                    const int c = at / 2 / subs, sub = at / 2 - c * subs;
+                    uint32_t l[3], h[3];
+                    code_digits(d[slot], at & 1, l, h);
+                    uint32_t *o = digits + (sub * C + c) * 2 * kRow + (at & 1) * 3;
+#pragma unroll
+                    for (int k = 0; k < 3; k++) {
+                        o[k] = l[k];
+                        o[kRow + k] = h[k];
+                    }
+                    const float v = f16_value(static_cast<uint16_t>(scale[slot]));
+                    if ((at & 1) == 0) d1[sub * C + c] = fabsf(v) <= 65504.0f ? v : __builtin_nanf("");
+                }
+                fetch(at + 2 * kFew, slot);
             }
-            if (j == 0) powers[sub * C + c] = s.powers;
         }
         __syncthreads();
 #pragma unroll
@@ -328,25 +384,43 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
                         x[1][i] = two[1];
                     }
                 }
-                const int at = ((i0 + k) * 4 + g) * C;
-                const u32x2 *dig = reinterpret_cast<const u32x2 *>(digits + (at * 4 + row_a) * 12);
-                const u32x2 f0 = dig[0], f1 = dig[1], f2 = dig[2];
-                const i32x8 a = frag(u32x4{f0[0], f0[1], f1[0], f1[1]}, f2);
-                const int power = static_cast<int>(powers[at + row_a / 4] >> (8 * (row_a & 3)));
+                i32x8 a[(C + 1) / 2];
+                float s1[C];
+#pragma unroll
+                for (int m = 0; m < (C + 1) / 2; m++) {
+                    const u32x2 *dig = reinterpret_cast<const u32x2 *>(digits + row[m] + (i0 + k) * stride[m]);
+                    const u32x2 f0 = dig[0], f1 = dig[1], f2 = dig[2];
+                    a[m] = frag(u32x4{f0[0], f0[1], f1[0], f1[1]}, f2);
+                }
+#pragma unroll
+                for (int c = 0; c < C; c++) s1[c] = d1[((i0 + k) * 4 + g) * C + c];
 #pragma unroll
                 for (int i = 0; i < N; i++) {
                     const auto h = __builtin_amdgcn_permlane16_swap(x[k % 2][i], x[k % 2][i], false, false);
-                    const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, signs(h[0], h[1]), f32x4{0.0f, 0.0f, 0.0f, 0.0f},
-                                                                                     kFp6, kFp4, 0, power, 0, kOne);
+                    const i32x8 w = signs(h[0], h[1]);
                     const float d = f16_value(static_cast<uint16_t>(d0[q][i][k / 2] >> (16 * (k & 1))));
-                    acc[i] = fmaf(d, (t[0] + t[1]) + (t[2] + t[3]), acc[i]);
+#pragma unroll
+                    for (int m = 0; m < (C + 1) / 2; m++) {
+                        const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[m], w, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp6, kFp4, 0,
+                                                                                         power, 0, kOne);
+                        acc[i][2 * m] = fmaf(d * s1[2 * m], t[0] + t[1], acc[i][2 * m]);
+                        if (2 * m + 1 < C) acc[i][(2 * m + 1) % C] = fmaf(d * s1[(2 * m + 1) % C], t[2] + t[3], acc[i][(2 * m + 1) % C]);
+                    }
                 }
             }
         }
     }
     const int tw = TILES * groups;   // the workgroup's tiles
 #pragma unroll
-    for (int i = 0; i < N; i++) red[((kpart * tw + i % TILES * groups + ipart) * S + i / TILES) * 64 + lane] = acc[i];
+    for (int i = 0; i < N; i++) {
+#pragma unroll
+        for (int c = 0; c < C; c++) {   // the four sub-blocks' sums
+            float v = acc[i][c];
+            v += __shfl_xor(v, 16);
+            v += __shfl_xor(v, 32);
+            if (g == c) red[((kpart * tw + i % TILES * groups + ipart) * S + i / TILES) * 64 + lane] = v;
+        }
+    }
     __syncthreads();
     for (int i = tid; i < n * 4 * tw; i += kFew) {   // eight lanes together hold 32 rows where blocks are written (tw even)
         const int c = i / (4 * tw), quad = i % (4 * tw);
@@ -844,16 +918,16 @@ void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epi
             go(Two{}, One{});
         else
             go(One{}, One{});
-    } else if constexpr (C <= 2) {
-        if (C == 1 && quads > 2 * f.kw && !e.y_q8) {
-            if constexpr (C == 1) go(One{}, Four{});
-        } else if (quads > 2 * f.kw) {
-            if constexpr (C == 1) go(Two{}, Four{});
-        } else if (full >= 2 * 224 || e.y_q8) {
+    } else if (quads <= 2 * f.kw) {
+        if (full >= 2 * 224 || e.y_q8)
             go(Two{}, Two{});
-        } else {
+        else
             go(One{}, Two{});
-        }
+    } else if constexpr (C <= 2) {
+        if (e.y_q8)
+            go(Two{}, Four{});
+        else
+            go(One{}, Four{});
     }
 }
 
