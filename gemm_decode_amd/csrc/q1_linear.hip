@@ -137,6 +137,54 @@ __device__ __forceinline__ void finish(const Weight &w0, const Weight &w1, const
     }
 }
 
+// One value: the outer operands of row r and column c, asked for before the sums are there,
+struct Outer {
+    float bias[2], residual;
+};
+template <int S>
+__device__ __forceinline__ Outer load_outer(const Weight &w0, const Weight &w1, const Epilogue &e, int64_t c, int64_t r, bool live) {
+    Outer o = {{0.0f, 0.0f}, 0.0f};
+    if (live) {
+        if (w0.bias) o.bias[0] = w0.bias[r];
+        if (S == 2 && w1.bias) o.bias[1] = w1.bias[r];
+        if (e.residual) {
+            const int64_t at = c * e.rows + r;
+            o.residual = e.dtype == GD_F32 ? static_cast<const float *>(e.residual)[at]
+                                           : e.dtype == GD_F16 ? static_cast<float>(static_cast<const _Float16 *>(e.residual)[at])
+                                                               : static_cast<float>(static_cast<const __bf16 *>(e.residual)[at]);
+        }
+    }
+    return o;
+}
+// and what becomes of it. Where q8_0 blocks are written, 32 lanes hold the rows of one
+// (r % 32 = lane % 32) and all of them call this.
+template <int S>
+__device__ __forceinline__ void finish_one(const Epilogue &e, const Outer &o, float v, float u, int64_t c, int64_t r, bool live) {
+    v = activate(v + o.bias[0], e.act);
+    if (S == 2) v *= u + o.bias[1];
+    v += o.residual;
+    const int64_t at = c * e.rows + r;
+    if (e.y && live) {
+        if (e.dtype == GD_F32)
+            static_cast<float *>(e.y)[at] = v;
+        else if (e.dtype == GD_F16)
+            static_cast<_Float16 *>(e.y)[at] = static_cast<_Float16>(v);
+        else
+            static_cast<__bf16 *>(e.y)[at] = static_cast<__bf16>(v);
+    }
+    if (e.y_q8) {
+        float a = max8(fabsf(v));
+        a = fmaxf(a, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, a), 0x140, 0xF, 0xF, false)));
+        a = fmaxf(a, __shfl_xor(a, 16));
+        const uint32_t q = codes_of(f32x4{v, 0.0f, 0.0f, 0.0f}, a);
+        if (live) {
+            uint16_t *b = e.y_q8 + at / 32 * 17;   // 34 bytes = 17 halves
+            reinterpret_cast<uint8_t *>(b + 1)[r % 32] = static_cast<uint8_t>(q);
+            if (r % 32 == 0) b[0] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(a > 0.0f ? scale_of(a) : 0.0f));
+        }
+    }
+}
+
 // ------------------------------------------------------------- operands
 // The matrix instructions take 6-bit floats (e2m3) for the activations and 4-bit ones
 // (e2m1) for the weights, 32 of a lane with a power of two for all of them. A weight is its
@@ -250,7 +298,7 @@ constexpr int kBlocks = C == 4 ? 64 : 128;
 
 struct FewShape {
     int64_t nb;   // blocks of a row
-    int kw;       // waves along K: 1, 2, 4 or 8
+    int kw, kw_log;   // waves along K: 1, 2, 4 or 8
 };
 
 // Half of a sub-block, its places 16 part .. 16 part + 15, as the three words each of l and h.
@@ -277,98 +325,113 @@ __device__ __forceinline__ void code_digits(const uint32_t d[8], int part, uint3
     words(rh, h);
 }
 
+// Sum over the four 16-lane rows of a wave, in all of them.
+__device__ __forceinline__ float sum_rows(float v) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto p = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, static_cast<uint32_t>(p[0])) +
+                                                        __builtin_bit_cast(float, static_cast<uint32_t>(p[1])));
+    const auto q = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    return __builtin_bit_cast(float, static_cast<uint32_t>(q[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(q[1]));
+}
+
 template <int C, int S, int TILES, int Q>
 __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, const uint16_t *__restrict__ a_q8, Epilogue e,
                                                          FewShape f) {
     constexpr int N = TILES * S;   // a wave's tiles of both weights
     constexpr int kRow = 6;        // words of a row of digits
+    constexpr int kHalves = kBlocks<C> * 8 / kFew;   // half sub-blocks of a chunk's column and thread
     __shared__ __attribute__((aligned(16))) uint32_t digits[kBlocks<C> * 4 * C * 2 * kRow + 8];   // and a row of zeros
     __shared__ __attribute__((aligned(16))) float d1[kBlocks<C> * 4 * C];
     __shared__ __attribute__((aligned(16))) float red[8 * N * 64];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
-    const int g = lane / 16, n16 = lane % 16, n = static_cast<int>(e.n);
-    const int kpart = wave % f.kw, ipart = wave / f.kw, groups = 8 / f.kw;
-    const int nb = static_cast<int>(f.nb), nb8 = (nb + 7) / 8;
-    const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * TILES * groups, last = (e.rows + 15) / 16 - 1;
-    const Signs signs(g & 1);
-    const u32x2 *bits[N];
-    const uint16_t *scales[N];
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        const Weight &w = i / TILES ? w1 : w0;
-        int64_t tile = tile0 + i % TILES * groups + ipart;
-        tile = tile <= last ? tile : last;
-        const int in64 = static_cast<int>(tile % 4) * 16 + n16;
-        bits[i] = w.bits + tile / 4 * nb * 128 + (g & 1) * 64 + in64;
-        scales[i] = w.scales + tile / 4 * nb8 * 512 + in64 * 8;
-    }
-    // The lane's row of an instruction: of columns 2 m and 2 m + 1, digit n16 % 2 of column
-    // 2 m + n16 / 2 % 2, where n16 / 4 is its sub-block.
-    const int power = n16 % 2 ? 134 : 130;   // 2^7 and 2^3: e2m3 codes are eighths
-    int row[(C + 1) / 2], stride[(C + 1) / 2];
-#pragma unroll
-    for (int m = 0; m < (C + 1) / 2; m++) {
-        const int c = 2 * m + n16 / 2 % 2;
-        const bool mine = n16 / 4 == g && c < n;
-        row[m] = mine ? ((g * C + c) * 2 + n16 % 2) * kRow : kBlocks<C> * 4 * C * 2 * kRow;
-        stride[m] = mine ? 4 * C * 2 * kRow : 0;
-    }
-    if (tid < 8) digits[kBlocks<C> * 4 * C * 2 * kRow + tid] = 0;
+    const int g = lane / 16, n16 = lane % 16, n = static_cast<int>(e.n), nb = static_cast<int>(f.nb), nb8 = (nb + 7) / 8;
+    const int kpart = wave & (f.kw - 1), ipart = wave >> f.kw_log, groups_log = 3 - f.kw_log;
+    const int tw = TILES << groups_log;   // the workgroup's tiles
+    const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * tw;
     float acc[N][C];
 #pragma unroll
     for (int i = 0; i < N; i++)
 #pragma unroll
         for (int c = 0; c < C; c++) acc[i][c] = 0.0f;
+    Outer outer;
     for (int b0 = 0; b0 < nb; b0 += kBlocks<C>) {
         const int blocks = nb - b0 < kBlocks<C> ? nb - b0 : kBlocks<C>;
-        // Half sub-blocks, one to a thread at a time; the first two loads go out before the weights'.
-        const int subs = blocks * 4, halves = subs * 2 * n;
-        uint32_t d[2][8], scale[2];
-        const auto fetch = [&](int i, int slot) {
-            if (i < halves) {
-                const int c = i / 2 / subs, sub = i / 2 - c * subs;
-                scale[slot] = load_block(a_q8 + ((static_cast<int64_t>(c) * nb + b0) * 4 + sub) * 17, d[slot]);
+        // The codes first (without a branch around the loads: behind one, the compiler waits for
+        // all that is on its way),
+        uint32_t d[C][kHalves][8], scale[C][kHalves];
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            const uint16_t *column = a_q8 + (static_cast<int64_t>(c < n ? c : 0) * nb + b0) * 68;
+#pragma unroll
+            for (int k = 0; k < kHalves; k++) {
+                const int i = tid + k * kFew < blocks * 8 ? tid + k * kFew : blocks * 8 - 1;
+                scale[c][k] = load_block(column + i / 2 * 17, d[c][k]);
             }
-        };
-        fetch(tid, 0);
-        fetch(tid + kFew, 1);
+        }
+        if (b0 == 0) {   // then what the thread's sum meets,
+            const int i = tid < n * 16 * tw ? tid : 0, c = i / (16 * tw);
+            const int64_t r = tile0 * 16 + (i - c * 16 * tw);
+            outer = load_outer<S>(w0, w1, e, c, r, r < e.rows);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // then the weights.
         u32x2 word[Q][N][2], d0[Q][N];
+        const int last = static_cast<int>((e.rows + 15) / 16 - 1);
 #pragma unroll
-        for (int q = 0; q < Q; q++) {
-            int i0 = 4 * (kpart + q * f.kw);
-            i0 = b0 + (i0 < blocks ? i0 : 0);   // past the end: loaded, not used
+        for (int i = 0; i < N; i++) {
+            const Weight &w = i / TILES ? w1 : w0;
+            int tile = static_cast<int>(tile0) + ((i % TILES) << groups_log) + ipart;
+            tile = tile <= last ? tile : last;
+            const uint8_t *bits = reinterpret_cast<const uint8_t *>(w.bits) + (static_cast<int64_t>(tile / 4) * nb * 1024 + tile % 4 * 128);
+            const uint8_t *scales = reinterpret_cast<const uint8_t *>(w.scales) + (static_cast<int64_t>(tile / 4) * nb8 * 1024 + tile % 4 * 256);
 #pragma unroll
-            for (int i = 0; i < N; i++) {
+            for (int q = 0; q < Q; q++) {
+                int i0 = 4 * (kpart + q * f.kw);
+                i0 = b0 + (i0 < blocks ? i0 : 0);   // past the end: loaded, not used
 #pragma unroll
                 for (int k = 0; k < 2; k++) {   // block i0 + 2 k + g / 2, half g % 2
                     const int b = i0 + 2 * k + (g >> 1);
-                    word[q][i][k] = __builtin_nontemporal_load(bits[i] + static_cast<int64_t>(b < nb ? b : nb - 1) * 128);
+                    const uint32_t at = static_cast<uint32_t>(b < nb ? b : nb - 1) * 1024u + static_cast<uint32_t>((g & 1) * 512 + n16 * 8);
+                    word[q][i][k] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(bits + at));
                 }
-                d0[q][i] = *reinterpret_cast<const u32x2 *>(scales[i] + i0 / 8 * 512 + i0 % 8);
+                d0[q][i] = *reinterpret_cast<const u32x2 *>(scales + (i0 / 8 * 1024 + i0 % 8 * 2) + static_cast<uint32_t>(n16 * 16));
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         if (b0) __syncthreads();
-        for (int i = tid; i < halves; i += 2 * kFew) {
+        if (tid < 8) digits[kBlocks<C> * 4 * C * 2 * kRow + tid] = 0;
 #pragma unroll
-            for (int slot = 0; slot < 2; slot++) {
-                const int at = i + slot * kFew;
-                if (at < halves) {
-                    const int c = at / 2 / subs, sub = at / 2 - c * subs;
-                    uint32_t l[3], h[3];
-                    code_digits(d[slot], at & 1, l, h);
-                    uint32_t *o = digits + (sub * C + c) * 2 * kRow + (at & 1) * 3;
+        for (int c = 0; c < C; c++)
 #pragma unroll
-                    for (int k = 0; k < 3; k++) {
-                        o[k] = l[k];
-                        o[kRow + k] = h[k];
+            for (int k = 0; k < kHalves; k++) {
+                const int i = tid + k * kFew;
+                uint32_t l[3], h[3];
+                code_digits(d[c][k], i & 1, l, h);
+                const float v = f16_value(static_cast<uint16_t>(scale[c][k]));
+                if (i < blocks * 8 && c < n) {
+                    uint32_t *o = digits + (i / 2 * C + c) * 2 * kRow + (i & 1) * 3;
+#pragma unroll
+                    for (int j = 0; j < 3; j++) {
+                        o[j] = l[j];
+                        o[kRow + j] = h[j];
                     }
-                    const float v = f16_value(static_cast<uint16_t>(scale[slot]));
-                    if ((at & 1) == 0) d1[sub * C + c] = fabsf(v) <= 65504.0f ? v : __builtin_nanf("");
+                    if ((i & 1) == 0) d1[i / 2 * C + c] = fabsf(v) <= 65504.0f ? v : __builtin_nanf("");
                 }
-                fetch(at + 2 * kFew, slot);
             }
-        }
         __syncthreads();
+        // The lane's row of an instruction: of columns 2 m and 2 m + 1, digit n16 % 2 of column
+        // 2 m + n16 / 2 % 2, where n16 / 4 is its sub-block.
+        const Signs signs(g & 1);
+        const int power = n16 % 2 ? 134 : 130;   // 2^7 and 2^3: e2m3 codes are eighths
+        int row[(C + 1) / 2], stride[(C + 1) / 2];
+#pragma unroll
+        for (int m = 0; m < (C + 1) / 2; m++) {
+            const int c = 2 * m + n16 / 2 % 2;
+            const bool mine = n16 / 4 == g && c < n;
+            row[m] = mine ? ((g * C + c) * 2 + n16 % 2) * kRow : kBlocks<C> * 4 * C * 2 * kRow;
+            stride[m] = mine ? 4 * C * 2 * kRow : 0;
+        }
 #pragma unroll
         for (int q = 0; q < Q; q++) {
             const int i0 = 4 * (kpart + q * f.kw);
@@ -410,26 +473,29 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
             }
         }
     }
-    const int tw = TILES * groups;   // the workgroup's tiles
 #pragma unroll
     for (int i = 0; i < N; i++) {
+        float v = 0.0f;   // of the lane's column, g
 #pragma unroll
-        for (int c = 0; c < C; c++) {   // the four sub-blocks' sums
-            float v = acc[i][c];
-            v += __shfl_xor(v, 16);
-            v += __shfl_xor(v, 32);
-            if (g == c) red[((kpart * tw + i % TILES * groups + ipart) * S + i / TILES) * 64 + lane] = v;
+        for (int c = 0; c < C; c++) {
+            const float s = sum_rows(acc[i][c]);
+            v = g == c ? s : v;
         }
+        red[((kpart * S + i / TILES) * tw + ((i % TILES) << groups_log) + ipart) * 64 + lane] = v;
     }
     __syncthreads();
-    for (int i = tid; i < n * 4 * tw; i += kFew) {   // eight lanes together hold 32 rows where blocks are written (tw even)
-        const int c = i / (4 * tw), quad = i % (4 * tw);
-        f32x4 v[2] = {};
-        for (int k = 0; k < f.kw; k++)
+    for (int i = tid; i < n * 16 * tw; i += kFew) {   // 32 lanes together hold 32 rows where blocks are written (tw even)
+        const int c = i / (16 * tw), rr = i - c * 16 * tw;
+        const int64_t r = tile0 * 16 + rr;
+        const bool live = r < e.rows;
+        if (i >= kFew) outer = load_outer<S>(w0, w1, e, c, r, live);
+        float v[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int s = 0; s < S; s++)
-                v[s] += *reinterpret_cast<const f32x4 *>(red + ((k * tw + quad / 4) * S + s) * 64 + c * 16 + quad % 4 * 4);
-        finish<S>(w0, w1, e, v[0], v[1], c, tile0 * 16 + 4 * quad);
+        for (int k = 0; k < 8; k++)
+            if (k < f.kw)
+#pragma unroll
+                for (int s = 0; s < S; s++) v[s] += red[((k * S + s) * tw + rr / 16) * 64 + c * 16 + rr % 16];
+        finish_one<S>(e, outer, v[0], v[1], c, r, live);
     }
 }
 
@@ -898,9 +964,12 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
 
 template <int C, int S>
 void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, hipStream_t hs) {
-    FewShape f = {K / 128, 1};
+    FewShape f = {K / 128, 1, 0};
     const int64_t chunk = f.nb < kBlocks<C> ? f.nb : kBlocks<C>, quads = (chunk + 3) / 4, tiles = (e.rows + 15) / 16;
-    while (f.kw < 8 && f.kw < quads) f.kw *= 2;
+    while (f.kw < 8 && f.kw < quads) {
+        f.kw *= 2;
+        f.kw_log++;
+    }
     const auto go = [&](auto tiles_, auto q) {
         constexpr int TILES = decltype(tiles_)::value, Q = decltype(q)::value;
         const int64_t per = TILES * (8 / f.kw);
