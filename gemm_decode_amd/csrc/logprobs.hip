@@ -1,10 +1,18 @@
 // logprobs.hip -- log probabilities of given tokens, entropy and the k largest logits of
-// each row of logits.
+// each row of logits, in one pass over them.
 //
 // With m the largest logit, d_j = z_j - z_m <= 0 (z the scaled, possibly capped logit) and
 // S the sum of exp(d_j) over all tokens but m, log sum exp(z) = z_m + log1p(S): so
 //   lp_j = d_j - log1p(S),   entropy = log1p(S) - (sum exp(d_j) d_j) / (1 + S),
-// and a token that the model is sure of keeps its small log probability's digits.
+// and a token that the model is sure of keeps its small log probability's digits. A wave
+// keeps S and D = sum exp(d) d against the largest logit it has met; when a larger one comes,
+// the one before joins S and both are rescaled. Exponents are to the base 2.
+//
+// The k largest: a wave keeps those of its own logits in LDS, and the smallest that can still
+// be among the row's (the k-th largest of any wave). Of most vectors no lane's largest logit
+// reaches that, so that the selection costs a comparison.
+#include <type_traits>
+
 #include "gd_internal.h"
 #include "gd_types.h"
 
@@ -12,8 +20,15 @@ namespace {
 
 using namespace gd;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kMaxK = 64;
+constexpr int kRoom = 512;           // candidates of a wave
+constexpr int kMinPart = 2048;       // tokens of a part of a row at least
+constexpr int kFill = 512;           // parts of all rows that fill the device
 constexpr float kInf = __builtin_inff();
+constexpr float kLog2e = 1.44269504f;
+constexpr double kLn2 = 0.693147180559945309;
+typedef unsigned long long u64;
 
 struct Task {
     const void *logits;
@@ -23,9 +38,21 @@ struct Task {
     float *top_logprobs;
     int64_t stride, n_given, k, n, V;
     float scale, softcap;
+    int64_t parts, part;   // of a row; tokens of one
+    uint8_t *workspace;    // a Part and k keys for each part
 };
 
-// An unsigned key that orders as the logits do (0 and -0 alike), larger logits first.
+// What is known of a part of a row: its largest logit (raw), S and D against it, whether it
+// holds a NaN or an infinity.
+struct Part {
+    double S, D;
+    float top;
+    uint32_t bad;
+    uint64_t unused;
+};
+
+// An unsigned key that orders as the logits do (0 and -0 alike), and with the token's place
+// behind it one number for each token: the larger the earlier in the answer's order.
 __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -33,88 +60,378 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float logit_of(uint32_t key) {
     return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
+__device__ __forceinline__ u64 order_of(float x, uint32_t place) { return static_cast<u64>(key_of(x)) << 32 | ~place; }
 
-// z_j - z_m for the largest logit m; -infinity for a banned token.
-__device__ __forceinline__ float below(const Task &t, float x, float m) {
-    if (t.softcap > 0.0f) {
-        if (x == -kInf) return x;
-        return t.scale * t.softcap * (tanhf(x / t.softcap) - tanhf(m / t.softcap));
+// The capped logit over the cap, tanh(x / cap); -infinity stays.
+struct Cap {
+    float to_exp, c;   // 2 log2(e) / cap; what the logit (over the cap) is multiplied by
+    bool on;
+    __device__ __forceinline__ Cap(float softcap, float scale)
+        : to_exp(softcap > 0.0f ? 2.0f * kLog2e / softcap : 0.0f), c(softcap > 0.0f ? scale * softcap * kLog2e : scale * kLog2e),
+          on(softcap > 0.0f) {}
+    __device__ __forceinline__ float operator()(float x) const {
+        if (!on) return x;
+        const float t = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * to_exp)), 1.0f);
+        return x == -kInf ? x : t;
     }
-    return t.scale * (x - m);
-}
+};
 
-template <typename V, typename F>
-__device__ V over_workgroup(V v, F join, V *red) {
-    for (int o = 32; o >= 1; o >>= 1) v = join(v, __shfl_xor(v, o));
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
-    __syncthreads();
-    v = red[0];
-    for (int w = 1; w < kThreads / 64; w++) v = join(v, red[w]);
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }   // a NaN stays
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
     return v;
 }
 
-// Plain: a workgroup per row, a pass for the maximum, one for the sums and one per alternative.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void logprobs_plain_kernel(Task t) {
-    __shared__ double sums[kThreads / 64];
-    __shared__ unsigned long long keys[kThreads / 64];
-    const int64_t row = blockIdx.x;
-    const T *x = static_cast<const T *>(t.logits) + row * t.stride;
-    const auto largest = [](unsigned long long a, unsigned long long b) { return a > b ? a : b; };
-    const auto plus = [](double a, double b) { return a + b; };
-    // (key, place from behind): one number per token, the larger the earlier in the order
-    const auto ordered = [&](int64_t j) {
-        return static_cast<unsigned long long>(key_of(static_cast<float>(x[j]))) << 32 | (0xffffffffull - j);
-    };
-    unsigned long long best = 0;
-    double odd = 0.0;
-    for (int64_t j = threadIdx.x; j < t.V; j += kThreads) {
-        const float v = static_cast<float>(x[j]);
-        if (!(v < kInf)) odd = 1.0;   // NaN or infinity
-        best = largest(best, ordered(j));
+// A wave's candidates: the `count` first of room[], at most kRoom.
+struct Best {
+    u64 *room, *shared;   // shared: the largest of the waves' k-th largest (0: none has k)
+    int count, k;
+    u64 least;            // only larger ones are taken
+    float least_logit;    // and its logit
+
+    __device__ __forceinline__ void raise(u64 to) {
+        least = to > least ? to : least;
+        least_logit = least ? logit_of(static_cast<uint32_t>(least >> 32)) : -kInf;
     }
-    odd = over_workgroup(odd, plus, sums);
-    best = over_workgroup(best, largest, keys);
-    const float m = logit_of(static_cast<uint32_t>(best >> 32));
-    const int64_t at = 0xffffffffll - static_cast<int64_t>(best & 0xffffffffu);
-    const bool bad = odd > 0.0, none = !bad && m == -kInf;
-    double S = 0.0, D = 0.0;
-    if (!bad && !none)
-        for (int64_t j = threadIdx.x; j < t.V; j += kThreads) {
-            const float d = below(t, static_cast<float>(x[j]), m);
-            if (j != at && d > -200.0f) {
-                const double e = exp(static_cast<double>(d));
-                S += e;
-                D += e * d;
+    // The k-th largest of R 64 numbers, the lanes' v (no two alike; 0: none).
+    template <int R>
+    __device__ __forceinline__ u64 kth(const u64 (&v)[R]) const {
+        u64 at = 0;
+        for (int b = 63; b >= 0; b--) {   // the largest number that k of them reach
+            const u64 next = at | u64{1} << b;
+            int reach = 0;
+#pragma unroll
+            for (int r = 0; r < R; r++) reach += __popcll(__ballot(v[r] >= next));
+            if (reach >= k) at = next;
+        }
+        return at;
+    }
+    template <int R>
+    __device__ __forceinline__ void keep() {   // the k largest only
+        const int lane = threadIdx.x % 64;
+        u64 v[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) v[r] = r * 64 + lane < count ? room[r * 64 + lane] : 0;
+        const u64 at = kth<R>(v);
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const u64 stay = __ballot(v[r] >= at && v[r] > 0);
+            if (v[r] >= at && v[r] > 0) room[n + __popcll(stay & ((u64{1} << lane) - 1))] = v[r];
+            n += __popcll(stay);
+        }
+        count = n;
+        if (n >= k) {
+            raise(at);
+            if (lane == 0) atomicMax(shared, at);
+        }
+    }
+    __device__ __forceinline__ void shrink() {
+        if (count <= k) return;
+        if (count <= 128)
+            keep<2>();
+        else
+            keep<kRoom / 64>();
+    }
+    __device__ __forceinline__ void add(float x, uint32_t place, bool live) {
+        const u64 o = order_of(x, place), lane_bit = u64{1} << (threadIdx.x % 64);
+        const u64 in = __ballot(live && o > least);
+        if (!in) return;
+        if (in & lane_bit) room[count + __popcll(in & (lane_bit - 1))] = o;
+        count += __popcll(in);
+        if (count > kRoom - 64) shrink();
+    }
+};
+
+// What a wave has met so far: the largest logit (-infinity before there is one), capped in
+// ref, and the lanes' shares of S and D against it.
+struct Met {
+    float top, ref, S, D;
+    bool bad;
+};
+
+// `N` logits of each lane join, x[i] the token place[i / PER] + i % PER; PER: of one vector.
+template <int N, int PER, bool kEntropy>
+__device__ __forceinline__ void absorb(Met &w, Best &best, const Cap &cap, const float (&x)[N], const uint32_t (&place)[(N + PER - 1) / PER]) {
+    constexpr int G = (N + PER - 1) / PER;
+    float most[G], mine = -kInf;
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+        most[g] = x[g * PER];
+#pragma unroll
+        for (int i = g * PER + 1; i < g * PER + PER && i < N; i++) most[g] = max_nan(most[g], x[i]);
+        mine = max_nan(mine, most[g]);
+    }
+    w.bad |= !(mine < kInf);
+    const bool rise = __any(mine > w.top);
+    float one = 0.0f;
+    if (rise) {   // a larger one: what was the largest joins the others, in lane 0
+        const float top = wave_max(mine), ref = cap(top);
+        if (w.top > -kInf) {
+            const float d = fmaxf((w.ref - ref) * cap.c, -1000.0f), f = __builtin_amdgcn_exp2f(d);
+            if (kEntropy) w.D = f * fmaf(d, w.S, w.D);
+            w.S *= f;
+            if (threadIdx.x % 64 == 0) {
+                w.S += f;
+                if (kEntropy) w.D = fmaf(f, d, w.D);
             }
         }
-    S = over_workgroup(S, plus, sums);
-    D = over_workgroup(D, plus, sums);
-    const double lse = log1p(S);
-    const auto lp_of = [&](float v) {
-        return bad ? __builtin_nanf("") : none ? -kInf : static_cast<float>(static_cast<double>(below(t, v, m)) - lse);
+        w.top = top;
+        w.ref = ref;
+    }
+    const float ref = w.top > -kInf ? w.ref : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        float d = (cap(x[i]) - ref) * cap.c;
+        if (kEntropy) d = fmaxf(d, -1000.0f);   // no 0 times infinity (a NaN is known of already)
+        float e = __builtin_amdgcn_exp2f(d);
+        if (rise && x[i] == w.top) {
+            one += 1.0f;
+            e = 0.0f;
+        }
+        w.S += e;
+        if (kEntropy) w.D = fmaf(e, d, w.D);
+    }
+    if (rise) {   // one of those that are the largest stays out, the others count in full
+        const u64 has = __ballot(one > 0.0f);
+        if (static_cast<int>(threadIdx.x % 64) == __ffsll(has) - 1) one -= 1.0f;
+        w.S += one;
+    }
+    if (best.k && __any(mine >= best.least_logit)) {
+        best.raise(*best.shared);
+        if (best.least == 0 && N >= 8) {   // none yet: k lanes' largest are k candidates
+            const u64 v[1] = {mine > -kInf ? static_cast<u64>(key_of(mine)) << 32 : 0};
+            best.raise(best.kth<1>(v));   // (0 if there are not so many; below all tokens of this logit otherwise)
+        }
+#pragma unroll
+        for (int g = 0; g < G; g++)
+            if (__any(most[g] >= best.least_logit)) {
+#pragma unroll 1
+                for (int i = 0; i < PER; i++) {
+                    float v = x[g * PER];
+#pragma unroll
+                    for (int j = 1; j < PER && g * PER + j < N; j++) v = i == j ? x[g * PER + j] : v;
+                    best.add(v, place[g] + i, v > -kInf);
+                }
+            }
+        if (best.count >= 2 * best.k) best.shrink();
+    }
+}
+
+// Both parts' sums against the larger logit. c: as Cap's.
+__device__ __forceinline__ void join(Part &a, const Part &b, const Cap &cap) {
+    a.bad |= b.bad;
+    if (!(b.top > -kInf)) return;
+    if (!(a.top > -kInf)) {
+        const uint32_t bad = a.bad;
+        a = b;
+        a.bad = bad;
+        return;
+    }
+    const bool first = a.top >= b.top;
+    const Part &hi = first ? a : b, &lo = first ? b : a;
+    const double d = (static_cast<double>(cap(lo.top)) - static_cast<double>(cap(hi.top))) * cap.c, f = exp2(d);
+    const double S = hi.S + f * (lo.S + 1.0), D = hi.D + f * (lo.D + d * (lo.S + 1.0));
+    a.top = hi.top;
+    a.S = S;
+    a.D = D;
+}
+
+// The k largest of `count` orders in LDS, by their ranks, to out[]. Called by the workgroup.
+__device__ void sort_best(const u64 *in, int count, int k, u64 *out) {
+    for (int i = threadIdx.x; i < k; i += kThreads) out[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+        const u64 v = in[i];
+        int rank = 0;
+        for (int j = 0; j < count; j++) rank += in[j] > v ? 1 : 0;
+        if (rank < k) out[rank] = v;
+    }
+    __syncthreads();
+}
+
+// What a row answers, once `all` is known of it and best[] is sorted.
+template <typename T>
+__device__ void answer(const Task &t, const Cap &cap, int64_t row, const Part &all, const u64 *best) {
+    const bool bad = all.bad || all.top == kInf, none = !(all.top > -kInf);
+    const double lse = log1p(all.S), y = cap(all.top);
+    const auto lp_of = [&](float x) {
+        if (bad) return __builtin_nanf("");
+        if (none || x == -kInf) return -kInf;
+        return static_cast<float>((static_cast<double>(cap(x)) - y) * cap.c * kLn2 - lse);
     };
-    if (threadIdx.x == 0 && t.entropy)
-        t.entropy[row] = bad ? __builtin_nanf("") : none ? 0.0f : static_cast<float>(lse - D / (1.0 + S));
+    if (t.entropy && threadIdx.x == 0)
+        t.entropy[row] = bad ? __builtin_nanf("") : none ? 0.0f : static_cast<float>(lse - kLn2 * all.D / (1.0 + all.S));
+    const T *x = static_cast<const T *>(t.logits) + row * t.stride;
     for (int64_t i = threadIdx.x; i < t.n_given; i += kThreads) {
         const int64_t id = t.tokens[row * t.n_given + i];
         t.logprobs[row * t.n_given + i] = id >= 0 && id < t.V ? lp_of(static_cast<float>(x[id])) : 0.0f;
     }
-    unsigned long long before = ~0ull;
-    for (int64_t i = 0; i < t.k; i++) {
-        unsigned long long next = 0;
-        for (int64_t j = threadIdx.x; j < t.V; j += kThreads) {
-            const unsigned long long o = ordered(j);
-            if (o < before) next = largest(next, o);
+    for (int i = threadIdx.x; i < t.k; i += kThreads) {
+        const u64 o = best[i];
+        t.top_ids[row * t.k + i] = o && !bad ? static_cast<int64_t>(~static_cast<uint32_t>(o)) : -1;
+        t.top_logprobs[row * t.k + i] = bad ? __builtin_nanf("") : o ? lp_of(logit_of(static_cast<uint32_t>(o >> 32))) : -kInf;
+    }
+}
+
+// A part of a row: whole 16-byte vectors, U of them a thread at a time with the next ones on
+// their way, and the tokens before and behind them one by one.
+template <typename T, int U, bool kEntropy>
+__global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
+    constexpr int PER = 16 / sizeof(T);
+    typedef T Vec __attribute__((ext_vector_type(PER)));
+    __shared__ u64 room[kWaves][kRoom];
+    __shared__ u64 sorted[kMaxK], shared;
+    __shared__ Part parts[kWaves];
+    __shared__ int counts[kWaves];
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+    const int64_t row = blockIdx.y, first = blockIdx.x * t.part;
+    const int64_t length = first + t.part < t.V ? t.part : t.V - first;   // at least 1
+    const T *x = static_cast<const T *>(t.logits) + row * t.stride + first;
+    int head = static_cast<int>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T));
+    head = head < length ? head : static_cast<int>(length);
+    const uint32_t vectors = static_cast<uint32_t>((length - head) / PER);
+    const int tail = static_cast<int>(length - head - static_cast<int64_t>(vectors) * PER);
+    const Vec *body = reinterpret_cast<const Vec *>(x + head);
+    const Cap cap(t.softcap, t.scale);
+    Met met = {-kInf, 0.0f, 0.0f, 0.0f, false};
+    Best best = {room[wave], &shared, 0, static_cast<int>(t.k), 0, -kInf};
+    if (tid == 0) shared = 0;
+    __syncthreads();
+    Vec next[U];
+    const auto load = [&](uint32_t v) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const uint32_t at = v + u * kThreads + tid;
+            next[u] = body[at < vectors ? at : vectors - 1];   // clamped: loaded, not used
         }
-        before = next = over_workgroup(next, largest, keys);
-        if (threadIdx.x == 0) {
-            const float v = next ? logit_of(static_cast<uint32_t>(next >> 32)) : -kInf;
-            t.top_ids[row * t.k + i] = !bad && v > -kInf ? 0xffffffffll - static_cast<int64_t>(next & 0xffffffffu) : -1;
-            t.top_logprobs[row * t.k + i] = bad ? __builtin_nanf("") : v > -kInf ? lp_of(v) : -kInf;
+    };
+    if (vectors) load(0);
+    for (uint32_t v = 0; v < vectors; v += U * kThreads) {
+        float e[U * PER];
+        uint32_t place[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const uint32_t at = v + u * kThreads + tid;
+            place[u] = static_cast<uint32_t>(first) + head + at * PER;
+#pragma unroll
+            for (int i = 0; i < PER; i++) e[u * PER + i] = at < vectors ? static_cast<float>(next[u][i]) : -kInf;
+        }
+        if (v + U * kThreads < vectors) load(v + U * kThreads);
+        absorb<U * PER, PER, kEntropy>(met, best, cap, e, place);
+    }
+    {   // the ends: fewer than PER tokens each, of wave 0
+        const int at = lane < head ? lane : lane < head + tail ? static_cast<int>(length) - tail + lane - head : -1;
+        const float e[1] = {wave == 0 && at >= 0 ? static_cast<float>(x[at]) : -kInf};
+        const uint32_t place[1] = {static_cast<uint32_t>(first) + (at >= 0 ? at : 0)};
+        if (head + tail > 0 && wave == 0) absorb<1, 1, kEntropy>(met, best, cap, e, place);
+    }
+    if (best.count > kMaxK) best.shrink();
+    {
+        const double S = wave_sum(static_cast<double>(met.S)), D = wave_sum(static_cast<double>(met.D));
+        const bool bad = __any(met.bad);
+        if (lane == 0) {
+            parts[wave] = Part{S, D, met.top, bad ? 1u : 0u, 0};
+            counts[wave] = best.count;
         }
     }
+    __syncthreads();
+    int total = 0;
+    if (t.k) {   // the waves' candidates side by side, those that can still be among the k
+        const u64 least = shared;
+        u64 mine[kWaves * kMaxK / kThreads];
+        int at[kWaves * kMaxK / kThreads];
+        static_assert(kWaves * kMaxK == kThreads, "a candidate a thread");
+        const int c = counts[wave];
+        mine[0] = lane < c ? room[wave][lane] : 0;
+        if (mine[0] < least) mine[0] = 0;
+        const u64 in = __ballot(mine[0] > 0);
+        __syncthreads();
+        if (lane == 0) counts[wave] = __popcll(in);
+        __syncthreads();
+        at[0] = __popcll(in & ((u64{1} << lane) - 1));
+        for (int w = 0; w < kWaves; w++) {
+            if (w < wave) at[0] += counts[w];
+            total += counts[w];
+        }
+        u64 *list = room[0];
+        if (mine[0]) list[at[0]] = mine[0];
+        __syncthreads();
+        sort_best(list, total, static_cast<int>(t.k), sorted);
+    }
+    Part all = parts[0];
+    for (int w = 1; w < kWaves; w++) join(all, parts[w], cap);
+    if (t.parts == 1) {
+        answer<T>(t, cap, row, all, sorted);
+        return;
+    }
+    uint8_t *out = t.workspace + (row * t.parts + blockIdx.x) * (sizeof(Part) + 8 * t.k);
+    if (tid == 0) *reinterpret_cast<Part *>(out) = all;
+    if (tid < t.k) reinterpret_cast<u64 *>(out + sizeof(Part))[tid] = sorted[tid];
+}
+
+// The parts of a row joined, by one workgroup.
+constexpr int kMost = 2048;   // candidates of a row at a time
+static_assert(kFill + kMaxK <= kMost, "the parts' first ones");
+template <typename T>
+__global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Task t) {
+    __shared__ u64 list[kMost], sorted[kMaxK];
+    __shared__ Part parts[kThreads];
+    __shared__ int count;
+    const int64_t row = blockIdx.x, size = sizeof(Part) + 8 * t.k;
+    const uint8_t *in = t.workspace + row * t.parts * size;
+    const Cap cap(t.softcap, t.scale);
+    const int k = static_cast<int>(t.k), tid = threadIdx.x;
+    Part all = {0.0, 0.0, -kInf, 0, 0};
+    for (int64_t p = tid; p < t.parts; p += kThreads) join(all, *reinterpret_cast<const Part *>(in + p * size), cap);
+    parts[tid] = all;
+    __syncthreads();
+    for (int o = kThreads / 2; o >= 1; o >>= 1) {
+        if (tid < o && tid + o < t.parts) {
+            join(all, parts[tid + o], cap);
+            parts[tid] = all;
+        }
+        __syncthreads();
+    }
+    all = parts[0];
+    if (k) {
+        const auto entry = [&](int64_t p, int i) { return reinterpret_cast<const u64 *>(in + p * size + sizeof(Part))[i]; };
+        // The k-th largest of the parts' first ones is reached by k: what lies below is not of the k.
+        const int heads = static_cast<int>((k + t.parts - 1) / t.parts);   // of each part: at most kFill + k in all
+        for (int i = tid; i < t.parts * heads; i += kThreads) list[i] = entry(i / heads, i % heads);
+        __syncthreads();
+        sort_best(list, static_cast<int>(t.parts) * heads, k, sorted);
+        const u64 least = sorted[k - 1];
+        // The others, as many parts at a time as there is room for, behind the k best so far.
+        const int64_t fit = (kMost - kMaxK) / k;
+        for (int64_t p0 = 0; p0 < t.parts; p0 += fit) {
+            const int many = static_cast<int>((t.parts - p0 < fit ? t.parts - p0 : fit) * k), kept = p0 ? k : 0;
+            if (tid == 0) count = kept;
+            for (int i = tid; i < kept; i += kThreads) list[i] = sorted[i];
+            __syncthreads();
+            for (int i = tid; i < many; i += kThreads) {
+                const u64 o = entry(p0 + i / k, i % k);
+                if (o && o >= least) list[atomicAdd(&count, 1)] = o;   // in any order: no two are alike
+            }
+            __syncthreads();
+            sort_best(list, count, k, sorted);
+        }
+    }
+    answer<T>(t, cap, row, all, sorted);
+}
+
+// Rows are cut until there are kFill parts in all, into parts of kMinPart tokens at least.
+int64_t parts_of(int64_t n, int64_t V) {
+    const int64_t want = (kFill + n - 1) / n, most = (V + kMinPart - 1) / kMinPart;
+    return want < most ? want : most;
 }
 
 int check_sizes(const char *name, int64_t n, int64_t V, int64_t k) {
@@ -130,7 +447,10 @@ extern "C" int token_logprobs_workspace_bytes(int64_t n, int64_t V, int64_t k, s
     GD_REQUIRE(bytes, GD_EINVAL, "token_logprobs_workspace_bytes: null pointer");
     const int st = check_sizes("token_logprobs_workspace_bytes", n, V, k);
     if (st) return st;
-    *bytes = 0;
+    // Every smaller call's parts: at most kFill + n in all, and as many as fit into V.
+    const int64_t most = (V + kMinPart - 1) / kMinPart;
+    const int64_t parts = most == 1 ? 0 : n * most < kFill + n ? n * most : kFill + n;   // below 2^44
+    *bytes = static_cast<size_t>(parts * (static_cast<int64_t>(sizeof(Part)) + 8 * k));
     clear_error();
     return GD_OK;
 }
@@ -156,11 +476,51 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
     GD_REQUIRE(aligned(logits, dtype_size(dtype)) && aligned(tokens, 8) && aligned(logprobs, 4) && aligned(entropy, 4) &&
                    aligned(top_ids, 8) && aligned(top_logprobs, 4) && aligned(workspace, 16),
                GD_EALIGN, "%s: a pointer is not aligned to its element (the workspace: 16)", name);
-    (void)workspace_bytes;
-    const Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, n, V, scale, softcap};
-    dispatch_dtype(dtype, [&](auto e) {
-        hipLaunchKernelGGL((logprobs_plain_kernel<decltype(e)>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0,
-                           as_stream(stream), t);
+    Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, n, V, scale, softcap,
+              parts_of(n, V), 0, static_cast<uint8_t *>(workspace)};
+    if (t.parts > 1) {
+        t.part = (V + t.parts - 1) / t.parts;
+        t.part = (t.part + kMinPart - 1) / kMinPart * kMinPart;
+        t.parts = (V + t.part - 1) / t.part;
+    } else {
+        t.part = V;
+    }
+    if (t.parts > 1) {
+        const uint64_t need = static_cast<uint64_t>(n * t.parts) * (sizeof(Part) + 8 * static_cast<uint64_t>(k));
+        GD_REQUIRE(workspace, GD_EINVAL, "%s: null workspace", name);
+        GD_REQUIRE(workspace_bytes >= need, GD_ERANGE, "%s: workspace of %zu bytes, %llu are needed", name, workspace_bytes,
+                   (unsigned long long)need);
+    }
+    const hipStream_t hs = as_stream(stream);
+    dispatch_dtype(dtype, [&](auto one) {
+        using T = decltype(one);
+        const auto go = [&](auto u, auto ent) {
+            // The grid's second axis is limited to 65535 rows.
+            for (int64_t from = 0; from < n; from += 65535) {
+                Task s = t;
+                const int64_t rows = n - from < 65535 ? n - from : 65535;
+                s.logits = static_cast<const T *>(logits) + from * stride;
+                if (tokens) s.tokens += from * n_given;
+                if (logprobs) s.logprobs += from * n_given;
+                if (entropy) s.entropy += from;
+                if (top_ids) s.top_ids += from * k;
+                if (top_logprobs) s.top_logprobs += from * k;
+                hipLaunchKernelGGL((logprobs_part_kernel<T, decltype(u)::value, decltype(ent)::value>),
+                                   dim3(static_cast<uint32_t>(t.parts), static_cast<uint32_t>(rows)), dim3(kThreads), 0, hs, s);
+            }
+        };
+        constexpr int PER = 16 / sizeof(T);
+        const auto size = [&](auto ent) {
+            if (t.part > kMinPart)
+                go(std::integral_constant<int, 4>{}, ent);
+            else
+                go(std::integral_constant<int, 8 / PER>{}, ent);
+        };
+        if (entropy)
+            size(std::true_type{});
+        else
+            size(std::false_type{});
+        if (t.parts > 1) hipLaunchKernelGGL((logprobs_join_kernel<T>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, hs, t);
     });
     return check_launch(name);
 }
