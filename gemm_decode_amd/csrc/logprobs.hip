@@ -62,17 +62,23 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 }
 __device__ __forceinline__ u64 order_of(float x, uint32_t place) { return static_cast<u64>(key_of(x)) << 32 | ~place; }
 
-// The capped logit over the cap, tanh(x / cap); -infinity stays.
+// What exponents are taken of: the logit, or over the cap tanh(x / cap); -infinity stays.
+template <bool kOn>
 struct Cap {
-    float to_exp, c;   // 2 log2(e) / cap; what the logit (over the cap) is multiplied by
-    bool on;
-    __device__ __forceinline__ Cap(float softcap, float scale)
-        : to_exp(softcap > 0.0f ? 2.0f * kLog2e / softcap : 0.0f), c(softcap > 0.0f ? scale * softcap * kLog2e : scale * kLog2e),
-          on(softcap > 0.0f) {}
+    float over, c;   // 1 / softcap; what comes out is multiplied by c
+    __device__ __forceinline__ Cap(float softcap, float scale) : over(kOn ? 1.0f / softcap : 1.0f), c(kOn ? scale * softcap * kLog2e : scale * kLog2e) {}
     __device__ __forceinline__ float operator()(float x) const {
-        if (!on) return x;
-        const float t = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * to_exp)), 1.0f);
+        if (!kOn) return x;
+        const float t = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * over * (2.0f * kLog2e))), 1.0f);
         return x == -kInf ? x : t;
+    }
+    // The same where |x / softcap| <= kSmall: an odd polynomial, within 1.4e-7.
+    static constexpr float kSmall = 0.7f;
+    __device__ __forceinline__ float small(float x) const {
+        if (!kOn) return x;
+        const float u = x * over, s = u * u;
+        const float q = fmaf(fmaf(fmaf(0.0135997012f, s, -0.0506746806f), s, 0.132769167f), s, -0.33330065f);
+        return fmaf(u * s, q, u);
     }
 };
 
@@ -101,18 +107,42 @@ struct Best {
         least = to > least ? to : least;
         least_logit = least ? logit_of(static_cast<uint32_t>(least >> 32)) : -kInf;
     }
-    // The k-th largest of R 64 numbers, the lanes' v (no two alike; 0: none).
-    template <int R>
-    __device__ __forceinline__ u64 kth(const u64 (&v)[R]) const {
-        u64 at = 0;
-        for (int b = 63; b >= 0; b--) {   // the largest number that k of them reach
-            const u64 next = at | u64{1} << b;
-            int reach = 0;
+    // The largest number that at least `k_` of R 64 numbers, the lanes', reach (0: there are not so
+    // many above 0); `reach`: how many do.
+    template <int R, typename U>
+    __device__ __forceinline__ static U reached(const U (&v)[R], int k_, int &reach) {
+        U at = 0;
+        reach = 64 * R;
+#pragma unroll 1
+        for (int b = 8 * sizeof(U) - 1; b >= 0; b--) {
+            const U next = at | U{1} << b;
+            int n = 0;
 #pragma unroll
-            for (int r = 0; r < R; r++) reach += __popcll(__ballot(v[r] >= next));
-            if (reach >= k) at = next;
+            for (int r = 0; r < R; r++) n += __popcll(__ballot(v[r] >= next));
+            if (n >= k_) {
+                at = next;
+                reach = n;
+            }
         }
         return at;
+    }
+    // The k-th largest of R 64 orders (no two alike but 0: none).
+    template <int R>
+    __device__ __forceinline__ u64 kth(const u64 (&v)[R]) const {
+        uint32_t key[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) key[r] = static_cast<uint32_t>(v[r] >> 32);
+        int reach;
+        const uint32_t at = reached<R>(key, k, reach);
+        if (at == 0 || reach == k) return static_cast<u64>(at) << 32;   // all of this logit are among them
+        int above = 0;
+        uint32_t low[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            above += __popcll(__ballot(key[r] > at));
+            low[r] = key[r] == at ? static_cast<uint32_t>(v[r]) : 0;
+        }
+        return static_cast<u64>(at) << 32 | reached<R>(low, k - above, reach);
     }
     template <int R>
     __device__ __forceinline__ void keep() {   // the k largest only
@@ -131,12 +161,14 @@ struct Best {
         count = n;
         if (n >= k) {
             raise(at);
-            if (lane == 0) atomicMax(shared, at);
+            if (lane == 0 && at > *shared) atomicMax(shared, at);
         }
     }
     __device__ __forceinline__ void shrink() {
         if (count <= k) return;
-        if (count <= 128)
+        if (count <= 64)
+            keep<1>();
+        else if (count <= 128)
             keep<2>();
         else
             keep<kRoom / 64>();
@@ -155,14 +187,16 @@ struct Best {
 // ref, and the lanes' shares of S and D against it.
 struct Met {
     float top, ref, S, D;
+    float low, high;   // logits between them need no care (see absorb)
     bool bad;
 };
 
 // `N` logits of each lane join, x[i] the token place[i / PER] + i % PER; PER: of one vector.
-template <int N, int PER, bool kEntropy>
-__device__ __forceinline__ void absorb(Met &w, Best &best, const Cap &cap, const float (&x)[N], const uint32_t (&place)[(N + PER - 1) / PER]) {
+template <int N, int PER, bool kEntropy, bool kCap>
+__device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap, const float (&x)[N],
+                                       const uint32_t (&place)[(N + PER - 1) / PER]) {
     constexpr int G = (N + PER - 1) / PER;
-    float most[G], mine = -kInf;
+    float most[G], mine = -kInf, least = kInf;
 #pragma unroll
     for (int g = 0; g < G; g++) {
         most[g] = x[g * PER];
@@ -170,10 +204,10 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap &cap, const
         for (int i = g * PER + 1; i < g * PER + PER && i < N; i++) most[g] = max_nan(most[g], x[i]);
         mine = max_nan(mine, most[g]);
     }
+#pragma unroll
+    for (int i = 0; i < N; i++) least = fminf(least, x[i]);
     w.bad |= !(mine < kInf);
-    const bool rise = __any(mine > w.top);
-    float one = 0.0f;
-    if (rise) {   // a larger one: what was the largest joins the others, in lane 0
+    if (__any(mine > w.top)) {   // a larger one: what was the largest joins the others, in lane 0
         const float top = wave_max(mine), ref = cap(top);
         if (w.top > -kInf) {
             const float d = fmaxf((w.ref - ref) * cap.c, -1000.0f), f = __builtin_amdgcn_exp2f(d);
@@ -186,63 +220,79 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap &cap, const
         }
         w.top = top;
         w.ref = ref;
-    }
-    const float ref = w.top > -kInf ? w.ref : 0.0f;
+        w.low = kCap ? -Cap<kCap>::kSmall / cap.over : fmaxf(ref - 1000.0f / cap.c, -3e38f);
+        w.high = kCap ? Cap<kCap>::kSmall / cap.over : kInf;
+        float one = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        float d = (cap(x[i]) - ref) * cap.c;
-        if (kEntropy) d = fmaxf(d, -1000.0f);   // no 0 times infinity (a NaN is known of already)
-        float e = __builtin_amdgcn_exp2f(d);
-        if (rise && x[i] == w.top) {
-            one += 1.0f;
-            e = 0.0f;
+        for (int i = 0; i < N; i++) {
+            const float d = fmaxf((cap(x[i]) - ref) * cap.c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
+            const bool is = x[i] == top;
+            one += is ? 1.0f : 0.0f;
+            w.S += is ? 0.0f : e;
+            if (kEntropy) w.D = fmaf(e, d, w.D);
         }
-        w.S += e;
-        if (kEntropy) w.D = fmaf(e, d, w.D);
-    }
-    if (rise) {   // one of those that are the largest stays out, the others count in full
+        // One of those that are the largest stays out, the others count in full.
         const u64 has = __ballot(one > 0.0f);
         if (static_cast<int>(threadIdx.x % 64) == __ffsll(has) - 1) one -= 1.0f;
         w.S += one;
+    } else if (__all(least >= w.low && mine <= w.high)) {   // no 0 times infinity in D, and a short tanh
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float d = (cap.small(x[i]) - w.ref) * cap.c, e = __builtin_amdgcn_exp2f(d);
+            w.S += e;
+            if (kEntropy) w.D = fmaf(e, d, w.D);
+        }
+    } else {
+        const float ref = w.top > -kInf ? w.ref : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float d = fmaxf((cap(x[i]) - ref) * cap.c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
+            w.S += e;
+            if (kEntropy) w.D = fmaf(e, d, w.D);
+        }
     }
     if (best.k && __any(mine >= best.least_logit)) {
         best.raise(*best.shared);
         if (best.least == 0 && N >= 8) {   // none yet: k lanes' largest are k candidates
-            const u64 v[1] = {mine > -kInf ? static_cast<u64>(key_of(mine)) << 32 : 0};
-            best.raise(best.kth<1>(v));   // (0 if there are not so many; below all tokens of this logit otherwise)
+            const uint32_t v[1] = {mine > -kInf ? key_of(mine) : 0};
+            int reach;
+            best.raise(static_cast<u64>(Best::reached<1>(v, best.k, reach)) << 32);   // below all tokens of this logit
         }
 #pragma unroll
         for (int g = 0; g < G; g++)
             if (__any(most[g] >= best.least_logit)) {
-#pragma unroll 1
-                for (int i = 0; i < PER; i++) {
+                uint32_t in = 0;
+#pragma unroll
+                for (int i = 0; i < PER && g * PER + i < N; i++) in |= x[g * PER + i] >= best.least_logit ? 1u << i : 0u;
+                while (__any(in != 0)) {   // a lane's one after the other
+                    const int j = in ? __builtin_ctz(in) : 0;
                     float v = x[g * PER];
 #pragma unroll
-                    for (int j = 1; j < PER && g * PER + j < N; j++) v = i == j ? x[g * PER + j] : v;
-                    best.add(v, place[g] + i, v > -kInf);
+                    for (int i = 1; i < PER && g * PER + i < N; i++) v = i == j ? x[g * PER + i] : v;
+                    best.add(v, place[g] + j, in != 0 && v > -kInf);
+                    in &= in - 1;
                 }
             }
         if (best.count >= 2 * best.k) best.shrink();
     }
 }
 
-// Both parts' sums against the larger logit. c: as Cap's.
-__device__ __forceinline__ void join(Part &a, const Part &b, const Cap &cap) {
-    a.bad |= b.bad;
-    if (!(b.top > -kInf)) return;
-    if (!(a.top > -kInf)) {
-        const uint32_t bad = a.bad;
-        a = b;
-        a.bad = bad;
-        return;
-    }
+// Both parts' sums against the larger logit.
+template <bool kCap>
+__device__ __forceinline__ void join(Part &a, const Part &b, const Cap<kCap> &cap) {
     const bool first = a.top >= b.top;
-    const Part &hi = first ? a : b, &lo = first ? b : a;
-    const double d = (static_cast<double>(cap(lo.top)) - static_cast<double>(cap(hi.top))) * cap.c, f = exp2(d);
-    const double S = hi.S + f * (lo.S + 1.0), D = hi.D + f * (lo.D + d * (lo.S + 1.0));
-    a.top = hi.top;
-    a.S = S;
-    a.D = D;
+    const float hi = first ? a.top : b.top, lo = first ? b.top : a.top;
+    const double HS = first ? a.S : b.S, HD = first ? a.D : b.D, LS = first ? b.S : a.S, LD = first ? b.D : a.D;
+    a.bad |= b.bad;
+    a.top = hi;
+    a.S = HS;
+    a.D = HD;
+    if (lo > -kInf) {
+        const double d = fmax((static_cast<double>(cap(lo)) - cap(hi)) * cap.c, -1000.0);
+        const double f = __builtin_amdgcn_exp2f(static_cast<float>(d));
+        a.S += f * (LS + 1.0);
+        a.D += f * (LD + d * (LS + 1.0));
+    }
 }
 
 // The k largest of `count` orders in LDS, by their ranks, to out[]. Called by the workgroup.
@@ -252,28 +302,43 @@ __device__ void sort_best(const u64 *in, int count, int k, u64 *out) {
     for (int i = threadIdx.x; i < count; i += kThreads) {
         const u64 v = in[i];
         int rank = 0;
+#pragma unroll 8
         for (int j = 0; j < count; j++) rank += in[j] > v ? 1 : 0;
         if (rank < k) out[rank] = v;
     }
     __syncthreads();
 }
 
-// What a row answers, once `all` is known of it and best[] is sorted.
+// The first given token of a thread: asked for before it is needed.
+struct Given {
+    int64_t id;
+    float x;
+};
 template <typename T>
-__device__ void answer(const Task &t, const Cap &cap, int64_t row, const Part &all, const u64 *best) {
+__device__ __forceinline__ Given given(const Task &t, int64_t row, int64_t i) {
+    Given g = {-1, 0.0f};
+    if (i < t.n_given) {
+        g.id = t.tokens[row * t.n_given + i];
+        if (g.id >= 0 && g.id < t.V) g.x = static_cast<float>((static_cast<const T *>(t.logits) + row * t.stride)[g.id]);
+    }
+    return g;
+}
+
+// What a row answers, once `all` is known of it and best[] is sorted.
+template <typename T, bool kCap>
+__device__ __forceinline__ void answer(const Task &t, const Cap<kCap> &cap, int64_t row, const Part &all, const u64 *best, Given g) {
     const bool bad = all.bad || all.top == kInf, none = !(all.top > -kInf);
-    const double lse = log1p(all.S), y = cap(all.top);
+    const float lse = log1pf(static_cast<float>(all.S)), y = cap(all.top);
     const auto lp_of = [&](float x) {
         if (bad) return __builtin_nanf("");
         if (none || x == -kInf) return -kInf;
         return static_cast<float>((static_cast<double>(cap(x)) - y) * cap.c * kLn2 - lse);
     };
     if (t.entropy && threadIdx.x == 0)
-        t.entropy[row] = bad ? __builtin_nanf("") : none ? 0.0f : static_cast<float>(lse - kLn2 * all.D / (1.0 + all.S));
-    const T *x = static_cast<const T *>(t.logits) + row * t.stride;
+        t.entropy[row] = bad ? __builtin_nanf("") : none ? 0.0f : lse - static_cast<float>(kLn2 * all.D) / (1.0f + static_cast<float>(all.S));
     for (int64_t i = threadIdx.x; i < t.n_given; i += kThreads) {
-        const int64_t id = t.tokens[row * t.n_given + i];
-        t.logprobs[row * t.n_given + i] = id >= 0 && id < t.V ? lp_of(static_cast<float>(x[id])) : 0.0f;
+        t.logprobs[row * t.n_given + i] = g.id >= 0 && g.id < t.V ? lp_of(g.x) : 0.0f;
+        g = given<T>(t, row, i + kThreads);
     }
     for (int i = threadIdx.x; i < t.k; i += kThreads) {
         const u64 o = best[i];
@@ -284,7 +349,7 @@ __device__ void answer(const Task &t, const Cap &cap, int64_t row, const Part &a
 
 // A part of a row: whole 16-byte vectors, U of them a thread at a time with the next ones on
 // their way, and the tokens before and behind them one by one.
-template <typename T, int U, bool kEntropy>
+template <typename T, int U, bool kEntropy, bool kCap>
 __global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
     constexpr int PER = 16 / sizeof(T);
     typedef T Vec __attribute__((ext_vector_type(PER)));
@@ -301,8 +366,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
     const uint32_t vectors = static_cast<uint32_t>((length - head) / PER);
     const int tail = static_cast<int>(length - head - static_cast<int64_t>(vectors) * PER);
     const Vec *body = reinterpret_cast<const Vec *>(x + head);
-    const Cap cap(t.softcap, t.scale);
-    Met met = {-kInf, 0.0f, 0.0f, 0.0f, false};
+    const Cap<kCap> cap(t.softcap, t.scale);
+    Met met = {-kInf, 0.0f, 0.0f, 0.0f, kInf, -kInf, false};
     Best best = {room[wave], &shared, 0, static_cast<int>(t.k), 0, -kInf};
     if (tid == 0) shared = 0;
     __syncthreads();
@@ -314,25 +379,31 @@ __global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
             next[u] = body[at < vectors ? at : vectors - 1];   // clamped: loaded, not used
         }
     };
+    Given asked = {-1, 0.0f};
     if (vectors) load(0);
+    if (t.parts == 1) asked = given<T>(t, row, tid);
     for (uint32_t v = 0; v < vectors; v += U * kThreads) {
+        if (v + U * kThreads > vectors) {
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (v + u * kThreads + tid >= vectors) next[u] = Vec(static_cast<T>(-kInf));
+        }
         float e[U * PER];
         uint32_t place[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const uint32_t at = v + u * kThreads + tid;
-            place[u] = static_cast<uint32_t>(first) + head + at * PER;
+            place[u] = static_cast<uint32_t>(first) + head + (v + u * kThreads + tid) * PER;
 #pragma unroll
-            for (int i = 0; i < PER; i++) e[u * PER + i] = at < vectors ? static_cast<float>(next[u][i]) : -kInf;
+            for (int i = 0; i < PER; i++) e[u * PER + i] = static_cast<float>(next[u][i]);
         }
         if (v + U * kThreads < vectors) load(v + U * kThreads);
-        absorb<U * PER, PER, kEntropy>(met, best, cap, e, place);
+        absorb<U * PER, PER, kEntropy, kCap>(met, best, cap, e, place);
     }
     {   // the ends: fewer than PER tokens each, of wave 0
         const int at = lane < head ? lane : lane < head + tail ? static_cast<int>(length) - tail + lane - head : -1;
         const float e[1] = {wave == 0 && at >= 0 ? static_cast<float>(x[at]) : -kInf};
         const uint32_t place[1] = {static_cast<uint32_t>(first) + (at >= 0 ? at : 0)};
-        if (head + tail > 0 && wave == 0) absorb<1, 1, kEntropy>(met, best, cap, e, place);
+        if (head + tail > 0 && wave == 0) absorb<1, 1, kEntropy, kCap>(met, best, cap, e, place);
     }
     if (best.count > kMaxK) best.shrink();
     {
@@ -370,7 +441,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
     Part all = parts[0];
     for (int w = 1; w < kWaves; w++) join(all, parts[w], cap);
     if (t.parts == 1) {
-        answer<T>(t, cap, row, all, sorted);
+        answer<T, kCap>(t, cap, row, all, sorted, asked);
         return;
     }
     uint8_t *out = t.workspace + (row * t.parts + blockIdx.x) * (sizeof(Part) + 8 * t.k);
@@ -380,52 +451,53 @@ __global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
 
 // The parts of a row joined, by one workgroup.
 constexpr int kMost = 2048;   // candidates of a row at a time
-static_assert(kFill + kMaxK <= kMost, "the parts' first ones");
-template <typename T>
+template <typename T, bool kCap>
 __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Task t) {
-    __shared__ u64 list[kMost], sorted[kMaxK];
+    __shared__ u64 stage[kMost], list[kMost], sorted[kMaxK];
     __shared__ Part parts[kThreads];
     __shared__ int count;
     const int64_t row = blockIdx.x, size = sizeof(Part) + 8 * t.k;
     const uint8_t *in = t.workspace + row * t.parts * size;
-    const Cap cap(t.softcap, t.scale);
+    const Cap<kCap> cap(t.softcap, t.scale);
     const int k = static_cast<int>(t.k), tid = threadIdx.x;
+    const Given asked = given<T>(t, row, tid);
+    const auto entry = [&](int64_t p, int i) { return reinterpret_cast<const u64 *>(in + p * size + sizeof(Part))[i]; };
     Part all = {0.0, 0.0, -kInf, 0, 0};
     for (int64_t p = tid; p < t.parts; p += kThreads) join(all, *reinterpret_cast<const Part *>(in + p * size), cap);
     parts[tid] = all;
-    __syncthreads();
-    for (int o = kThreads / 2; o >= 1; o >>= 1) {
-        if (tid < o && tid + o < t.parts) {
-            join(all, parts[tid + o], cap);
-            parts[tid] = all;
-        }
-        __syncthreads();
-    }
-    all = parts[0];
-    if (k) {
-        const auto entry = [&](int64_t p, int i) { return reinterpret_cast<const u64 *>(in + p * size + sizeof(Part))[i]; };
-        // The k-th largest of the parts' first ones is reached by k: what lies below is not of the k.
-        const int heads = static_cast<int>((k + t.parts - 1) / t.parts);   // of each part: at most kFill + k in all
-        for (int i = tid; i < t.parts * heads; i += kThreads) list[i] = entry(i / heads, i % heads);
-        __syncthreads();
-        sort_best(list, static_cast<int>(t.parts) * heads, k, sorted);
-        const u64 least = sorted[k - 1];
-        // The others, as many parts at a time as there is room for, behind the k best so far.
+    if (k) {   // as many parts' candidates at a time as there is room for, behind the k best so far
         const int64_t fit = (kMost - kMaxK) / k;
         for (int64_t p0 = 0; p0 < t.parts; p0 += fit) {
-            const int many = static_cast<int>((t.parts - p0 < fit ? t.parts - p0 : fit) * k), kept = p0 ? k : 0;
-            if (tid == 0) count = kept;
+            const int fits = static_cast<int>(t.parts - p0 < fit ? t.parts - p0 : fit), kept = p0 ? k : 0;
+            for (int i = tid; i < fits * k; i += kThreads) stage[i] = entry(p0 + i / k, i % k);
             for (int i = tid; i < kept; i += kThreads) list[i] = sorted[i];
+            if (tid == 0) count = kept;
             __syncthreads();
-            for (int i = tid; i < many; i += kThreads) {
-                const u64 o = entry(p0 + i / k, i % k);
+            // The k-th largest of the parts' first ones is reached by k: what lies below is not of the k.
+            const int heads = (k + fits - 1) / fits;   // of each part
+            u64 *first = list + kMaxK;
+            for (int i = tid; i < fits * heads; i += kThreads) first[i] = stage[i / heads * k + i % heads];
+            __syncthreads();
+            sort_best(first, fits * heads, k, sorted);
+            const u64 least = sorted[k - 1];
+            __syncthreads();
+            for (int i = tid; i < fits * k; i += kThreads) {
+                const u64 o = stage[i];
                 if (o && o >= least) list[atomicAdd(&count, 1)] = o;   // in any order: no two are alike
             }
             __syncthreads();
             sort_best(list, count, k, sorted);
         }
     }
-    answer<T>(t, cap, row, all, sorted);
+    __syncthreads();
+    for (int o = kThreads / 2; o >= 1; o >>= 1) {
+        if (tid < o && tid + o < t.parts) {
+            join(all, parts[tid + o], cap);
+            parts[tid] = all;
+        }
+        if (o < t.parts) __syncthreads();
+    }
+    answer<T, kCap>(t, cap, row, parts[0], sorted, asked);
 }
 
 // Rows are cut until there are kFill parts in all, into parts of kMinPart tokens at least.
@@ -494,7 +566,7 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
     const hipStream_t hs = as_stream(stream);
     dispatch_dtype(dtype, [&](auto one) {
         using T = decltype(one);
-        const auto go = [&](auto u, auto ent) {
+        const auto go = [&](auto u, auto ent, auto capped) {
             // The grid's second axis is limited to 65535 rows.
             for (int64_t from = 0; from < n; from += 65535) {
                 Task s = t;
@@ -505,22 +577,25 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
                 if (entropy) s.entropy += from;
                 if (top_ids) s.top_ids += from * k;
                 if (top_logprobs) s.top_logprobs += from * k;
-                hipLaunchKernelGGL((logprobs_part_kernel<T, decltype(u)::value, decltype(ent)::value>),
+                hipLaunchKernelGGL((logprobs_part_kernel<T, decltype(u)::value, decltype(ent)::value, decltype(capped)::value>),
                                    dim3(static_cast<uint32_t>(t.parts), static_cast<uint32_t>(rows)), dim3(kThreads), 0, hs, s);
             }
         };
         constexpr int PER = 16 / sizeof(T);
-        const auto size = [&](auto ent) {
+        const auto with = [&](auto ent, auto capped) {
             if (t.part > kMinPart)
-                go(std::integral_constant<int, 4>{}, ent);
+                go(std::integral_constant<int, 4>{}, ent, capped);
             else
-                go(std::integral_constant<int, 8 / PER>{}, ent);
+                go(std::integral_constant<int, 8 / PER>{}, ent, capped);
+            if (t.parts > 1)
+                hipLaunchKernelGGL((logprobs_join_kernel<T, decltype(capped)::value>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, hs, t);
         };
-        if (entropy)
-            size(std::true_type{});
+        const std::true_type yes;
+        const std::false_type no;
+        if (softcap > 0.0f)
+            entropy ? with(yes, yes) : with(no, yes);
         else
-            size(std::false_type{});
-        if (t.parts > 1) hipLaunchKernelGGL((logprobs_join_kernel<T>), dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, hs, t);
+            entropy ? with(yes, no) : with(no, no);
     });
     return check_launch(name);
 }
