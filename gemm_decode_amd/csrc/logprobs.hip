@@ -72,13 +72,28 @@ struct Cap {
         const float t = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * over * (2.0f * kLog2e))), 1.0f);
         return x == -kInf ? x : t;
     }
-    // The same where |x / softcap| <= kSmall: an odd polynomial, within 1.4e-7.
-    static constexpr float kSmall = 0.7f;
-    __device__ __forceinline__ float small(float x) const {
-        if (!kOn) return x;
-        const float u = x * over, s = u * u;
-        const float q = fmaf(fmaf(fmaf(0.0135997012f, s, -0.0506746806f), s, 0.132769167f), s, -0.33330065f);
-        return fmaf(u * s, q, u);
+    static constexpr float kSmall = 0.7f;   // of |x / softcap|, see Exponent
+};
+
+// (cap(x) - ref) c for many x: plainly, or with a cap where |x / softcap| <= kSmall as x times an
+// odd polynomial, within 1.4e-7 of tanh (times c). a[]: its coefficients in powers of x^2.
+template <bool kCap>
+struct Exponent {
+    float ref, c, off, a[4];
+    __device__ __forceinline__ Exponent(const Cap<kCap> &cap, float ref_) : ref(ref_), c(cap.c) {
+        if (!kCap) return;
+        const float s = cap.over * cap.over;
+        a[0] = -0.33330065f * s;
+        a[1] = 0.132769167f * s * s;
+        a[2] = -0.0506746806f * s * s * s;
+        a[3] = 0.0135997012f * s * s * s * s;
+        c = cap.c * cap.over;
+        off = -ref * cap.c;
+    }
+    __device__ __forceinline__ float operator()(float x) const {
+        if (!kCap) return (x - ref) * c;
+        const float s = x * x, q = fmaf(fmaf(fmaf(a[3], s, a[2]), s, a[1]), s, a[0]);
+        return fmaf(fmaf(x * s, q, x), c, off);
     }
 };
 
@@ -191,9 +206,10 @@ struct Met {
     bool bad;
 };
 
-// `N` logits of each lane join, x[i] the token place[i / PER] + i % PER; PER: of one vector.
+// `N` logits of each lane join (and may be changed), x[i] the token place[i / PER] + i % PER;
+// PER: of one vector.
 template <int N, int PER, bool kEntropy, bool kCap>
-__device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap, const float (&x)[N],
+__device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap, float (&x)[N],
                                        const uint32_t (&place)[(N + PER - 1) / PER]) {
     constexpr int G = (N + PER - 1) / PER;
     float most[G], mine = -kInf, least = kInf;
@@ -207,56 +223,14 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
 #pragma unroll
     for (int i = 0; i < N; i++) least = fminf(least, x[i]);
     w.bad |= !(mine < kInf);
-    if (__any(mine > w.top)) {   // a larger one: what was the largest joins the others, in lane 0
-        const float top = wave_max(mine), ref = cap(top);
-        if (w.top > -kInf) {
-            const float d = fmaxf((w.ref - ref) * cap.c, -1000.0f), f = __builtin_amdgcn_exp2f(d);
-            if (kEntropy) w.D = f * fmaf(d, w.S, w.D);
-            w.S *= f;
-            if (threadIdx.x % 64 == 0) {
-                w.S += f;
-                if (kEntropy) w.D = fmaf(f, d, w.D);
-            }
-        }
-        w.top = top;
-        w.ref = ref;
-        w.low = kCap ? -Cap<kCap>::kSmall / cap.over : fmaxf(ref - 1000.0f / cap.c, -3e38f);
-        w.high = kCap ? Cap<kCap>::kSmall / cap.over : kInf;
-        float one = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const float d = fmaxf((cap(x[i]) - ref) * cap.c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
-            const bool is = x[i] == top;
-            one += is ? 1.0f : 0.0f;
-            w.S += is ? 0.0f : e;
-            if (kEntropy) w.D = fmaf(e, d, w.D);
-        }
-        // One of those that are the largest stays out, the others count in full.
-        const u64 has = __ballot(one > 0.0f);
-        if (static_cast<int>(threadIdx.x % 64) == __ffsll(has) - 1) one -= 1.0f;
-        w.S += one;
-    } else if (__all(least >= w.low && mine <= w.high)) {   // no 0 times infinity in D, and a short tanh
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const float d = (cap.small(x[i]) - w.ref) * cap.c, e = __builtin_amdgcn_exp2f(d);
-            w.S += e;
-            if (kEntropy) w.D = fmaf(e, d, w.D);
-        }
-    } else {
-        const float ref = w.top > -kInf ? w.ref : 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const float d = fmaxf((cap(x[i]) - ref) * cap.c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
-            w.S += e;
-            if (kEntropy) w.D = fmaf(e, d, w.D);
-        }
-    }
     if (best.k && __any(mine >= best.least_logit)) {
         best.raise(*best.shared);
         if (best.least == 0 && N >= 8) {   // none yet: k lanes' largest are k candidates
             const uint32_t v[1] = {mine > -kInf ? key_of(mine) : 0};
             int reach;
-            best.raise(static_cast<u64>(Best::reached<1>(v, best.k, reach)) << 32);   // below all tokens of this logit
+            const u64 to = static_cast<u64>(Best::reached<1>(v, best.k, reach)) << 32;   // below all tokens of this logit
+            best.raise(to);
+            if (threadIdx.x % 64 == 0 && to > *best.shared) atomicMax(best.shared, to);
         }
 #pragma unroll
         for (int g = 0; g < G; g++)
@@ -274,6 +248,61 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
                 }
             }
         if (best.count >= 2 * best.k) best.shrink();
+    }
+    if (__any(mine > w.top)) {   // a larger one: what was the largest joins the others, in lane 0
+        const float top = wave_max(mine), ref = cap(top);
+        if (w.top > -kInf) {
+            const float d = fmaxf((w.ref - ref) * cap.c, -1000.0f), f = __builtin_amdgcn_exp2f(d);
+            if (kEntropy) w.D = f * fmaf(d, w.S, w.D);
+            w.S *= f;
+            if (threadIdx.x % 64 == 0) {
+                w.S += f;
+                if (kEntropy) w.D = fmaf(f, d, w.D);
+            }
+        }
+        w.top = top;
+        w.ref = ref;
+        const float small = fminf(Cap<kCap>::kSmall / cap.over, 1e9f);   // (x^9 stays in range)
+        w.low = kCap ? -small : fmaxf(ref - 1000.0f / cap.c, -3e38f);
+        w.high = kCap ? small : kInf;
+        // The new one stays out of S: the first of them in the first lane that has one.
+        // What stands in its place counts for nothing; where the short way below is taken, which
+        // has no -infinity, what it counts for is taken off S again.
+        const bool small_enough = __all(least >= w.low && mine <= w.high);
+        const float out = small_enough ? w.low : -kInf;
+        const bool chosen = static_cast<int>(threadIdx.x % 64) == __ffsll(__ballot(mine == top)) - 1;
+        bool here = chosen;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const bool is = here && x[i] == top;
+            x[i] = is ? out : x[i];
+            here = here && !is;
+        }
+        if (small_enough) {
+            const Exponent<kCap> of(cap, ref);
+            const float d = of(out), e = __builtin_amdgcn_exp2f(d);
+            if (chosen) {
+                w.S -= e;
+                if (kEntropy) w.D = fmaf(-e, d, w.D);
+            }
+        }
+    }
+    if (__all(least >= w.low && mine <= w.high)) {   // no 0 times infinity in D, and a short tanh
+        const Exponent<kCap> of(cap, w.ref);
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float d = of(x[i]), e = __builtin_amdgcn_exp2f(d);
+            w.S += e;
+            if (kEntropy) w.D = fmaf(e, d, w.D);
+        }
+    } else {
+        const float ref = w.top > -kInf ? w.ref : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float d = fmaxf((cap(x[i]) - ref) * cap.c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
+            w.S += e;
+            if (kEntropy) w.D = fmaf(e, d, w.D);
+        }
     }
 }
 
@@ -401,7 +430,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
     }
     {   // the ends: fewer than PER tokens each, of wave 0
         const int at = lane < head ? lane : lane < head + tail ? static_cast<int>(length) - tail + lane - head : -1;
-        const float e[1] = {wave == 0 && at >= 0 ? static_cast<float>(x[at]) : -kInf};
+        float e[1] = {wave == 0 && at >= 0 ? static_cast<float>(x[at]) : -kInf};
         const uint32_t place[1] = {static_cast<uint32_t>(first) + (at >= 0 ? at : 0)};
         if (head + tail > 0 && wave == 0) absorb<1, 1, kEntropy, kCap>(met, best, cap, e, place);
     }
