@@ -99,16 +99,28 @@ struct Exponent {
 
 __device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }   // a NaN stays
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
+// Over the lanes of a wave, in all of them: four steps within rows of 16, then the rows.
+template <typename F>
+__device__ __forceinline__ float over_wave(float v, F join) {
+    const auto dpp = [&](auto control) {
+        v = join(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(control)::value, 0xF, 0xF, false)));
+    };
+    dpp(std::integral_constant<int, 0xB1>{});    // lane ^ 1
+    dpp(std::integral_constant<int, 0x4E>{});    // lane ^ 2
+    dpp(std::integral_constant<int, 0x141>{});   // the other four of eight
+    dpp(std::integral_constant<int, 0x140>{});   // the other eight of 16
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t w = __builtin_bit_cast(uint32_t, join(__builtin_bit_cast(float, static_cast<uint32_t>(p[0])),
+                                                         __builtin_bit_cast(float, static_cast<uint32_t>(p[1]))));
+    const auto q = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return join(__builtin_bit_cast(float, static_cast<uint32_t>(q[0])), __builtin_bit_cast(float, static_cast<uint32_t>(q[1])));
 }
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+__device__ __forceinline__ float wave_max(float v) {
+    return over_wave(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return over_wave(v, [](float a, float b) { return a + b; });
 }
 
 // A wave's candidates: the `count` first of room[], at most kRoom.
@@ -379,7 +391,7 @@ __device__ __forceinline__ void answer(const Task &t, const Cap<kCap> &cap, int6
 // A part of a row: whole 16-byte vectors, U of them a thread at a time with the next ones on
 // their way, and the tokens before and behind them one by one.
 template <typename T, int U, bool kEntropy, bool kCap>
-__global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
+__global__ __launch_bounds__(kThreads, 4) void logprobs_part_kernel(Task t) {
     constexpr int PER = 16 / sizeof(T);
     typedef T Vec __attribute__((ext_vector_type(PER)));
     __shared__ u64 room[kWaves][kRoom];
@@ -436,7 +448,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_part_kernel(Task t) {
     }
     if (best.count > kMaxK) best.shrink();
     {
-        const double S = wave_sum(static_cast<double>(met.S)), D = wave_sum(static_cast<double>(met.D));
+        const double S = wave_sum(met.S), D = wave_sum(met.D);
         const bool bad = __any(met.bad);
         if (lane == 0) {
             parts[wave] = Part{S, D, met.top, bad ? 1u : 0u, 0};
