@@ -506,37 +506,55 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
 constexpr int64_t kStepBytes = 4 * 1536;
 constexpr int kStepHalves = 2;   // sub-blocks of a step: the two halves of a wave
 
+// A thread takes a sub-block of a column, or half of one (kHalf: few columns, where the way
+// through the arithmetic is what takes time).
+template <bool kHalf>
 __global__ __launch_bounds__(256) void q1_digits_kernel(const uint16_t *__restrict__ a_q8, uint8_t *__restrict__ out, int64_t n,
                                                         int64_t steps) {
-    const int lane = threadIdx.x % 64;
-    const int64_t step = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64, tile = blockIdx.y;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, half = kHalf ? wave % 2 : 0;
+    const int64_t step = kHalf ? static_cast<int64_t>(blockIdx.x) * 2 + wave / 2 : static_cast<int64_t>(blockIdx.x) * 4 + wave;
+    const int64_t tile = blockIdx.y, c = tile * 32 + lane % 32;
     if (step >= steps) return;
-    const int64_t c = tile * 32 + lane % 32;
     uint32_t d[8] = {}, h = 0;
     if (c < n) h = load_block(a_q8 + ((c * steps + step) * kStepHalves + lane / 32) * 17, d);
     const Scale s(h);
-    uint32_t r[8][4];   // by places 4 k .. 4 k + 3
-#pragma unroll
-    for (int j = 0; j < 4; j++) digits8(d, j, s.m, r + 2 * j);
     uint8_t *o = out + (tile * steps + step) * kStepBytes;
+    uint32_t w[2][4][3];   // three words for each half and digit
+#pragma unroll
+    for (int k = 0; k < (kHalf ? 1 : 2); k++) {
+        uint32_t r[4][4];   // by places 4 i .. 4 i + 3 of the half
+        const int j = kHalf ? 2 * half : 2 * k;
+        digits8(d, j, s.m, r);
+        digits8(d, j + 1, s.m, r + 2);
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+            w[k][p][0] = r[0][p] | r[1][p] << 24;
+            w[k][p][1] = r[1][p] >> 8 | r[2][p] << 16;
+            w[k][p][2] = r[2][p] >> 16 | r[3][p] << 8;
+        }
+    }
 #pragma unroll
     for (int p = 0; p < 4; p++, o += 1536) {
-        uint32_t w[6];
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            w[3 * k] = r[4 * k][p] | r[4 * k + 1][p] << 24;
-            w[3 * k + 1] = r[4 * k + 1][p] >> 8 | r[4 * k + 2][p] << 16;
-            w[3 * k + 2] = r[4 * k + 2][p] >> 16 | r[4 * k + 3][p] << 8;
+        uint32_t *lo = reinterpret_cast<uint32_t *>(o) + lane * 4, *hi = reinterpret_cast<uint32_t *>(o + 1024) + lane * 2;
+        if (!kHalf) {
+            *reinterpret_cast<u32x4 *>(lo) = u32x4{w[0][p][0], w[0][p][1], w[0][p][2], w[1][p][0]};
+            *reinterpret_cast<u32x2 *>(hi) = u32x2{w[1][p][1], w[1][p][2]};
+        } else if (half == 0) {
+            *reinterpret_cast<u32x2 *>(lo) = u32x2{w[0][p][0], w[0][p][1]};
+            lo[2] = w[0][p][2];
+        } else {
+            lo[3] = w[0][p][0];
+            *reinterpret_cast<u32x2 *>(hi) = u32x2{w[0][p][1], w[0][p][2]};
         }
-        reinterpret_cast<u32x4 *>(o)[lane] = u32x4{w[0], w[1], w[2], w[3]};
-        reinterpret_cast<u32x2 *>(o + 1024)[lane] = u32x2{w[4], w[5]};
     }
-    reinterpret_cast<uint32_t *>(out + gridDim.y * steps * kStepBytes)[(tile * steps + step) * 64 + lane] = s.powers;
+    if (half == 0) reinterpret_cast<uint32_t *>(out + gridDim.y * steps * kStepBytes)[(tile * steps + step) * 64 + lane] = s.powers;
 }
 
 struct ManyShape {
     int64_t nb, col_tiles, row_tiles;   // blocks of a row, tiles of 32 columns, of 32 rows
     int64_t col_groups, row_groups;     // of a workgroup's tiles
+    int64_t slices, share;              // of K, and the blocks of one
+    float *parts;                       // sums of the slices, [slices][S][n][32 row_tiles]
 };
 
 // t += the products of one digit. (The builtin takes the digit's byte as an immediate.)
@@ -584,12 +602,41 @@ __device__ __forceinline__ void put_tile(const f32x16 &v, float *to, int g, int 
 }
 
 // Workgroups with consecutive numbers go to the eight dies in turn: each die takes a run of
-// row groups with all their column groups, so that a weight is read by one die.
-__device__ __forceinline__ bool place(const ManyShape &f, int64_t &col_group, int64_t &row_group) {
-    const int64_t total = f.col_groups * f.row_groups, id = blockIdx.x, per = (total + 7) / 8, at = id % 8 * per + id / 8;
+// row groups with all their slices and column groups, so that a weight is read by one die.
+__device__ __forceinline__ bool place(const ManyShape &f, int64_t &col_group, int64_t &row_group, int64_t &slice) {
+    const int64_t total = f.col_groups * f.row_groups * f.slices, id = blockIdx.x, per = (total + 7) / 8, at = id % 8 * per + id / 8;
     col_group = at % f.col_groups;
-    row_group = at / f.col_groups;
-    return at < total;
+    slice = at / f.col_groups % f.slices;
+    row_group = at / f.col_groups / f.slices;
+    return id / 8 < per && at < total;
+}
+
+// Sums of four rows: finished, or a slice's share kept for the joining launch.
+template <int S>
+__device__ __forceinline__ void emit(const Weight &w0, const Weight &w1, const Epilogue &e, const ManyShape &f, int64_t slice, f32x4 v,
+                                     f32x4 u, int64_t c, int64_t r) {
+    if (f.slices == 1) {
+        finish<S>(w0, w1, e, v, u, c, r);
+    } else if (c < e.n && r < 32 * f.row_tiles) {
+        float *to = f.parts + (slice * S * e.n + c) * 32 * f.row_tiles + r;
+        *reinterpret_cast<f32x4 *>(to) = v;
+        if (S == 2) *reinterpret_cast<f32x4 *>(to + e.n * 32 * f.row_tiles) = u;
+    }
+}
+
+template <int S>
+__global__ __launch_bounds__(256) void q1_join_kernel(Weight w0, Weight w1, Epilogue e, ManyShape f) {
+    const int64_t quads = 8 * f.row_tiles, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;   // eight lanes to 32 rows
+    if (i >= e.n * quads) return;
+    const int64_t c = i / quads, r = i % quads * 4, next = S * e.n * 32 * f.row_tiles;
+    const float *from = f.parts + c * 32 * f.row_tiles + r;
+    f32x4 v[2] = {};
+#pragma unroll 4
+    for (int64_t s = 0; s < f.slices; s++, from += next) {
+        v[0] += *reinterpret_cast<const f32x4 *>(from);
+        if (S == 2) v[1] += *reinterpret_cast<const f32x4 *>(from + e.n * 32 * f.row_tiles);
+    }
+    finish<S>(w0, w1, e, v[0], v[1], c, r);
 }
 
 // Loads of 16 (or 4) bytes a lane from base + `at` (per lane) to LDS, lane after lane from `to`
@@ -627,9 +674,10 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 32, n32 = lane % 32;
     const int64_t nb = f.nb, nb8 = (nb + 7) / 8, steps = 2 * nb;
-    int64_t col, row0;
-    if (!place(f, col, row0)) return;
+    int64_t col, row0, slice;
+    if (!place(f, col, row0, slice)) return;
     row0 = (row0 * kWaves + wave) * TN;
+    const int from = static_cast<int>(slice * f.share);   // the slice's first block
     // Where a block lies for the wave: three of the 12 KiB of digits (two steps are together), the
     // powers of one step, the signs and scales of its tiles, two at a time. Signs 16 bytes a
     // lane, the rows 2 (lane % 16) and one more of half lane / 16 % 2; scales those of a block
@@ -650,11 +698,11 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     const uint32_t lane16 = lane * 16, lane4 = lane * 4;
     const uint32_t base = __builtin_amdgcn_readfirstlane(
         static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds)));
-    const int blocks = static_cast<int>(nb);
+    const int blocks = static_cast<int>(nb - from < f.share ? nb - from : f.share);
     // The kIssued loads of block i, two of them in each part but the first; past the end the last
     // block's again, into a buffer not read.
     const auto stage = [&](int i, uint32_t to, int part) {
-        const uint32_t b = i < blocks ? i : blocks - 1;
+        const uint32_t b = from + (i < blocks ? i : blocks - 1);
         if (part == 0) {
             lds_load16<3>(chunk + b * static_cast<uint32_t>(2 * kStepBytes), lane16, to + wave * 3072);
         } else if (part == 1) {
@@ -733,7 +781,7 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     uint32_t at = 0;
     for (int b = 0; b < blocks; b++) {
         const Step second = read(at, 1);
-        const uint8_t *sc = lds + at + (kScales + wave * 512 + n32 * 4 + (b & 1) * 2);
+        const uint8_t *sc = lds + at + (kScales + wave * 512 + n32 * 4 + ((from + b) & 1) * 2);
 #pragma unroll
         for (int i = 0; i < NT; i++) d0[i] = f16_value(*reinterpret_cast<const uint16_t *>(sc + i * 128));
         __builtin_amdgcn_sched_barrier(0);
@@ -782,7 +830,7 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     float *own = reinterpret_cast<float *>(lds) + wave * S * kTile;   // a wave's own: its LDS accesses stay in order
-    const int from = lane / 8 * kPitch + lane % 8 * 4;
+    const int mine = lane / 8 * kPitch + lane % 8 * 4;
 #pragma unroll
     for (int i = 0; i < TN; i++) {
 #pragma unroll
@@ -790,9 +838,9 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
         for (int q = 0; q < 4; q++)
-            finish<S>(w0, w1, e, *reinterpret_cast<const f32x4 *>(own + from + q * 8 * kPitch),
-                         *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + from + q * 8 * kPitch),
-                         col * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
+            emit<S>(w0, w1, e, f, slice, *reinterpret_cast<const f32x4 *>(own + mine + q * 8 * kPitch),
+                    *reinterpret_cast<const f32x4 *>(own + (S - 1) * kTile + mine + q * 8 * kPitch), col * 32 + 8 * q + lane / 8,
+                    (row0 + i) * 32 + lane % 8 * 4);
         __builtin_amdgcn_wave_barrier();
     }
 }
@@ -807,13 +855,13 @@ __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight 
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 32, n32 = lane % 32;
     const int64_t nb = f.nb, nb8 = (nb + 7) / 8, steps = 2 * nb;
-    int64_t col0, row0;
-    if (!place(f, col0, row0)) return;
+    int64_t col0, row0, slice;
+    if (!place(f, col0, row0, slice)) return;
     col0 *= TM;
     row0 *= TN;
-    const int64_t share = (nb + KS - 1) / KS;
-    int64_t b = wave * share < nb ? wave * share : nb;
-    const int64_t end = b + share < nb ? b + share : nb;
+    const int64_t stop = (slice + 1) * f.share < nb ? (slice + 1) * f.share : nb, share = (f.share + KS - 1) / KS;
+    int64_t b = slice * f.share + wave * share;
+    const int64_t end = b + share < stop ? b + share : stop;
     const uint8_t *frags[TM];
     const uint32_t *powers[TM];
     const u32x2 *bits[NT];
@@ -908,7 +956,7 @@ __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight 
 #pragma unroll
             for (int s = 0; s < S; s++)
                 v[s] += *reinterpret_cast<const f32x4 *>(sums + (k * TM * NT + m * NT + s * TN + i) * kTile + from + q * 8 * kPitch);
-        finish<S>(w0, w1, e, v[0], v[1], (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
+        emit<S>(w0, w1, e, f, slice, v[0], v[1], (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
     }
 }
 
@@ -923,9 +971,12 @@ int check_sizes(const char *name, int64_t K, int64_t n_act) {
     return GD_OK;
 }
 
-// The activations as the matrix cores read them: 100 bytes for 32 elements.
+// The activations as the matrix cores read them, 100 bytes for 32 elements, and the sums of
+// slices of K.
+int64_t digits_bytes(int64_t K, int64_t n_act) { return (n_act + 31) / 32 * 100 * K; }   // below 2^42
+int64_t parts_bytes(int64_t n_act) { return n_act < 32 ? n_act << 19 : INT64_C(1) << 24; }
 int64_t workspace_need(int64_t K, int64_t n_act) {
-    return n_act <= kFewColumns ? 0 : (n_act + 31) / 32 * 100 * K;   // below 2^42
+    return n_act <= kFewColumns ? 0 : digits_bytes(K, n_act) + parts_bytes(n_act);
 }
 
 int check(const char *name, const Weight *w, int count, const void *a_q8, const Epilogue &e, int64_t K, int32_t dtype,
@@ -961,6 +1012,8 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
                GD_EINVAL, "%s: y and y_q8 must not overlap a_q8, residual or each other", name);
     return GD_OK;
 }
+
+constexpr int64_t kWideFrom = 16, kWideWant = 512, kSplitRows = 2, kSplitWant = 512;
 
 template <int C, int S>
 void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, hipStream_t hs) {
@@ -1003,23 +1056,42 @@ void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epi
 template <int S>
 void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, uint8_t *workspace,
               hipStream_t hs) {
-    ManyShape f = {K / 128, (e.n + 31) / 32, (e.rows + 31) / 32, 0, 0};
-    hipLaunchKernelGGL(q1_digits_kernel, dim3(static_cast<uint32_t>((2 * f.nb + 3) / 4), static_cast<uint32_t>(f.col_tiles)), dim3(256),
-                       0, hs, a_q8, workspace, e.n, 2 * f.nb);
-    const auto groups = [&](int64_t col, int64_t row) {   // of so many tiles; the grid
+    ManyShape f = {K / 128, (e.n + 31) / 32, (e.rows + 31) / 32, 0, 0, 1, K / 128, reinterpret_cast<float *>(workspace + digits_bytes(K, e.n))};
+    const auto cut = [](int64_t steps, int64_t by) { return static_cast<uint32_t>((steps + by - 1) / by); };
+    if (f.col_tiles * f.nb < 1024)
+        hipLaunchKernelGGL((q1_digits_kernel<true>), dim3(cut(2 * f.nb, 2), static_cast<uint32_t>(f.col_tiles)), dim3(256), 0, hs, a_q8,
+                           workspace, e.n, 2 * f.nb);
+    else
+        hipLaunchKernelGGL((q1_digits_kernel<false>), dim3(cut(2 * f.nb, 4), static_cast<uint32_t>(f.col_tiles)), dim3(256), 0, hs, a_q8,
+                           workspace, e.n, 2 * f.nb);
+    const auto groups = [&](int64_t col, int64_t row) {   // of so many tiles
         f.col_groups = (f.col_tiles + col - 1) / col;
         f.row_groups = (f.row_tiles + row - 1) / row;
         return f.col_groups * f.row_groups;
     };
-    const auto grid = [](int64_t g) { return dim3(static_cast<uint32_t>((g + 7) / 8 * 8)); };
+    // Slices of K, of `least` blocks at least, until there are `want` workgroups or no room for their sums.
+    const auto slice = [&](int64_t have, int64_t want, int64_t least) {
+        const int64_t room = parts_bytes(e.n) / (S * e.n * f.row_tiles * 128);
+        int64_t z = (want + have - 1) / have;
+        z = z < f.nb / least ? z : f.nb / least;
+        z = z < room ? z : room;
+        if (z < 1) z = 1;
+        f.share = (f.nb + z - 1) / z;
+        f.slices = (f.nb + f.share - 1) / f.share;
+        return dim3(static_cast<uint32_t>((have * f.slices + 7) / 8 * 8));
+    };
     constexpr int TN = 4 / S;
     const int64_t wide = groups(1, 4 * TN);
-    if (wide >= 256) {
-        hipLaunchKernelGGL((q1_wide_kernel<TN, S>), grid(wide), dim3(256), 0, hs, w0, w1, workspace, e, f);
+    if (wide >= kWideFrom) {
+        const dim3 grid = slice(wide, kWideWant, 8);
+        hipLaunchKernelGGL((q1_wide_kernel<TN, S>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
     } else {
-        const int64_t split = groups(1, 1);
-        hipLaunchKernelGGL((q1_split_kernel<1, 1, S, 8>), grid(split), dim3(512), 0, hs, w0, w1, workspace, e, f);
+        const int64_t have = groups(1, kSplitRows / S);
+        const dim3 grid = slice(have, kSplitWant, 2);
+        hipLaunchKernelGGL((q1_split_kernel<1, kSplitRows / S, S, 4>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
     }
+    if (f.slices > 1)
+        hipLaunchKernelGGL((q1_join_kernel<S>), dim3(static_cast<uint32_t>((e.n * f.row_tiles * 8 + 255) / 256)), dim3(256), 0, hs, w0, w1, e, f);
 }
 
 template <int S>

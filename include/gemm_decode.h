@@ -562,9 +562,9 @@ int q1_q8_gated(const void *gate_bits, const void *gate_scales, const void *up_b
                 void *y_q8, int64_t rows, int64_t K, int64_t n_act, int32_t dtype, void *workspace,
                 size_t workspace_bytes, void *stream);
 
-/* Workspace bytes of both: 0 up to four columns, else 100 * K per column, the
- * columns rounded up to 32, over 32 (the activations as the matrix cores read
- * them). Grows with n_act: one for the largest call serves every smaller one of
+/* Workspace bytes of both: 0 up to four columns, else 100 * K for each 32 columns
+ * (the activations as the matrix cores read them) and 512 KiB a column, at most 16
+ * MiB (sums of slices of K). One for the largest call serves every smaller one of
  * the same K. Host only. Errors: GD_EINVAL, GD_ESHAPE, GD_ERANGE. */
 int q1_q8_linear_workspace_bytes(int64_t K, int64_t n_act, size_t *bytes);
 

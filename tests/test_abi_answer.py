@@ -36,7 +36,7 @@ def test_linear_refusals(gd):
         assert call(bias=FAKE + 2) == ALIGN and call(y=FAR + 2) == ALIGN and call(y=FAR + 1, dt=F16) == ALIGN
         assert call(q=2 * FAR + 1) == ALIGN
         assert call(rows=(1 << 31) - 32) == RANGE and call(K=1 << 21) == RANGE and call(n=(1 << 20) + 1) == RANGE
-        assert call(n=5) == INVAL and call(n=5, ws=FAKE, wb=100 * 256 - 1) == RANGE and call(n=5, ws=FAKE + 8, wb=1 << 20) == ALIGN
+        assert call(n=5) == INVAL and call(n=5, ws=FAKE, wb=100 * 256 + 5 * (1 << 19) - 1) == RANGE and call(n=5, ws=FAKE + 8, wb=1 << 24) == ALIGN
         assert call(rows=BIG) == RANGE and call(n=BIG) == RANGE and call(K=BIG) == RANGE
         assert call(y=FAKE) == INVAL and call(q=FAKE) == INVAL and call(q=FAR) == INVAL   # on top of what is read or written
     assert linear(res=FAKE + 2) == ALIGN
@@ -48,8 +48,8 @@ def test_linear_workspace(gd):
     L, b = gd.lib(), ctypes.c_size_t(7)
     f = L.q1_q8_linear_workspace_bytes
     assert f(256, 4, ctypes.byref(b)) == 0 and b.value == 0
-    assert f(256, 5, ctypes.byref(b)) == 0 and b.value == 100 * 256
-    assert f(256, 33, ctypes.byref(b)) == 0 and b.value == 200 * 256
+    assert f(256, 5, ctypes.byref(b)) == 0 and b.value == 100 * 256 + 5 * (1 << 19)
+    assert f(256, 33, ctypes.byref(b)) == 0 and b.value == 200 * 256 + (1 << 24)
     assert f(256, 5, None) == INVAL and f(0, 5, ctypes.byref(b)) == INVAL and f(256, 0, ctypes.byref(b)) == INVAL
     assert f(130, 5, ctypes.byref(b)) == SHAPE and f(1 << 21, 5, ctypes.byref(b)) == RANGE and f(256, BIG, ctypes.byref(b)) == RANGE
 
