@@ -1013,7 +1013,7 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
     return GD_OK;
 }
 
-constexpr int64_t kWideFrom = 16, kWideWant = 512, kSplitRows = 2, kSplitWant = 512;
+constexpr int64_t kWideFrom = 3500, kManyGroups = 384;
 
 template <int C, int S>
 void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, hipStream_t hs) {
@@ -1072,7 +1072,7 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
     // Slices of K, of `least` blocks at least, until there are `want` workgroups or no room for their sums.
     const auto slice = [&](int64_t have, int64_t want, int64_t least) {
         const int64_t room = parts_bytes(e.n) / (S * e.n * f.row_tiles * 128);
-        int64_t z = (want + have - 1) / have;
+        int64_t z = want / have;
         z = z < f.nb / least ? z : f.nb / least;
         z = z < room ? z : room;
         if (z < 1) z = 1;
@@ -1082,13 +1082,18 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
     };
     constexpr int TN = 4 / S;
     const int64_t wide = groups(1, 4 * TN);
-    if (wide >= kWideFrom) {
-        const dim3 grid = slice(wide, kWideWant, 8);
+    if (wide * f.nb >= kWideFrom) {
+        const dim3 grid = slice(wide, 512 + wide - 1, 8);
         hipLaunchKernelGGL((q1_wide_kernel<TN, S>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
     } else {
-        const int64_t have = groups(1, kSplitRows / S);
-        const dim3 grid = slice(have, kSplitWant, 2);
-        hipLaunchKernelGGL((q1_split_kernel<1, kSplitRows / S, S, 4>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
+        const int64_t have = groups(1, 2 / S);
+        if (have >= kManyGroups) {
+            const dim3 grid = slice(have, 1, 8);
+            hipLaunchKernelGGL((q1_split_kernel<1, 2 / S, S, 4>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
+        } else {
+            const dim3 grid = slice(have, 256, 8);
+            hipLaunchKernelGGL((q1_split_kernel<1, 2 / S, S, 8>), grid, dim3(512), 0, hs, w0, w1, workspace, e, f);
+        }
     }
     if (f.slices > 1)
         hipLaunchKernelGGL((q1_join_kernel<S>), dim3(static_cast<uint32_t>((e.n * f.row_tiles * 8 + 255) / 256)), dim3(256), 0, hs, w0, w1, e, f);
