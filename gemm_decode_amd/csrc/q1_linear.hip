@@ -504,7 +504,6 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
 // elements (a step) a fragment of 1536 bytes per digit (16 bytes of each lane, then 8), and
 // behind all of them a word of each lane with the digits' powers of two.
 constexpr int64_t kStepBytes = 4 * 1536;
-constexpr int kStepHalves = 2;   // sub-blocks of a step: the two halves of a wave
 
 // A thread takes a sub-block of a column, or half of one (kHalf: few columns, where the way
 // through the arithmetic is what takes time).
@@ -516,7 +515,7 @@ __global__ __launch_bounds__(256) void q1_digits_kernel(const uint16_t *__restri
     const int64_t tile = blockIdx.y, c = tile * 32 + lane % 32;
     if (step >= steps) return;
     uint32_t d[8] = {}, h = 0;
-    if (c < n) h = load_block(a_q8 + ((c * steps + step) * kStepHalves + lane / 32) * 17, d);
+    if (c < n) h = load_block(a_q8 + ((c * steps + step) * 2 + lane / 32) * 17, d);
     const Scale s(h);
     uint8_t *o = out + (tile * steps + step) * kStepBytes;
     uint32_t w[2][4][3];   // three words for each half and digit
@@ -552,7 +551,7 @@ __global__ __launch_bounds__(256) void q1_digits_kernel(const uint16_t *__restri
 
 struct ManyShape {
     int64_t nb, col_tiles, row_tiles;   // blocks of a row, tiles of 32 columns, of 32 rows
-    int64_t col_groups, row_groups;     // of a workgroup's tiles
+    int64_t row_groups;                 // of a workgroup's tiles
     int64_t slices, share;              // of K, and the blocks of one
     float *parts;                       // sums of the slices, [slices][S][n][32 row_tiles]
 };
@@ -563,15 +562,12 @@ __device__ __forceinline__ f32x16 mma(i32x8 a, i32x8 b, f32x16 t, uint32_t power
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, t, kFp6, kFp4, P, static_cast<int>(powers), 0, kOne);
 }
 
-// One step of TM x NT tiles: t[m][i] += a[m] w[i], the four digits one after the other so that
-// TM NT instructions stand between two on the same sums.
-template <int TM, int NT>
-__device__ __forceinline__ void step(f32x16 (&t)[TM][NT], const i32x8 (&a)[TM][4], const i32x8 (&w)[NT], const uint32_t (&powers)[TM]) {
+// One step of NT tiles: t[i] += a w[i], the four digits one after the other.
+template <int NT>
+__device__ __forceinline__ void step(f32x16 (&t)[NT], const i32x8 (&a)[4], const i32x8 (&w)[NT], uint32_t powers) {
     const auto digit = [&](auto p) {
 #pragma unroll
-        for (int m = 0; m < TM; m++)
-#pragma unroll
-            for (int i = 0; i < NT; i++) t[m][i] = mma<decltype(p)::value>(a[m][decltype(p)::value], w[i], t[m][i], powers[m]);
+        for (int i = 0; i < NT; i++) t[i] = mma<decltype(p)::value>(a[decltype(p)::value], w[i], t[i], powers);
     };
     digit(std::integral_constant<int, 0>{});
     digit(std::integral_constant<int, 1>{});
@@ -580,15 +576,13 @@ __device__ __forceinline__ void step(f32x16 (&t)[TM][NT], const i32x8 (&a)[TM][4
 }
 
 // acc += d0 t, d0 of the lane's weight row.
-template <int TM, int NT>
-__device__ __forceinline__ void fold(f32x16 (&acc)[TM][NT], const f32x16 (&t)[TM][NT], const uint16_t (&d0)[NT]) {
+template <int NT>
+__device__ __forceinline__ void fold(f32x16 (&acc)[NT], const f32x16 (&t)[NT], const uint16_t (&d0)[NT]) {
 #pragma unroll
     for (int i = 0; i < NT; i++) {
         const float d = f16_value(d0[i]);
 #pragma unroll
-        for (int m = 0; m < TM; m++)
-#pragma unroll
-            for (int k = 0; k < 16; k++) acc[m][i][k] = fmaf(d, t[m][i][k], acc[m][i][k]);
+        for (int k = 0; k < 16; k++) acc[i][k] = fmaf(d, t[i][k], acc[i][k]);
     }
 }
 
@@ -602,12 +596,12 @@ __device__ __forceinline__ void put_tile(const f32x16 &v, float *to, int g, int 
 }
 
 // Workgroups with consecutive numbers go to the eight dies in turn: each die takes a run of
-// row groups with all their slices and column groups, so that a weight is read by one die.
-__device__ __forceinline__ bool place(const ManyShape &f, int64_t &col_group, int64_t &row_group, int64_t &slice) {
-    const int64_t total = f.col_groups * f.row_groups * f.slices, id = blockIdx.x, per = (total + 7) / 8, at = id % 8 * per + id / 8;
-    col_group = at % f.col_groups;
-    slice = at / f.col_groups % f.slices;
-    row_group = at / f.col_groups / f.slices;
+// row groups with all their slices and columns, so that a weight is read by one die.
+__device__ __forceinline__ bool place(const ManyShape &f, int64_t &col, int64_t &row_group, int64_t &slice) {
+    const int64_t total = f.col_tiles * f.row_groups * f.slices, id = blockIdx.x, per = (total + 7) / 8, at = id % 8 * per + id / 8;
+    col = at % f.col_tiles;
+    slice = at / f.col_tiles % f.slices;
+    row_group = at / f.col_tiles / f.slices;
     return id / 8 < per && at < total;
 }
 
@@ -845,33 +839,26 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     }
 }
 
-// Batches: KS waves share the sums of TM tiles of 32 columns and NT = TN S tiles of 32 weight
-// rows by K, each loading its digits to registers a block ahead.
-template <int TM, int TN, int S, int KS>
+// Batches: KS waves share the sums of 32 columns and NT = TN S tiles of 32 weight rows by K,
+// each loading its digits to registers a block ahead, and add them up in LDS.
+template <int TN, int S, int KS>
 __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
                                                               ManyShape f) {
     constexpr int NT = TN * S;
-    __shared__ __attribute__((aligned(16))) float sums[KS * TM * NT * kTile];
+    __shared__ __attribute__((aligned(16))) float sums[KS * NT * kTile];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 32, n32 = lane % 32;
     const int64_t nb = f.nb, nb8 = (nb + 7) / 8, steps = 2 * nb;
-    int64_t col0, row0, slice;
-    if (!place(f, col0, row0, slice)) return;
-    col0 *= TM;
+    int64_t col, row0, slice;
+    if (!place(f, col, row0, slice)) return;
     row0 *= TN;
     const int64_t stop = (slice + 1) * f.share < nb ? (slice + 1) * f.share : nb, share = (f.share + KS - 1) / KS;
     int64_t b = slice * f.share + wave * share;
     const int64_t end = b + share < stop ? b + share : stop;
-    const uint8_t *frags[TM];
-    const uint32_t *powers[TM];
+    const uint8_t *frags = digits + col * steps * kStepBytes + lane * 16;
+    const uint32_t *powers = reinterpret_cast<const uint32_t *>(digits + f.col_tiles * steps * kStepBytes) + col * steps * 64 + lane;
     const u32x2 *bits[NT];
     const uint16_t *scales[NT];
-#pragma unroll
-    for (int m = 0; m < TM; m++) {
-        const int64_t tile = col0 + m < f.col_tiles ? col0 + m : f.col_tiles - 1;
-        frags[m] = digits + tile * steps * kStepBytes + lane * 16;
-        powers[m] = reinterpret_cast<const uint32_t *>(digits + f.col_tiles * steps * kStepBytes) + tile * steps * 64 + lane;
-    }
 #pragma unroll
     for (int i = 0; i < NT; i++) {
         const Weight &w = i / TN ? w1 : w0;
@@ -882,17 +869,15 @@ __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight 
         scales[i] = w.scales + rt / 2 * nb8 * 512 + in64 * 8;
     }
     const Signs signs(g);
-    f32x16 acc[TM][NT];
+    f32x16 acc[NT];
 #pragma unroll
-    for (int m = 0; m < TM; m++)
-#pragma unroll
-        for (int i = 0; i < NT; i++) acc[m][i] = f32x16{};
+    for (int i = 0; i < NT; i++) acc[i] = f32x16{};
     struct Loads {
         u32x2 bits[NT];
         uint16_t scales[NT];
-        uint32_t powers[2][TM];
-        u32x4 lo[TM][2][4];
-        u32x2 hi[TM][2][4];
+        uint32_t powers[2];
+        u32x4 lo[2][4];
+        u32x2 hi[2][4];
     };
     const auto load = [&](int64_t i) {
         Loads l;
@@ -902,35 +887,29 @@ __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight 
             l.scales[k] = scales[k][i / 8 * 512 + i % 8];
         }
 #pragma unroll
-        for (int m = 0; m < TM; m++)
+        for (int s = 0; s < 2; s++) {
+            l.powers[s] = powers[(2 * i + s) * 64];
 #pragma unroll
-            for (int s = 0; s < 2; s++) {
-                l.powers[s][m] = powers[m][(2 * i + s) * 64];
-#pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    const uint8_t *src = frags[m] + (2 * i + s) * kStepBytes + 1536 * p;
-                    l.lo[m][s][p] = *reinterpret_cast<const u32x4 *>(src);
-                    l.hi[m][s][p] = *reinterpret_cast<const u32x2 *>(src + 1024 - lane * 8);
-                }
+            for (int p = 0; p < 4; p++) {
+                const uint8_t *src = frags + (2 * i + s) * kStepBytes + 1536 * p;
+                l.lo[s][p] = *reinterpret_cast<const u32x4 *>(src);
+                l.hi[s][p] = *reinterpret_cast<const u32x2 *>(src + 1024 - lane * 8);
             }
+        }
         return l;
     };
     if (b < end) {
         Loads l = load(b);
         for (; b < end; b++) {
             const Loads ahead = load(b + 1 < end ? b + 1 : b);
-            f32x16 t[TM][NT];
+            f32x16 t[NT];
 #pragma unroll
-            for (int m = 0; m < TM; m++)
-#pragma unroll
-                for (int i = 0; i < NT; i++) t[m][i] = f32x16{};
+            for (int i = 0; i < NT; i++) t[i] = f32x16{};
 #pragma unroll
             for (int s = 0; s < 2; s++) {
-                i32x8 a[TM][4], x[NT];
+                i32x8 a[4], x[NT];
 #pragma unroll
-                for (int m = 0; m < TM; m++)
-#pragma unroll
-                    for (int p = 0; p < 4; p++) a[m][p] = frag(l.lo[m][s][p], l.hi[m][s][p]);
+                for (int p = 0; p < 4; p++) a[p] = frag(l.lo[s][p], l.hi[s][p]);
 #pragma unroll
                 for (int i = 0; i < NT; i++) {
                     const auto h = __builtin_amdgcn_permlane32_swap(l.bits[i][s], l.bits[i][s], false, false);
@@ -943,24 +922,23 @@ __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight 
         }
     }
 #pragma unroll
-    for (int m = 0; m < TM; m++)
-#pragma unroll
-        for (int i = 0; i < NT; i++) put_tile(acc[m][i], sums + (wave * TM * NT + m * NT + i) * kTile, g, n32);
+    for (int i = 0; i < NT; i++) put_tile(acc[i], sums + (wave * NT + i) * kTile, g, n32);
     __syncthreads();
     const int from = lane / 8 * kPitch + lane % 8 * 4;
-    for (int j = wave; j < TM * TN * 4; j += KS) {   // eight columns of a tile at a time
-        const int q = j % 4, i = j / 4 % TN, m = j / 4 / TN;
+    for (int j = wave; j < TN * 4; j += KS) {   // eight columns of a tile at a time
+        const int q = j % 4, i = j / 4;
         f32x4 v[2] = {};
 #pragma unroll
         for (int k = 0; k < KS; k++)
 #pragma unroll
-            for (int s = 0; s < S; s++)
-                v[s] += *reinterpret_cast<const f32x4 *>(sums + (k * TM * NT + m * NT + s * TN + i) * kTile + from + q * 8 * kPitch);
-        emit<S>(w0, w1, e, f, slice, v[0], v[1], (col0 + m) * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
+            for (int s = 0; s < S; s++) v[s] += *reinterpret_cast<const f32x4 *>(sums + (k * NT + s * TN + i) * kTile + from + q * 8 * kPitch);
+        emit<S>(w0, w1, e, f, slice, v[0], v[1], col * 32 + 8 * q + lane / 8, (row0 + i) * 32 + lane % 8 * 4);
     }
 }
 
 constexpr int64_t kMaxK = INT64_C(1) << 20, kMaxColumns = INT64_C(1) << 20;
+// so that a launch's threads stay below 2^32
+constexpr int64_t kMaxRows = INT64_C(1) << 26, kMaxOutputs = INT64_C(1) << 36;
 constexpr int64_t kFewColumns = 4;   // so many columns take no workspace
 
 int check_sizes(const char *name, int64_t K, int64_t n_act) {
@@ -990,7 +968,7 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
     if (st) return st;
     GD_REQUIRE(!e.y_q8 || e.rows % 32 == 0, GD_ESHAPE, "%s: rows (%lld) must be a multiple of 32 for q8_0 blocks", name,
                (long long)e.rows);
-    GD_REQUIRE(e.rows <= (INT64_C(1) << 31) - 64, GD_ERANGE, "%s: rows too large", name);
+    GD_REQUIRE(e.rows <= kMaxRows && e.rows * e.n <= kMaxOutputs, GD_ERANGE, "%s: rows or n_act too large", name);
     const int64_t size = dtype_size(dtype);
     for (int i = 0; i < count; i++)
         GD_REQUIRE(aligned(w[i].bits, 16) && aligned(w[i].scales, 16) && aligned(w[i].bias, 4), GD_EALIGN,
@@ -998,7 +976,7 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
     GD_REQUIRE(aligned(a_q8, 2) && aligned(e.y_q8, 2) && aligned(e.residual, size) && aligned(e.y, size) &&
                    aligned(workspace, 16),
                GD_EALIGN, "%s: a_q8 and y_q8 must be 2-byte aligned, residual and y to their element, workspace 16", name);
-    const int64_t need = workspace_need(K, e.n), bytes = e.n * e.rows * size;   // below 2^53
+    const int64_t need = workspace_need(K, e.n), bytes = e.n * e.rows * size;   // below 2^39
     GD_REQUIRE(need == 0 || workspace, GD_EINVAL, "%s: null workspace", name);
     GD_REQUIRE(static_cast<uint64_t>(need) <= workspace_bytes || need == 0, GD_ERANGE, "%s: workspace of %zu bytes, %lld are needed",
                name, workspace_bytes, (long long)need);
@@ -1056,7 +1034,7 @@ void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epi
 template <int S>
 void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, uint8_t *workspace,
               hipStream_t hs) {
-    ManyShape f = {K / 128, (e.n + 31) / 32, (e.rows + 31) / 32, 0, 0, 1, K / 128, reinterpret_cast<float *>(workspace + digits_bytes(K, e.n))};
+    ManyShape f = {K / 128, (e.n + 31) / 32, (e.rows + 31) / 32, 0, 1, K / 128, reinterpret_cast<float *>(workspace + digits_bytes(K, e.n))};
     const auto cut = [](int64_t steps, int64_t by) { return static_cast<uint32_t>((steps + by - 1) / by); };
     if (f.col_tiles * f.nb < 1024)
         hipLaunchKernelGGL((q1_digits_kernel<true>), dim3(cut(2 * f.nb, 2), static_cast<uint32_t>(f.col_tiles)), dim3(256), 0, hs, a_q8,
@@ -1064,10 +1042,9 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
     else
         hipLaunchKernelGGL((q1_digits_kernel<false>), dim3(cut(2 * f.nb, 4), static_cast<uint32_t>(f.col_tiles)), dim3(256), 0, hs, a_q8,
                            workspace, e.n, 2 * f.nb);
-    const auto groups = [&](int64_t col, int64_t row) {   // of so many tiles
-        f.col_groups = (f.col_tiles + col - 1) / col;
-        f.row_groups = (f.row_tiles + row - 1) / row;
-        return f.col_groups * f.row_groups;
+    const auto groups = [&](int64_t tiles) {   // of so many tiles of rows
+        f.row_groups = (f.row_tiles + tiles - 1) / tiles;
+        return f.col_tiles * f.row_groups;
     };
     // Slices of K, of `least` blocks at least, until there are `want` workgroups or no room for their sums.
     const auto slice = [&](int64_t have, int64_t want, int64_t least) {
@@ -1081,18 +1058,18 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
         return dim3(static_cast<uint32_t>((have * f.slices + 7) / 8 * 8));
     };
     constexpr int TN = 4 / S;
-    const int64_t wide = groups(1, 4 * TN);
+    const int64_t wide = groups(4 * TN);
     if (wide * f.nb >= kWideFrom) {
         const dim3 grid = slice(wide, 512 + wide - 1, 8);
         hipLaunchKernelGGL((q1_wide_kernel<TN, S>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
     } else {
-        const int64_t have = groups(1, 2 / S);
+        const int64_t have = groups(2 / S);
         if (have >= kManyGroups) {
             const dim3 grid = slice(have, 1, 8);
-            hipLaunchKernelGGL((q1_split_kernel<1, 2 / S, S, 4>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
+            hipLaunchKernelGGL((q1_split_kernel<2 / S, S, 4>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
         } else {
             const dim3 grid = slice(have, 256, 8);
-            hipLaunchKernelGGL((q1_split_kernel<1, 2 / S, S, 8>), grid, dim3(512), 0, hs, w0, w1, workspace, e, f);
+            hipLaunchKernelGGL((q1_split_kernel<2 / S, S, 8>), grid, dim3(512), 0, hs, w0, w1, workspace, e, f);
         }
     }
     if (f.slices > 1)

@@ -546,9 +546,9 @@ int ternary_dequantize_act(const uint32_t *planes, const float *x_scale, void *y
  *   workspace  device, q1_q8_linear_workspace_bytes(K, n_act) bytes, 16-byte
  *              aligned (NULL where that is 0); calls that share it must be
  *              ordered.
- * bias, residual and y are aligned to their element. Limits: rows <= 2^31 - 64,
- * n_act <= 2^20, K <= 2^20. Errors: GD_EINVAL, GD_ESHAPE (K % 128, rows % 32),
- * GD_EALIGN, GD_ERANGE (limits, workspace too small), GD_EHIP. */
+ * bias, residual and y are aligned to their element. Limits: rows <= 2^26,
+ * n_act <= 2^20, rows * n_act <= 2^36, K <= 2^20. Errors: GD_EINVAL, GD_ESHAPE
+ * (K % 128, rows % 32), GD_EALIGN, GD_ERANGE (limits, workspace too small), GD_EHIP. */
 int q1_q8_linear(const void *bits_plane, const void *scale_plane, const void *a_q8, const float *bias,
                  int32_t act, const void *residual, void *y, void *y_q8, int64_t rows, int64_t K,
                  int64_t n_act, int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);

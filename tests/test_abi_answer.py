@@ -37,6 +37,7 @@ def test_linear_refusals(gd):
         assert call(q=2 * FAR + 1) == ALIGN
         assert call(rows=(1 << 31) - 32) == RANGE and call(K=1 << 21) == RANGE and call(n=(1 << 20) + 1) == RANGE
         assert call(n=5) == INVAL and call(n=5, ws=FAKE, wb=100 * 256 + 5 * (1 << 19) - 1) == RANGE and call(n=5, ws=FAKE + 8, wb=1 << 24) == ALIGN
+        assert call(rows=(1 << 26) + 32) == RANGE and call(rows=1 << 26, n=1025, ws=FAKE, wb=1 << 30) == RANGE
         assert call(rows=BIG) == RANGE and call(n=BIG) == RANGE and call(K=BIG) == RANGE
         assert call(y=FAKE) == INVAL and call(q=FAKE) == INVAL and call(q=FAR) == INVAL   # on top of what is read or written
     assert linear(res=FAKE + 2) == ALIGN
