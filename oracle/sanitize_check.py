@@ -67,7 +67,8 @@ def main() -> int:
             return 2
         env = dict(base, LD_PRELOAD=clang_rt[-1])
         rc = _run([sys.executable, "-m", "pytest", "-q", "-m", "not gpu", "-p", "no:cacheprovider",
-                   os.path.join(tmp, "tests", "test_abi.py"), os.path.join(tmp, "tests", "test_abi_layer.py")], env, tmp)
+                   *(os.path.join(tmp, "tests", name) for name in ("test_abi.py", "test_abi_layer.py", "test_abi_answer.py"))],
+                  env, tmp)
     return rc
 
 
