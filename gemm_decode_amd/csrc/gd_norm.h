@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "gd_quant.h"
 #include "gd_types.h"
@@ -106,14 +107,37 @@ __device__ __forceinline__ double rsqrt_f64(double x) {
     return y;
 }
 
+// v by an operation over a wave, in all its lanes, without LDS: with the lanes 32, 16, 8, 4, 2
+// and 1 away in turn (8 and 4 by rotations of 16 lanes, which meet the same value there).
+template <typename F>
+__device__ __forceinline__ double over_wave(double v, F f) {
+    typedef uint32_t Words __attribute__((ext_vector_type(2)));
+    const auto joined = [](uint32_t lo, uint32_t hi) { return __builtin_bit_cast(double, Words{lo, hi}); };
+    Words w = __builtin_bit_cast(Words, v);
+    auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[0], false, false), hi = __builtin_amdgcn_permlane32_swap(w[1], w[1], false, false);
+    v = f(joined(lo[0], hi[0]), joined(lo[1], hi[1]));
+    w = __builtin_bit_cast(Words, v);
+    lo = __builtin_amdgcn_permlane16_swap(w[0], w[0], false, false);
+    hi = __builtin_amdgcn_permlane16_swap(w[1], w[1], false, false);
+    v = f(joined(lo[0], hi[0]), joined(lo[1], hi[1]));
+    const auto with = [&](auto ctrl) {
+        const Words u = __builtin_bit_cast(Words, v);
+        constexpr int kCtrl = decltype(ctrl)::value;
+        v = f(v, joined(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u[0]), kCtrl, 0xF, 0xF, false)),
+                        static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u[1]), kCtrl, 0xF, 0xF, false))));
+    };
+    with(std::integral_constant<int, 0x128>{});   // row_ror:8
+    with(std::integral_constant<int, 0x124>{});   // row_ror:4
+    with(std::integral_constant<int, 0x4E>{});    // quad_perm [2,3,0,1]
+    with(std::integral_constant<int, 0xB1>{});    // quad_perm [1,0,3,2]
+    return v;
+}
+
 // Sum (and max) over a row's waves; every thread gets them.
 template <int kWaves, bool kMax>
 __device__ __forceinline__ void group_sum_max(double &sum, double &mx, double (*red)[2]) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-        sum += __shfl_xor(sum, o);
-        if (kMax) mx = fmax(mx, __shfl_xor(mx, o));
-    }
+    sum = over_wave(sum, [](double a, double b) { return a + b; });
+    if (kMax) mx = over_wave(mx, [](double a, double b) { return fmax(a, b); });
     if (kWaves == 1) return;
     if (threadIdx.x % 64 == 0) {
         red[threadIdx.x / 64][0] = sum;

@@ -27,19 +27,18 @@ struct Sandwich {
     float *x_scale;
     int64_t n, K, n_gates;
     double residual_scale, block_scale;
+    double per;   // 1 / K
     float eps;
 };
 
-// Four elements of h: r1 is the block's factor (1 without a norm behind it).
+// Four elements of h: factor is the block's scale and, with a norm behind it, its rstd.
 template <typename T>
-__device__ __forceinline__ f32x4 join4(const Sandwich<T> &s, f32x4 x, f32x4 res, f32x4 post, f32x4 gate, double r1,
-                                       double block_scale) {
+__device__ __forceinline__ f32x4 join4(const Sandwich<T> &s, f32x4 x, f32x4 res, f32x4 post, f32x4 gate, double factor) {
     f32x4 h;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        double u = static_cast<double>(x[j]) * r1 * static_cast<double>(post[j]) * static_cast<double>(gate[j]);
-        u = __builtin_fma(block_scale, u, s.residual_scale * static_cast<double>(res[j]));
-        h[j] = static_cast<float>(static_cast<T>(static_cast<float>(u)));
+        const double u = static_cast<double>(x[j]) * factor * static_cast<double>(post[j]);
+        h[j] = static_cast<float>(static_cast<T>(static_cast<float>(__builtin_fma(u, static_cast<double>(gate[j]), s.residual_scale * static_cast<double>(res[j])))));
     }
     return h;
 }
@@ -58,12 +57,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
     const int nq = static_cast<int>(s.K / 4);
     const T *x = s.x + row * s.K, *res = s.residual + row * s.K;
     T *h_out = s.h_out ? s.h_out + row * s.K : nullptr;
-    double block_scale = s.block_scale;
+    double factor = s.block_scale;
     const T *gate = s.gate;
     if (gate) {
         int64_t g = s.gate_index ? s.gate_index[row] : s.n_gates == 1 ? 0 : row;
         if (g < 0 || g >= s.n_gates) {
-            block_scale = 0.0;
+            factor = 0.0;
             g = 0;
         }
         gate += g * s.K;
@@ -86,7 +85,6 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
         load_side(at, post + i, gates + i);
         load_groups<2, float>(s.weight, nullptr, at, w + i);
     }
-    double r1 = 1.0;
     if (s.post_weight) {
 #pragma unroll
         for (int i = 0; i < R; i++)
@@ -97,7 +95,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
             ss += square4(v[0]) + square4(v[1]);
         }
         group_sum_max<W, false>(ss, amax, red[0]);
-        r1 = rsqrt_f64(ss / static_cast<double>(s.K) + static_cast<double>(s.eps));
+        factor *= rsqrt_f64(__builtin_fma(ss, s.per, static_cast<double>(s.eps)));
         ss = 0.0;
     }
     float top = 0.0f;
@@ -107,7 +105,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
         if (e4 >= nq) continue;
 #pragma unroll
         for (int j = i; j < i + 2; j++) {
-            h[j] = join4(s, h[j], r[j], post[j], gates[j], r1, block_scale);
+            h[j] = join4(s, h[j], r[j], post[j], gates[j], factor);
             ss += square4(h[j]);
             if (kTernary) top = fmaxf(top, Products(h[j], w[j]).absmax());
         }
@@ -126,7 +124,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
         load_groups<2, T>(res, nullptr, e4, rr);
         load_side(e4, pp, gg);
 #pragma unroll
-        for (int j = 0; j < 2; j++) v[j] = join4(s, v[j], rr[j], pp[j], gg[j], r1, block_scale);
+        for (int j = 0; j < 2; j++) v[j] = join4(s, v[j], rr[j], pp[j], gg[j], factor);
     };
     for (int e4 = R * kT + 2 * tid; e4 < nq; e4 += 2 * kT) {
         f32x4 v[2];
@@ -139,7 +137,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
         }
     }
     group_sum_max<W, kTernary>(ss, amax, red[1]);
-    const double rstd127 = rsqrt_f64(ss / static_cast<double>(s.K) + static_cast<double>(s.eps)) * (1.0 / 127.0);
+    const double rstd127 = rsqrt_f64(__builtin_fma(ss, s.per, static_cast<double>(s.eps))) * (1.0 / 127.0);
     const float r32 = static_cast<float>(rstd127);
     const float row_top = static_cast<float>(amax), row_inv = row_top > 0.0f ? recip127(row_top) : 0.0f;
     if (kTernary && tid == 0) s.x_scale[row] = amax > 0.0 ? static_cast<float>(amax * rstd127) : 0.0f;
@@ -227,19 +225,25 @@ void launch(const Args &a, hipStream_t hs) {
         using T = decltype(t);
         const Sandwich<T> s = {static_cast<const T *>(a.x), a.post_weight, static_cast<const T *>(a.gate), a.gate_index,
                                static_cast<const T *>(a.residual), a.weight, static_cast<T *>(a.h_out), a.out, a.x_scale,
-                               a.n, a.K, a.n_gates, a.residual_scale, a.block_scale, a.eps};
+                               a.n, a.K, a.n_gates, a.residual_scale, a.block_scale, 1.0 / static_cast<double>(a.K),
+                               a.eps};
         const auto go = [&](auto r, auto w) {
             constexpr int W = decltype(w)::value;
             const dim3 grid(static_cast<uint32_t>(W == 1 ? (a.n + 3) / 4 : a.n));
             hipLaunchKernelGGL((rmsnorm_sandwich_kernel<T, decltype(r)::value, W, kTernary>), grid,
                                dim3(W == 1 ? 256 : 64 * W), 0, hs, s);
         };
-        // The split of the norm without the first half.
+        // As the norm without the first half: a wave per row where many rows are short; eight waves
+        // a row for few rows, whose latency counts (one row of 4096 f32 5.3 us with its reader,
+        // with four waves 5.7); of many rows four, half the sums over waves (4099 rows of 4096 bf16
+        // 51.9 us with their reader, with eight waves 53.8, with two 57).
         const bool many = a.n >= 1024;
         if (a.K <= 512 && many)
             go(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
         else if (a.K <= 1024 && many)
             go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+        else if (a.K <= 4096 && many)
+            go(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
         else if (a.K <= 4096)
             go(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
         else

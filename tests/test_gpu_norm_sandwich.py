@@ -67,7 +67,7 @@ def check(form, got, h, w, T, want):
 
 
 # One wave a row and eight, rows that fill the registers and rows past them.
-@pytest.mark.parametrize("n,K", [(1, 32), (3, 96), (2, 4096), (5, 2560), (2, 4128), (3, 8192), (2, 8224), (1, 20000),
+@pytest.mark.parametrize("n,K", [(1, 32), (3, 96), (2, 4096), (5, 2560), (2, 4128), (3, 8192), (2, 8224), (1, 20000), (1030, 4096), (1024, 2560),
                                  (1025, 512), (1030, 992), (1024, 1056)])
 @pytest.mark.parametrize("form", ["q8_0", "ternary"])
 @pytest.mark.parametrize("T", TYPES)
