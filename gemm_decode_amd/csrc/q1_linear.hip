@@ -294,11 +294,14 @@ __device__ __forceinline__ i32x8 frag(u32x4 lo, u32x2 hi) {
 // as a few memory latencies, and this hides the digits behind one.
 constexpr int kFew = 512;
 template <int C>
-constexpr int kBlocks = C == 4 ? 64 : 128;
+constexpr int kBlocks = C < 4 ? 128 : 256 / C;
 
 struct FewShape {
     int64_t nb;   // blocks of a row
     int kw, kw_log;   // waves along K: 1, 2, 4 or 8
+    int slices, share;   // of K, and the blocks of one
+    int64_t row_tiles;   // tiles of 32 rows
+    float *parts;        // sums of the slices, [slices][S][n][32 row_tiles]
 };
 
 // Half of a sub-block, its places 16 part .. 16 part + 15, as the three words each of l and h.
@@ -325,14 +328,21 @@ __device__ __forceinline__ void code_digits(const uint32_t d[8], int part, uint3
     words(rh, h);
 }
 
+// Sums of a's two halves in the lower half of a wave and of b's in the upper one, and likewise
+// of neighbouring 16-lane rows: a's in even rows, b's in odd ones.
+__device__ __forceinline__ float halves(float a, float b) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    return __builtin_bit_cast(float, static_cast<uint32_t>(p[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(p[1]));
+}
+__device__ __forceinline__ float rows16(float a, float b) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    return __builtin_bit_cast(float, static_cast<uint32_t>(p[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(p[1]));
+}
+
 // Sum over the four 16-lane rows of a wave, in all of them.
 __device__ __forceinline__ float sum_rows(float v) {
-    const uint32_t a = __builtin_bit_cast(uint32_t, v);
-    const auto p = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-    const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, static_cast<uint32_t>(p[0])) +
-                                                        __builtin_bit_cast(float, static_cast<uint32_t>(p[1])));
-    const auto q = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-    return __builtin_bit_cast(float, static_cast<uint32_t>(q[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(q[1]));
+    v = halves(v, v);
+    return rows16(v, v);
 }
 
 template <int C, int S, int TILES, int Q>
@@ -340,36 +350,45 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
                                                          FewShape f) {
     constexpr int N = TILES * S;   // a wave's tiles of both weights
     constexpr int kRow = 6;        // words of a row of digits
-    constexpr int kHalves = kBlocks<C> * 8 / kFew;   // half sub-blocks of a chunk's column and thread
-    __shared__ __attribute__((aligned(16))) uint32_t digits[kBlocks<C> * 4 * C * 2 * kRow + 8];   // and a row of zeros
+    constexpr int kShare = C < 4 ? 2 : 1;                                         // threads to a sub-block
+    constexpr int kPer = kBlocks<C> * 4 * kShare, kItems = C * kPer / kFew;        // threads' items in a chunk's column, a thread's
+    constexpr int kColumn = kBlocks<C> * 4 * 2 * kRow + 32, kZeros = C * kColumn;   // words of a column's digits, of all
+    constexpr int M = (C + 3) / 4, kWords = kZeros + 8, kSums = 8 * N * 64 * M;
+    constexpr bool kShared = C > 4;   // the sums where the digits were
+    __shared__ __attribute__((aligned(16))) uint32_t digits[kShared && kSums > kWords ? kSums : kWords];   // and a row of zeros
     __shared__ __attribute__((aligned(16))) float d1[kBlocks<C> * 4 * C];
-    __shared__ __attribute__((aligned(16))) float red[8 * N * 64];
+    __shared__ __attribute__((aligned(16))) float own[kShared ? 4 : kSums];
+    float *red = kShared ? reinterpret_cast<float *>(digits) : own;
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int g = lane / 16, n16 = lane % 16, n = static_cast<int>(e.n), nb = static_cast<int>(f.nb), nb8 = (nb + 7) / 8;
     const int kpart = wave & (f.kw - 1), ipart = wave >> f.kw_log, groups_log = 3 - f.kw_log;
     const int tw = TILES << groups_log;   // the workgroup's tiles
-    const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * tw;
+    const uint32_t group = C > 4 ? blockIdx.x / static_cast<uint32_t>(f.slices) : blockIdx.x;
+    const int slice = C > 4 ? static_cast<int>(blockIdx.x - group * static_cast<uint32_t>(f.slices)) : 0;
+    const int first = C > 4 ? slice * f.share : 0, stop = C > 4 && first + f.share < nb ? first + f.share : nb;
+    const int64_t tile0 = static_cast<int64_t>(group) * tw;
+    // Where a column's digits start: so that the 16 rows that an instruction reads, four columns of
+    // four neighbouring sub-blocks (12 words apart), lie in banks of their own.
+    const auto column_at = [](int c) { return c * kColumn + (c & 1) * 2 + (c & 2) * 8; };
     float acc[N][C];
 #pragma unroll
     for (int i = 0; i < N; i++)
 #pragma unroll
         for (int c = 0; c < C; c++) acc[i][c] = 0.0f;
     Outer outer;
-    for (int b0 = 0; b0 < nb; b0 += kBlocks<C>) {
-        const int blocks = nb - b0 < kBlocks<C> ? nb - b0 : kBlocks<C>;
+    for (int b0 = first; b0 < stop; b0 += kBlocks<C>) {
+        const int blocks = stop - b0 < kBlocks<C> ? stop - b0 : kBlocks<C>;
         // The codes first (without a branch around the loads: behind one, the compiler waits for
         // all that is on its way),
-        uint32_t d[C][kHalves][8], scale[C][kHalves];
+        uint32_t d[kItems][8], scale[kItems];
+        const auto column_of = [&](int k) { return kPer < kFew ? tid / kPer + k * (kFew / kPer) : k * kFew / kPer; };
+        const auto item_of = [&](int k) { return kPer < kFew ? tid % kPer : tid + k * kFew % kPer; };
 #pragma unroll
-        for (int c = 0; c < C; c++) {
-            const uint16_t *column = a_q8 + (static_cast<int64_t>(c < n ? c : 0) * nb + b0) * 68;
-#pragma unroll
-            for (int k = 0; k < kHalves; k++) {
-                const int i = tid + k * kFew < blocks * 8 ? tid + k * kFew : blocks * 8 - 1;
-                scale[c][k] = load_block(column + i / 2 * 17, d[c][k]);
-            }
+        for (int k = 0; k < kItems; k++) {
+            const int c = column_of(k), i = item_of(k) < blocks * 4 * kShare ? item_of(k) : blocks * 4 * kShare - 1;
+            scale[k] = load_block(a_q8 + (static_cast<int64_t>(c < n ? c : 0) * nb + b0) * 68 + i / kShare * 17, d[k]);
         }
-        if (b0 == 0) {   // then what the thread's sum meets,
+        if (C <= 4 && b0 == 0) {   // then what the thread's sum meets,
             const int i = tid < n * 16 * tw ? tid : 0, c = i / (16 * tw);
             const int64_t r = tile0 * 16 + (i - c * 16 * tw);
             outer = load_outer<S>(w0, w1, e, c, r, r < e.rows);
@@ -399,38 +418,46 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (b0) __syncthreads();
-        if (tid < 8) digits[kBlocks<C> * 4 * C * 2 * kRow + tid] = 0;
+        if (b0 != first) __syncthreads();
+        if (tid < 8) digits[kZeros + tid] = 0;
 #pragma unroll
-        for (int c = 0; c < C; c++)
+        for (int k = 0; k < kItems; k++) {
+            const int c = column_of(k), i = item_of(k);
+            const float v = f16_value(static_cast<uint16_t>(scale[k]));
 #pragma unroll
-            for (int k = 0; k < kHalves; k++) {
-                const int i = tid + k * kFew;
+            for (int part = 0; part < 2; part += kShare) {
+                const int mine = kShare == 2 ? i & 1 : part;
                 uint32_t l[3], h[3];
-                code_digits(d[c][k], i & 1, l, h);
-                const float v = f16_value(static_cast<uint16_t>(scale[c][k]));
-                if (i < blocks * 8 && c < n) {
-                    uint32_t *o = digits + (i / 2 * C + c) * 2 * kRow + (i & 1) * 3;
+                code_digits(d[k], mine, l, h);
+                if (i < blocks * 4 * kShare && c < n) {
+                    uint32_t *o = digits + column_at(c) + i / kShare * 2 * kRow + mine * 3;
 #pragma unroll
                     for (int j = 0; j < 3; j++) {
                         o[j] = l[j];
                         o[kRow + j] = h[j];
                     }
-                    if ((i & 1) == 0) d1[i / 2 * C + c] = fabsf(v) <= 65504.0f ? v : __builtin_nanf("");
+                    if (mine == 0) d1[i / kShare * C + c] = fabsf(v) <= 65504.0f ? v : __builtin_nanf("");
                 }
             }
+        }
         __syncthreads();
-        // The lane's row of an instruction: of columns 2 m and 2 m + 1, digit n16 % 2 of column
-        // 2 m + n16 / 2 % 2, where n16 / 4 is its sub-block.
         const Signs signs(g & 1);
-        const int power = n16 % 2 ? 134 : 130;   // 2^7 and 2^3: e2m3 codes are eighths
-        int row[(C + 1) / 2], stride[(C + 1) / 2];
+        const auto frag_at = [&](int at) {
+            const u32x2 *dig = reinterpret_cast<const u32x2 *>(digits + at);
+            const u32x2 f0 = dig[0], f1 = dig[1], f2 = dig[2];
+            return frag(u32x4{f0[0], f0[1], f1[0], f1[1]}, f2);
+        };
+        const auto multiply = [&](i32x8 a, i32x8 w, f32x4 t, int power) {
+            return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, w, t, kFp6, kFp4, 0, power, 0, kOne);
+        };
+        // The lane's row of an instruction, where n16 / 4 is its sub-block: up to two columns,
+        // digit n16 % 2 of column n16 / 2 % 2; more, both digits in turn of column 4 m + n16 % 4.
+        constexpr int kL = 130, kH = 134;   // 2^3 and 2^7: e2m3 codes are eighths
+        int row[M];
 #pragma unroll
-        for (int m = 0; m < (C + 1) / 2; m++) {
-            const int c = 2 * m + n16 / 2 % 2;
-            const bool mine = n16 / 4 == g && c < n;
-            row[m] = mine ? ((g * C + c) * 2 + n16 % 2) * kRow : kBlocks<C> * 4 * C * 2 * kRow;
-            stride[m] = mine ? 4 * C * 2 * kRow : 0;
+        for (int m = 0; m < M; m++) {
+            const int c = C > 2 ? 4 * m + n16 % 4 : n16 / 2 % 2;
+            row[m] = n16 / 4 == g && c < n ? column_at(c) + (g * 2 + (C > 2 ? 0 : n16 % 2)) * kRow : -1;
         }
 #pragma unroll
         for (int q = 0; q < Q; q++) {
@@ -447,55 +474,84 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
                         x[1][i] = two[1];
                     }
                 }
-                i32x8 a[(C + 1) / 2];
-                float s1[C];
-#pragma unroll
-                for (int m = 0; m < (C + 1) / 2; m++) {
-                    const u32x2 *dig = reinterpret_cast<const u32x2 *>(digits + row[m] + (i0 + k) * stride[m]);
-                    const u32x2 f0 = dig[0], f1 = dig[1], f2 = dig[2];
-                    a[m] = frag(u32x4{f0[0], f0[1], f1[0], f1[1]}, f2);
-                }
-#pragma unroll
-                for (int c = 0; c < C; c++) s1[c] = d1[((i0 + k) * 4 + g) * C + c];
-#pragma unroll
-                for (int i = 0; i < N; i++) {
+                const auto at = [&](int m) { return row[m] >= 0 ? row[m] + (i0 + k) * (4 * 2 * kRow) : kZeros; };
+                const float *s1 = d1 + ((i0 + k) * 4 + g) * C;
+                const auto sign_of = [&](int i) {
                     const auto h = __builtin_amdgcn_permlane16_swap(x[k % 2][i], x[k % 2][i], false, false);
-                    const i32x8 w = signs(h[0], h[1]);
-                    const float d = f16_value(static_cast<uint16_t>(d0[q][i][k / 2] >> (16 * (k & 1))));
+                    return signs(h[0], h[1]);
+                };
+                const auto scale_of = [&](int i) { return f16_value(static_cast<uint16_t>(d0[q][i][k / 2] >> (16 * (k & 1)))); };
+                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                if constexpr (C <= 2) {
+                    const i32x8 a = frag_at(at(0));
+                    float s[C];
 #pragma unroll
-                    for (int m = 0; m < (C + 1) / 2; m++) {
-                        const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[m], w, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp6, kFp4, 0,
-                                                                                         power, 0, kOne);
-                        acc[i][2 * m] = fmaf(d * s1[2 * m], t[0] + t[1], acc[i][2 * m]);
-                        if (2 * m + 1 < C) acc[i][(2 * m + 1) % C] = fmaf(d * s1[(2 * m + 1) % C], t[2] + t[3], acc[i][(2 * m + 1) % C]);
+                    for (int c = 0; c < C; c++) s[c] = s1[c];
+#pragma unroll
+                    for (int i = 0; i < N; i++) {
+                        const f32x4 t = multiply(a, sign_of(i), zero, n16 % 2 ? kH : kL);
+                        const float d0f = scale_of(i);
+#pragma unroll
+                        for (int c = 0; c < C; c++) acc[i][c] = fmaf(d0f * s[c], t[2 * c] + t[2 * c + 1], acc[i][c]);
+                    }
+                } else {
+                    i32x8 w[N];
+                    float d0f[N];
+#pragma unroll
+                    for (int i = 0; i < N; i++) {
+                        w[i] = sign_of(i);
+                        d0f[i] = scale_of(i);
+                    }
+#pragma unroll
+                    for (int m = 0; m < M; m++) {
+                        const i32x8 l = frag_at(at(m)), h = frag_at(row[m] >= 0 ? at(m) + kRow : kZeros);
+                        const f32x4 s = *reinterpret_cast<const f32x4 *>(s1 + 4 * m);
+                        f32x4 t[N];
+#pragma unroll
+                        for (int i = 0; i < N; i++) t[i] = multiply(h, w[i], zero, kH);
+#pragma unroll
+                        for (int i = 0; i < N; i++) t[i] = multiply(l, w[i], t[i], kL);
+#pragma unroll
+                        for (int i = 0; i < N; i++)
+#pragma unroll
+                            for (int c = 0; c < 4; c++) acc[i][4 * m + c] = fmaf(d0f[i] * s[c], t[i][c], acc[i][4 * m + c]);
                     }
                 }
             }
         }
     }
+    if (kShared) __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        float v = 0.0f;   // of the lane's column, g
+        float *to = red + ((kpart * S + i / TILES) * tw + ((i % TILES) << groups_log) + ipart) * 64 * M + lane;
 #pragma unroll
-        for (int c = 0; c < C; c++) {
-            const float s = sum_rows(acc[i][c]);
-            v = g == c ? s : v;
+        for (int m = 0; m < M; m++) {   // of the lane's column, 4 m + g
+            if constexpr (C == 1)
+                to[0] = sum_rows(acc[i][0]);
+            else if constexpr (C == 2)
+                to[0] = rows16(halves(acc[i][0], acc[i][0]), halves(acc[i][1], acc[i][1]));
+            else
+                to[64 * m] = rows16(halves(acc[i][4 * m], acc[i][4 * m + 2]), halves(acc[i][4 * m + 1], acc[i][4 * m + 3]));
         }
-        red[((kpart * S + i / TILES) * tw + ((i % TILES) << groups_log) + ipart) * 64 + lane] = v;
     }
     __syncthreads();
     for (int i = tid; i < n * 16 * tw; i += kFew) {   // 32 lanes together hold 32 rows where blocks are written (tw even)
         const int c = i / (16 * tw), rr = i - c * 16 * tw;
         const int64_t r = tile0 * 16 + rr;
         const bool live = r < e.rows;
-        if (i >= kFew) outer = load_outer<S>(w0, w1, e, c, r, live);
+        if (C > 4 || i >= kFew) outer = load_outer<S>(w0, w1, e, c, r, live && (C <= 4 || f.slices == 1));
         float v[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < 8; k++)
             if (k < f.kw)
 #pragma unroll
-                for (int s = 0; s < S; s++) v[s] += red[((k * S + s) * tw + rr / 16) * 64 + c * 16 + rr % 16];
-        finish_one<S>(e, outer, v[0], v[1], c, r, live);
+                for (int s = 0; s < S; s++) v[s] += red[((k * S + s) * tw + rr / 16) * 64 * M + c * 16 + rr % 16];
+        if (C <= 4 || f.slices == 1) {
+            finish_one<S>(e, outer, v[0], v[1], c, r, live);
+        } else if (r < 32 * f.row_tiles) {
+#pragma unroll
+            for (int s = 0; s < S; s++) f.parts[((static_cast<int64_t>(slice) * S + s) * n + c) * 32 * f.row_tiles + r] = v[s];
+        }
     }
 }
 
@@ -618,19 +674,30 @@ __device__ __forceinline__ void emit(const Weight &w0, const Weight &w1, const E
     }
 }
 
+// One value a thread; all that it needs is asked for at once: the call is a memory latency long.
 template <int S>
-__global__ __launch_bounds__(256) void q1_join_kernel(Weight w0, Weight w1, Epilogue e, ManyShape f) {
-    const int64_t quads = 8 * f.row_tiles, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;   // eight lanes to 32 rows
-    if (i >= e.n * quads) return;
-    const int64_t c = i / quads, r = i % quads * 4, next = S * e.n * 32 * f.row_tiles;
-    const float *from = f.parts + c * 32 * f.row_tiles + r;
-    f32x4 v[2] = {};
-#pragma unroll 4
-    for (int64_t s = 0; s < f.slices; s++, from += next) {
-        v[0] += *reinterpret_cast<const f32x4 *>(from);
-        if (S == 2) v[1] += *reinterpret_cast<const f32x4 *>(from + e.n * 32 * f.row_tiles);
+__global__ __launch_bounds__(256) void q1_join_kernel(Weight w0, Weight w1, Epilogue e, int slices, int64_t row_tiles,
+                                                      const float *__restrict__ parts) {
+    const int64_t padded = 32 * row_tiles, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;   // 32 lanes to 32 rows
+    if (i >= e.n * padded) return;
+    const int64_t c = i / padded, r = i % padded, next = S * e.n * padded;
+    const bool live = r < e.rows;
+    const Outer outer = load_outer<S>(w0, w1, e, c, r, live);
+    const float *from = parts + i;
+    float v[2] = {0.0f, 0.0f};
+    constexpr int kAtOnce = 8;
+    for (int s = 0; s < slices; s += kAtOnce) {
+        float p[kAtOnce][S];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++)
+#pragma unroll
+            for (int j = 0; j < S; j++) p[k][j] = from[(s + k < slices ? s + k : s) * next + j * e.n * padded];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++)
+#pragma unroll
+            for (int j = 0; j < S; j++) v[j] += s + k < slices ? p[k][j] : 0.0f;
     }
-    finish<S>(w0, w1, e, v[0], v[1], c, r);
+    finish_one<S>(e, outer, v[0], v[1], c, r, live);
 }
 
 // Loads of 16 (or 4) bytes a lane from base + `at` (per lane) to LDS, lane after lane from `to`
@@ -992,15 +1059,33 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
 }
 
 constexpr int64_t kWideFrom = 3500, kManyGroups = 384;
+// Up to so many workgroups of four tiles a wave the kernel without an operand pass is the faster
+// one: of 8 columns 14336 x 4096 9.6 us against 15.6, 49152 x 4096 (768 workgroups) 25.8 against
+// 28.4, gated (1536) 43.2 against 40.1; of 13 (a workgroup a CU, and twice the matrix
+// instructions a column) 28672 x 4096 (224) 20.3 against 25.4, 49152 x 4096 (384) 37.7 against 29.9.
+constexpr int64_t kCus = 256, kSomeGroups8 = 1024, kSomeGroups16 = kCus;
 
-template <int C, int S>
-void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, hipStream_t hs) {
-    FewShape f = {K / 128, 1, 0};
-    const int64_t chunk = f.nb < kBlocks<C> ? f.nb : kBlocks<C>, quads = (chunk + 3) / 4, tiles = (e.rows + 15) / 16;
+template <int S>
+void join(const Weight &w0, const Weight &w1, const Epilogue &e, int64_t slices, int64_t row_tiles, const float *parts, hipStream_t hs) {
+    hipLaunchKernelGGL((q1_join_kernel<S>), dim3(static_cast<uint32_t>((e.n * row_tiles * 32 + 255) / 256)), dim3(256), 0, hs, w0, w1, e,
+                       static_cast<int>(slices), row_tiles, parts);
+}
+
+// As many waves along K as a chunk has quads of blocks; the number of these.
+template <int C>
+int64_t waves_along_k(FewShape &f) {
+    const int64_t quads = ((f.nb < kBlocks<C> ? f.nb : kBlocks<C>) + 3) / 4;
     while (f.kw < 8 && f.kw < quads) {
         f.kw *= 2;
         f.kw_log++;
     }
+    return quads;
+}
+
+template <int C, int S>
+void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, hipStream_t hs) {
+    FewShape f = {K / 128, 1, 0, 1, static_cast<int>(K / 128), 0, nullptr};
+    const int64_t quads = waves_along_k<C>(f), tiles = (e.rows + 15) / 16;
     const auto go = [&](auto tiles_, auto q) {
         constexpr int TILES = decltype(tiles_)::value, Q = decltype(q)::value;
         const int64_t per = TILES * (8 / f.kw);
@@ -1029,6 +1114,40 @@ void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epi
         else
             go(One{}, Four{});
     }
+}
+
+// Up to 16 columns; false where the launches below for more of them are the faster ones.
+template <int C, int S>
+bool run_some(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epilogue &e, int64_t K, uint8_t *workspace,
+              hipStream_t hs) {
+    FewShape f = {K / 128, 1, 0, 1, static_cast<int>(K / 128), (e.rows + 31) / 32, reinterpret_cast<float *>(workspace)};
+    const int64_t chunks = (f.nb + kBlocks<C> - 1) / kBlocks<C>, tiles = (e.rows + 15) / 16;
+    waves_along_k<C>(f);
+    const auto groups_of = [&](int64_t t) { return (tiles + t * (8 / f.kw) - 1) / (t * (8 / f.kw)); };   // of t tiles a wave
+    if (groups_of(4 / S) > (C == 8 ? kSomeGroups8 : kSomeGroups16)) return false;
+    const auto go = [&](auto tiles_) {
+        constexpr int TILES = decltype(tiles_)::value;
+        const int64_t groups = groups_of(TILES), room = parts_bytes(e.n) / (S * e.n * f.row_tiles * 128);
+        int64_t z = kCus / groups;
+        z = z < chunks ? z : chunks;
+        z = z < room ? z : room;
+        if (z < 1) z = 1;
+        f.share = static_cast<int>((chunks + z - 1) / z * kBlocks<C>);
+        f.slices = static_cast<int>((f.nb + f.share - 1) / f.share);
+        hipLaunchKernelGGL((q1_few_kernel<C, S, TILES, 1>), dim3(static_cast<uint32_t>(groups * f.slices)), dim3(kFew), 0, hs, w0, w1, a_q8, e,
+                           f);
+    };
+    // As few tiles a wave as let all chunks of K side by side in workgroups of their own (4096 x
+    // 4096, 8 columns: one tile 7.1 us, two 7.6, four 9.2; 6144 x 4096: 9.4, 7.9, 9.3; 11000 x 4096:
+    // 13.3, 11.1, 9.6; 4096 x 14336, 13 columns: 23.2, 16.8, 15.5).
+    if (groups_of(1) * chunks <= kCus && !(e.y_q8 && f.kw == 8))   // (blocks of 32 rows need two tiles in a workgroup)
+        go(std::integral_constant<int, 1>{});
+    else if (S == 2 || groups_of(2) * chunks <= kCus)
+        go(std::integral_constant<int, 2>{});
+    else
+        go(std::integral_constant<int, 4 / S>{});
+    if (f.slices > 1) join<S>(w0, w1, e, f.slices, f.row_tiles, f.parts, hs);
+    return true;
 }
 
 template <int S>
@@ -1072,21 +1191,21 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
             hipLaunchKernelGGL((q1_split_kernel<2 / S, S, 8>), grid, dim3(512), 0, hs, w0, w1, workspace, e, f);
         }
     }
-    if (f.slices > 1)
-        hipLaunchKernelGGL((q1_join_kernel<S>), dim3(static_cast<uint32_t>((e.n * f.row_tiles * 8 + 255) / 256)), dim3(256), 0, hs, w0, w1, e, f);
+    if (f.slices > 1) join<S>(w0, w1, e, f.slices, f.row_tiles, f.parts, hs);
 }
 
 template <int S>
 void run(const Weight &w0, const Weight &w1, const void *a_q8, const Epilogue &e, int64_t K, void *workspace, hipStream_t hs) {
     const uint16_t *a = static_cast<const uint16_t *>(a_q8);
+    uint8_t *space = static_cast<uint8_t *>(workspace);
     if (e.n == 1)
         run_few<1, S>(w0, w1, a, e, K, hs);
     else if (e.n == 2)
         run_few<2, S>(w0, w1, a, e, K, hs);
     else if (e.n <= kFewColumns)
         run_few<4, S>(w0, w1, a, e, K, hs);
-    else
-        run_many<S>(w0, w1, a, e, K, static_cast<uint8_t *>(workspace), hs);
+    else if (!(e.n <= 8 && run_some<8, S>(w0, w1, a, e, K, space, hs)) && !(e.n > 8 && e.n <= 16 && run_some<16, S>(w0, w1, a, e, K, space, hs)))
+        run_many<S>(w0, w1, a, e, K, space, hs);
 }
 
 }  // namespace
