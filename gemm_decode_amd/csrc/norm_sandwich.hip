@@ -59,13 +59,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
     T *h_out = s.h_out ? s.h_out + row * s.K : nullptr;
     double factor = s.block_scale;
     const T *gate = s.gate;
+    bool dropped = false;   // nothing of the block is taken, whatever it holds
     if (gate) {
         int64_t g = s.gate_index ? s.gate_index[row] : s.n_gates == 1 ? 0 : row;
-        if (g < 0 || g >= s.n_gates) {
-            factor = 0.0;
-            g = 0;
-        }
-        gate += g * s.K;
+        dropped = g < 0 || g >= s.n_gates;
+        gate = dropped ? nullptr : gate + g * s.K;
+        if (dropped) factor = 0.0;
     }
     const auto group_of = [&](int i) { return i * kT + 2 * tid; };
     const f32x4 ones = {1.0f, 1.0f, 1.0f, 1.0f};
@@ -95,7 +94,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
             ss += square4(v[0]) + square4(v[1]);
         }
         group_sum_max<W, false>(ss, amax, red[0]);
-        factor *= rsqrt_f64(__builtin_fma(ss, s.per, static_cast<double>(s.eps)));
+        if (!dropped) factor *= rsqrt_f64(__builtin_fma(ss, s.per, static_cast<double>(s.eps)));
         ss = 0.0;
     }
     float top = 0.0f;
@@ -103,6 +102,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
     for (int i = 0; i < R; i += 2) {
         const int e4 = group_of(i);
         if (e4 >= nq) continue;
+        if (dropped) h[i] = h[i + 1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = i; j < i + 2; j++) {
             h[j] = join4(s, h[j], r[j], post[j], gates[j], factor);
@@ -123,6 +123,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
         load_groups<2, T>(x, nullptr, e4, v);
         load_groups<2, T>(res, nullptr, e4, rr);
         load_side(e4, pp, gg);
+        if (dropped) v[0] = v[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < 2; j++) v[j] = join4(s, v[j], rr[j], pp[j], gg[j], factor);
     };
@@ -207,8 +208,9 @@ int check(const char *name, const Args &a) {
     return GD_OK;
 }
 
-// After the other checks: h_out is x or residual, or apart from them, and from the gates.
-int check_in_place(const char *name, const Args &a) {
+// After the other checks: h_out is x or residual, or apart from them, and from the gates; the
+// 8-bit output (out_bytes) and its scales are apart from all of them.
+int check_in_place(const char *name, const Args &a, int64_t out_bytes) {
     const int64_t size = dtype_size(a.dtype), bytes = a.n * a.K * size;   // below 2^55
     GD_REQUIRE((a.h_out == a.x || !overlaps(a.x, bytes, bytes, 1, a.h_out, bytes)) &&
                    (a.h_out == a.residual || !overlaps(a.residual, bytes, bytes, 1, a.h_out, bytes)),
@@ -216,6 +218,15 @@ int check_in_place(const char *name, const Args &a) {
     const int64_t gates = a.gate ? a.n_gates * a.K * size : 0;
     GD_REQUIRE(!a.gate || !a.h_out || !overlaps(a.gate, gates, gates, 1, a.h_out, bytes), GD_EINVAL,
                "%s: h_out must not overlap gate", name);
+    const void *outs[2] = {a.out, a.x_scale};
+    const int64_t sizes[2] = {out_bytes, a.n * 4};
+    for (int i = 0; i < 2; i++)
+        GD_REQUIRE(!outs[i] || (!overlaps(a.x, bytes, bytes, 1, outs[i], sizes[i]) && !overlaps(a.residual, bytes, bytes, 1, outs[i], sizes[i]) &&
+                                (!a.gate || !overlaps(a.gate, gates, gates, 1, outs[i], sizes[i])) &&
+                                (!a.h_out || !overlaps(a.h_out, bytes, bytes, 1, outs[i], sizes[i]))),
+                   GD_EINVAL, "%s: the 8-bit output and its scales must not overlap x, residual, gate or h_out", name);
+    GD_REQUIRE(!a.x_scale || !overlaps(a.out, out_bytes, out_bytes, 1, a.x_scale, sizes[1]), GD_EINVAL,
+               "%s: planes and x_scale must not overlap", name);
     return GD_OK;
 }
 
@@ -263,7 +274,7 @@ extern "C" int rmsnorm_sandwich_q8_0(const void *x, const float *post_weight, co
     int st = check(name, a);
     if (st) return st;
     GD_REQUIRE(aligned(a_q8, 2), GD_EALIGN, "%s: a_q8 must be 2-byte aligned", name);
-    st = check_in_place(name, a);
+    st = check_in_place(name, a, n * (K / 32) * 34);
     if (st) return st;
     launch<false>(a, as_stream(stream));
     return check_launch(name);
@@ -281,7 +292,7 @@ extern "C" int rmsnorm_sandwich_ternary_act(const void *x, const float *post_wei
     if (st) return st;
     GD_REQUIRE(x_scale, GD_EINVAL, "%s: null pointer", name);
     GD_REQUIRE(aligned(planes, 4) && aligned(x_scale, 4), GD_EALIGN, "%s: planes and x_scale must be 4-byte aligned", name);
-    st = check_in_place(name, a);
+    st = check_in_place(name, a, n * K);
     if (st) return st;
     launch<true>(a, as_stream(stream));
     return check_launch(name);

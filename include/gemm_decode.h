@@ -482,11 +482,12 @@ int rmsnorm_ternary_act(const void *x, const void *residual, const float *weight
  *   post_weight  device f32 [K] or NULL.
  *   gate         device dtype [n_gates][K], or NULL (1; n_gates is ignored).
  *   gate_index   device int32 [n], the gate of each row; a row whose index is
- *                outside [0, n_gates) takes nothing of its block (h =
- *                residual_scale * residual). NULL: needs n_gates = 1 (one for
+ *                outside [0, n_gates) takes nothing of its block, whatever that
+ *                holds (h = residual_scale * residual). NULL: needs n_gates = 1 (one for
  *                all rows: a scale per channel) or n_gates = n (each row its own).
  *   weight, h_out, a_q8, limits, errors  as rmsnorm_q8_0; h_out may be x or
- *                residual itself, must not overlap them otherwise, nor gate.
+ *                residual itself, must not overlap them otherwise, nor gate;
+ *                a_q8 must not overlap any of them.
  * All pointers but gate_index (4) and a_q8 (2) 16-byte aligned; finite
  * residual_scale and block_scale; n_gates < 2^23. */
 int rmsnorm_sandwich_q8_0(const void *x, const float *post_weight, const void *gate, int64_t n_gates,
@@ -741,6 +742,7 @@ int attn_decode_q8_workspace_bytes(int64_t n_seqs, int64_t n_q, int64_t n_heads,
  *   workspace   device, token_logprobs_workspace_bytes(...) bytes, 16-byte
  *               aligned (NULL where that is 0); calls that share it must be
  *               ordered.
+ * The outputs must not overlap logits, tokens or each other.
  * Accuracy: log probabilities and entropies within 2^-17 of their magnitude (of a
  * confident token's as well, whose log probability is next to 0) plus 2^-100; with
  * a softcap 2^-20 * scale * softcap more. One of n_given, k and entropy

@@ -158,3 +158,27 @@ def test_streams_and_graph(gd):
         h.zero_(), a.zero_()
         graph.replay()
         assert torch.equal(h, want[0]) and torch.equal(a, want[1])
+
+
+@pytest.mark.parametrize("K", [96, 4096, 8224, 20000])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("eps", [EPS, 0.0])
+def test_rows_that_take_nothing_of_their_block(gd, K, post, eps):
+    """Whatever the block's output and the gates hold there: NaN, infinities, zeros (with eps = 0 too)."""
+    n, T = 6, torch.float16
+    g = torch.Generator().manual_seed(K)
+    x, res = (torch.randn(n, K, generator=g).to(T) for _ in range(2))
+    gate = torch.randn(2, K, generator=g).to(T)
+    gate[0, 1] = float("inf")
+    x[0], x[1, K - 1], x[2, 0], x[3] = float("nan"), float("inf"), -float("inf"), 0
+    index = torch.tensor([-1, 2, -7, 1 << 30, 1, -1], dtype=torch.int32)
+    x, res, gate, index = (t.cuda() for t in (x, res, gate, index))
+    w = torch.ones(K, device="cuda")
+    h, a = torch.empty_like(x), torch.empty(n * K // 32 * 34, dtype=torch.uint8, device="cuda")
+    gd.rmsnorm_sandwich_q8_0(x, w if post else None, res, w, h, a, n, K, eps, gate=gate, gate_index=index, residual_scale=0.5)
+    rows = [0, 1, 2, 3, 5]
+    want = (res.double() * 0.5).to(T)
+    assert torch.equal(h[rows], want[rows]) and not torch.equal(h[4], want[4]) and bool(h[4].isfinite().all())
+    alone = torch.empty_like(a)
+    gd.rmsnorm_q8_0(want, None, w, None, alone, n, K, eps)
+    assert torch.equal(a.view(n, -1)[rows], alone.view(n, -1)[rows])
