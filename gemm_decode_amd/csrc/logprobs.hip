@@ -541,9 +541,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Task t) {
     answer<T, kCap>(t, cap, row, parts[0], sorted, asked);
 }
 
-// Rows are cut until there are kFill parts in all, into parts of kMinPart tokens at least.
+// Rows are cut into up to kFill parts in all, two workgroups a CU, of kMinPart tokens at least.
+// (A few parts more, and some CUs have three: 61 rows of 50021 f16 without alternatives 8.7 us,
+// with 549 parts 10.1; 400 rows of 100003 uncut 36.5, cut in two 39.5. Half as many parts: 16
+// rows of 50021 with 20 alternatives 15.8 us -> 17.5, 32 of 128256 17.5 -> 21.3.)
 int64_t parts_of(int64_t n, int64_t V) {
-    const int64_t want = (kFill + n - 1) / n, most = (V + kMinPart - 1) / kMinPart;
+    const int64_t want = n < kFill ? kFill / n : 1, most = (V + kMinPart - 1) / kMinPart;
     return want < most ? want : most;
 }
 
@@ -560,9 +563,9 @@ extern "C" int token_logprobs_workspace_bytes(int64_t n, int64_t V, int64_t k, s
     GD_REQUIRE(bytes, GD_EINVAL, "token_logprobs_workspace_bytes: null pointer");
     const int st = check_sizes("token_logprobs_workspace_bytes", n, V, k);
     if (st) return st;
-    // Every smaller call's parts: at most kFill + n in all, and as many as fit into V.
+    // Every smaller call's parts: at most kFill in all, and as many as fit into V.
     const int64_t most = (V + kMinPart - 1) / kMinPart;
-    const int64_t parts = most == 1 ? 0 : n * most < kFill + n ? n * most : kFill + n;   // below 2^44
+    const int64_t parts = most == 1 ? 0 : n * most < kFill ? n * most : kFill;
     *bytes = static_cast<size_t>(parts * (static_cast<int64_t>(sizeof(Part)) + 8 * k));
     clear_error();
     return GD_OK;
@@ -603,6 +606,20 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
         GD_REQUIRE(workspace, GD_EINVAL, "%s: null workspace", name);
         GD_REQUIRE(workspace_bytes >= need, GD_ERANGE, "%s: workspace of %zu bytes, %llu are needed", name, workspace_bytes,
                    (unsigned long long)need);
+    }
+    const int64_t size = dtype_size(dtype);
+    const struct {
+        const void *at;
+        int64_t bytes;
+    } outs[4] = {{logprobs, n * n_given * 4}, {entropy, n * 4}, {top_ids, n * k * 8}, {top_logprobs, n * k * 4}};
+    for (int i = 0; i < 4; i++) {
+        if (!outs[i].at || !outs[i].bytes) continue;
+        GD_REQUIRE(!overlaps(logits, stride * size, V * size, n, outs[i].at, outs[i].bytes) &&
+                       (!n_given || !overlaps(tokens, n * n_given * 8, n * n_given * 8, 1, outs[i].at, outs[i].bytes)),
+                   GD_EINVAL, "%s: an output must not overlap logits or tokens", name);
+        for (int j = 0; j < i; j++)
+            GD_REQUIRE(!outs[j].at || !outs[j].bytes || !overlaps(outs[j].at, outs[j].bytes, outs[j].bytes, 1, outs[i].at, outs[i].bytes),
+                       GD_EINVAL, "%s: outputs must not overlap each other", name);
     }
     const hipStream_t hs = as_stream(stream);
     dispatch_dtype(dtype, [&](auto one) {

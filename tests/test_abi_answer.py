@@ -78,6 +78,41 @@ def test_sandwich_refusals(gd):
         assert call(h=FAKE + 16) == INVAL and call(r=FAR, h=FAR + 256) == INVAL and call(g=2 * FAR, h=2 * FAR) == INVAL
 
 
+def test_outputs_on_top_of_inputs_are_refused(gd):
+    """Any output on any input, or on another output, by one byte."""
+    L = gd.lib()
+    n, K, A = 3, 64, [FAKE * (i + 1) for i in range(8)]
+    ends = {"x": n * K * 4, "r": n * K * 4, "g": K * 4, "h": n * K * 4}
+    for q8 in (True, False):
+        def norm(**kw):
+            at = dict(zip("xrghos", A), **kw)
+            given = (at["o"],) if q8 else (at["o"], at["s"])
+            fn = L.rmsnorm_sandwich_q8_0 if q8 else L.rmsnorm_sandwich_ternary_act
+            return fn(at["x"], A[7], at["g"], 1, None, at["r"], 1.0, 1.0, A[7], at["h"], *given, n, K, 1e-5, F32, None)
+        for name, bytes_ in ends.items():
+            base = dict(zip("xrgh", A))[name]
+            for out in ("o",) if q8 else ("o", "s"):
+                assert norm(**{out: base}) == INVAL and norm(**{out: base + bytes_ - 4}) == INVAL
+                assert "overlap" in L.gemm_decode_last_error().decode()
+        if not q8:
+            assert norm(s=A[4] + n * K - 4) == INVAL and "overlap" in L.gemm_decode_last_error().decode()
+
+    V, m, k = 100, 2, 5
+
+    def logprobs(**kw):
+        at = dict(zip("xtleio", A), **kw)
+        return L.token_logprobs(at["x"], 104, at["t"], m, at["l"], at["e"], at["i"], at["o"], k, n, V, 1.0, 0.0, F32, None, 0, None)
+    outs = {"l": n * m * 4, "e": n * 4, "i": n * k * 8, "o": n * k * 4}
+    for name in outs:
+        for base, last in ((A[0], 2 * 104 * 4 + V * 4 - 8), (A[1], n * m * 8 - 8)):
+            assert logprobs(**{name: base}) == INVAL and logprobs(**{name: base + last}) == INVAL
+            assert "overlap" in L.gemm_decode_last_error().decode()
+        for other, bytes_ in outs.items():
+            if other != name:
+                assert logprobs(**{name: dict(zip("xtleio", A))[other] + bytes_ // 8 * 8 - 8}) == INVAL
+                assert "overlap" in L.gemm_decode_last_error().decode()
+
+
 def test_logprobs_refusals(gd):
     L = gd.lib()
 
