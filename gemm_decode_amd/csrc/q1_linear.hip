@@ -1,5 +1,13 @@
 // q1_linear.hip -- Q1_0 . q8_0 products with an epilogue: bias, activation, residual or the
 // product with a second weight's sums, and the output in the stream's type or as q8_0 blocks.
+//
+//   v[c][r] = sum over blocks of 128 of d0 sum over sub-blocks of 32 of d1 sum (+-1) q
+//
+// on the matrix cores, every product exact. One launch up to four columns (a token) and, with a
+// second one that joins slices of K, up to 16 (q1_few_kernel); for more the activations are laid
+// out once as operands (q1_digits_kernel), and a batch's weights are taken by waves that share
+// K (q1_split_kernel), a prompt's by waves side by side with all they read in LDS
+// (q1_wide_kernel). All end in the same epilogue, of sums in f32.
 #include <type_traits>
 
 #include "gd_internal.h"
@@ -282,19 +290,26 @@ __device__ __forceinline__ i32x8 frag(u32x4 lo, u32x2 hi) {
 
 // ------------------------------------------------- up to four columns
 // For few columns the digits are those of the codes alone, q = 16 h + l with l in [0, 16) and h
-// in [-8, 8), which takes a quarter of the work, and d1 is multiplied to the sums. A 16 x 16 x
-// 128 instruction takes a block of 16 weight rows; its other 16 rows are, for each of the four
-// sub-blocks, l and h of two columns, zero outside that sub-block. So a lane's four results
-// are the whole sums of one sub-block, one weight row and two columns, and acc += (d0 d1)
-// (l + h) rounds once (d0 d1 has 22 bits).
+// in [-8, 8), which takes a quarter of the work (5.6 vector instructions a code instead of 22),
+// and d1 is multiplied to the sums. A 16 x 16 x 128 instruction takes a block of 16 weight rows;
+// its other 16 rows are, for each of the four sub-blocks, l and h of two columns, or one of the
+// two of four columns, zero outside that sub-block. So a lane's four results are the whole sums
+// of one sub-block and one weight row, and acc += (d0 d1) (l + h) rounds once (d0 d1 has 22 bits).
 //
 // A workgroup of eight waves holds the digits of kBlocks blocks in LDS and takes 16-row tiles
 // of the weights, kw waves sharing a tile by its K in quads of blocks. A wave's loads of its
 // TILES tiles and Q quads all go out before the digits are worked out: the call is as long
-// as a few memory latencies, and this hides the digits behind one.
+// as a few memory latencies, and this hides the digits behind one. Beyond four columns K is cut
+// into slices for workgroups of their own, and another launch joins their sums.
+//
+// What it takes, replayed from a graph (1.8 us of it the launch): one column 4.2 us at 4096 x
+// 4096, 6.7 at 4096 x 14336 and, gated, 8.7 at 14336 x 4096 (16.5 MB of weights, 1.9 TB/s);
+// four 6.2, 11.3 and 10.8; eight at 4096 x 4096 7.0; 13 at 4096 x 14336 15.4. The weights' bytes
+// alone would take 0.3 to 2.4 us: it is the chain of launch, loads, digits, barrier, products
+// and sums over waves that counts.
 constexpr int kFew = 512;
 template <int C>
-constexpr int kBlocks = C < 4 ? 128 : 256 / C;
+constexpr int kBlocks = C < 4 ? 128 : 256 / C;   // digits of 49 KiB (a column 25)
 
 struct FewShape {
     int64_t nb;   // blocks of a row
@@ -561,8 +576,10 @@ __global__ __launch_bounds__(kFew, 2) void q1_few_kernel(Weight w0, Weight w1, c
 // behind all of them a word of each lane with the digits' powers of two.
 constexpr int64_t kStepBytes = 4 * 1536;
 
-// A thread takes a sub-block of a column, or half of one (kHalf: few columns, where the way
-// through the arithmetic is what takes time).
+// A thread takes a sub-block of a column, or half of one (kHalf: below 1024 blocks, where the
+// way through the arithmetic is what takes time: 5 columns of 4096 10.5 us in all instead of
+// 11.1; 2039 of 14336 262 instead of 271 with whole ones). 2039 columns of 14336 take 30 us,
+// 31 MB read and 97 written.
 template <bool kHalf>
 __global__ __launch_bounds__(256) void q1_digits_kernel(const uint16_t *__restrict__ a_q8, uint8_t *__restrict__ out, int64_t n,
                                                         int64_t steps) {
@@ -721,6 +738,12 @@ __device__ __forceinline__ void lds_load4(const void *base, uint32_t at, uint32_
 // kBuffers blocks before it is used. A wave has the digits of a step in registers, reads the
 // next step's, and goes through its tiles, four instructions on the same sums each. Two
 // workgroups on a CU, so that one wave of a SIMD works while the other one waits for its own.
+//
+// 2039 columns at 4096 x 14336 take 220 to 230 us (1.05 PFLOP/s of products, 4.2 of the digits'),
+// gated 509 at 14336 x 4096 129. The instructions alone, on such operands, would take 163: fed
+// without a pause on random digits the cores' clock falls (21.5 ns an instruction; 16.4 on
+// constant ones), and here they are busy for 61 % of the cycles at 1.7 GHz. Without the loads
+// and the barrier the same products took 207.
 template <int TN, int S>
 __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
                                                          ManyShape f) {
@@ -907,7 +930,9 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
 }
 
 // Batches: KS waves share the sums of 32 columns and NT = TN S tiles of 32 weight rows by K,
-// each loading its digits to registers a block ahead, and add them up in LDS.
+// each loading its digits to registers a block ahead, and add them up in LDS. 37 columns gated at
+// 6912 x 2560 take 14.4 us, 64 at 4096 x 4096 14.3: three launches of 4 to 5 us, each a few
+// latencies long.
 template <int TN, int S, int KS>
 __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
                                                               ManyShape f) {
@@ -1058,6 +1083,12 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
     return GD_OK;
 }
 
+// With so many blocks for its workgroups to go through the wide kernel is the faster one: 64
+// columns at 4096 x 4096 (512) 20.6 us against 14.4, 256 (2048) 27.7 against 24.8, 509 (4096) 36
+// against 43, at 4096 x 14336 256 columns (7168) 49 against 56, 2039 (57344) 263 against 859; gated,
+// 37 at 14336 x 4096 (3584) 33 against 34. With fewer, four waves along K where that makes
+// kManyGroups workgroups, eight else: 256 columns at 4096 x 4096 (512) 24.8 and 26.6, gated 37 at
+// 6912 x 2560 (432) 14.8 and 16.7, 128 at 4096 x 4096 (256) 18.7 and 15.7.
 constexpr int64_t kWideFrom = 3500, kManyGroups = 384;
 // Up to so many workgroups of four tiles a wave the kernel without an operand pass is the faster
 // one: of 8 columns 14336 x 4096 9.6 us against 15.6, 49152 x 4096 (768 workgroups) 25.8 against
@@ -1095,6 +1126,9 @@ void run_few(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Epi
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
     using Four = std::integral_constant<int, 4>;
+    // More tiles a wave once they come to 224 workgroups: 4096 x 4096, one column: one tile 4.2 us,
+    // two 4.7, four 5.7; 14336 x 4096: 7.3, 6.2, 6.1; 32768 x 4096: 13.4, 9.6, 8.4. (Blocks of 32
+    // rows need two tiles in a workgroup.)
     const int64_t full = tiles * f.kw / 8;   // workgroups with a tile a wave
     if (quads <= f.kw) {
         if (full >= 4 * 224)
@@ -1165,11 +1199,13 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
         f.row_groups = (f.row_tiles + tiles - 1) / tiles;
         return f.col_tiles * f.row_groups;
     };
-    // Slices of K, of `least` blocks at least, until there are `want` workgroups or no room for their sums.
-    const auto slice = [&](int64_t have, int64_t want, int64_t least) {
+    // Slices of K, of eight blocks at least, until there are `want` workgroups or no room for their
+    // sums: 13 columns at 4096 x 14336 on the split kernel 17 us, unsliced 28; on the wide one
+    // 256 columns there 49 and 114, 37 gated at 14336 x 4096 33 and 42.
+    const auto slice = [&](int64_t have, int64_t want) {
         const int64_t room = parts_bytes(e.n) / (S * e.n * f.row_tiles * 128);
         int64_t z = want / have;
-        z = z < f.nb / least ? z : f.nb / least;
+        z = z < f.nb / 8 ? z : f.nb / 8;
         z = z < room ? z : room;
         if (z < 1) z = 1;
         f.share = (f.nb + z - 1) / z;
@@ -1179,15 +1215,15 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
     constexpr int TN = 4 / S;
     const int64_t wide = groups(4 * TN);
     if (wide * f.nb >= kWideFrom) {
-        const dim3 grid = slice(wide, 512 + wide - 1, 8);
+        const dim3 grid = slice(wide, 512 + wide - 1);
         hipLaunchKernelGGL((q1_wide_kernel<TN, S>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
     } else {
         const int64_t have = groups(2 / S);
         if (have >= kManyGroups) {
-            const dim3 grid = slice(have, 1, 8);
+            const dim3 grid = slice(have, 1);
             hipLaunchKernelGGL((q1_split_kernel<2 / S, S, 4>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
         } else {
-            const dim3 grid = slice(have, 256, 8);
+            const dim3 grid = slice(have, kCus);
             hipLaunchKernelGGL((q1_split_kernel<2 / S, S, 8>), grid, dim3(512), 0, hs, w0, w1, workspace, e, f);
         }
     }
