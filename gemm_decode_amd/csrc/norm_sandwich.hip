@@ -1,6 +1,11 @@
 // norm_sandwich.hip -- the norms behind and before a block in one pass over a row: the
 // block's output x is normed (rstd(x) * post_weight), gated and scaled, added to the scaled
 // residual, rounded to the stream's type (h), and h normed into an 8-bit output.
+//   u = x rstd(x) post_weight,  h = residual_scale residual + block_scale gate u,
+//   out = quantized h rstd(h) weight
+// 4099 rows of 4096 bf16 with gates to q8_0 take 38 us: 118 MB, 24 us as a copy; the vector units
+// are busy for four fifths of the time (56 instructions an element, a third of them f64 or to and
+// from it) and each row's two sums stand between its reads and its writes.
 //
 // h is worked out in f64 from values that f64 holds exactly, so that its rounding, and with
 // it the codes, do not depend on the order of the sums (up to f64's own rounding); codes and
