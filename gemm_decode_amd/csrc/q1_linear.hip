@@ -931,8 +931,8 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
 
 // Batches: KS waves share the sums of 32 columns and NT = TN S tiles of 32 weight rows by K,
 // each loading its digits to registers a block ahead, and add them up in LDS. 37 columns gated at
-// 6912 x 2560 take 14.4 us, 64 at 4096 x 4096 14.3: three launches of 4 to 5 us, each a few
-// latencies long.
+// 6912 x 2560 take 14.2 us, 64 at 4096 x 4096 15.6: two or three launches, each a few latencies
+// long, and what the digits take from L2 (12.5 KB for a wave's block; 54 MB in all for the former).
 template <int TN, int S, int KS>
 __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
                                                               ManyShape f) {
@@ -1084,12 +1084,10 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
 }
 
 // With so many blocks for its workgroups to go through the wide kernel is the faster one: 64
-// columns at 4096 x 4096 (512) 20.6 us against 14.4, 256 (2048) 27.7 against 24.8, 509 (4096) 36
-// against 43, at 4096 x 14336 256 columns (7168) 49 against 56, 2039 (57344) 263 against 859; gated,
-// 37 at 14336 x 4096 (3584) 33 against 34. With fewer, four waves along K where that makes
-// kManyGroups workgroups, eight else: 256 columns at 4096 x 4096 (512) 24.8 and 26.6, gated 37 at
-// 6912 x 2560 (432) 14.8 and 16.7, 128 at 4096 x 4096 (256) 18.7 and 15.7.
-constexpr int64_t kWideFrom = 3500, kManyGroups = 384;
+// columns at 4096 x 4096 (512) 20.6 us against 14.4, 509 (4096) 38.5 against 32.4, 1000 (8192) 55
+// against 63, gated, 37 at 14336 x 4096 (3584) 33.6 against 27.2, 200 at 14336 x 4096 (12544) 67
+// against 73, 2039 at 4096 x 14336 (57344) 263 against 859.
+constexpr int64_t kWideFrom = 8000;
 // Up to so many workgroups of four tiles a wave the kernel without an operand pass is the faster
 // one: of 8 columns 14336 x 4096 9.6 us against 15.6, 49152 x 4096 (768 workgroups) 25.8 against
 // 28.4, gated (1536) 43.2 against 40.1; of 13 (a workgroup a CU, and twice the matrix
@@ -1201,7 +1199,7 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
     };
     // Slices of K, of eight blocks at least, until there are `want` workgroups or no room for their
     // sums: 13 columns at 4096 x 14336 on the split kernel 17 us, unsliced 28; on the wide one
-    // 256 columns there 49 and 114, 37 gated at 14336 x 4096 33 and 42.
+    // 256 columns there 49 and 114.
     const auto slice = [&](int64_t have, int64_t want) {
         const int64_t room = parts_bytes(e.n) / (S * e.n * f.row_tiles * 128);
         int64_t z = want / have;
@@ -1218,14 +1216,28 @@ void run_many(const Weight &w0, const Weight &w1, const uint16_t *a_q8, const Ep
         const dim3 grid = slice(wide, 512 + wide - 1);
         hipLaunchKernelGGL((q1_wide_kernel<TN, S>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
     } else {
-        const int64_t have = groups(2 / S);
-        if (have >= kManyGroups) {
-            const dim3 grid = slice(have, 1);
-            hipLaunchKernelGGL((q1_split_kernel<2 / S, S, 4>), grid, dim3(256), 0, hs, w0, w1, workspace, e, f);
-        } else {
-            const dim3 grid = slice(have, kCus);
-            hipLaunchKernelGGL((q1_split_kernel<2 / S, S, 8>), grid, dim3(512), 0, hs, w0, w1, workspace, e, f);
-        }
+        const auto go = [&](auto tiles, auto ks, int64_t want) {
+            constexpr int T = decltype(tiles)::value, KS = decltype(ks)::value;
+            const dim3 grid = slice(groups(T / S), want);
+            hipLaunchKernelGGL((q1_split_kernel<T / S, S, KS>), grid, dim3(64 * KS), 0, hs, w0, w1, workspace, e, f);
+        };
+        using Two = std::integral_constant<int, 2>;
+        using Four = std::integral_constant<int, 4>;
+        using Eight = std::integral_constant<int, 8>;
+        // Four tiles read the digits, which the waves load for themselves, half as often as two, if
+        // they fill the device, alone or by slices: 64 columns at 4096 x 14336 23.2 us and 29.1, gated
+        // 37 at 6912 x 2560 14.2 and 17.8, 20 at 14336 x 4096 17.7 and 24.6. Where two tiles fill it
+        // without slices and K is short they save the joining launch: 128 at 4096 x 4096 18.0 and 19.7,
+        // 100 at 4096 x 14336, of 112 blocks, 38.8 and 32.2; and where neither does: 64 at 1024 x 1024
+        // 9.2 and 10.4. Four waves along K instead of eight once there is a workgroup for each CU:
+        // gated 100 at 6912 x 2560 (432) 20.4 and 23.6, 37 (216) 17.9 and 14.2.
+        const int64_t two = groups(2 / S), four = groups(4 / S), most = f.nb / 8 < 1 ? 1 : f.nb / 8;
+        if (four > kCus)
+            go(Four{}, Four{}, 1);
+        else if (two > kCus || ((two <= kCus / 2 || f.nb >= 64) && four * most >= kCus * 3 / 4))
+            go(Four{}, Eight{}, kCus);
+        else
+            go(Two{}, Eight{}, kCus);
     }
     if (f.slices > 1) join<S>(w0, w1, e, f.slices, f.row_tiles, f.parts, hs);
 }
