@@ -594,8 +594,10 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
     GD_REQUIRE(k == 0 || (top_ids && top_logprobs), GD_EINVAL, "%s: null top_ids or top_logprobs", name);
     GD_REQUIRE(n_given || k || entropy, GD_EINVAL, "%s: nothing is asked for", name);
     GD_REQUIRE(dtype_ok(dtype), GD_EINVAL, "%s: unknown dtype %d", name, dtype);
-    GD_REQUIRE(scale > 0.0f && scale <= 3.40282347e38f, GD_EINVAL, "%s: scale must be finite and > 0", name);
-    GD_REQUIRE(softcap >= 0.0f && softcap <= 1e30f, GD_EINVAL, "%s: softcap must be in [0, 1e30]", name);
+    // (Where 1 / softcap to the eighth and scale * softcap stay in f32's range.)
+    GD_REQUIRE(scale > 0.0f && scale <= 1e30f, GD_EINVAL, "%s: scale must be > 0 and at most 1e30", name);
+    GD_REQUIRE(softcap == 0.0f || (softcap >= 1e-4f && softcap <= 1e30f && static_cast<double>(scale) * softcap <= 1e30f), GD_EINVAL,
+               "%s: softcap must be 0 or in [1e-4, 1e30], times scale at most 1e30", name);
     GD_REQUIRE(n_given <= 65536 && n * n_given < (INT64_C(1) << 31) && stride <= (INT64_C(1) << 40), GD_ERANGE,
                "%s: n_given or stride too large", name);
     GD_REQUIRE(aligned(logits, dtype_size(dtype)) && aligned(tokens, 8) && aligned(logprobs, 4) && aligned(entropy, 4) &&

@@ -124,8 +124,9 @@ def test_logprobs_refusals(gd):
     assert call(dt=3) == INVAL
     for bad in (0.0, -1.0, float("nan"), float("inf")):
         assert call(s=bad) == INVAL
-    for bad in (-1.0, float("nan"), float("inf"), 2e30):
+    for bad in (-1.0, float("nan"), float("inf"), 2e30, 9e-5, 1e-40):
         assert call(c=bad) == INVAL
+    assert call(s=2e30) == INVAL and call(s=1e20, c=1e11) == INVAL
     assert call(x=FAKE + 2) == ALIGN and call(x=FAKE + 1, dt=BF16) == ALIGN and call(t=FAKE + 4) == ALIGN
     assert call(lp=FAKE + 2) == ALIGN and call(e=FAKE + 2) == ALIGN and call(i=FAKE + 4) == ALIGN and call(tl=FAKE + 2) == ALIGN
     assert call(k=65) == RANGE and call(n=1 << 23) == RANGE and call(V=(1 << 30) + 1, st=BIG) == RANGE

@@ -215,3 +215,27 @@ def test_streams_and_graphs(gd):
             graphs[j].replay()
         assert all(torch.equal(a, b) for o, w in zip(kept, want) for a, b in zip(o, w)), i
         assert all(torch.equal(a, b) for a, b in zip(call(0, outs(2)), want[0]))
+
+
+@pytest.mark.parametrize("scale,cap", [(1e30, 0.0), (1.0, 1e30), (1e-40, 0.0), (1.0, 1e-4), (1e30, 1e-4), (1e-30, 1e30)])
+def test_scales_and_caps_at_their_limits(gd, scale, cap):
+    """Ties, zeros, a banned token and wide logits; equal logits stay equally likely whatever the scale."""
+    V = 5003
+    x = torch.zeros(5, V)
+    x[1, 7], x[1, 9] = 2.0, 2.0
+    x[2] = torch.linspace(-30, 30, V)
+    x[3] = -1e30
+    x[3, 5] = 1e30
+    x[4, ::2] = -float("inf")
+    x = x.cuda()
+    lp, ent = torch.empty(5, 1, device="cuda"), torch.empty(5, device="cuda")
+    ids, tops = torch.empty(5, 3, dtype=torch.int64, device="cuda"), torch.empty(5, 3, device="cuda")
+    gd.token_logprobs(x, torch.tensor([[7]] * 5, device="cuda"), lp, ent, ids, tops, 5, V, scale=scale, softcap=cap)
+    for r in range(5):
+        w_lp, w_ent, w_ids, w_tops = answer.logprobs(x[r].cpu().numpy(), np.array([7]), 3, scale, cap)
+        assert np.array_equal(ids[r].cpu().numpy(), w_ids)
+        # what lies past f32's range, 2 (1 - 2^-25) 2^127, is rounded to -infinity
+        w_lp, w_tops = (np.where(w <= -(2 - 2.0 ** -24) * 2.0 ** 127, -np.inf, w) for w in (w_lp, w_tops))
+        near(lp[r], w_lp, cap, scale)
+        near(ent[r:r + 1], np.array([w_ent]), cap, scale)
+        near(tops[r], w_tops, cap, scale)
