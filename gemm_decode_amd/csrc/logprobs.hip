@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "gd_internal.h"
+#include "gd_norm.h"
 #include "gd_types.h"
 
 namespace {
@@ -318,22 +319,69 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
     }
 }
 
+// What a part adds to the sums against `top`, a logit as large as its own: its share of S and D
+// with its own largest logit, which it holds out of them; nothing if it has none.
+template <bool kCap>
+__device__ __forceinline__ void against(const Cap<kCap> &cap, float top, const Part &p, double &S, double &D) {
+    const double d = fmax((static_cast<double>(cap(p.top)) - cap(top)) * cap.c, -1000.0);
+    const double f = p.top > -kInf ? static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(d))) : 0.0;
+    S = f * (p.S + 1.0);
+    D = f * (p.D + d * (p.S + 1.0));
+}
+
 // Both parts' sums against the larger logit.
 template <bool kCap>
 __device__ __forceinline__ void join(Part &a, const Part &b, const Cap<kCap> &cap) {
-    const bool first = a.top >= b.top;
-    const float hi = first ? a.top : b.top, lo = first ? b.top : a.top;
-    const double HS = first ? a.S : b.S, HD = first ? a.D : b.D, LS = first ? b.S : a.S, LD = first ? b.D : a.D;
-    a.bad |= b.bad;
-    a.top = hi;
-    a.S = HS;
-    a.D = HD;
-    if (lo > -kInf) {
-        const double d = fmax((static_cast<double>(cap(lo)) - cap(hi)) * cap.c, -1000.0);
-        const double f = __builtin_amdgcn_exp2f(static_cast<float>(d));
-        a.S += f * (LS + 1.0);
-        a.D += f * (LD + d * (LS + 1.0));
+    const Part &hi = a.top >= b.top ? a : b, &lo = a.top >= b.top ? b : a;
+    double S, D;
+    against(cap, hi.top, lo, S, D);
+    a = Part{hi.S + S, hi.D + D, hi.top, a.bad | b.bad, 0};
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+    return gd::over_wave(v, [](double a, double b) { return a + b; });
+}
+
+// The threads' parts as one, in all of them: the largest logit first, then each part's share
+// against it, the first that has it being left as it is (joined two and two in five steps, one
+// row of 49152 took 0.8 us longer). waves[]: room of the workgroup's.
+template <bool kCap>
+__device__ __forceinline__ Part join_all(const Cap<kCap> &cap, const Part &mine, Part *waves) {
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const float most = wave_max(mine.top);
+    if (lane == 0) waves[wave].top = most;
+    __syncthreads();
+    float top = waves[0].top;
+    int holder = 0;
+#pragma unroll
+    for (int w = 1; w < kWaves; w++)
+        if (waves[w].top > top) {
+            top = waves[w].top;
+            holder = w;
+        }
+    double S, D;
+    against(cap, top, mine, S, D);
+    if (wave == holder && lane == __ffsll(__ballot(mine.top == top)) - 1) {
+        S = mine.S;
+        D = mine.D;
     }
+    S = wave_sum(S);
+    D = wave_sum(D);
+    const bool bad = __any(mine.bad);
+    if (lane == 0) {
+        waves[wave].S = S;
+        waves[wave].D = D;
+        waves[wave].bad = bad ? 1u : 0u;
+    }
+    __syncthreads();
+    Part all = {0.0, 0.0, top, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) {
+        all.S += waves[w].S;
+        all.D += waves[w].D;
+        all.bad |= waves[w].bad;
+    }
+    return all;
 }
 
 // The k largest of `count` orders in LDS, by their ranks, to out[]. Called by the workgroup.
@@ -394,8 +442,8 @@ __device__ __forceinline__ void answer(const Task &t, const Cap<kCap> &cap, int6
 // 2039 rows of 100003 bf16 (408 MB) take 122 us with a softcap and 94 without: some 22 and 18
 // vector instructions a logit (an exponential counts for four), 59 us for the bytes alone. Four waves
 // a SIMD (launch bounds) instead of two 133 -> 122. Few rows are a chain of latencies, of which
-// the selection is the longer half: one row of 49152 7.1 us and with 8 alternatives 12.0, both
-// launches together; 61 of 50021 f16 8.7 and with 20 alternatives 19.0. There each wave goes once
+// the selection is the longer half: one row of 49152 6.1 us and with 8 alternatives 11.1, both
+// launches together; 61 of 50021 f16 8.1 and with 20 alternatives 18.4. There each wave goes once
 // through some 1900 instructions, and waits for about half of the time, for memory, barriers and
 // the instructions themselves.
 template <typename T, int U, bool kEntropy, bool kCap>
@@ -487,8 +535,22 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_part_kernel(Task t) {
         __syncthreads();
         sort_best(list, total, static_cast<int>(t.k), sorted);
     }
-    Part all = parts[0];
-    for (int w = 1; w < kWaves; w++) join(all, parts[w], cap);
+    Part all = {0.0, 0.0, parts[0].top, 0, 0};
+    int holder = 0;
+#pragma unroll
+    for (int w = 1; w < kWaves; w++)
+        if (parts[w].top > all.top) {
+            all.top = parts[w].top;
+            holder = w;
+        }
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) {
+        double S, D;
+        against(cap, all.top, parts[w], S, D);
+        all.S += w == holder ? parts[w].S : S;
+        all.D += w == holder ? parts[w].D : D;
+        all.bad |= parts[w].bad;
+    }
     if (t.parts == 1) {
         answer<T, kCap>(t, cap, row, all, sorted, asked);
         return;
@@ -504,7 +566,7 @@ constexpr int kMost = 2048;   // candidates of a row at a time
 template <typename T, bool kCap>
 __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Task t) {
     __shared__ u64 stage[kMost], list[kMost], sorted[kMaxK];
-    __shared__ Part parts[kThreads];
+    __shared__ Part waves[kWaves];
     __shared__ int count;
     const int64_t row = blockIdx.x, size = sizeof(Part) + 8 * t.k;
     const uint8_t *in = t.workspace + row * t.parts * size;
@@ -514,7 +576,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Task t) {
     const auto entry = [&](int64_t p, int i) { return reinterpret_cast<const u64 *>(in + p * size + sizeof(Part))[i]; };
     Part all = {0.0, 0.0, -kInf, 0, 0};
     for (int64_t p = tid; p < t.parts; p += kThreads) join(all, *reinterpret_cast<const Part *>(in + p * size), cap);
-    parts[tid] = all;
+    all = join_all(cap, all, waves);
     if (k) {   // as many parts' candidates at a time as there is room for, behind the k best so far
         const int64_t fit = (kMost - kMaxK) / k;
         for (int64_t p0 = 0; p0 < t.parts; p0 += fit) {
@@ -540,14 +602,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Task t) {
         }
     }
     __syncthreads();
-    for (int o = kThreads / 2; o >= 1; o >>= 1) {
-        if (tid < o && tid + o < t.parts) {
-            join(all, parts[tid + o], cap);
-            parts[tid] = all;
-        }
-        if (o < t.parts) __syncthreads();
-    }
-    answer<T, kCap>(t, cap, row, parts[0], sorted, asked);
+    answer<T, kCap>(t, cap, row, all, sorted, asked);
 }
 
 // Rows are cut into up to kFill parts in all, two workgroups a CU, of kMinPart tokens at least.
