@@ -766,7 +766,7 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     // powers of one step, the signs and scales of its tiles, two at a time. Signs 16 bytes a
     // lane, the rows 2 (lane % 16) and one more of half lane / 16 % 2; scales those of a block
     // and its neighbour.
-    const uint8_t *chunk = digits + col * steps * kStepBytes + wave * 3072;
+    const uint8_t *chunk = digits + col * steps * kStepBytes + wave * static_cast<int>(2 * kStepBytes / kWaves);
     const uint8_t *power = digits + (f.col_tiles * steps * kStepBytes + (col * steps + wave % 2) * 256);
     const uint8_t *sign[2], *scale[2];
     uint32_t sign_at[2], scale_at[2];
@@ -788,7 +788,7 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
     const auto stage = [&](int i, uint32_t to, int part) {
         const uint32_t b = from + (i < blocks ? i : blocks - 1);
         if (part == 0) {
-            lds_load16<3>(chunk + b * static_cast<uint32_t>(2 * kStepBytes), lane16, to + wave * 3072);
+            lds_load16<3>(chunk + b * static_cast<uint32_t>(2 * kStepBytes), lane16, to + wave * static_cast<int>(2 * kStepBytes / kWaves));
         } else if (part == 1) {
             lds_load4(power + b * 512u, lane4, to + kPowers + wave * 256);
         } else {
