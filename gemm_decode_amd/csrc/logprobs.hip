@@ -136,13 +136,13 @@ struct Best {
         least_logit = least ? logit_of(static_cast<uint32_t>(least >> 32)) : -kInf;
     }
     // The largest number that at least `k_` of R 64 numbers, the lanes', reach (0: there are not so
-    // many above 0); `reach`: how many do.
+    // many above 0), its bits below `lowest` 0; `reach`: how many do.
     template <int R, typename U>
-    __device__ __forceinline__ static U reached(const U (&v)[R], int k_, int &reach) {
+    __device__ __forceinline__ static U reached(const U (&v)[R], int k_, int &reach, int lowest = 0) {
         U at = 0;
         reach = 64 * R;
 #pragma unroll 1
-        for (int b = 8 * sizeof(U) - 1; b >= 0; b--) {
+        for (int b = 8 * sizeof(U) - 1; b >= lowest; b--) {
             const U next = at | U{1} << b;
             int n = 0;
 #pragma unroll
@@ -238,10 +238,12 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
     w.bad |= !(mine < kInf);
     if (best.k && __any(mine >= best.least_logit)) {
         best.raise(*best.shared);
-        if (best.least == 0 && N >= 8) {   // none yet: k lanes' largest are k candidates
+        // None yet: k lanes' largest are k candidates. (To half of the bits: a step is some 50 cycles,
+        // one row of 49152 10.5 us instead of 11.1; to 12 of them there are too many, 11.7.)
+        if (best.least == 0 && N >= 8) {
             const uint32_t v[1] = {mine > -kInf ? key_of(mine) : 0};
             int reach;
-            const u64 to = static_cast<u64>(Best::reached<1>(v, best.k, reach)) << 32;   // below all tokens of this logit
+            const u64 to = static_cast<u64>(Best::reached<1>(v, best.k, reach, 16)) << 32;   // below all tokens of this logit
             best.raise(to);
             if (threadIdx.x % 64 == 0 && to > *best.shared) atomicMax(best.shared, to);
         }
