@@ -450,8 +450,8 @@ __device__ __forceinline__ void answer(const Task &t, const Cap<kCap> &cap, int6
 // 2039 rows of 100003 bf16 (408 MB) take 122 us with a softcap and 94 without: some 22 and 18
 // vector instructions a logit (an exponential counts for four), 59 us for the bytes alone. Four waves
 // a SIMD (launch bounds) instead of two 133 -> 122. Few rows are a chain of latencies, of which
-// the selection is the longer half: one row of 49152 6.1 us and with 8 alternatives 11.1, both
-// launches together; 61 of 50021 f16 8.1 and with 20 alternatives 18.4. There each wave goes once
+// the selection is the longer half: one row of 49152 6.1 us and with 8 alternatives 10.5, both
+// launches together; 61 of 50021 f16 8.1 and with 20 alternatives 17.3. There each wave goes once
 // through some 1900 instructions, and waits for about half of the time, for memory, barriers and
 // the instructions themselves.
 template <typename T, int U, bool kEntropy, bool kCap>
