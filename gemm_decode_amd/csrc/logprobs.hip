@@ -120,9 +120,6 @@ __device__ __forceinline__ float over_wave(float v, F join) {
 __device__ __forceinline__ float wave_max(float v) {
     return over_wave(v, [](float a, float b) { return fmaxf(a, b); });
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    return over_wave(v, [](float a, float b) { return a + b; });
-}
 
 // A wave's candidates: the `count` first of room[], at most kRoom.
 struct Best {
@@ -212,9 +209,12 @@ struct Best {
 };
 
 // What a wave has met so far: the largest logit (-infinity before there is one), capped in
-// ref, and the lanes' shares of S and D against it.
+// ref, and the lanes' shares of S and D against it. A step's terms are summed in f32, the steps in
+// f64: terms that are all alike all round the same way, which a chain of f32 sums over a row of
+// 2^18 tokens would bring to 2^-16 of S.
 struct Met {
-    float top, ref, S, D;
+    float top, ref;
+    double S, D;
     float low, high;   // logits between them need no care (see absorb)
     bool bad;
 };
@@ -264,16 +264,14 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             }
         if (best.count >= 2 * best.k) best.shrink();
     }
+    float S = 0.0f, D = 0.0f;   // of this step
     if (__any(mine > w.top)) {   // a larger one: what was the largest joins the others, in lane 0
         const float top = wave_max(mine), ref = cap(top);
         if (w.top > -kInf) {
-            const float d = fmaxf((w.ref - ref) * cap.c, -1000.0f), f = __builtin_amdgcn_exp2f(d);
-            if (kEntropy) w.D = f * fmaf(d, w.S, w.D);
-            w.S *= f;
-            if (threadIdx.x % 64 == 0) {
-                w.S += f;
-                if (kEntropy) w.D = fmaf(f, d, w.D);
-            }
+            const double d = fmaxf((w.ref - ref) * cap.c, -1000.0f), f = __builtin_amdgcn_exp2f(static_cast<float>(d));
+            const double own = threadIdx.x % 64 == 0 ? 1.0 : 0.0;
+            if (kEntropy) w.D = f * (w.D + d * (w.S + own));
+            w.S = f * (w.S + own);
         }
         w.top = top;
         w.ref = ref;
@@ -282,7 +280,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
         w.high = kCap ? small : kInf;
         // The new one stays out of S: the first of them in the first lane that has one.
         // What stands in its place counts for nothing; where the short way below is taken, which
-        // has no -infinity, what it counts for is taken off S again.
+        // has no -infinity, what it counts for is taken off S first.
         const bool small_enough = __all(least >= w.low && mine <= w.high);
         const float out = small_enough ? w.low : -kInf;
         const bool chosen = static_cast<int>(threadIdx.x % 64) == __ffsll(__ballot(mine == top)) - 1;
@@ -297,8 +295,8 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             const Exponent<kCap> of(cap, ref);
             const float d = of(out), e = __builtin_amdgcn_exp2f(d);
             if (chosen) {
-                w.S -= e;
-                if (kEntropy) w.D = fmaf(-e, d, w.D);
+                S = -e;
+                if (kEntropy) D = -e * d;
             }
         }
     }
@@ -307,18 +305,20 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const float d = of(x[i]), e = __builtin_amdgcn_exp2f(d);
-            w.S += e;
-            if (kEntropy) w.D = fmaf(e, d, w.D);
+            S += e;
+            if (kEntropy) D = fmaf(e, d, D);
         }
     } else {
         const float ref = w.top > -kInf ? w.ref : 0.0f;
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const float d = fmaxf((cap(x[i]) - ref) * cap.c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
-            w.S += e;
-            if (kEntropy) w.D = fmaf(e, d, w.D);
+            S += e;
+            if (kEntropy) D = fmaf(e, d, D);
         }
     }
+    w.S += S;
+    if (kEntropy) w.D += D;
 }
 
 // What a part adds to the sums against `top`, a logit as large as its own: its share of S and D
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_part_kernel(Task t) {
     const int tail = static_cast<int>(length - head - static_cast<int64_t>(vectors) * PER);
     const Vec *body = reinterpret_cast<const Vec *>(x + head);
     const Cap<kCap> cap(t.softcap, t.scale);
-    Met met = {-kInf, 0.0f, 0.0f, 0.0f, kInf, -kInf, false};
+    Met met = {-kInf, 0.0f, 0.0, 0.0, kInf, -kInf, false};
     Best best = {room[wave], &shared, 0, static_cast<int>(t.k), 0, -kInf};
     if (tid == 0) shared = 0;
     __syncthreads();

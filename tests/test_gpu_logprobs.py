@@ -239,3 +239,28 @@ def test_scales_and_caps_at_their_limits(gd, scale, cap):
         near(lp[r], w_lp, cap, scale)
         near(ent[r:r + 1], np.array([w_ent]), cap, scale)
         near(tops[r], w_tops, cap, scale)
+
+
+@pytest.mark.parametrize("V", [1 << 18, 1 << 20, 1 << 22, 1 << 24])
+@pytest.mark.parametrize("high", [3.5, 6.25])
+def test_sums_of_long_rows(gd, V, high):
+    """Rows that are not cut, equal logits below one that every wave meets first: their terms all round the same way. With a
+    token 30 ahead of them, whose log probability is the sum itself, and without."""
+    n = 257
+    T = torch.float16
+    x = torch.zeros(n, V, dtype=T, device="cuda")
+    at = [100, 700, 1300, 1900]   # one of each wave's first vectors
+    x[:, at] = high
+    lp, ent = torch.empty(n, 1, device="cuda"), torch.empty(n, device="cuda")
+    for ahead in (False, True):
+        token = V // 2 + 1700 if ahead else at[0]
+        if ahead:
+            x[:, token] = 30.0
+            s = (V - 5) * np.exp(-30.0) + 4 * np.exp(high - 30.0)
+            d = 30 * (V - 5) * np.exp(-30.0) + (30 - high) * 4 * np.exp(high - 30.0)
+        else:
+            s, d = 3 + (V - 4) * np.exp(-high), high * (V - 4) * np.exp(-high)
+        gd.token_logprobs(x, torch.full((n, 1), token, device="cuda"), lp, ent, None, None, n, V)
+        for r in (0, n - 1):
+            near(lp[r], np.array([-np.log1p(s)]), 0, 1)
+            near(ent[r:r + 1], np.array([np.log1p(s) + d / (1 + s)]), 0, 1)
