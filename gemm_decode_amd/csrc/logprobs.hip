@@ -268,7 +268,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
     if (__any(mine > w.top)) {   // a larger one: what was the largest joins the others, in lane 0
         const float top = wave_max(mine), ref = cap(top);
         if (w.top > -kInf) {
-            const double d = fmaxf((w.ref - ref) * cap.c, -1000.0f), f = __builtin_amdgcn_exp2f(static_cast<float>(d));
+            const double d = fmax((static_cast<double>(w.ref) - ref) * cap.c, -1000.0), f = __builtin_amdgcn_exp2f(static_cast<float>(d));
             const double own = threadIdx.x % 64 == 0 ? 1.0 : 0.0;
             if (kEntropy) w.D = f * (w.D + d * (w.S + own));
             w.S = f * (w.S + own);
@@ -276,7 +276,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
         w.top = top;
         w.ref = ref;
         const float small = fminf(Cap<kCap>::kSmall / cap.over, 1e9f);   // (x^9 stays in range)
-        w.low = kCap ? -small : fmaxf(ref - 1000.0f / cap.c, -3e38f);
+        w.low = kCap ? -small : fmaxf(ref - fminf(1000.0f / cap.c, 3e38f), -3e38f);   // (differences stay in range)
         w.high = kCap ? small : kInf;
         // The new one stays out of S: the first of them in the first lane that has one.
         // What stands in its place counts for nothing; where the short way below is taken, which
@@ -309,10 +309,11 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             if (kEntropy) D = fmaf(e, d, D);
         }
     } else {
-        const float ref = w.top > -kInf ? w.ref : 0.0f;
+        // (half of the difference: that of two logits may leave f32's range)
+        const float ref = w.top > -kInf ? 0.5f * w.ref : 0.0f, c = 2.0f * cap.c;
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const float d = fmaxf((cap(x[i]) - ref) * cap.c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
+            const float d = fmaxf(fmaf(0.5f, cap(x[i]), -ref) * c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
             S += e;
             if (kEntropy) D = fmaf(e, d, D);
         }

@@ -264,3 +264,20 @@ def test_sums_of_long_rows(gd, V, high):
         for r in (0, n - 1):
             near(lp[r], np.array([-np.log1p(s)]), 0, 1)
             near(ent[r:r + 1], np.array([np.log1p(s) + d / (1 + s)]), 0, 1)
+
+
+@pytest.mark.parametrize("scale", [1e-36, 1e-37, 1e-38])
+def test_logits_whose_differences_leave_f32(gd, scale):
+    """Scales so small that logits of both ends of f32's range are next to each other."""
+    V = 5003
+    g = torch.Generator().manual_seed(1)
+    x = torch.empty(6, V)
+    x[0], x[0, 4000] = -2.9e38, 3e38
+    x[1], x[1, 7] = -3.4e38, 3.4e38
+    x[2] = torch.rand(V, generator=g).mul(2).sub(1) * 3.4e38
+    x[3] = torch.linspace(-3.4e38, 3.4e38, V)
+    x[4], x[4, ::2] = 3.3e38, -float("inf")
+    x[4, 1] = -3.3e38
+    x[5] = -3.4e38
+    run(gd, x.cuda(), given(6, V, 3, 2), 5, scale)
+    run(gd, x[3:4].cuda(), given(1, V, 1, 2), 5, scale)
