@@ -11,6 +11,7 @@
 // The k largest: a wave keeps those of its own logits in LDS, and the smallest that can still
 // be among the row's (the k-th largest of any wave). Of most vectors no lane's largest logit
 // reaches that, so that the selection costs a comparison.
+#include <algorithm>
 #include <type_traits>
 
 #include "gd_internal.h"
@@ -38,7 +39,7 @@ struct Task {
     int64_t *top_ids;
     float *top_logprobs;
     int64_t stride, n_given, k, n, V;
-    float scale, softcap;
+    float over, c, small;   // see Cap
     int64_t parts, part;   // of a row; tokens of one
     uint8_t *workspace;    // a Part and k keys for each part
 };
@@ -63,31 +64,36 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 }
 __device__ __forceinline__ u64 order_of(float x, uint32_t place) { return static_cast<u64>(key_of(x)) << 32 | ~place; }
 
-// What exponents are taken of: the logit, or over the cap tanh(x / cap); -infinity stays.
+// tanh(u) up to kSmall: u (1 + s q(s)), s = u^2, within 1.4e-7 (of u itself where that is small).
+constexpr float kSmall = 0.7f;
+constexpr float kTanh[4] = {-0.33330065f, 0.132769167f, -0.0506746806f, 0.0135997012f};
+
+// What exponents are taken of: the logit, or over the cap tanh(x / cap); -infinity stays. Where x
+// is small next to the cap the digits are those of x, not of the cap.
 template <bool kOn>
 struct Cap {
-    float over, c;   // 1 / softcap; what comes out is multiplied by c
-    __device__ __forceinline__ Cap(float softcap, float scale) : over(kOn ? 1.0f / softcap : 1.0f), c(kOn ? scale * softcap * kLog2e : scale * kLog2e) {}
+    float over, c, small;   // 1 / softcap; what comes out is multiplied by c; up to `small` Exponent may be used
+    __device__ __forceinline__ explicit Cap(const Task &t) : over(t.over), c(t.c), small(t.small) {}
     __device__ __forceinline__ float operator()(float x) const {
         if (!kOn) return x;
-        const float t = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * over * (2.0f * kLog2e))), 1.0f);
-        return x == -kInf ? x : t;
+        const float u = x * over, s = u * u, q = fmaf(fmaf(fmaf(kTanh[3], s, kTanh[2]), s, kTanh[1]), s, kTanh[0]);
+        const float t = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * (2.0f * kLog2e))), 1.0f);
+        return x == -kInf ? x : s <= kSmall * kSmall ? fmaf(u * s, q, u) : t;
     }
-    static constexpr float kSmall = 0.7f;   // of |x / softcap|, see Exponent
 };
 
-// (cap(x) - ref) c for many x: plainly, or with a cap where |x / softcap| <= kSmall as x times an
-// odd polynomial, within 1.4e-7 of tanh (times c). a[]: its coefficients in powers of x^2.
+// (cap(x) - ref) c for many x: plainly, or with a cap, where |x / softcap| <= kSmall, as x times an
+// odd polynomial. a[]: its coefficients in powers of x^2.
 template <bool kCap>
 struct Exponent {
     float ref, c, off, a[4];
     __device__ __forceinline__ Exponent(const Cap<kCap> &cap, float ref_) : ref(ref_), c(cap.c) {
         if (!kCap) return;
         const float s = cap.over * cap.over;
-        a[0] = -0.33330065f * s;
-        a[1] = 0.132769167f * s * s;
-        a[2] = -0.0506746806f * s * s * s;
-        a[3] = 0.0135997012f * s * s * s * s;
+        a[0] = kTanh[0] * s;
+        a[1] = kTanh[1] * s * s;
+        a[2] = kTanh[2] * s * s * s;
+        a[3] = kTanh[3] * s * s * s * s;
         c = cap.c * cap.over;
         off = -ref * cap.c;
     }
@@ -208,6 +214,11 @@ struct Best {
     }
 };
 
+// d where it is an exponent that counts: up to 0 (tanh's roundings, times a large cap, may pass it)
+// and down to where the exponential is 0.
+__device__ __forceinline__ float exponent(float d) { return __builtin_amdgcn_fmed3f(d, -1000.0f, 0.0f); }
+__device__ __forceinline__ double exponent(double d) { return fmin(fmax(d, -1000.0), 0.0); }
+
 // What a wave has met so far: the largest logit (-infinity before there is one), capped in
 // ref, and the lanes' shares of S and D against it. A step's terms are summed in f32, the steps in
 // f64: terms that are all alike all round the same way, which a chain of f32 sums over a row of
@@ -215,7 +226,7 @@ struct Best {
 struct Met {
     float top, ref;
     double S, D;
-    float low, high;   // logits between them need no care (see absorb)
+    float low;   // logits from here on need no care (see absorb), without a cap
     bool bad;
 };
 
@@ -264,25 +275,24 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             }
         if (best.count >= 2 * best.k) best.shrink();
     }
+    const auto is_easy = [&]() { return kCap ? least >= -cap.small && mine <= cap.small : least >= w.low; };
     float S = 0.0f, D = 0.0f;   // of this step
     if (__any(mine > w.top)) {   // a larger one: what was the largest joins the others, in lane 0
         const float top = wave_max(mine), ref = cap(top);
         if (w.top > -kInf) {
-            const double d = fmax((static_cast<double>(w.ref) - ref) * cap.c, -1000.0), f = __builtin_amdgcn_exp2f(static_cast<float>(d));
+            const double d = exponent((static_cast<double>(w.ref) - ref) * cap.c), f = __builtin_amdgcn_exp2f(static_cast<float>(d));
             const double own = threadIdx.x % 64 == 0 ? 1.0 : 0.0;
             if (kEntropy) w.D = f * (w.D + d * (w.S + own));
             w.S = f * (w.S + own);
         }
         w.top = top;
         w.ref = ref;
-        const float small = fminf(Cap<kCap>::kSmall / cap.over, 1e9f);   // (x^9 stays in range)
-        w.low = kCap ? -small : fmaxf(ref - fminf(1000.0f / cap.c, 3e38f), -3e38f);   // (differences stay in range)
-        w.high = kCap ? small : kInf;
+        if (!kCap) w.low = fmaxf(ref - fminf(1000.0f / cap.c, 3e38f), -3e38f);   // (differences stay in range)
         // The new one stays out of S: the first of them in the first lane that has one.
         // What stands in its place counts for nothing; where the short way below is taken, which
         // has no -infinity, what it counts for is taken off S first.
-        const bool small_enough = __all(least >= w.low && mine <= w.high);
-        const float out = small_enough ? w.low : -kInf;
+        const bool easy = __all(is_easy());
+        const float out = easy ? (kCap ? -cap.small : w.low) : -kInf;
         const bool chosen = static_cast<int>(threadIdx.x % 64) == __ffsll(__ballot(mine == top)) - 1;
         bool here = chosen;
 #pragma unroll
@@ -291,7 +301,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             x[i] = is ? out : x[i];
             here = here && !is;
         }
-        if (small_enough) {
+        if (easy) {
             const Exponent<kCap> of(cap, ref);
             const float d = of(out), e = __builtin_amdgcn_exp2f(d);
             if (chosen) {
@@ -300,7 +310,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             }
         }
     }
-    if (__all(least >= w.low && mine <= w.high)) {   // no 0 times infinity in D, and a short tanh
+    if (__all(is_easy())) {   // no 0 times infinity in D, and a short tanh
         const Exponent<kCap> of(cap, w.ref);
 #pragma unroll
         for (int i = 0; i < N; i++) {
@@ -313,7 +323,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
         const float ref = w.top > -kInf ? 0.5f * w.ref : 0.0f, c = 2.0f * cap.c;
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const float d = fmaxf(fmaf(0.5f, cap(x[i]), -ref) * c, -1000.0f), e = __builtin_amdgcn_exp2f(d);
+            const float d = exponent(fmaf(0.5f, cap(x[i]), -ref) * c), e = __builtin_amdgcn_exp2f(d);
             S += e;
             if (kEntropy) D = fmaf(e, d, D);
         }
@@ -326,7 +336,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
 // with its own largest logit, which it holds out of them; nothing if it has none.
 template <bool kCap>
 __device__ __forceinline__ void against(const Cap<kCap> &cap, float top, const Part &p, double &S, double &D) {
-    const double d = fmax((static_cast<double>(cap(p.top)) - cap(top)) * cap.c, -1000.0);
+    const double d = exponent((static_cast<double>(cap(p.top)) - cap(top)) * cap.c);
     const double f = p.top > -kInf ? static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(d))) : 0.0;
     S = f * (p.S + 1.0);
     D = f * (p.D + d * (p.S + 1.0));
@@ -430,7 +440,7 @@ __device__ __forceinline__ void answer(const Task &t, const Cap<kCap> &cap, int6
     const auto lp_of = [&](float x) {
         if (bad) return __builtin_nanf("");
         if (none || x == -kInf) return -kInf;
-        return static_cast<float>((static_cast<double>(cap(x)) - y) * cap.c * kLn2 - lse);
+        return static_cast<float>(fmin((static_cast<double>(cap(x)) - y) * cap.c, 0.0) * kLn2 - lse);
     };
     if (t.entropy && threadIdx.x == 0)
         t.entropy[row] = bad ? __builtin_nanf("") : none ? 0.0f : lse - static_cast<float>(kLn2 * all.D) / (1.0f + static_cast<float>(all.S));
@@ -472,8 +482,8 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_part_kernel(Task t) {
     const uint32_t vectors = static_cast<uint32_t>((length - head) / PER);
     const int tail = static_cast<int>(length - head - static_cast<int64_t>(vectors) * PER);
     const Vec *body = reinterpret_cast<const Vec *>(x + head);
-    const Cap<kCap> cap(t.softcap, t.scale);
-    Met met = {-kInf, 0.0f, 0.0, 0.0, kInf, -kInf, false};
+    const Cap<kCap> cap(t);
+    Met met = {-kInf, 0.0f, 0.0, 0.0, kInf, false};
     Best best = {room[wave], &shared, 0, static_cast<int>(t.k), 0, -kInf};
     if (tid == 0) shared = 0;
     __syncthreads();
@@ -579,7 +589,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Task t) {
     __shared__ int count;
     const int64_t row = blockIdx.x, size = sizeof(Part) + 8 * t.k;
     const uint8_t *in = t.workspace + row * t.parts * size;
-    const Cap<kCap> cap(t.softcap, t.scale);
+    const Cap<kCap> cap(t);
     const int k = static_cast<int>(t.k), tid = threadIdx.x;
     const Given asked = given<T>(t, row, tid);
     const auto entry = [&](int64_t p, int i) { return reinterpret_cast<const u64 *>(in + p * size + sizeof(Part))[i]; };
@@ -667,7 +677,10 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
     GD_REQUIRE(aligned(logits, dtype_size(dtype)) && aligned(tokens, 8) && aligned(logprobs, 4) && aligned(entropy, 4) &&
                    aligned(top_ids, 8) && aligned(top_logprobs, 4) && aligned(workspace, 16),
                GD_EALIGN, "%s: a pointer is not aligned to its element (the workspace: 16)", name);
-    Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, n, V, scale, softcap,
+    const float over = softcap > 0.0f ? 1.0f / softcap : 1.0f, c = (softcap > 0.0f ? scale * softcap : scale) * kLog2e;
+    // (x^9 stays in range, and both terms of an exponent below 2e4, so that their roundings are small)
+    const float small = std::min({kSmall / over, 1e9f, 1e4f / (c * over)});
+    Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, n, V, over, c, small,
               parts_of(n, V), 0, static_cast<uint8_t *>(workspace)};
     if (t.parts > 1) {
         t.part = (V + t.parts - 1) / t.parts;

@@ -281,3 +281,31 @@ def test_logits_whose_differences_leave_f32(gd, scale):
     x[5] = -3.4e38
     run(gd, x.cuda(), given(6, V, 3, 2), 5, scale)
     run(gd, x[3:4].cuda(), given(1, V, 1, 2), 5, scale)
+
+
+@pytest.mark.parametrize("cap,size,scale", [(cap, size, scale) for cap in (1e4, 1e6, 1e10, 1e30)
+                                            for size, scale in ((50.0, 1.0), (50.0, 0.5), (3000.0, 0.01), (1e8, 1e-6), (1e9, 1e-7))
+                                            if cap >= 20 * size])
+def test_caps_far_above_the_logits(gd, cap, size, scale):
+    """A cap of 20 times the logits and more: they are held to 2^-20 of the largest of them (every value in z comes from at most 8
+    roundings, 2^-21 of itself, and is taken against the largest's)."""
+    V = 9001
+    g = torch.Generator().manual_seed(3)
+    x = torch.rand(6, V, generator=g).mul(2).sub(1).mul(size)
+    x[1, ::3] = -float("inf")
+    x[2] = size
+    x[3] = -size
+    x[3, 5] = size
+    x[4] = x[4].sort().values
+    x[5, 7] = 2e30 if cap == 1e30 else x[5, 7]
+    x = x.cuda()
+    for n, rows in ((6, range(5 + (cap < 1e30))), (300, [0, 4, 299])):
+        many = x.repeat(n // 6, 1).contiguous()
+        lp, ent = torch.empty(n, 1, device="cuda"), torch.empty(n, device="cuda")
+        gd.token_logprobs(many, torch.full((n, 1), 11, device="cuda"), lp, ent, None, None, n, V, scale=scale, softcap=cap)
+        assert not bool(lp.isnan().any()) and not bool(ent.isnan().any())
+        for r in rows:
+            w_lp, w_ent, _, _ = answer.logprobs(many[r].cpu().numpy(), np.array([11]), 0, scale, cap)
+            if r % 6 != 5 or cap < 1e30:
+                near(lp[r], w_lp, size, scale)
+                near(ent[r:r + 1], np.array([w_ent]), size, scale)
