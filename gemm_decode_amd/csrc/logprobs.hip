@@ -30,6 +30,7 @@ constexpr int kFill = 512;           // parts of all rows that fill the device
 constexpr float kInf = __builtin_inff();
 constexpr float kLog2e = 1.44269504f;
 constexpr double kLn2 = 0.693147180559945309;
+constexpr float kNear = 24.0f;       // a step this far below the largest logit (to the base 2) has one of its own
 typedef unsigned long long u64;
 
 struct Task {
@@ -39,7 +40,7 @@ struct Task {
     int64_t *top_ids;
     float *top_logprobs;
     int64_t stride, n_given, k, n, V;
-    float over, c, small;   // see Cap
+    float c, more, small;   // see Cap
     int64_t parts, part;   // of a row; tokens of one
     uint8_t *workspace;    // a Part and k keys for each part
 };
@@ -72,8 +73,10 @@ constexpr float kTanh[4] = {-0.33330065f, 0.132769167f, -0.0506746806f, 0.013599
 // is small next to the cap the digits are those of x, not of the cap.
 template <bool kOn>
 struct Cap {
-    float over, c, small;   // 1 / softcap; what comes out is multiplied by c; up to `small` Exponent may be used
-    __device__ __forceinline__ explicit Cap(const Task &t) : over(t.over), c(t.c), small(t.small) {}
+    float over, c;   // 1 / softcap; what comes out is multiplied by c
+    float rest;      // what c lacks by its rounding, without a cap
+    float small;     // up to which Exponent may be used, with one
+    __device__ __forceinline__ explicit Cap(const Task &t) : over(kOn ? t.more : 1.0f), c(t.c), rest(kOn ? 0.0f : t.more), small(t.small) {}
     __device__ __forceinline__ float operator()(float x) const {
         if (!kOn) return x;
         const float u = x * over, s = u * u, q = fmaf(fmaf(fmaf(kTanh[3], s, kTanh[2]), s, kTanh[1]), s, kTanh[0]);
@@ -219,6 +222,15 @@ struct Best {
 __device__ __forceinline__ float exponent(float d) { return __builtin_amdgcn_fmed3f(d, -1000.0f, 0.0f); }
 __device__ __forceinline__ double exponent(double d) { return fmin(fmax(d, -1000.0), 0.0); }
 
+// The exponential of (a - b) c for an a up to b, to f32's last bits however far they are apart
+// (an exponent rounded to f32 is off by up to |exponent| 2^-25).
+template <bool kCap>
+__device__ __forceinline__ double apart(const Cap<kCap> &cap, float a, float b, double &d) {
+    d = exponent((static_cast<double>(a) - b) * (kCap ? cap.c : static_cast<double>(cap.c) + cap.rest));
+    const float hi = static_cast<float>(d), e = __builtin_amdgcn_exp2f(hi);
+    return kCap ? e : e * (1.0 + kLn2 * (d - hi));
+}
+
 // What a wave has met so far: the largest logit (-infinity before there is one), capped in
 // ref, and the lanes' shares of S and D against it. A step's terms are summed in f32, the steps in
 // f64: terms that are all alike all round the same way, which a chain of f32 sums over a row of
@@ -226,7 +238,7 @@ __device__ __forceinline__ double exponent(double d) { return fmin(fmax(d, -1000
 struct Met {
     float top, ref;
     double S, D;
-    float low;   // logits from here on need no care (see absorb), without a cap
+    float low, near;   // without a cap: logits from here on need no care, or no largest one of their own (see absorb)
     bool bad;
 };
 
@@ -275,25 +287,29 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             }
         if (best.count >= 2 * best.k) best.shrink();
     }
+    // (The ends, a logit a lane, have one way only: they are short, and code that runs once is fetched first.)
+    constexpr bool kEnds = N == 1;
     const auto is_easy = [&]() { return kCap ? least >= -cap.small && mine <= cap.small : least >= w.low; };
-    float S = 0.0f, D = 0.0f;   // of this step
+    bool chosen = false;   // the lane that holds the step's new largest logit
+    float out = -kInf;     // what stands in its place
     if (__any(mine > w.top)) {   // a larger one: what was the largest joins the others, in lane 0
         const float top = wave_max(mine), ref = cap(top);
         if (w.top > -kInf) {
-            const double d = exponent((static_cast<double>(w.ref) - ref) * cap.c), f = __builtin_amdgcn_exp2f(static_cast<float>(d));
+            double d;
+            const double f = apart(cap, w.ref, ref, d);
             const double own = threadIdx.x % 64 == 0 ? 1.0 : 0.0;
             if (kEntropy) w.D = f * (w.D + d * (w.S + own));
             w.S = f * (w.S + own);
         }
         w.top = top;
         w.ref = ref;
+        if (!kCap) w.near = ref - kNear / cap.c;
         if (!kCap) w.low = fmaxf(ref - fminf(1000.0f / cap.c, 3e38f), -3e38f);   // (differences stay in range)
         // The new one stays out of S: the first of them in the first lane that has one.
         // What stands in its place counts for nothing; where the short way below is taken, which
         // has no -infinity, what it counts for is taken off S first.
-        const bool easy = __all(is_easy());
-        const float out = easy ? (kCap ? -cap.small : w.low) : -kInf;
-        const bool chosen = static_cast<int>(threadIdx.x % 64) == __ffsll(__ballot(mine == top)) - 1;
+        if (__all(is_easy())) out = kCap ? -cap.small : w.low;
+        chosen = static_cast<int>(threadIdx.x % 64) == __ffsll(__ballot(mine == top)) - 1;
         bool here = chosen;
 #pragma unroll
         for (int i = 0; i < N; i++) {
@@ -301,17 +317,32 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             x[i] = is ? out : x[i];
             here = here && !is;
         }
-        if (easy) {
-            const Exponent<kCap> of(cap, ref);
-            const float d = of(out), e = __builtin_amdgcn_exp2f(d);
-            if (chosen) {
-                S = -e;
-                if (kEntropy) D = -e * d;
-            }
+        if (!kCap) {   // the largest of the others
+            mine = -kInf;
+#pragma unroll
+            for (int i = 0; i < N; i++) mine = max_nan(mine, x[i]);
         }
     }
+    // A step whose logits all lie far below the largest one, as next to a token that the model is sure
+    // of, is summed against its own largest one: an f32 exponent d against the other is off by up to
+    // |d| 2^-22.4, and so is its exponential.
+    float ref = w.top > -kInf ? w.ref : 0.0f;
+    double down = 0.0, factor = 1.0;
+    if (!kCap && !__any(mine >= w.near)) {
+        const float most_here = wave_max(mine);
+        if (most_here > -kInf) {
+            factor = apart(cap, most_here, ref, down);
+            ref = most_here;
+        }
+    }
+    float S = 0.0f, D = 0.0f;
     if (__all(is_easy())) {   // no 0 times infinity in D, and a short tanh
-        const Exponent<kCap> of(cap, w.ref);
+        const Exponent<kCap> of(cap, ref);
+        if (chosen) {   // (what stands there counts for nothing)
+            const float d = of(out), e = __builtin_amdgcn_exp2f(d);
+            S = -e;
+            if (kEntropy) D = -e * d;
+        }
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const float d = of(x[i]), e = __builtin_amdgcn_exp2f(d);
@@ -320,24 +351,23 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
         }
     } else {
         // (half of the difference: that of two logits may leave f32's range)
-        const float ref = w.top > -kInf ? 0.5f * w.ref : 0.0f, c = 2.0f * cap.c;
+        const float half = 0.5f * ref, c = 2.0f * cap.c;
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const float d = exponent(fmaf(0.5f, cap(x[i]), -ref) * c), e = __builtin_amdgcn_exp2f(d);
+            const float d = exponent(fmaf(0.5f, cap(x[i]), -half) * c), e = __builtin_amdgcn_exp2f(d);
             S += e;
             if (kEntropy) D = fmaf(e, d, D);
         }
     }
-    w.S += S;
-    if (kEntropy) w.D += D;
+    if (kEntropy) w.D += factor * (D + down * S);
+    w.S += factor * S;
 }
-
 // What a part adds to the sums against `top`, a logit as large as its own: its share of S and D
 // with its own largest logit, which it holds out of them; nothing if it has none.
 template <bool kCap>
 __device__ __forceinline__ void against(const Cap<kCap> &cap, float top, const Part &p, double &S, double &D) {
-    const double d = exponent((static_cast<double>(cap(p.top)) - cap(top)) * cap.c);
-    const double f = p.top > -kInf ? static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(d))) : 0.0;
+    double d;
+    const double e = apart(cap, cap(p.top), cap(top), d), f = p.top > -kInf ? e : 0.0;
     S = f * (p.S + 1.0);
     D = f * (p.D + d * (p.S + 1.0));
 }
@@ -483,7 +513,7 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_part_kernel(Task t) {
     const int tail = static_cast<int>(length - head - static_cast<int64_t>(vectors) * PER);
     const Vec *body = reinterpret_cast<const Vec *>(x + head);
     const Cap<kCap> cap(t);
-    Met met = {-kInf, 0.0f, 0.0, 0.0, kInf, false};
+    Met met = {-kInf, 0.0f, 0.0, 0.0, kInf, kInf, false};
     Best best = {room[wave], &shared, 0, static_cast<int>(t.k), 0, -kInf};
     if (tid == 0) shared = 0;
     __syncthreads();
@@ -678,9 +708,10 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
                    aligned(top_ids, 8) && aligned(top_logprobs, 4) && aligned(workspace, 16),
                GD_EALIGN, "%s: a pointer is not aligned to its element (the workspace: 16)", name);
     const float over = softcap > 0.0f ? 1.0f / softcap : 1.0f, c = (softcap > 0.0f ? scale * softcap : scale) * kLog2e;
+    const float more = softcap > 0.0f ? over : static_cast<float>(scale / kLn2 - c);
     // (x^9 stays in range, and both terms of an exponent below 2e4, so that their roundings are small)
     const float small = std::min({kSmall / over, 1e9f, 1e4f / (c * over)});
-    Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, n, V, over, c, small,
+    Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, n, V, c, more, small,
               parts_of(n, V), 0, static_cast<uint8_t *>(workspace)};
     if (t.parts > 1) {
         t.part = (V + t.parts - 1) / t.parts;

@@ -309,3 +309,24 @@ def test_caps_far_above_the_logits(gd, cap, size, scale):
             if r % 6 != 5 or cap < 1e30:
                 near(lp[r], w_lp, size, scale)
                 near(ent[r:r + 1], np.array([w_ent]), size, scale)
+
+
+# Scales, leading logits and the others, 50 to 62 below in z: where f32's (x - top) c, c = f32(scale log2 e), is off by 0.95
+# to 1.28 times the bound, in both directions.
+FAR = [(1.0, 60.0, 0.0), (0.7123311758041382, 3.426105499267578, -66.76596069335938),
+       (1.4191744327545166, 2.1121349334716797, -33.11961364746094), (0.7089429497718811, 8.91403579711914, -70.07681274414062),
+       (1.486048698425293, 2.554197311401367, -35.12963104248047), (1.408717155456543, 3.893655776977539, -38.69828796386719),
+       (1.456974983215332, 8.258298873901367, -32.92291259765625), (1.3893790245056152, 9.705148696899414, -34.919105529785156)]
+
+
+@pytest.mark.parametrize("scale,top,rest", FAR)
+def test_tokens_far_ahead(gd, scale, top, rest):
+    """The leading token first, in the middle and last, of one wave's rows, rows cut into parts and long whole ones, banned
+    tokens among them."""
+    for n, V in ((1, 256), (1, 50000), (300, 50000)):
+        for place in (0, V // 2, V - 1):
+            x = torch.full((n + 1, V), rest, device="cuda")
+            x[-1, 5::7] = -float("inf")
+            x[:, place] = top
+            tokens = torch.tensor([[place, 6]] * (n + 1), device="cuda")
+            run(gd, x, tokens, 1, scale, rows=[0, n])
