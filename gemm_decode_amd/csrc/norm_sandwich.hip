@@ -99,7 +99,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
             ss += square4(v[0]) + square4(v[1]);
         }
         group_sum_max<W, false>(ss, amax, red[0]);
-        if (!dropped) factor *= rsqrt_f64(__builtin_fma(ss, s.per, static_cast<double>(s.eps)));
+        const double mean = __builtin_fma(ss, s.per, static_cast<double>(s.eps));
+        if (!dropped) factor *= mean == 0.0 ? 0.0 : rsqrt_f64(mean);   // a row of zeros without eps
         ss = 0.0;
     }
     float top = 0.0f;

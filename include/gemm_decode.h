@@ -477,7 +477,8 @@ int rmsnorm_ternary_act(const void *x, const void *residual, const float *weight
  *   u = x * rstd(x) * post_weight     (u = x without post_weight)
  *   h = residual_scale * residual + block_scale * gate * u
  * in f64, rounded to f32 and then to dtype, and the norm of h quantized as above.
- * rstd(x) = 1 / sqrt(mean over the row of x^2 + eps), the same eps as h's.
+ * rstd(x) = 1 / sqrt(mean over the row of x^2 + eps), the same eps as h's; u = 0 for
+ * a row of zeros, where eps is 0 too.
  *   x, residual  device dtype [n][K].
  *   post_weight  device f32 [K] or NULL.
  *   gate         device dtype [n_gates][K], or NULL (1; n_gates is ignored).

@@ -182,3 +182,29 @@ def test_rows_that_take_nothing_of_their_block(gd, K, post, eps):
     alone = torch.empty_like(a)
     gd.rmsnorm_q8_0(want, None, w, None, alone, n, K, eps)
     assert torch.equal(a.view(n, -1)[rows], alone.view(n, -1)[rows])
+
+
+@pytest.mark.parametrize("n,K", [(3, 96), (3, 4096), (3, 8224), (1030, 512), (1030, 1056)])
+@pytest.mark.parametrize("form", ["q8_0", "ternary"])
+def test_blocks_of_zeros_without_eps(gd, n, K, form):
+    """A row whose block put out zeros adds nothing to the stream where eps is 0, as where it is not."""
+    for T in TYPES:
+        g = torch.Generator().manual_seed(n + K)
+        x, res = (torch.randn(n, K, generator=g).to(T).cuda() for _ in range(2))
+        w, post = (torch.randn(K, generator=g).add(1).cuda() for _ in range(2))
+        gate = torch.randn(1, K, generator=g).to(T).cuda()
+        x[1] = 0
+        h = torch.empty_like(x)
+        outs = []
+        for h_out in (h, None):
+            out = (torch.empty(n * (K // 32) * 34, dtype=torch.uint8, device="cuda"),) if form == "q8_0" else \
+                (torch.empty(n * 8 * (K // 32), dtype=torch.int32, device="cuda"), torch.empty(n, device="cuda"))
+            of = gd.rmsnorm_sandwich_q8_0 if form == "q8_0" else gd.rmsnorm_sandwich_ternary_act
+            of(x, post, res, w, h_out, *out, n, K, 0.0, gate=gate, residual_scale=0.75)
+            outs.append(out)
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+        want = (res[1].double() * 0.75).float().to(T)
+        assert torch.equal(h[1], want) and bool(h.isfinite().all())
+        alone = [torch.empty(o.numel() // n, dtype=o.dtype, device="cuda") for o in outs[0]]
+        (gd.rmsnorm_q8_0 if form == "q8_0" else gd.rmsnorm_ternary_act)(want, None, w, None, *alone, 1, K, 0.0)
+        assert all(torch.equal(a.view(n, -1)[1], b) for a, b in zip(outs[0], alone))
