@@ -71,11 +71,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
         gate = dropped ? nullptr : gate + g * s.K;
         if (dropped) factor = 0.0;
     }
+    const float *post_weight = dropped ? nullptr : s.post_weight;   // (a whole workgroup's, or a wave's without barriers)
     const auto group_of = [&](int i) { return i * kT + 2 * tid; };
     const f32x4 ones = {1.0f, 1.0f, 1.0f, 1.0f};
     const auto load_side = [&](int64_t at, f32x4 *post, f32x4 *gates) {
         post[0] = post[1] = gates[0] = gates[1] = ones;
-        if (s.post_weight) load_groups<2, float>(s.post_weight, nullptr, at, post);
+        if (post_weight) load_groups<2, float>(post_weight, nullptr, at, post);
         if (gate) load_groups<2, T>(gate, nullptr, at, gates);
     };
     f32x4 h[R], r[R], w[R], post[R], gates[R];
@@ -89,7 +90,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
         load_side(at, post + i, gates + i);
         load_groups<2, float>(s.weight, nullptr, at, w + i);
     }
-    if (s.post_weight) {
+    if (post_weight) {
 #pragma unroll
         for (int i = 0; i < R; i++)
             if (group_of(i - i % 2) < nq) ss += square4(h[i]);
@@ -100,7 +101,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_sandwich_kernel
         }
         group_sum_max<W, false>(ss, amax, red[0]);
         const double mean = __builtin_fma(ss, s.per, static_cast<double>(s.eps));
-        if (!dropped) factor *= mean == 0.0 ? 0.0 : rsqrt_f64(mean);   // a row of zeros without eps
+        factor *= mean == 0.0 ? 0.0 : rsqrt_f64(mean);   // a row of zeros without eps
         ss = 0.0;
     }
     float top = 0.0f;

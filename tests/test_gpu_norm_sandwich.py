@@ -208,3 +208,21 @@ def test_blocks_of_zeros_without_eps(gd, n, K, form):
         alone = [torch.empty(o.numel() // n, dtype=o.dtype, device="cuda") for o in outs[0]]
         (gd.rmsnorm_q8_0 if form == "q8_0" else gd.rmsnorm_ternary_act)(want, None, w, None, *alone, 1, K, 0.0)
         assert all(torch.equal(a.view(n, -1)[1], b) for a, b in zip(outs[0], alone))
+
+
+@pytest.mark.parametrize("n,K", [(3, 96), (3, 4096), (3, 8224), (1030, 512), (1030, 1056)])
+@pytest.mark.parametrize("form", ["q8_0", "ternary"])
+def test_rows_without_a_gate_take_nothing_of_the_weight_behind_the_block(gd, n, K, form):
+    """h = residual_scale residual there, whatever post_weight holds (infinities and NaN)."""
+    for T in TYPES:
+        g = torch.Generator().manual_seed(n + K)
+        x, res = (torch.randn(n, K, generator=g).to(T).cuda() for _ in range(2))
+        w, post = (torch.randn(K, generator=g).add(1).cuda() for _ in range(2))
+        post[1], post[K - 1] = float("inf"), float("nan")
+        gate = torch.randn(1, K, generator=g).to(T).cuda()
+        index = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+        h = torch.empty_like(x)
+        got = call(gd, form, x, post, res, w, h, n, K, gate=gate, gate_index=index, residual_scale=0.75)
+        check(form, got, h, w, T, 0.75 * f64(res))
+        bare = call(gd, form, x, post, res, w, None, n, K, gate=gate, gate_index=index, residual_scale=0.75)
+        assert all(torch.equal(a, b) for a, b in zip(got, bare))
