@@ -330,3 +330,21 @@ def test_tokens_far_ahead(gd, scale, top, rest):
             x[:, place] = top
             tokens = torch.tensor([[place, 6]] * (n + 1), device="cuda")
             run(gd, x, tokens, 1, scale, rows=[0, n])
+
+
+def test_rows_past_one_grid(gd):
+    """More rows than a launch takes: all outputs beside the borders."""
+    n, V, k, m = 2 * 65535 + 3, 37, 3, 2
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(n, V, generator=g).mul(3).half().cuda()
+    tokens = torch.randint(-1, V, (n, m), generator=g).cuda()
+    run(gd, x, tokens, k, rows=[0, 1, 65533, 65534, 65535, 65536, 131069, 131070, 131071, n - 1])
+
+
+@pytest.mark.parametrize("m", [256, 257, 1000])
+def test_many_tokens_of_a_row(gd, m):
+    """More given tokens than a workgroup has threads, of whole rows and of rows cut into parts."""
+    for n, V in ((3, 1000), (2, 50021), (300, 3001)):
+        g = torch.Generator().manual_seed(m)
+        x = torch.randn(n, V, generator=g).mul(3).cuda()
+        run(gd, x, given(n, V, m, m), 2, rows=[0, n - 1])
