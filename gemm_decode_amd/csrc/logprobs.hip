@@ -39,7 +39,7 @@ struct Task {
     float *logprobs, *entropy;
     int64_t *top_ids;
     float *top_logprobs;
-    int64_t stride, n_given, k, n, V;
+    int64_t stride, n_given, k, V;
     float c, more, small;   // see Cap
     int64_t parts, part;   // of a row; tokens of one
     uint8_t *workspace;    // a Part and k keys for each part
@@ -564,23 +564,21 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_part_kernel(Task t) {
     int total = 0;
     if (t.k) {   // the waves' candidates side by side, those that can still be among the k
         const u64 least = shared;
-        u64 mine[kWaves * kMaxK / kThreads];
-        int at[kWaves * kMaxK / kThreads];
         static_assert(kWaves * kMaxK == kThreads, "a candidate a thread");
         const int c = counts[wave];
-        mine[0] = lane < c ? room[wave][lane] : 0;
-        if (mine[0] < least) mine[0] = 0;
-        const u64 in = __ballot(mine[0] > 0);
+        u64 mine = lane < c ? room[wave][lane] : 0;
+        if (mine < least) mine = 0;
+        const u64 in = __ballot(mine > 0);
         __syncthreads();
         if (lane == 0) counts[wave] = __popcll(in);
         __syncthreads();
-        at[0] = __popcll(in & ((u64{1} << lane) - 1));
+        int at = __popcll(in & ((u64{1} << lane) - 1));
         for (int w = 0; w < kWaves; w++) {
-            if (w < wave) at[0] += counts[w];
+            if (w < wave) at += counts[w];
             total += counts[w];
         }
         u64 *list = room[0];
-        if (mine[0]) list[at[0]] = mine[0];
+        if (mine) list[at] = mine;
         __syncthreads();
         sort_best(list, total, static_cast<int>(t.k), sorted);
     }
@@ -711,7 +709,7 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
     const float more = softcap > 0.0f ? over : static_cast<float>(scale / kLn2 - c);
     // (x^9 stays in range, and both terms of an exponent below 2e4, so that their roundings are small)
     const float small = std::min({kSmall / over, 1e9f, 1e4f / (c * over)});
-    Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, n, V, c, more, small,
+    Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, V, c, more, small,
               parts_of(n, V), 0, static_cast<uint8_t *>(workspace)};
     if (t.parts > 1) {
         t.part = (V + t.parts - 1) / t.parts;
