@@ -327,11 +327,13 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
     // of, is summed against its own largest one: an f32 exponent d against the other is off by up to
     // |d| 2^-22.4, and so is its exponential.
     float ref = w.top > -kInf ? w.ref : 0.0f;
-    double down = 0.0, factor = 1.0;
+    float down = 0.0f, factor = 1.0f;
     if (!kCap && !__any(mine >= w.near)) {
         const float most_here = wave_max(mine);
         if (most_here > -kInf) {
-            factor = apart(cap, most_here, ref, down);
+            double d;
+            factor = static_cast<float>(apart(cap, most_here, ref, d));
+            down = static_cast<float>(d);
             ref = most_here;
         }
     }
@@ -359,7 +361,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             if (kEntropy) D = fmaf(e, d, D);
         }
     }
-    if (kEntropy) w.D += factor * (D + down * S);
+    if (kEntropy) w.D += factor * fmaf(down, S, D);
     w.S += factor * S;
 }
 // What a part adds to the sums against `top`, a logit as large as its own: its share of S and D
