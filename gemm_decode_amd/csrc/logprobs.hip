@@ -490,12 +490,12 @@ __device__ __forceinline__ void answer(const Task &t, const Cap<kCap> &cap, int6
 // A part of a row: whole 16-byte vectors, U of them a thread at a time with the next ones on
 // their way, and the tokens before and behind them one by one.
 //
-// 2039 rows of 100003 bf16 (408 MB) take 122 us with a softcap and 94 without: some 22 and 18
+// 2039 rows of 100003 bf16 (408 MB) take 116 us with a softcap and 95 without: some 22 and 18
 // vector instructions a logit (an exponential counts for four), 59 us for the bytes alone. Four waves
-// a SIMD (launch bounds) instead of two 133 -> 122. Few rows are a chain of latencies, of which
-// the selection is the longer half: one row of 49152 6.1 us and with 8 alternatives 10.5, both
-// launches together; 61 of 50021 f16 8.1 and with 20 alternatives 17.3. There each wave goes once
-// through some 1900 instructions, and waits for about half of the time, for memory, barriers and
+// a SIMD (launch bounds) instead of two saved 8 % of it. Few rows are a chain of latencies, of which
+// the selection is the longer half: one row of 49152 5.8 us and with 8 alternatives 10.4, both
+// launches together; 61 of 50021 f16 8.1 and with 20 alternatives 17.4. There each wave goes once
+// through some 2000 instructions, and waits for about half of the time, for memory, barriers and
 // the instructions themselves.
 template <typename T, int U, bool kEntropy, bool kCap>
 __global__ __launch_bounds__(kThreads, 4) void logprobs_part_kernel(Task t) {
@@ -655,9 +655,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Task t) {
 }
 
 // Rows are cut into up to kFill parts in all, two workgroups a CU, of kMinPart tokens at least.
-// (A few parts more, and some CUs have three: 61 rows of 50021 f16 without alternatives 8.7 us,
-// with 549 parts 10.1; 400 rows of 100003 uncut 36.5, cut in two 39.5. Half as many parts: 16
-// rows of 50021 with 20 alternatives 15.8 us -> 17.5, 32 of 128256 17.5 -> 21.3.)
+// (A few parts more, and some CUs have three: 61 rows of 50021 f16 without alternatives 8.1 us,
+// with 549 parts 9.6; 400 rows of 100003 f32 uncut 30.6, cut in two 37.3. Half as many parts: 16
+// rows of 50021 with 20 alternatives 13.7 us -> 16.0, 32 of 128256 15.4 -> 18.8.)
 int64_t parts_of(int64_t n, int64_t V) {
     const int64_t want = n < kFill ? kFill / n : 1, most = (V + kMinPart - 1) / kMinPart;
     return want < most ? want : most;

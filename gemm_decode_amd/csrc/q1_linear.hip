@@ -931,7 +931,7 @@ __global__ __launch_bounds__(256, 2) void q1_wide_kernel(Weight w0, Weight w1, c
 
 // Batches: KS waves share the sums of 32 columns and NT = TN S tiles of 32 weight rows by K,
 // each loading its digits to registers a block ahead, and add them up in LDS. 37 columns gated at
-// 6912 x 2560 take 14.2 us, 64 at 4096 x 4096 15.6: two or three launches, each a few latencies
+// 6912 x 2560 take 13.5 to 14.2 us, 64 at 4096 x 4096 15.1 to 15.6: two or three launches, each a few latencies
 // long, and what the digits take from L2 (12.5 KB for a wave's block; 54 MB in all for the former).
 template <int TN, int S, int KS>
 __global__ __launch_bounds__(64 * KS, 2) void q1_split_kernel(Weight w0, Weight w1, const uint8_t *__restrict__ digits, Epilogue e,
@@ -1083,10 +1083,10 @@ int check(const char *name, const Weight *w, int count, const void *a_q8, const 
     return GD_OK;
 }
 
-// With so many blocks for its workgroups to go through the wide kernel is the faster one: 64
-// columns at 4096 x 4096 (512) 20.6 us against 14.4, 509 (4096) 38.5 against 32.4, 1000 (8192) 55
-// against 63, gated, 37 at 14336 x 4096 (3584) 33.6 against 27.2, 200 at 14336 x 4096 (12544) 67
-// against 73, 2039 at 4096 x 14336 (57344) 263 against 859.
+// With so many blocks for its workgroups to go through the wide kernel is the faster one (both
+// on one card): 64 columns at 4096 x 4096 (512) 20.1 us against 15.1, 509 (4096) 40.8 against 34.4,
+// 1000 (8192) 56 against 65, gated, 37 at 14336 x 4096 (3584) 33.3 against 26.2, 200 at 14336 x 4096
+// (12544) 69 against 76, 2039 at 4096 x 14336 (57344) 254 against 420.
 constexpr int64_t kWideFrom = 8000;
 // Up to so many workgroups of four tiles a wave the kernel without an operand pass is the faster
 // one: of 8 columns 14336 x 4096 9.6 us against 15.6, 49152 x 4096 (768 workgroups) 25.8 against
