@@ -698,7 +698,7 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
     GD_REQUIRE(k == 0 || (top_ids && top_logprobs), GD_EINVAL, "%s: null top_ids or top_logprobs", name);
     GD_REQUIRE(n_given || k || entropy, GD_EINVAL, "%s: nothing is asked for", name);
     GD_REQUIRE(dtype_ok(dtype), GD_EINVAL, "%s: unknown dtype %d", name, dtype);
-    // (Where 1 / softcap to the eighth and scale * softcap stay in f32's range.)
+    // (Where scale * softcap stays in f32's range.)
     GD_REQUIRE(scale > 0.0f && scale <= 1e30f, GD_EINVAL, "%s: scale must be > 0 and at most 1e30", name);
     GD_REQUIRE(softcap == 0.0f || (softcap >= 1e-4f && softcap <= 1e30f && static_cast<double>(scale) * softcap <= 1e30f), GD_EINVAL,
                "%s: softcap must be 0 or in [1e-4, 1e30], times scale at most 1e30", name);
@@ -709,8 +709,9 @@ extern "C" int token_logprobs(const void *logits, int64_t stride, const int64_t 
                GD_EALIGN, "%s: a pointer is not aligned to its element (the workspace: 16)", name);
     const float over = softcap > 0.0f ? 1.0f / softcap : 1.0f, c = (softcap > 0.0f ? scale * softcap : scale) * kLog2e;
     const float more = softcap > 0.0f ? over : static_cast<float>(scale / kLn2 - c);
-    // (x^9 stays in range, and both terms of an exponent below 2e4, so that their roundings are small)
-    const float small = std::min({kSmall / over, 1e9f, 1e4f / (c * over)});
+    // Where 1 / softcap to the eighth and x^9 stay in range (none otherwise: the careful way), and both terms
+    // of an exponent below 2e4, so that their roundings are small.
+    const float small = softcap >= 0x1p-11f && softcap <= 0x1p12f ? std::min(kSmall / over, 1e4f / (c * over)) : -1.0f;
     Task t = {logits, tokens, logprobs, entropy, top_ids, top_logprobs, stride, n_given, k, V, c, more, small,
               parts_of(n, V), 0, static_cast<uint8_t *>(workspace)};
     if (t.parts > 1) {

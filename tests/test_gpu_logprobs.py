@@ -348,3 +348,14 @@ def test_many_tokens_of_a_row(gd, m):
         g = torch.Generator().manual_seed(m)
         x = torch.randn(n, V, generator=g).mul(3).cuda()
         run(gd, x, given(n, V, m, m), 2, rows=[0, n - 1])
+
+
+@pytest.mark.parametrize("cap", [1e-4, 1e-3, 1.0, 4e3, 5e3, 1e5, 1e8, 1e12, 1e30])
+def test_caps_next_to_the_logits(gd, cap):
+    """Logits up to the cap and up to twice it, at every magnitude of both that is accepted."""
+    V, scale = 9001, 10.0 / cap
+    g = torch.Generator().manual_seed(6)
+    for most in (0.1, 0.69, 2.0):
+        x = torch.rand(3, V, generator=g).mul(2).sub(1).mul(most * cap).cuda()
+        run(gd, x, given(3, V, 2, 2), 3, scale, cap)
+        run(gd, x.repeat(100, 1).contiguous(), given(300, V, 2, 2), 3, scale, cap, rows=[0, 1, 2])
