@@ -59,7 +59,7 @@ def logprobs(x, tokens, k: int, scale: float = 1.0, cap: float = 0.0):
     x = np.asarray(x, np.float64)
     scale, cap = float(np.float32(scale)), float(np.float32(cap))
     if np.isnan(x).any() or (x == np.inf).any():
-        return np.where(tokens < 0, 0.0, np.nan), np.nan, np.full(k, -1), np.full(k, np.nan)
+        return np.where((tokens >= 0) & (tokens < len(x)), np.nan, 0.0), np.nan, np.full(k, -1), np.full(k, np.nan)
     banned = x == -np.inf
     with np.errstate(invalid="ignore", divide="ignore"):
         z = scale * (cap * np.tanh(x / cap) if cap else x)

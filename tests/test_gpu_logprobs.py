@@ -359,3 +359,12 @@ def test_caps_next_to_the_logits(gd, cap):
         x = torch.rand(3, V, generator=g).mul(2).sub(1).mul(most * cap).cuda()
         run(gd, x, given(3, V, 2, 2), 3, scale, cap)
         run(gd, x.repeat(100, 1).contiguous(), given(300, V, 2, 2), 3, scale, cap, rows=[0, 1, 2])
+
+
+@pytest.mark.parametrize("V", [3, 5003, 50021])
+def test_tokens_outside_the_vocabulary_are_padding(gd, V):
+    """Of whole rows and of rows cut into parts, of rows that hold a NaN or an infinity too."""
+    x = torch.zeros(5, V)
+    x[1, 0], x[2, V - 1], x[3] = float("nan"), float("inf"), -float("inf")
+    tokens = torch.tensor([[-1, V, 1, V + 1, 1 << 40, -(1 << 40)]] * 5).cuda()
+    run(gd, x.cuda(), tokens, 2)

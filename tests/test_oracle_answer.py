@@ -58,3 +58,10 @@ def test_logprobs_of_rows_with_little_left():
     for bad in (np.nan, inf):
         lp, entropy, ids, tops = answer.logprobs(np.array([bad, 1.0]), np.array([1, -1]), 1)
         assert np.isnan(lp[0]) and lp[1] == 0 and np.isnan(entropy) and ids[0] == -1 and np.isnan(tops[0])
+
+
+def test_tokens_outside_the_vocabulary_are_padding():
+    """Of rows that hold a NaN or an infinity too."""
+    for x in ([1.0, 2.0], [np.nan, 2.0], [np.inf, 2.0], [-np.inf, -np.inf]):
+        lp = answer.logprobs(np.array(x), np.array([-1, 2, 7]), 1)[0]
+        assert list(lp) == [0, 0, 0]
