@@ -289,8 +289,6 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
             }
         if (best.count >= 2 * best.k) best.shrink();
     }
-    // (The ends, a logit a lane, have one way only: they are short, and code that runs once is fetched first.)
-    constexpr bool kEnds = N == 1;
     const auto is_easy = [&]() { return kCap ? least >= -cap.small && mine <= cap.small : least >= w.low; };
     bool chosen = false;   // the lane that holds the step's new largest logit
     float out = -kInf;     // what stands in its place
@@ -366,6 +364,7 @@ __device__ __forceinline__ void absorb(Met &w, Best &best, const Cap<kCap> &cap,
     if (kEntropy) w.D += factor * fmaf(down, S, D);
     w.S += factor * S;
 }
+
 // What a part adds to the sums against `top`, a logit as large as its own: its share of S and D
 // with its own largest logit, which it holds out of them; nothing if it has none.
 template <bool kCap>

@@ -747,9 +747,9 @@ int attn_decode_q8_workspace_bytes(int64_t n_seqs, int64_t n_q, int64_t n_heads,
  * Accuracy: log probabilities and entropies within 2^-17 of their magnitude (of a
  * confident token's as well, whose log probability is next to 0) plus 2^-100 (V 2^-119
  * past 2^19 tokens: f32 exponentials end at 2^-126); with a softcap 2^-20 * scale *
- * softcap more. One of n_given, k and entropy is asked for. Limits: 1 <= V <= 2^30, 1 <= n < 2^23, n_given <= 65536, k <= 64,
- * n * n_given < 2^31, 0 < scale <= 1e30, softcap 0 or in [1e-4, 1e30] and scale *
- * softcap <= 1e30.
+ * softcap more. One of n_given, k and entropy is asked for. Limits: 1 <= V <= 2^30,
+ * 1 <= n < 2^23, n_given <= 65536, k <= 64, n * n_given < 2^31, 0 < scale <= 1e30,
+ * softcap 0 or in [1e-4, 1e30] and scale * softcap <= 1e30.
  * Errors: GD_EINVAL, GD_EALIGN, GD_ERANGE, GD_EHIP. */
 int token_logprobs(const void *logits, int64_t stride, const int64_t *tokens, int64_t n_given,
                    float *logprobs, float *entropy, int64_t *top_ids, float *top_logprobs, int64_t k,
